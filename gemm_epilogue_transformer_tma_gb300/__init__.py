@@ -28,6 +28,7 @@ PARTIAL_COLS = 128
 STATUS_NAMES = {
     0: "CODA_OK", 1: "CODA_ERR_INVALID_ARG", 2: "CODA_ERR_ALIGNMENT", 3: "CODA_ERR_UNSUPPORTED",
     4: "CODA_ERR_WORKSPACE_TOO_SMALL", 5: "CODA_ERR_CUDA", 6: "CODA_ERR_TIMEOUT", 7: "CODA_ERR_LABEL_RANGE",
+    8: "CODA_ERR_POSITION_RANGE",
 }
 
 
@@ -96,6 +97,18 @@ SIGNATURES = {
     "coda_rope_table": (_INT, [_P, _P, _P, _I64, _I64, _F32, _P]),
     "coda_gemm_qkv_rope": (_INT, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P]),
     "coda_rope_apply": (_INT, [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P]),
+    "coda_qknorm_rope": (_INT, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _F32, _P]),
+    "coda_qknorm_rope_bwd_workspace_bytes": (_SZ, [_I64, _I64]),
+    "coda_qknorm_rope_bwd": (_INT, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ,
+                                    _I64, _I64, _I64, _I64, _I64, _F32, _P]),
+    "coda_fp8_block_scale_bytes": (_SZ, [_I64, _I64]),
+    "coda_fp8_block_quantize": (_INT, [_P, _P, _INT, _P, _P, _P, _P, _I64, _I64, _P]),
+    "coda_fp8_block_quantize_weight": (_INT, [_P, _P, _INT, _P, _P, _P, _I64, _I64, _P]),
+    "coda_fp8_block_dequantize": (_INT, [_P, _P, _P, _INT, _INT, _P, _I64, _I64, _P]),
+    "coda_gemm_fp8_block": (_INT, [_P, _P, _INT, _INT, _P, _P, _INT, _INT, _P, _P, _I64, _I64, _I64, _P]),
+    "coda_lmhead_policy_workspace_bytes": (_SZ, [_I64, _I64, _I64, _INT]),
+    "coda_lmhead_policy": (_INT, [_P, _P, _P, _P, _P, _P, _P, _P, _F32, _F32, _F32, _F32, _P, _P, _P, _P, _P, _SZ,
+                                  _I64, _I64, _I64, _P]),
     "coda_fp8_quantize": (_INT, [_P, _P, _P, _P, _P, _I64, _I64, _P]),
     "coda_fp8_quantize_e5m2": (_INT, [_P, _P, _P, _P, _P, _I64, _I64, _P]),
     "coda_swiglu_bwd_fp8": (_INT, [_P, _P, _P, _P, _INT, _P, _P, _P, _I64, _I64, _I64, _P]),
@@ -162,6 +175,19 @@ def handle(device: int | None = None) -> int:
 def _stream(stream=None) -> int:
     s = torch.cuda.current_stream() if stream is None else stream
     return s.cuda_stream
+
+
+def _stream_on(t: torch.Tensor, stream=None) -> int:
+    """The given stream, or the current one of t's device."""
+    s = torch.cuda.current_stream(t.device) if stream is None else stream
+    return s.cuda_stream
+
+
+def _together(*tensors):
+    """Every given tensor on the first one's device (the handle's)."""
+    for t in tensors[1:]:
+        if t is not None and t.device != tensors[0].device:
+            raise ValueError(f"tensors on {tensors[0].device} and {t.device}")
 
 
 def _ptr(t: torch.Tensor | None, dtype=None, name="tensor") -> int | None:
@@ -629,6 +655,58 @@ def coda_rope_apply(qkv, cos_t, sin_t, n_q_heads, n_kv_heads, head_dim=128, stre
                                           _stream(stream)), "coda_rope_apply")
 
 
+def coda_qknorm_rope(qkv, gq, gk, cos_t, sin_t, out, n_q_heads, n_kv_heads, head_dim=128, eps=1e-6,
+                     positions=None, stream=None):
+    """RMSNorm of the q and k heads (weights gq, gk), then RoPE, in one pass;
+    out may be qkv (see include/coda.h)."""
+    M = qkv.shape[0]
+    S = cos_t.shape[0]
+    _shape(qkv, (M, (n_q_heads + 2 * n_kv_heads) * head_dim), "qkv")
+    _shape(out, qkv.shape, "out")
+    _head_shapes(gq, gk, cos_t, sin_t, positions, M, S, n_kv_heads, head_dim)
+    _together(qkv, gq, gk, cos_t, sin_t, positions, out)
+    _check(load_library().coda_qknorm_rope(
+        _h(qkv), _ptr(qkv, BF, "qkv"), _ptr(gq, BF, "gq"), _ptr(gk, BF, "gk"), _ptr(cos_t, F32, "cos_t"),
+        _ptr(sin_t, F32, "sin_t"), _ptr(positions, I32, "positions"), _ptr(out, BF, "out"), M, n_q_heads, n_kv_heads,
+        head_dim, S, eps, _stream_on(qkv, stream)), "coda_qknorm_rope")
+
+
+def _head_shapes(gq, gk, cos_t, sin_t, positions, M, S, n_kv_heads, head_dim):
+    _shape(gq, (head_dim,), "gq")
+    if gk is not None or n_kv_heads > 0:
+        _shape(gk, (head_dim,), "gk")
+    _shape(cos_t, (S, head_dim // 2), "cos_t")
+    _shape(sin_t, (S, head_dim // 2), "sin_t")
+    if positions is not None:
+        _shape(positions, (M,), "positions")
+
+
+def coda_qknorm_rope_bwd_workspace_bytes(M: int, head_dim: int) -> int:
+    return load_library().coda_qknorm_rope_bwd_workspace_bytes(M, head_dim)
+
+
+def coda_qknorm_rope_bwd(dout, qkv, gq, gk, cos_t, sin_t, dqkv, dgq, dgk, ws, n_q_heads, n_kv_heads, head_dim=128,
+                         eps=1e-6, positions=None, stream=None):
+    """Backward of coda_qknorm_rope from dout and its input qkv; dqkv may be
+    dout or qkv (see include/coda.h)."""
+    M = qkv.shape[0]
+    S = cos_t.shape[0]
+    _shape(qkv, (M, (n_q_heads + 2 * n_kv_heads) * head_dim), "qkv")
+    _shape(dout, qkv.shape, "dout")
+    _shape(dqkv, qkv.shape, "dqkv")
+    _head_shapes(gq, gk, cos_t, sin_t, positions, M, S, n_kv_heads, head_dim)
+    _shape(dgq, (head_dim,), "dgq")
+    if dgk is not None or n_kv_heads > 0:
+        _shape(dgk, (head_dim,), "dgk")
+    _together(dgq, dout, qkv, gq, gk, cos_t, sin_t, positions, dqkv, dgk, ws)
+    _check(load_library().coda_qknorm_rope_bwd(
+        _h(dgq), _ptr(dout, BF, "dout"), _ptr(qkv, BF, "qkv"), _ptr(gq, BF, "gq"), _ptr(gk, BF, "gk"),
+        _ptr(cos_t, F32, "cos_t"), _ptr(sin_t, F32, "sin_t"), _ptr(positions, I32, "positions"),
+        _ptr(dqkv, BF, "dqkv"), _ptr(dgq, F32, "dgq"), _ptr(dgk, F32, "dgk"), _ptr(ws, None, "ws"),
+        ws.numel() * ws.element_size(), M, n_q_heads, n_kv_heads, head_dim, S, eps, _stream_on(dgq, stream)),
+        "coda_qknorm_rope_bwd")
+
+
 U8 = torch.uint8
 
 
@@ -767,6 +845,76 @@ def coda_gemm_rowscale_swiglu_fp8(Hq, sH, W2gq, sW2, rstd, out, z_save=None, fla
                                                         _stream(stream)), "coda_gemm_rowscale_swiglu_fp8")
 
 
+def coda_fp8_block_scale_bytes(rows: int, K: int) -> int:
+    """Bytes of the packed block scales of an operand with `rows` rows and a
+    contracted extent K."""
+    return load_library().coda_fp8_block_scale_bytes(rows, K)
+
+
+def _scales(s, rows, K, name):
+    if s is not None:
+        _shape(s, (coda_fp8_block_scale_bytes(rows, K),), name)
+
+
+def coda_fp8_block_quantize(src, q_row, s_row, q_col, s_col, fmt: int = E4M3, stream=None):
+    """Codes of src with a scale for each 1 x 128 block (q_row, s_row) and /
+    or each 128 x 1 block (q_col, s_col); a pair may be None (see
+    include/coda.h)."""
+    rows, cols = src.shape
+    for q, s, r, k, n in ((q_row, s_row, rows, cols, "row"), (q_col, s_col, cols, rows, "col")):
+        if (q is None) != (s is None):
+            raise ValueError(f"q_{n} and s_{n} come together")
+        if q is not None:
+            _shape(q, (rows, cols), f"q_{n}")
+            _scales(s, r, k, f"s_{n}")
+    _together(src, q_row, s_row, q_col, s_col)
+    _check(load_library().coda_fp8_block_quantize(
+        _h(src), _ptr(src, BF, "src"), int(fmt), _ptr(q_row, U8, "q_row"), _ptr(s_row, U8, "s_row"),
+        _ptr(q_col, U8, "q_col"), _ptr(s_col, U8, "s_col"), rows, cols, _stream_on(src, stream)),
+        "coda_fp8_block_quantize")
+
+
+def coda_fp8_block_quantize_weight(W, q, s, s_t, fmt: int = E4M3, stream=None):
+    """Codes of W [N, K] with a scale for each 128 x 128 block; s for the
+    product over K, s_t for the one over N (see include/coda.h)."""
+    N, K = W.shape
+    _shape(q, (N, K), "q")
+    _scales(s, N, K, "s")
+    _scales(s_t, K, N, "s_t")
+    _together(W, q, s, s_t)
+    _check(load_library().coda_fp8_block_quantize_weight(
+        _h(W), _ptr(W, BF, "W"), int(fmt), _ptr(q, U8, "q"), _ptr(s, U8, "s"), _ptr(s_t, U8, "s_t"), N, K,
+        _stream_on(W, stream)), "coda_fp8_block_quantize_weight")
+
+
+def coda_fp8_block_dequantize(q, s, col_blocks: bool, dst, fmt: int = E4M3, stream=None):
+    """dst = the bf16 values of codes q with packed scales s of blocks along
+    the rows, or along the columns with col_blocks (see include/coda.h)."""
+    rows, cols = q.shape
+    _shape(dst, (rows, cols), "dst")
+    _scales(s, *((cols, rows) if col_blocks else (rows, cols)), "s")
+    _together(q, s, dst)
+    _check(load_library().coda_fp8_block_dequantize(
+        _h(q), _ptr(q, U8, "q"), _ptr(s, U8, "s"), int(col_blocks), int(fmt), _ptr(dst, BF, "dst"), rows, cols,
+        _stream_on(q, stream)), "coda_fp8_block_dequantize")
+
+
+def coda_gemm_fp8_block(A, a_mn_major: bool, a_format: int, sA, B, b_mn_major: bool, b_format: int, sB, C,
+                        M: int, N: int, K: int, stream=None):
+    """C[M,N] = A B on 8-bit codes with packed block scales along K (see
+    include/coda.h)."""
+    _shape(A, (K, M) if a_mn_major else (M, K), "A")
+    _shape(B, (K, N) if b_mn_major else (N, K), "B")
+    _shape(C, (M, N), "C")
+    _scales(sA, M, K, "sA")
+    _scales(sB, N, K, "sB")
+    _together(C, A, sA, B, sB)
+    _check(load_library().coda_gemm_fp8_block(
+        _h(C), _ptr(A, U8, "A"), int(a_mn_major), int(a_format), _ptr(sA, U8, "sA"), _ptr(B, U8, "B"),
+        int(b_mn_major), int(b_format), _ptr(sB, U8, "sB"), _ptr(C, BF, "C"), M, N, K, _stream_on(C, stream)),
+        "coda_gemm_fp8_block")
+
+
 def coda_lmhead_ce_workspace_bytes(M: int, d: int, V: int, with_grads: bool) -> int:
     return load_library().coda_lmhead_ce_workspace_bytes(M, d, V, int(with_grads))
 
@@ -826,6 +974,36 @@ def coda_lmhead_ce_fp8(Hq, sH, Wq, sW, labels, loss, lse, argmax, dHs, dWt, ws, 
         _ptr(labels, I32, "labels"), _ptr(loss, F32, "loss"), _ptr(lse, F32, "lse"), _ptr(argmax, I32, "argmax"),
         _ptr(dHs, BF, "dHs"), _ptr(dWt, BF, "dWt"), _ptr(ws, None, "ws"), ws.numel() * ws.element_size(), M, d, V,
         _stream(stream)), "coda_lmhead_ce_fp8")
+
+
+def coda_lmhead_policy_workspace_bytes(M: int, d: int, V: int, with_grads: bool) -> int:
+    return load_library().coda_lmhead_policy_workspace_bytes(M, d, V, int(with_grads))
+
+
+def coda_lmhead_policy(Hs, Wt, labels, advantage, weight, logp_old, logp_ref, clip_low: float, clip_high: float,
+                       kl_coef: float, temperature: float, stats, logp, dHs, dWt, ws, stream=None):
+    """Clipped policy loss with a KL term on the LM head; weight, logp_old,
+    logp_ref and the gradients dHs, dWt may be None (see include/coda.h)."""
+    M, d = Hs.shape
+    V = Wt.shape[0]
+    _shape(Wt, (V, d), "Wt")
+    for t, n in ((labels, "labels"), (advantage, "advantage"), (weight, "weight"), (logp_old, "logp_old"),
+                 (logp_ref, "logp_ref"), (logp, "logp")):
+        if t is not None:
+            _shape(t, (M,), n)
+    _shape(stats, (4,), "stats")
+    if (dHs is None) != (dWt is None):
+        raise ValueError("dHs and dWt come together")
+    if dHs is not None:
+        _shape(dHs, (M, d), "dHs")
+        _shape(dWt, (V, d), "dWt")
+    _together(Hs, Wt, labels, advantage, weight, logp_old, logp_ref, stats, logp, dHs, dWt, ws)
+    _check(load_library().coda_lmhead_policy(
+        _h(Hs), _ptr(Hs, BF, "Hs"), _ptr(Wt, BF, "Wt"), _ptr(labels, I32, "labels"),
+        _ptr(advantage, F32, "advantage"), _ptr(weight, F32, "weight"), _ptr(logp_old, F32, "logp_old"),
+        _ptr(logp_ref, F32, "logp_ref"), clip_low, clip_high, kl_coef, temperature, _ptr(stats, F32, "stats"),
+        _ptr(logp, F32, "logp"), _ptr(dHs, BF, "dHs"), _ptr(dWt, BF, "dWt"), _ptr(ws, None, "ws"),
+        ws.numel() * ws.element_size(), M, d, V, _stream_on(Hs, stream)), "coda_lmhead_policy")
 
 
 def coda_unfused_workspace_bytes(M: int, d: int, N2: int) -> int:

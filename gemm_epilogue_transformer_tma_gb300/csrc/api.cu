@@ -130,6 +130,19 @@ struct Check {
   }
 };
 
+// The handle's device as the current one for a call's duration: a caller may
+// hold tensors and streams of another device.
+struct OnDevice {
+  int prev = -1;
+  explicit OnDevice(int device) {
+    int cur = -1;
+    if (cudaGetDevice(&cur) == cudaSuccess && cur != device && cudaSetDevice(device) == cudaSuccess) prev = cur;
+  }
+  ~OnDevice() {
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+};
+
 size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -172,6 +185,19 @@ bool make_tmap_store_bf16(CUtensorMap* m, const void* base, uint64_t cols, uint6
 
 bool make_tmap_store_u8_sw32(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t ld) {
   return make_tmap_store(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, CU_TENSOR_MAP_SWIZZLE_32B, base, cols, rows, ld);
+}
+
+bool make_tmap_scale_chunks(CUtensorMap* m, const void* base, uint64_t chunks) {
+  std::call_once(g_encode_once, resolve_encode);
+  if (g_encode == nullptr) return false;
+  const cuuint64_t dims[2] = {128, chunks};  // 32-bit words, one per row of a chunk
+  const cuuint64_t strides[1] = {512};
+  const cuuint32_t box[2] = {128, 1};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
 }
 
 bool make_tmap_store_f32(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t ld) {
@@ -266,6 +292,7 @@ const char* coda_status_string(coda_status_t s) {
     case CODA_ERR_CUDA: return "CUDA runtime or driver error";
     case CODA_ERR_TIMEOUT: return "an in-kernel wait hit its time limit";
     case CODA_ERR_LABEL_RANGE: return "a label was outside [0, V)";
+    case CODA_ERR_POSITION_RANGE: return "a position was outside the rotary table";
   }
   return "unknown status";
 }
@@ -282,6 +309,7 @@ coda_status_t coda_sync_status(coda_handle_t h, void* stream, int32_t* device_bi
   if (bits & (DEV_ERR_TIMEOUT_PRODUCER | DEV_ERR_TIMEOUT_MMA | DEV_ERR_TIMEOUT_EPILOGUE | DEV_ERR_TIMEOUT_DRAIN))
     return CODA_ERR_TIMEOUT;
   if (bits & DEV_ERR_LABEL_RANGE) return CODA_ERR_LABEL_RANGE;
+  if (bits & DEV_ERR_POSITION_RANGE) return CODA_ERR_POSITION_RANGE;
   return CODA_OK;
 }
 
@@ -652,6 +680,150 @@ coda_status_t coda_rope_apply(coda_handle_t h, void* qkv, const float* cos_t, co
   const int64_t N = (n_q_heads + 2 * n_kv_heads) * head_dim;
   return from_cuda(launch_rope_apply(ctx_of(h, stream), static_cast<bf16*>(qkv), cos_t, sin_t, M, N,
                                      (n_q_heads + n_kv_heads) * head_dim, head_dim, S));
+}
+
+coda_status_t coda_qknorm_rope(coda_handle_t h, const void* qkv, const void* gq, const void* gk, const float* cos_t,
+                               const float* sin_t, const int32_t* positions, void* out, int64_t M, int64_t n_q_heads,
+                               int64_t n_kv_heads, int64_t head_dim, int64_t S, float eps, void* stream) {
+  CODA_TRY(Check()
+               .handle(h)
+               .rows(M)
+               .mptr(qkv, M)
+               .ptr(gq)
+               .mptr(gk, n_kv_heads)
+               .ptr(cos_t)
+               .ptr(sin_t)
+               .opt_sptr(positions)
+               .mptr(out, M)
+               .st);
+  CODA_TRY(check_heads(n_q_heads, n_kv_heads, head_dim, S));
+  if (!(eps >= 0.f) || std::isinf(eps)) return CODA_ERR_INVALID_ARG;
+  if (head_dim > 512) return CODA_ERR_UNSUPPORTED;
+  if (M == 0) return CODA_OK;
+  const OnDevice dev(h->device);
+  return from_cuda(launch_qknorm_rope(ctx_of(h, stream), static_cast<const bf16*>(qkv), static_cast<const bf16*>(gq),
+                                      static_cast<const bf16*>(gk), cos_t, sin_t, positions, static_cast<bf16*>(out),
+                                      M, int(n_q_heads), int(n_kv_heads), int(head_dim), S, eps));
+}
+
+size_t coda_qknorm_rope_bwd_workspace_bytes(int64_t M, int64_t head_dim) {
+  if (M <= 0 || head_dim <= 0 || head_dim > 512) return 0;
+  return size_t(qknorm_max_parts()) * 2 * head_dim * sizeof(float);
+}
+
+coda_status_t coda_qknorm_rope_bwd(coda_handle_t h, const void* dout, const void* qkv, const void* gq, const void* gk,
+                                   const float* cos_t, const float* sin_t, const int32_t* positions, void* dqkv,
+                                   float* dgq, float* dgk, void* ws, size_t ws_bytes, int64_t M, int64_t n_q_heads,
+                                   int64_t n_kv_heads, int64_t head_dim, int64_t S, float eps, void* stream) {
+  CODA_TRY(Check()
+               .handle(h)
+               .rows(M)
+               .mptr(dout, M)
+               .mptr(qkv, M)
+               .ptr(gq)
+               .mptr(gk, n_kv_heads)
+               .ptr(cos_t)
+               .ptr(sin_t)
+               .opt_sptr(positions)
+               .mptr(dqkv, M)
+               .ptr(dgq)
+               .mptr(dgk, n_kv_heads)
+               .mptr(ws, M)
+               .st);
+  CODA_TRY(check_heads(n_q_heads, n_kv_heads, head_dim, S));
+  if (!(eps >= 0.f) || std::isinf(eps)) return CODA_ERR_INVALID_ARG;
+  if (head_dim > 512 || n_q_heads + 2 * n_kv_heads > 1024) return CODA_ERR_UNSUPPORTED;
+  if (ws_bytes < coda_qknorm_rope_bwd_workspace_bytes(M, head_dim)) return CODA_ERR_WORKSPACE_TOO_SMALL;
+  const OnDevice dev(h->device);
+  const LaunchCtx cx = ctx_of(h, stream);
+  if (M == 0) {  // an empty batch: the weight gradients are empty sums
+    CODA_CUDA(cudaMemsetAsync(dgq, 0, size_t(head_dim) * 4, cx.stream));
+    if (n_kv_heads > 0) CODA_CUDA(cudaMemsetAsync(dgk, 0, size_t(head_dim) * 4, cx.stream));
+    return CODA_OK;
+  }
+  return from_cuda(launch_qknorm_rope_bwd(cx, static_cast<const bf16*>(dout), static_cast<const bf16*>(qkv),
+                                          static_cast<const bf16*>(gq), static_cast<const bf16*>(gk), cos_t, sin_t,
+                                          positions, static_cast<bf16*>(dqkv), dgq, dgk, static_cast<float*>(ws), M,
+                                          int(n_q_heads), int(n_kv_heads), int(head_dim), S, eps));
+}
+
+// ---------------------------------------------------------------------------
+size_t coda_fp8_block_scale_bytes(int64_t rows, int64_t K) {
+  if (rows <= 0 || K <= 0 || rows > kMaxExtent || K > kMaxExtent) return 0;
+  return size_t(cdiv(rows, 128)) * size_t(cdiv(K, 512)) * 512;
+}
+
+coda_status_t coda_fp8_block_quantize(coda_handle_t h, const void* src, int format, void* q_row, void* s_row,
+                                      void* q_col, void* s_col, int64_t rows, int64_t cols, void* stream) {
+  CODA_TRY(Check().handle(h).rows(rows).mptr(src, rows).cols(cols).st);
+  CODA_TRY(Check().opt_ptr(q_row).opt_ptr(s_row).opt_ptr(q_col).opt_ptr(s_col).st);
+  if (format != 0 && format != 1) return CODA_ERR_INVALID_ARG;
+  if (cols % 16 != 0) return CODA_ERR_ALIGNMENT;
+  if (rows == 0) return CODA_OK;
+  if ((q_row == nullptr) != (s_row == nullptr) || (q_col == nullptr) != (s_col == nullptr) ||
+      (q_row == nullptr && q_col == nullptr) || (q_row != nullptr && q_row == q_col))
+    return CODA_ERR_INVALID_ARG;
+  const OnDevice dev(h->device);
+  return from_cuda(launch_fp8_block_quantize(ctx_of(h, stream), static_cast<const bf16*>(src), format == 1,
+                                             static_cast<uint8_t*>(q_row), static_cast<uint8_t*>(s_row),
+                                             static_cast<uint8_t*>(q_col), static_cast<uint8_t*>(s_col), false, rows,
+                                             cols));
+}
+
+coda_status_t coda_fp8_block_quantize_weight(coda_handle_t h, const void* W, int format, void* q, void* s, void* s_t,
+                                             int64_t N, int64_t K, void* stream) {
+  CODA_TRY(Check().handle(h).ptr(W).ptr(q).ptr(s).ptr(s_t).rows(N).cols(K).st);
+  if (N == 0 || (format != 0 && format != 1)) return CODA_ERR_INVALID_ARG;
+  if (K % 16 != 0) return CODA_ERR_ALIGNMENT;
+  const OnDevice dev(h->device);
+  return from_cuda(launch_fp8_block_quantize(ctx_of(h, stream), static_cast<const bf16*>(W), format == 1,
+                                             static_cast<uint8_t*>(q), static_cast<uint8_t*>(s), nullptr,
+                                             static_cast<uint8_t*>(s_t), true, N, K));
+}
+
+coda_status_t coda_fp8_block_dequantize(coda_handle_t h, const void* q, const void* s, int col_blocks, int format,
+                                        void* dst, int64_t rows, int64_t cols, void* stream) {
+  CODA_TRY(Check().handle(h).rows(rows).mptr(q, rows).mptr(s, rows).mptr(dst, rows).cols(cols).st);
+  if (format != 0 && format != 1) return CODA_ERR_INVALID_ARG;
+  if (cols % 16 != 0) return CODA_ERR_ALIGNMENT;
+  if (rows == 0) return CODA_OK;
+  const OnDevice dev(h->device);
+  return from_cuda(launch_fp8_block_dequantize(ctx_of(h, stream), static_cast<const uint8_t*>(q),
+                                               static_cast<const uint8_t*>(s), format == 1, col_blocks != 0,
+                                               static_cast<bf16*>(dst), rows, cols));
+}
+
+coda_status_t coda_gemm_fp8_block(coda_handle_t h, const void* A, int a_mn_major, int a_format, const void* sA,
+                                  const void* B, int b_mn_major, int b_format, const void* sB, void* C, int64_t M,
+                                  int64_t N, int64_t K, void* stream) {
+  if ((a_format != 0 && a_format != 1) || (b_format != 0 && b_format != 1)) return CODA_ERR_INVALID_ARG;
+  if (a_mn_major && !b_mn_major) return CODA_ERR_UNSUPPORTED;
+  // as coda_gemm_fp8: with both operands MN-major K is a token count, any >= 0
+  const bool k_rows = a_mn_major && b_mn_major;
+  const int64_t n_ops = k_rows && K == 0 ? 0 : M;
+  const int64_t n_b = k_rows ? K : 1;
+  CODA_TRY(Check()
+               .handle(h)
+               .rows(M)
+               .mptr(A, n_ops)
+               .mptr(sA, n_ops)
+               .mptr(B, n_b)
+               .mptr(sB, n_b)
+               .mptr(C, M)
+               .cols(N)
+               .st);
+  CODA_TRY((k_rows ? Check().rows(K) : Check().cols(K)).st);
+  if (!k_rows && K % 16 != 0) return CODA_ERR_ALIGNMENT;
+  if (a_mn_major && M % 16 != 0) return CODA_ERR_ALIGNMENT;
+  if (b_mn_major && N % 16 != 0) return CODA_ERR_ALIGNMENT;
+  if (M == 0) return CODA_OK;
+  const OnDevice dev(h->device);
+  if (K == 0)
+    return from_cuda(cudaMemsetAsync(C, 0, size_t(M) * N * 2, static_cast<cudaStream_t>(stream)));
+  return from_cuda(gemm_fp8_block(ctx_of(h, stream), static_cast<const uint8_t*>(A), a_mn_major != 0, a_format,
+                                  static_cast<const uint8_t*>(sA), static_cast<const uint8_t*>(B), b_mn_major != 0,
+                                  b_format, static_cast<const uint8_t*>(sB), static_cast<bf16*>(C), int(M), int(N),
+                                  int(K)));
 }
 
 // ---------------------------------------------------------------------------
@@ -1033,6 +1205,110 @@ coda_status_t coda_lmhead_ce_fp8(coda_handle_t h, const void* Hq, const float* s
                                     static_cast<bf16*>(dWt) + v0 * d, int(M), int(d), int(Vc)));
   }
   CODA_CUDA(launch_f32_to_bf16(cx, w.dH32, static_cast<bf16*>(dHs), M * d));
+  return CODA_OK;
+}
+
+namespace {
+// the cross-entropy's workspace, then the policy loss's per-row arrays
+struct PolicyWs {
+  CeWs ce;
+  int32_t* labels;
+  float* lse;
+  float* row_scale;
+  float4* terms;
+  size_t bytes;
+};
+
+PolicyWs policy_layout(uint8_t* base, int64_t M, int64_t d, int64_t V, bool grads) {
+  PolicyWs w{};
+  w.ce = ce_layout(base, M, d, V, grads);
+  size_t off = w.ce.bytes;
+  auto take = [&](size_t b) {
+    uint8_t* p = base ? base + off : nullptr;
+    off += align256(b);
+    return p;
+  };
+  w.labels = reinterpret_cast<int32_t*>(take(size_t(M) * 4));
+  w.lse = reinterpret_cast<float*>(take(size_t(M) * 4));
+  w.terms = reinterpret_cast<float4*>(take(size_t(M) * 16));
+  if (grads) w.row_scale = reinterpret_cast<float*>(take(size_t(M) * 4));
+  w.bytes = off;
+  return w;
+}
+}  // namespace
+
+size_t coda_lmhead_policy_workspace_bytes(int64_t M, int64_t d, int64_t V, int with_grads) {
+  if (M <= 0 || d <= 0 || V <= 0) return 0;
+  return policy_layout(nullptr, M, d, V, with_grads != 0).bytes;
+}
+
+coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt, const int32_t* labels,
+                                 const float* advantage, const float* weight, const float* logp_old,
+                                 const float* logp_ref, float clip_low, float clip_high, float kl_coef,
+                                 float temperature, float* stats, float* logp, void* dHs, void* dWt, void* ws,
+                                 size_t ws_bytes, int64_t M, int64_t d, int64_t V, void* stream) {
+  CODA_TRY(Check()
+               .handle(h)
+               .ptr(Hs)
+               .ptr(Wt)
+               .sptr(labels)
+               .sptr(advantage)
+               .opt_sptr(weight)
+               .opt_sptr(logp_old)
+               .opt_sptr(logp_ref)
+               .sptr(stats)
+               .sptr(logp)
+               .opt_ptr(dHs)
+               .opt_ptr(dWt)
+               .ptr(ws)
+               .rows(M)
+               .cols(d)
+               .cols(V)
+               .st);
+  if (M == 0) return CODA_ERR_INVALID_ARG;  // as coda_lmhead_ce
+  if (!(clip_low >= 0.f && clip_low <= 1.f) || !(clip_high >= 0.f)) return CODA_ERR_INVALID_ARG;
+  if (!(kl_coef >= 0.f) || std::isinf(kl_coef) || !(temperature > 0.f) || std::isinf(temperature))
+    return CODA_ERR_INVALID_ARG;
+  const bool grads = dHs != nullptr;
+  if (grads != (dWt != nullptr)) return CODA_ERR_INVALID_ARG;
+  if (ws_bytes < coda_lmhead_policy_workspace_bytes(M, d, V, grads)) return CODA_ERR_WORKSPACE_TOO_SMALL;
+  const OnDevice dev(h->device);
+  const PolicyWs w = policy_layout(static_cast<uint8_t*>(ws), M, d, V, grads);
+  const int64_t T = cdiv(V, ce_tile_cols());
+  LaunchCtx cx = ctx_of(h, stream);
+  const bf16* Hb = static_cast<const bf16*>(Hs);
+  const bf16* Wb = static_cast<const bf16*>(Wt);
+  CODA_CUDA(launch_policy_labels(cx, labels, weight, M, V, w.labels, w.ce.zy));
+  LaunchCtx cl = cx;  // the logits carry 1 / temperature
+  cl.scale_host = 1.0f / temperature;
+  CODA_CUDA(gemm_ce_stats(cl, Hb, Wb, w.labels, w.ce.pmax, w.ce.psum, w.ce.parg, w.ce.zy, int(M), int(d), int(V),
+                          int(T)));
+  PolicyRows r{};
+  r.labels_in = w.labels;
+  r.adv = advantage;
+  r.weight = weight;
+  r.old = logp_old;
+  r.ref = logp_ref;
+  r.uniform = 1.0f / static_cast<float>(M);
+  r.lo = 1.0f - clip_low;
+  r.hi = 1.0f + clip_high;
+  r.beta = kl_coef;
+  r.inv_temp = cl.scale_host;
+  r.lse = w.lse;
+  r.logp = logp;
+  r.row_scale = w.row_scale;
+  r.terms = w.terms;
+  CODA_CUDA(launch_policy_rows(cx, w.ce.pmax, w.ce.psum, w.ce.zy, r, M, T, V, stats));
+  if (!grads) return CODA_OK;
+  const int64_t chunk = h->ce_chunk;
+  for (int64_t v0 = 0; v0 < V; v0 += chunk) {
+    const int64_t Vc = std::min<int64_t>(chunk, V - v0);
+    const bf16* Wc = Wb + v0 * d;
+    CODA_CUDA(gemm_ce_grad(cl, Hb, Wc, w.labels, w.lse, w.ce.dL, int(M), int(d), int(Vc), int(v0), 0.f, w.row_scale));
+    CODA_CUDA(gemm_group_ce_bwd(cx, w.ce.dL, Wc, Hb, w.ce.dH32, v0 > 0, static_cast<bf16*>(dWt) + v0 * d, int(M),
+                                int(d), int(Vc)));
+  }
+  CODA_CUDA(launch_f32_to_bf16(cx, w.ce.dH32, static_cast<bf16*>(dHs), M * d));
   return CODA_OK;
 }
 

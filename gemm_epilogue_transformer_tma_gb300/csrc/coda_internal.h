@@ -57,6 +57,9 @@ bool make_tmap_store_u8_sw32(CUtensorMap* m, const void* base, uint64_t cols, ui
 bool make_tmap_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_inner,
                   uint32_t box_outer);
 
+// Packed block scales as `chunks` rows of 512 bytes, loaded one at a time.
+bool make_tmap_scale_chunks(CUtensorMap* m, const void* base, uint64_t chunks);
+
 // Launch `kern` on c.stream with programmatic stream serialization: its
 // prologue may overlap the tail of the previous kernel in the stream.  Every
 // library kernel calls griddep_wait() before its first global-memory access,
@@ -134,10 +137,12 @@ cudaError_t gemm_dgrad_swiglu_bwd(const LaunchCtx& c, const __nv_bfloat16* dYb, 
 cudaError_t gemm_ce_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt, const int32_t* labels,
                           float* pmax, float* psum, int32_t* parg, float* zy, int M, int d, int V, int T);
 
-// dL chunk = (softmax - onehot) / M for vocabulary rows [v0, v0 + Vc).
+// dL chunk = (softmax - onehot) / M for vocabulary rows [v0, v0 + Vc), or
+// row_scale[m] (softmax - onehot) with row_scale != null.  The logits are
+// c.scale_host H Wt^T, as in gemm_ce_stats.
 cudaError_t gemm_ce_grad(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt_chunk,
                          const int32_t* labels, const float* lse, __nv_bfloat16* dL, int M, int d, int Vc, int v0,
-                         float inv_M);
+                         float inv_M, const float* row_scale = nullptr);
 
 // qkv = X Wqkv with RoPE (head_dim 128) on the first rot_cols columns.
 cudaError_t gemm_qkv_rope(const LaunchCtx& c, const __nv_bfloat16* X, const __nv_bfloat16* Wqkv_t,
@@ -208,6 +213,12 @@ cudaError_t gemm_group_ce_bwd_fp8(const LaunchCtx& c, const uint8_t* dLq, float 
                                   const float* sW, const uint8_t* Hq, const float* sH, float* dH32, bool accumulate,
                                   __nv_bfloat16* dWc, int M, int d, int Vc);
 
+// C = bf16(A B) on 8-bit operands with packed power-of-two scales for blocks
+// of 128 along K (gemm_block.cuh); operands and formats as gemm_store_fp8.
+cudaError_t gemm_fp8_block(const LaunchCtx& c, const uint8_t* A, bool a_mn, int a_fmt, const uint8_t* sA,
+                           const uint8_t* B, bool b_mn, int b_fmt, const uint8_t* sB, __nv_bfloat16* C, int M, int N,
+                           int K);
+
 int ce_tile_cols();    // vocabulary columns per CE statistics tile
 int prms_tile_cols();  // columns per partial-RMS tile of GEMM1
 
@@ -245,6 +256,42 @@ cudaError_t launch_swiglu_bwd_fp8(const LaunchCtx& c, const __nv_bfloat16* dY, c
 cudaError_t launch_swiglu_bwd_fp8_delayed(const LaunchCtx& c, const __nv_bfloat16* dY, const __nv_bfloat16* z,
                                           const float* rstd, float* state, uint8_t* dPq, float* cvec, int64_t M,
                                           int64_t F, int64_t d, int e5m2);
+// block quantisation (fp8_block.cu): codes and packed scales of blocks along
+// the rows (q_row, s_row) and / or along the columns (q_col, s_col); with
+// tile, 128 x 128 blocks: codes q_row, scales s_row and, transposed, s_col
+cudaError_t launch_fp8_block_quantize(const LaunchCtx& c, const __nv_bfloat16* src, bool e5m2, uint8_t* q_row,
+                                      uint8_t* s_row, uint8_t* q_col, uint8_t* s_col, bool tile, int64_t rows,
+                                      int64_t cols);
+cudaError_t launch_fp8_block_dequantize(const LaunchCtx& c, const uint8_t* q, const uint8_t* s, bool e5m2, bool col,
+                                        __nv_bfloat16* dst, int64_t rows, int64_t cols);
+// norm of the q and k heads, then RoPE (qknorm.cu); x may be out
+cudaError_t launch_qknorm_rope(const LaunchCtx& c, const __nv_bfloat16* x, const __nv_bfloat16* gq,
+                               const __nv_bfloat16* gk, const float* cos_t, const float* sin_t, const int32_t* pos,
+                               __nv_bfloat16* out, int64_t M, int n_q, int n_kv, int D, int64_t S, float eps);
+// its backward; part: fp32 [qknorm_max_parts()][2][D]; dx may be dy or x
+cudaError_t launch_qknorm_rope_bwd(const LaunchCtx& c, const __nv_bfloat16* dy, const __nv_bfloat16* x,
+                                   const __nv_bfloat16* gq, const __nv_bfloat16* gk, const float* cos_t,
+                                   const float* sin_t, const int32_t* pos, __nv_bfloat16* dx, float* dgq, float* dgk,
+                                   float* part, int64_t M, int n_q, int n_kv, int D, int64_t S, float eps);
+int qknorm_max_parts();
+// the policy loss's row kernels (policy.cu)
+struct PolicyRows {
+  const int32_t* labels_in;  // from launch_policy_labels
+  const float* adv;
+  const float* weight;       // or null: uniform
+  const float* old;          // or null: the current log-probabilities (ratio 1)
+  const float* ref;          // or null: no KL term
+  float uniform;             // weight of every row when weight is null
+  float lo, hi, beta, inv_temp;
+  float* lse;
+  float* logp;
+  float* row_scale;          // factor of (softmax - onehot), or null
+  float4* terms;
+};
+cudaError_t launch_policy_labels(const LaunchCtx& c, const int32_t* labels, const float* weight, int64_t M, int64_t V,
+                                 int32_t* out, float* zy);
+cudaError_t launch_policy_rows(const LaunchCtx& c, const float* pmax, const float* psum, const float* zy,
+                               const PolicyRows& p, int64_t M, int64_t T, int64_t V, float* stats);
 // unfused ablation kernels
 cudaError_t launch_add_rmsnorm(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_bfloat16* R,
                                const __nv_bfloat16* g, __nv_bfloat16* H, float* rstd, __nv_bfloat16* Nrm, int64_t M,

@@ -1,0 +1,374 @@
+// GEMM on 8-bit codes with a power-of-two scale for each block of 128 along
+// the contraction:
+//   C[m, n] = bf16( sum_b sA[m, b] sB[n, b] sum_{k in block b} A[m, k] B[n, k] )
+// The scales are applied by the tensor core: tcgen05.mma kind::mxf8f6f4 takes
+// one scale byte per row of A and of B for 32 elements of K, read from tensor
+// memory, so a block of 128 is four MMAs with the same byte and the fp32
+// accumulator never leaves TMEM between blocks.  (Scaling in the epilogue
+// warps instead would read all 128 x 256 accumulators back every 128 of K,
+// 256 FMA clocks and as many TMEM reads against 512 clocks of MMA.)
+//
+// Scale path: a 512-byte chunk of the packed array holds 128 rows x 4
+// k-blocks, one 32-bit word per row.  The producer fetches the chunks of four
+// k-blocks with the first of them, tcgen05.cp copies a chunk to four TMEM
+// columns, replicated to the four lane quadrants, and the instruction
+// descriptor's scale ids pick byte (k-block mod 4) of every word.
+//
+// Pair kernel: the SM-pair schedule of gemm_tc2.cuh (256 x 256 tiles, a
+// cluster of two CTAs, one elected issuer).  Two 256-column accumulators and
+// the scales do not fit the 512 TMEM columns side by side, so the
+// accumulators overlap in 32 columns: [0, 256) and [224, 480), scales in
+// [480, 504).  The epilogue drains the shared columns first; the next tile's
+// MMAs start once every epilogue warp of the pair has read them.  That wait,
+// one commit, one 32-column read and one arrival, is the only gap between
+// tiles (240-column tiles would have none, and 6 % more operand traffic per
+// MAC).
+#pragma once
+
+#include "gemm_tc2.cuh"
+
+namespace coda {
+
+// D (+)= A B with per-32 block scales, e4m3 / e5m2 operands, SM pair.
+__device__ __forceinline__ void umma_mxf8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void umma_mxf8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// A 32-row x 16-byte chunk of shared memory to 4 TMEM columns of all four
+// lane quadrants, in the CTA (or in both CTAs of the pair, each from its own
+// shared memory).  Executes in order with the MMAs of the same thread.
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// Shared-memory descriptor of such a chunk: no swizzle, 8 rows of 16 bytes
+// every 128 bytes.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
+}
+
+// Instruction descriptor of kind::mxf8f6f4 with E8M0 scales: operand formats
+// at bits 7 and 10, majors at 15 and 16, N / 8 at 17, scale type at 23,
+// M / 16 at 24; the scale ids (bits 4 and 29) are OR-ed in per k-block.
+__host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return (static_cast<uint32_t>(a_mn_major) << 15) | (static_cast<uint32_t>(b_mn_major) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t idesc_scale_id(uint32_t id) { return (id << 4) | (id << 29); }
+
+constexpr int kScaleChunk = 512;  // bytes: 128 rows x 4 k-blocks
+
+struct BlockPairSmem {
+  static constexpr int STAGES = 6;
+  static constexpr int A_BYTES = 128 * 128;  // this CTA's 128 rows of A
+  static constexpr int B_BYTES = 128 * 128;  // this CTA's 128 rows of B
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+  // scale chunks of a stage that starts a group of four k-blocks: this CTA's
+  // A rows, then all 256 B rows (each CTA's MMA half scales all of N)
+  static constexpr int SF_BYTES = 3 * kScaleChunk;
+  static constexpr int SF_RING_BYTES = STAGES * SF_BYTES;
+  static constexpr int EPI_WARPS = 4;
+  static constexpr int STORE_BYTES = EPI_WARPS * 2 * STORE_SLOT_BYTES;
+  static constexpr int BAR_BYTES = 512;
+  static constexpr int TOTAL = RING_BYTES + SF_RING_BYTES + STORE_BYTES + BAR_BYTES + 1024;
+  static_assert(TOTAL <= MAX_DYN_SMEM, "shared memory budget");
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int ACC_STEP = 224;  // TMEM column of the second accumulator
+  static constexpr int SF_COL = 480;    // two buffers of 4 (A) + 8 (B) columns
+  // bytes both CTAs' fill of k-block kb of a tile puts on the full barrier, per CTA
+  static __device__ __forceinline__ uint32_t fill_bytes(int kb) {
+    return static_cast<uint32_t>(STAGE_BYTES + ((kb & 3) == 0 ? SF_BYTES : 0));
+  }
+};
+
+struct BlockGemmArgs {
+  CUtensorMap A, B;    // codes
+  CUtensorMap sA, sB;  // packed scales as rows of 512 bytes, one per chunk
+  CUtensorMap out;     // C [M][N] bf16, 32 x 32 boxes
+  int M, N;
+  int tiles_m, tiles_n, num_kb, group_m;
+  uint32_t f8_fmt;     // format bits of A and B
+};
+
+template <bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockPairSmem::THREADS, 1)
+    gemm_block_pair_kernel(const __grid_constant__ BlockGemmArgs g, const KernelCtl ctl) {
+  using L = BlockPairSmem;
+  constexpr int STAGES = L::STAGES;
+  constexpr int BN = 256;
+  constexpr uint32_t IDESC0 = idesc_mxf8(BM2, BN, A_MN, B_MN);
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sf_ring = smem + L::RING_BYTES + L::STORE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sf_ring + L::SF_RING_BYTES);  // leader's counts both halves
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;  // leader only: both CTAs' epilogues have read the shared columns
+  uint64_t* drain = tempty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* fill_report = reinterpret_cast<uint32_t*>(tmem_slot + 2);  // leader: the peer's fills + 1
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cluster_id = blockIdx.x >> 1;
+  const int num_clusters = gridDim.x >> 1;
+  const int num_tiles = g.tiles_m * g.tiles_n;
+  GemmShape sh{};  // tile_coords' view of the raster
+  sh.tiles_m = g.tiles_m;
+  sh.tiles_n = g.tiles_n;
+  sh.group_m = g.group_m;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&tfull[0], 1);
+    mbar_init(&tfull[1], 1);
+    mbar_init(tempty, 2 * L::EPI_WARPS);  // lane 0 of every epilogue warp of both CTAs
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *fill_report = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&g.A);
+    tma_prefetch_desc(&g.B);
+    tma_prefetch_desc(&g.sA);
+    tma_prefetch_desc(&g.sB);
+  }
+  // barriers of both CTAs initialised before anyone signals across the pair
+  cluster_sync_all();
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA
+    if (lane == 0) {
+      const uint32_t leader_full = mapa_shared(smem_u32(full), 0);
+      const int groups = (g.num_kb + 3) >> 2;  // scale chunks per 128 rows
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0, skipped = -1;
+      bool ok = true;
+      bool skip = ctl.skip_first_stage == 1 && cluster_id == 0 && leader;
+      if (ctl.skip_first_stage == 2 && cluster_id == 0 && !leader) ok = false;
+      for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
+        int tm, tn;
+        tile_coords(t, sh, tm, tn);
+        const int m0 = tm * BM2 + static_cast<int>(rank) * 128;
+        const int n0 = tn * BN + static_cast<int>(rank) * 128;
+        for (int kb = 0; kb < g.num_kb; ++kb) {
+          if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, ctl.timeout_ns)) {
+            if (!*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_PRODUCER);
+            ok = false;
+            break;
+          }
+          if (skip) {
+            skip = false;  // test hook: the leader never arms this stage
+            skipped = issued;
+          } else {
+            uint8_t* sa = smem + stage * L::STAGE_BYTES;
+            uint8_t* sb = sa + L::A_BYTES;
+            uint8_t* sf = sf_ring + stage * L::SF_BYTES;
+            const uint32_t bar = leader_full + static_cast<uint32_t>(stage * 8);
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * L::fill_bytes(kb));
+            if (!A_MN)
+              tma_load_2d_pair(sa, &g.A, bar, kb * 128, m0);
+            else
+              tma_load_2d_pair(sa, &g.A, bar, m0, kb * 128);
+            if (!B_MN)
+              tma_load_2d_pair(sb, &g.B, bar, kb * 128, n0);
+            else
+              tma_load_2d_pair(sb, &g.B, bar, n0, kb * 128);
+            if ((kb & 3) == 0) {
+              const int q = kb >> 2;
+              tma_load_2d_pair(sf, &g.sA, bar, 0, (m0 >> 7) * groups + q);
+              tma_load_2d_pair(sf + kScaleChunk, &g.sB, bar, 0, (2 * tn) * groups + q);
+              tma_load_2d_pair(sf + 2 * kScaleChunk, &g.sB, bar, 0, (2 * tn + 1) * groups + q);
+            }
+          }
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // every fill of both CTAs observed landed before shared memory can be
+      // released; fill i of the ring is k-block i mod num_kb of its tile
+      bool landed = true;
+      if (!leader) {
+        st_release_cluster_u32(mapa_shared(smem_u32(fill_report), 0), static_cast<uint32_t>(issued) + 1u);
+      } else {
+        uint32_t r;
+        landed = pair_report_wait(fill_report, ctl.timeout_ns, r) &&
+                 pair_ring_landed(issued, skipped, static_cast<int>(r) - 1, full, STAGES,
+                                  [&](int i, bool) { return L::fill_bytes(i % g.num_kb); }, ctl.timeout_ns);
+      }
+      if (!landed) {
+        atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
+        // far longer than any copy's latency, as in gemm_tc2_kernel
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA
+    if (lane == 0 && leader) {
+      const uint32_t idesc = IDESC0 | g.f8_fmt;
+      int stage = 0;
+      uint32_t phase = 0;
+      int it = 0;
+      uint32_t sf_buf = 0;
+      bool ok = true;
+      bool issued_any = false;
+      for (int t = cluster_id; t < num_tiles && ok; t += num_clusters, ++it) {
+        // the previous tile's shared columns have been read, and with them
+        // all of the tile before it, whose accumulator this one takes
+        if (it > 0 && !mbar_wait_bounded_cluster(tempty, static_cast<uint32_t>(it - 1) & 1u, abort_flag,
+                                                 ctl.timeout_ns)) {
+          if (!*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_MMA);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((it & 1) * L::ACC_STEP);
+        uint32_t sfa = 0;
+        for (int kb = 0; kb < g.num_kb; ++kb) {
+          if (!mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, ctl.timeout_ns)) {
+            if (!*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_MMA);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if ((kb & 3) == 0) {
+            const uint32_t sf = smem_u32(sf_ring + stage * L::SF_BYTES);
+            sfa = tmem_base + static_cast<uint32_t>(L::SF_COL) + sf_buf * 12u;
+            sf_buf ^= 1u;
+            tmem_cp_scales_pair(sfa, sdesc_scales(sf));
+            tmem_cp_scales_pair(sfa + 4, sdesc_scales(sf + kScaleChunk));
+            tmem_cp_scales_pair(sfa + 8, sdesc_scales(sf + 2 * kScaleChunk));
+          }
+          const uint32_t id = idesc | idesc_scale_id(static_cast<uint32_t>(kb) & 3u);
+          const uint32_t sa = smem_u32(smem + stage * L::STAGE_BYTES);
+          const uint32_t sb = sa + L::A_BYTES;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t ad = A_MN ? sdesc_sw128(sa + k * 4096, 128 * 128, 1024) : sdesc_sw128(sa + k * 32, 16, 1024);
+            const uint64_t bd = B_MN ? sdesc_sw128(sb + k * 4096, 128 * 128, 1024) : sdesc_sw128(sb + k * 32, 16, 1024);
+            umma_mxf8_pair(d_tmem, ad, bd, id, sfa, sfa + 4, (kb | k) != 0 ? 1u : 0u);
+          }
+          issued_any = true;
+          umma_commit_pair_multicast(&empty[stage], 0x3);
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair_multicast(&tfull[it & 1], 0x3);
+      }
+      // every MMA this thread issued has completed before TMEM is freed
+      if (issued_any) {
+        umma_commit_pair_local(drain);
+        if (!mbar_wait_timeout(drain, 0, ctl.timeout_ns)) atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- epilogue
+    const int quad = warp & 3;
+    const uint32_t leader_tempty = mapa_shared(smem_u32(tempty), 0);
+    const uint32_t slots = smem_u32(smem + L::RING_BYTES) + static_cast<uint32_t>((warp - 2) * 2 * STORE_SLOT_BYTES);
+    uint32_t stored = 0;  // 32-column blocks stored so far: they alternate between the two slots
+    int it = 0;
+    for (int t = cluster_id; t < num_tiles; t += num_clusters, ++it) {
+      int tm, tn;
+      tile_coords(t, sh, tm, tn);
+      const int acc = it & 1;
+      bool ok = mbar_wait_bounded(&tfull[acc], static_cast<uint32_t>(it >> 1) & 1u, abort_flag, ctl.timeout_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        if (lane == 0 && !*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_EPILOGUE);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t taddr =
+          tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * L::ACC_STEP);
+      const int m0 = (tm * 2 + static_cast<int>(rank)) * 128 + quad * 32;
+#pragma unroll 1
+      for (int j = 0; j < BN / 32; ++j) {
+        // the shared columns are the first accumulator's last block and the
+        // second one's first
+        const int blk = acc == 0 ? (j + BN / 32 - 1) % (BN / 32) : j;
+        float v[32];
+        tmem_ld32(taddr + static_cast<uint32_t>(blk * 32), v);
+        if (j == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(leader_tempty);
+        }
+        const int n0 = tn * BN + blk * 32;
+        if (n0 < g.N && m0 < g.M) {
+          const uint32_t slot = slots + (stored & 1u) * STORE_SLOT_BYTES;
+          ++stored;
+          if (lane == 0) bulk_wait_group_read1();
+          __syncwarp();
+          stage_bf16x32(slot, lane, v);
+          slots_publish();
+          if (lane == 0) {
+            tma_store_2d(&g.out, slot, n0, m0);
+            bulk_commit_group();
+          }
+        }
+      }
+    }
+    // the last stores have landed before shared memory is released
+    if (lane == 0) bulk_wait_group0();
+    __syncwarp();
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  // both CTAs done with the pair's TMEM and with each other's barriers
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+}  // namespace coda

@@ -20,7 +20,7 @@ cudaError_t gemm_ce_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv
 
 cudaError_t gemm_ce_grad(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt_chunk,
                          const int32_t* labels, const float* lse, __nv_bfloat16* dL, int M, int d, int Vc, int v0,
-                         float inv_M) {
+                         float inv_M, const float* row_scale) {
   CUtensorMap ta, tb;
   if (!make_operand_maps(&ta, &tb, H, false, Wt_chunk, false, M, Vc, d, b_box_rows(c))) return cudaErrorInvalidValue;
   EpiCeGrad::Params ep{};
@@ -29,6 +29,7 @@ cudaError_t gemm_ce_grad(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_
   ep.lse = lse;
   ep.inv_M = inv_M;
   ep.v0 = v0;
+  ep.row_scale = row_scale;
   return run_gemm<false, false, false, EpiCeGrad>(c, ta, tb, tb, M, Vc, d, (Vc + kBN - 1) / kBN, ep);
 }
 

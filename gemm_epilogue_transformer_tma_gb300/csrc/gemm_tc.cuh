@@ -1091,8 +1091,10 @@ struct EpiCeStats {
   }
 };
 
-// LM-head backward epilogue: dL = (exp(L - lse[m]) - [n == y_m]) / M into a
-// vocabulary-chunk buffer (column n of the chunk = vocabulary v0 + n), as bf16
+// LM-head backward epilogue: dL = s (exp(L - lse[m]) - [n == y_m]), s = 1 / M
+// (the mean cross-entropy) or a factor per row (row_scale: a weighted loss of
+// the label's log-probability; 0 gives an exact 0), into a vocabulary-chunk
+// buffer (column n of the chunk = vocabulary v0 + n), as bf16
 // or, with FP8 operands, as e5m2 codes of dL * code_inv (|dL| <= 1/M, so a
 // power-of-two scale fixed in advance never saturates).
 struct EpiCeGrad {
@@ -1107,12 +1109,14 @@ struct EpiCeGrad {
     int v0;
     int codes;
     float code_inv;  // the inverse of the codes' power-of-two scale
+    const float* row_scale;  // [M], or null: inv_M for every row
   };
   template <int BN>
   static __device__ __forceinline__ void run(const Params& p, const EpiCtx& c) {
     const bool row_ok = c.m < c.M;
     const float l = row_ok ? p.lse[c.m] : 0.f;
     const int y = row_ok ? p.labels[c.m] - p.v0 : -1;
+    const float s = p.row_scale == nullptr ? p.inv_M : row_ok ? p.row_scale[c.m] : 0.f;
 #pragma unroll 1
     for (int cc = c.c0; cc < c.c1; cc += 32) {
       float v[32];
@@ -1122,7 +1126,7 @@ struct EpiCeGrad {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const float e = __expf(v[i] * c.acc_scale - l) - ((n0 + i == y) ? 1.f : 0.f);
-          v[i] = e * p.inv_M;
+          v[i] = s == 0.f ? 0.f : e * s;
         }
         slots_acquire(c.lane);
         if (p.codes)

@@ -19,6 +19,7 @@ enum : int {
   DEV_ERR_TIMEOUT_EPILOGUE = 1 << 2,
   DEV_ERR_TIMEOUT_DRAIN = 1 << 3,
   DEV_ERR_LABEL_RANGE = 1 << 8,
+  DEV_ERR_POSITION_RANGE = 1 << 9,
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

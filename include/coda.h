@@ -55,7 +55,8 @@ typedef enum coda_status {
   CODA_ERR_WORKSPACE_TOO_SMALL = 4,
   CODA_ERR_CUDA = 5,               /* a CUDA runtime/driver call failed (launch, tensor map) */
   CODA_ERR_TIMEOUT = 6,            /* device: an in-kernel wait hit its time limit */
-  CODA_ERR_LABEL_RANGE = 7         /* device: a label outside [0, V) */
+  CODA_ERR_LABEL_RANGE = 7,        /* device: a label outside [0, V) */
+  CODA_ERR_POSITION_RANGE = 8      /* device: a position outside the rotary table */
 } coda_status_t;
 
 typedef struct coda_handle_s* coda_handle_t;
@@ -79,9 +80,10 @@ coda_status_t coda_destroy(coda_handle_t h);
 const char* coda_status_string(coda_status_t s);
 
 /* Synchronise `stream`, read and clear the device status word.  Returns
- * CODA_ERR_TIMEOUT or CODA_ERR_LABEL_RANGE if a kernel recorded that
- * condition since the last call, else CODA_OK.  If device_bits is not NULL it
- * receives the raw bit mask (bits 0-3: which wait timed out; bit 8: label
+ * CODA_ERR_TIMEOUT, CODA_ERR_LABEL_RANGE or CODA_ERR_POSITION_RANGE if a
+ * kernel recorded that condition since the last call (the first of them that
+ * applies), else CODA_OK.  If device_bits is not NULL it receives the raw bit
+ * mask (bits 0-3: which wait timed out; bit 8: label range; bit 9: position
  * range). */
 coda_status_t coda_sync_status(coda_handle_t h, void* stream, int32_t* device_bits);
 
@@ -473,6 +475,42 @@ coda_status_t coda_gemm_qkv_rope(coda_handle_t h, const void* X, const void* Wqk
 coda_status_t coda_rope_apply(coda_handle_t h, void* qkv, const float* cos_t, const float* sin_t, int64_t M,
                               int64_t n_q_heads, int64_t n_kv_heads, int64_t head_dim, int64_t S, void* stream);
 
+/* RMSNorm of every q and k head, then the rotation, in one pass over a packed
+ * qkv.  Per head x of D = head_dim values (weight g: gq for q heads, gk for k
+ * heads) of the row at position p:
+ *   n_i = x_i g_i / sqrt(mean_j x_j^2 + eps)
+ *   out_i = n_i cos - n_{i+D/2} sin, out_{i+D/2} = n_{i+D/2} cos + n_i sin
+ * (fp32, rounded to bf16 once).  v heads are copied; with out == qkv the call
+ * works in place and leaves them alone.  Position of row m: positions[m]
+ * (int32, device), or m mod S when positions is NULL.  A position outside
+ * [0, S) sets CODA_ERR_POSITION_RANGE in the status word; its heads are
+ * normalised and not rotated.
+ * qkv, out bf16 [M][(n_q_heads + 2 n_kv_heads) * head_dim]; gq, gk bf16
+ * [head_dim] (gk may be NULL with n_kv_heads == 0); cos_t, sin_t from
+ * coda_rope_table, [S][head_dim / 2]; positions 4-byte aligned.  head_dim a
+ * multiple of 16, at most 512 (CODA_ERR_UNSUPPORTED above); eps >= 0. */
+coda_status_t coda_qknorm_rope(coda_handle_t h, const void* qkv, const void* gq, const void* gk, const float* cos_t,
+                               const float* sin_t, const int32_t* positions, void* out, int64_t M, int64_t n_q_heads,
+                               int64_t n_kv_heads, int64_t head_dim, int64_t S, float eps, void* stream);
+
+/* Workspace of coda_qknorm_rope_bwd (0 for an empty batch). */
+size_t coda_qknorm_rope_bwd_workspace_bytes(int64_t M, int64_t head_dim);
+
+/* Backward of coda_qknorm_rope: from dout, the gradient of its out, and qkv,
+ * its input (before the norm), with dn the rotation of dout by -p and
+ * r = 1 / sqrt(mean x^2 + eps):
+ *   dqkv = r (dn g - x r^2 mean(dn g x))   (q and k heads; v heads: dout)
+ *   dgq, dgk = sum over rows and heads of dn x r
+ * dout, qkv, dqkv bf16 as qkv; dgq, dgk fp32 [head_dim], written (not
+ * accumulated), summed in an order fixed for the shape and the GPU.  dqkv may
+ * be dout (v heads then stay in place) or qkv.  At most 1024 heads
+ * (n_q_heads + 2 n_kv_heads).  M == 0 writes dgq = dgk = 0.  The rest as
+ * coda_qknorm_rope. */
+coda_status_t coda_qknorm_rope_bwd(coda_handle_t h, const void* dout, const void* qkv, const void* gq, const void* gk,
+                                   const float* cos_t, const float* sin_t, const int32_t* positions, void* dqkv,
+                                   float* dgq, float* dgk, void* ws, size_t ws_bytes, int64_t M, int64_t n_q_heads,
+                                   int64_t n_kv_heads, int64_t head_dim, int64_t S, float eps, void* stream);
+
 /* ------------------------------------------------------------------------ */
 /* FP8 operands (the write-up's 背景 section: FP8 speeds up the matmul, which  */
 /* raises the relative cost of the memory-bound operations the epilogues     */
@@ -590,6 +628,71 @@ coda_status_t coda_gemm_rowscale_swiglu_fp8(coda_handle_t h, const void* Hq, con
                                             int64_t d, int64_t N2, uint32_t flags, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* FP8 operands with a scale for each block of 128 values: a block's largest */
+/* value no longer sets the resolution of the whole tensor                   */
+/* ------------------------------------------------------------------------ */
+
+/* Block scales.  The scale of a block is the power of two that
+ * coda_fp8_quantize gives a tensor of the block's values (2^k with k >= -126,
+ * 1 for a block of zeros; e5m2: as coda_fp8_quantize_e5m2), kept as the byte
+ * k + 127.  A block that holds an infinity or a NaN gets the byte 255 and NaN
+ * codes.
+ *
+ * Packed scales of an operand with `rows` rows (its extent that is not
+ * contracted) and a contracted extent K, one byte per row and block of 128
+ * along K: 512-byte chunks of 128 rows x 4 blocks; row r, block b at byte
+ *   ((r / 128) * ceil(K / 512) + b / 4) * 512
+ *       + (r % 32) * 16 + ((r % 128) / 32) * 4 + b % 4
+ * Bytes of rows and blocks past the operand are written as 127 (scale 1). */
+size_t coda_fp8_block_scale_bytes(int64_t rows, int64_t K);
+
+/* Codes of src bf16 [rows][cols] with blocks of 1 x 128 along the rows
+ * (q_row, and s_row: packed scales of an operand with `rows` rows and K =
+ * cols), with blocks of 128 x 1 along the columns (q_col, and s_col: packed
+ * scales of an operand with `cols` rows and K = rows), or both from one read
+ * of src.  A pair that is not wanted is NULL.  Codes [rows][cols], 1 byte
+ * each, round to nearest even.  q_row is the operand of a product over cols
+ * (a layer's input in the forward), q_col, read MN-major, of one over rows
+ * (the weight gradient, which contracts over tokens).  format 0 = e4m3, 1 =
+ * e5m2.  cols a multiple of 16; any rows >= 0. */
+coda_status_t coda_fp8_block_quantize(coda_handle_t h, const void* src, int format, void* q_row, void* s_row,
+                                      void* q_col, void* s_col, int64_t rows, int64_t cols, void* stream);
+
+/* Codes of a weight W bf16 [N][K] with blocks of 128 x 128, so that the same
+ * codes serve the forward (product over K, scales s: N rows, contracted K)
+ * and the data gradient (product over N, scales s_t: K rows, contracted N).
+ * K a multiple of 16; N >= 1. */
+coda_status_t coda_fp8_block_quantize_weight(coda_handle_t h, const void* W, int format, void* q, void* s, void* s_t,
+                                             int64_t N, int64_t K, void* stream);
+
+/* dst bf16 [rows][cols] = the values that codes q [rows][cols] stand for, with
+ * packed scales s of blocks along the rows (col_blocks = 0; also a weight's
+ * s) or along the columns (col_blocks = 1): a tensor kept for the backward in
+ * 8 bits and restored.  Exact, except that values below 2^-126 are rounded
+ * and one that was rounded up past the largest bf16 value is an infinity.
+ * cols a multiple of 16. */
+coda_status_t coda_fp8_block_dequantize(coda_handle_t h, const void* q, const void* s, int col_blocks, int format,
+                                        void* dst, int64_t rows, int64_t cols, void* stream);
+
+/* GEMM on codes with block scales along the contraction:
+ *   C[m][n] = bf16( sum_b 2^(sA[m][b] - 127) 2^(sB[n][b] - 127)
+ *                         sum_{k in block b} A[m][k] B[k][n] )
+ * with fp32 accumulation, the scales applied by the tensor core.  A codes
+ * [M][K] (a_mn_major = 0) or [K][M] (1), sA packed scales of M rows and K;
+ * B codes [N][K] (0) or [K][N] (1), sB packed scales of N rows and K; formats
+ * and layouts as coda_gemm_fp8 (MN-major A with K-major B returns
+ * CODA_ERR_UNSUPPORTED).  A linear layer Y = X W^T and its gradients:
+ *   Y  = (q_row(X), s_row)       (Wq, s)
+ *   dX = (q_row(dY), s_row)      (Wq, s_t), B MN-major
+ *   dW = (q_col(dY), s_col)      (q_col(X), s_col), both MN-major, K = tokens
+ * C bf16 [M][N].  The contiguous extent of every operand a multiple of 16, N a
+ * multiple of 8.  With both operands MN-major any K >= 0 (K = 0 writes C = 0
+ * and A, B and their scales may be NULL).  M == 0 launches nothing. */
+coda_status_t coda_gemm_fp8_block(coda_handle_t h, const void* A, int a_mn_major, int a_format, const void* sA,
+                                  const void* B, int b_mn_major, int b_format, const void* sB, void* C, int64_t M,
+                                  int64_t N, int64_t K, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* LM head: blocked log-sum-exp cross-entropy epilogue (section 五种积木:     */
 /* block reduction "block log-sum-exp", stateful max / sum-exp)              */
 /* ------------------------------------------------------------------------ */
@@ -647,6 +750,41 @@ coda_status_t coda_lmhead_ce_fp8(coda_handle_t h, const void* Hq, const float* s
                                  const int32_t* labels, float* loss, float* lse, int32_t* argmax, void* dHs,
                                  void* dWt, void* ws, size_t ws_bytes, int64_t M, int64_t d, int64_t V,
                                  void* stream);
+
+/* Workspace of coda_lmhead_policy: that of coda_lmhead_ce and 28 bytes per
+ * row. */
+size_t coda_lmhead_policy_workspace_bytes(int64_t M, int64_t d, int64_t V, int with_grads);
+
+/* Clipped policy loss with a KL term on the LM head, without ever writing an
+ * [M][V] logits tensor.  With L = Hs Wt^T / temperature, per token m
+ *   lp = log softmax(L[m])[labels[m]]
+ *   r  = exp(lp - logp_old[m]),  A = advantage[m],  w = weight[m]
+ *   s  = min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *   x  = logp_ref[m] - lp,       kl = exp(x) - x - 1
+ *   loss = sum_m w (kl_coef kl - s)
+ * logp_old NULL: r = 1, its gradient that of exp(lp - stop(lp)) (the first
+ * update on fresh samples).  logp_ref NULL: no KL term.  weight NULL: 1 / M.
+ * The gradient flows through r where r A <= clip(r) A (inside the clip range
+ * and on its border) and through kl everywhere.
+ * stats fp32 [4] = {loss, sum -w s, sum w kl, sum of w where clipped}; logp
+ * fp32 [M] = lp.  A row of weight 0 (prompt, padding) adds nothing to stats
+ * and its dHs row is 0, whatever its advantage, logp_old and logp_ref hold;
+ * its label may be anything (one outside [0, V) gives the lp of column 0).
+ * Its Hs row must still be finite (it meets dL = 0 in dWt's contraction).
+ * For a row with weight, a label outside [0, V) sets CODA_ERR_LABEL_RANGE in
+ * the status word; the row then adds nothing, and its logp is 0.
+ * If dHs is not NULL the gradients of loss are produced as coda_lmhead_ce
+ * does: dHs = dL Wt, dWt = dL^T Hs.
+ * Hs bf16 [M][d], Wt bf16 [V][d], labels int32 [M], advantage, weight,
+ * logp_old, logp_ref fp32 [M] (these, stats and logp 4-byte aligned), dHs bf16
+ * [M][d] or NULL, dWt bf16 [V][d] (required iff dHs != NULL).  clip_low in
+ * [0, 1], clip_high >= 0 (infinity: no upper bound), kl_coef >= 0,
+ * temperature > 0, M >= 1. */
+coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt, const int32_t* labels,
+                                 const float* advantage, const float* weight, const float* logp_old,
+                                 const float* logp_ref, float clip_low, float clip_high, float kl_coef,
+                                 float temperature, float* stats, float* logp, void* dHs, void* dWt, void* ws,
+                                 size_t ws_bytes, int64_t M, int64_t d, int64_t V, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* unfused ablation: the same GEMM kernel with standalone memory-bound       */
