@@ -177,17 +177,38 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
-def _stream_on(t: torch.Tensor, stream=None) -> int:
-    """The given stream, or the current one of t's device."""
-    s = torch.cuda.current_stream(t.device) if stream is None else stream
-    return s.cuda_stream
+# The calls below that serve single tokens are as short as a kernel launch, so
+# their marshalling counts: one test per tensor on the way through (_arg), the
+# raw stream of the tensors' device (0.1 us; the Stream object's 2 us), and
+# the library object without its lock.
+def _on(t: torch.Tensor, stream):
+    """(library, handle, device index, stream) for a call on t's device."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("the tensors of a call must be CUDA tensors")
+    lib = _lib or load_library()
+    h = _handles.get(dev) or handle(dev)
+    return lib, h, dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _together(*tensors):
-    """Every given tensor on the first one's device (the handle's)."""
-    for t in tensors[1:]:
-        if t is not None and t.device != tensors[0].device:
-            raise ValueError(f"tensors on {tensors[0].device} and {t.device}")
+def _arg(t: torch.Tensor, dtype, shape: tuple, name: str, dev: int) -> int:
+    """The address of t, a contiguous tensor of that type and shape on device
+    dev."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _ptr(t, dtype, name)
+    _shape(t, shape, name)
+    raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
+
+
+def _opt(t, dtype, shape, name, dev):
+    return None if t is None else _arg(t, dtype, shape, name, dev)
+
+
+def _bytes(t: torch.Tensor, dev: int, name: str):
+    """(address, size in bytes) of a workspace on device dev."""
+    n = t.numel() * t.element_size()
+    return _arg(t, t.dtype, t.shape, name, dev), n
 
 
 def _ptr(t: torch.Tensor | None, dtype=None, name="tensor") -> int | None:
@@ -659,26 +680,16 @@ def coda_qknorm_rope(qkv, gq, gk, cos_t, sin_t, out, n_q_heads, n_kv_heads, head
                      positions=None, stream=None):
     """RMSNorm of the q and k heads (weights gq, gk), then RoPE, in one pass;
     out may be qkv (see include/coda.h)."""
-    M = qkv.shape[0]
-    S = cos_t.shape[0]
-    _shape(qkv, (M, (n_q_heads + 2 * n_kv_heads) * head_dim), "qkv")
-    _shape(out, qkv.shape, "out")
-    _head_shapes(gq, gk, cos_t, sin_t, positions, M, S, n_kv_heads, head_dim)
-    _together(qkv, gq, gk, cos_t, sin_t, positions, out)
-    _check(load_library().coda_qknorm_rope(
-        _h(qkv), _ptr(qkv, BF, "qkv"), _ptr(gq, BF, "gq"), _ptr(gk, BF, "gk"), _ptr(cos_t, F32, "cos_t"),
-        _ptr(sin_t, F32, "sin_t"), _ptr(positions, I32, "positions"), _ptr(out, BF, "out"), M, n_q_heads, n_kv_heads,
-        head_dim, S, eps, _stream_on(qkv, stream)), "coda_qknorm_rope")
-
-
-def _head_shapes(gq, gk, cos_t, sin_t, positions, M, S, n_kv_heads, head_dim):
-    _shape(gq, (head_dim,), "gq")
-    if gk is not None or n_kv_heads > 0:
-        _shape(gk, (head_dim,), "gk")
-    _shape(cos_t, (S, head_dim // 2), "cos_t")
-    _shape(sin_t, (S, head_dim // 2), "sin_t")
-    if positions is not None:
-        _shape(positions, (M,), "positions")
+    lib, h, dev, st = _on(qkv, stream)
+    M, S = qkv.shape[0], cos_t.shape[0]
+    full, g, tab = (M, (n_q_heads + 2 * n_kv_heads) * head_dim), (head_dim,), (S, head_dim // 2)
+    st = lib.coda_qknorm_rope(
+        h, _arg(qkv, BF, full, "qkv", dev), _arg(gq, BF, g, "gq", dev), _opt(gk, BF, g, "gk", dev),
+        _arg(cos_t, F32, tab, "cos_t", dev), _arg(sin_t, F32, tab, "sin_t", dev),
+        _opt(positions, I32, (M,), "positions", dev), _arg(out, BF, full, "out", dev), M, n_q_heads, n_kv_heads,
+        head_dim, S, eps, st)
+    if st:
+        _check(st, "coda_qknorm_rope")
 
 
 def coda_qknorm_rope_bwd_workspace_bytes(M: int, head_dim: int) -> int:
@@ -689,22 +700,17 @@ def coda_qknorm_rope_bwd(dout, qkv, gq, gk, cos_t, sin_t, dqkv, dgq, dgk, ws, n_
                          eps=1e-6, positions=None, stream=None):
     """Backward of coda_qknorm_rope from dout and its input qkv; dqkv may be
     dout or qkv (see include/coda.h)."""
-    M = qkv.shape[0]
-    S = cos_t.shape[0]
-    _shape(qkv, (M, (n_q_heads + 2 * n_kv_heads) * head_dim), "qkv")
-    _shape(dout, qkv.shape, "dout")
-    _shape(dqkv, qkv.shape, "dqkv")
-    _head_shapes(gq, gk, cos_t, sin_t, positions, M, S, n_kv_heads, head_dim)
-    _shape(dgq, (head_dim,), "dgq")
-    if dgk is not None or n_kv_heads > 0:
-        _shape(dgk, (head_dim,), "dgk")
-    _together(dgq, dout, qkv, gq, gk, cos_t, sin_t, positions, dqkv, dgk, ws)
-    _check(load_library().coda_qknorm_rope_bwd(
-        _h(dgq), _ptr(dout, BF, "dout"), _ptr(qkv, BF, "qkv"), _ptr(gq, BF, "gq"), _ptr(gk, BF, "gk"),
-        _ptr(cos_t, F32, "cos_t"), _ptr(sin_t, F32, "sin_t"), _ptr(positions, I32, "positions"),
-        _ptr(dqkv, BF, "dqkv"), _ptr(dgq, F32, "dgq"), _ptr(dgk, F32, "dgk"), _ptr(ws, None, "ws"),
-        ws.numel() * ws.element_size(), M, n_q_heads, n_kv_heads, head_dim, S, eps, _stream_on(dgq, stream)),
-        "coda_qknorm_rope_bwd")
+    lib, h, dev, st = _on(dgq, stream)
+    M, S = qkv.shape[0], cos_t.shape[0]
+    full, g, tab = (M, (n_q_heads + 2 * n_kv_heads) * head_dim), (head_dim,), (S, head_dim // 2)
+    st = lib.coda_qknorm_rope_bwd(
+        h, _arg(dout, BF, full, "dout", dev), _arg(qkv, BF, full, "qkv", dev), _arg(gq, BF, g, "gq", dev),
+        _opt(gk, BF, g, "gk", dev), _arg(cos_t, F32, tab, "cos_t", dev), _arg(sin_t, F32, tab, "sin_t", dev),
+        _opt(positions, I32, (M,), "positions", dev), _arg(dqkv, BF, full, "dqkv", dev),
+        _arg(dgq, F32, g, "dgq", dev), _opt(dgk, F32, g, "dgk", dev), *_bytes(ws, dev, "ws"), M, n_q_heads,
+        n_kv_heads, head_dim, S, eps, st)
+    if st:
+        _check(st, "coda_qknorm_rope_bwd")
 
 
 U8 = torch.uint8
@@ -851,68 +857,67 @@ def coda_fp8_block_scale_bytes(rows: int, K: int) -> int:
     return load_library().coda_fp8_block_scale_bytes(rows, K)
 
 
-def _scales(s, rows, K, name):
-    if s is not None:
-        _shape(s, (coda_fp8_block_scale_bytes(rows, K),), name)
+def _packed(rows: int, K: int) -> tuple:
+    """The shape of packed block scales (coda_fp8_block_scale_bytes)."""
+    return (-(-rows // 128) * -(-K // 512) * 512,)
 
 
 def coda_fp8_block_quantize(src, q_row, s_row, q_col, s_col, fmt: int = E4M3, stream=None):
     """Codes of src with a scale for each 1 x 128 block (q_row, s_row) and /
     or each 128 x 1 block (q_col, s_col); a pair may be None (see
     include/coda.h)."""
-    rows, cols = src.shape
-    for q, s, r, k, n in ((q_row, s_row, rows, cols, "row"), (q_col, s_col, cols, rows, "col")):
-        if (q is None) != (s is None):
-            raise ValueError(f"q_{n} and s_{n} come together")
-        if q is not None:
-            _shape(q, (rows, cols), f"q_{n}")
-            _scales(s, r, k, f"s_{n}")
-    _together(src, q_row, s_row, q_col, s_col)
-    _check(load_library().coda_fp8_block_quantize(
-        _h(src), _ptr(src, BF, "src"), int(fmt), _ptr(q_row, U8, "q_row"), _ptr(s_row, U8, "s_row"),
-        _ptr(q_col, U8, "q_col"), _ptr(s_col, U8, "s_col"), rows, cols, _stream_on(src, stream)),
-        "coda_fp8_block_quantize")
+    if (q_row is None) != (s_row is None) or (q_col is None) != (s_col is None):
+        raise ValueError("codes and their scales come together")
+    lib, h, dev, st = _on(src, stream)
+    shape = src.shape
+    rows, cols = shape
+    st = lib.coda_fp8_block_quantize(
+        h, _arg(src, BF, shape, "src", dev), fmt, _opt(q_row, U8, shape, "q_row", dev),
+        _opt(s_row, U8, _packed(rows, cols), "s_row", dev), _opt(q_col, U8, shape, "q_col", dev),
+        _opt(s_col, U8, _packed(cols, rows), "s_col", dev), rows, cols, st)
+    if st:
+        _check(st, "coda_fp8_block_quantize")
 
 
 def coda_fp8_block_quantize_weight(W, q, s, s_t, fmt: int = E4M3, stream=None):
     """Codes of W [N, K] with a scale for each 128 x 128 block; s for the
     product over K, s_t for the one over N (see include/coda.h)."""
-    N, K = W.shape
-    _shape(q, (N, K), "q")
-    _scales(s, N, K, "s")
-    _scales(s_t, K, N, "s_t")
-    _together(W, q, s, s_t)
-    _check(load_library().coda_fp8_block_quantize_weight(
-        _h(W), _ptr(W, BF, "W"), int(fmt), _ptr(q, U8, "q"), _ptr(s, U8, "s"), _ptr(s_t, U8, "s_t"), N, K,
-        _stream_on(W, stream)), "coda_fp8_block_quantize_weight")
+    lib, h, dev, st = _on(W, stream)
+    shape = W.shape
+    N, K = shape
+    st = lib.coda_fp8_block_quantize_weight(
+        h, _arg(W, BF, shape, "W", dev), fmt, _arg(q, U8, shape, "q", dev), _arg(s, U8, _packed(N, K), "s", dev),
+        _arg(s_t, U8, _packed(K, N), "s_t", dev), N, K, st)
+    if st:
+        _check(st, "coda_fp8_block_quantize_weight")
 
 
 def coda_fp8_block_dequantize(q, s, col_blocks: bool, dst, fmt: int = E4M3, stream=None):
     """dst = the bf16 values of codes q with packed scales s of blocks along
     the rows, or along the columns with col_blocks (see include/coda.h)."""
-    rows, cols = q.shape
-    _shape(dst, (rows, cols), "dst")
-    _scales(s, *((cols, rows) if col_blocks else (rows, cols)), "s")
-    _together(q, s, dst)
-    _check(load_library().coda_fp8_block_dequantize(
-        _h(q), _ptr(q, U8, "q"), _ptr(s, U8, "s"), int(col_blocks), int(fmt), _ptr(dst, BF, "dst"), rows, cols,
-        _stream_on(q, stream)), "coda_fp8_block_dequantize")
+    lib, h, dev, st = _on(q, stream)
+    shape = q.shape
+    rows, cols = shape
+    st = lib.coda_fp8_block_dequantize(
+        h, _arg(q, U8, shape, "q", dev),
+        _arg(s, U8, _packed(cols, rows) if col_blocks else _packed(rows, cols), "s", dev), bool(col_blocks), fmt,
+        _arg(dst, BF, shape, "dst", dev), rows, cols, st)
+    if st:
+        _check(st, "coda_fp8_block_dequantize")
 
 
 def coda_gemm_fp8_block(A, a_mn_major: bool, a_format: int, sA, B, b_mn_major: bool, b_format: int, sB, C,
                         M: int, N: int, K: int, stream=None):
     """C[M,N] = A B on 8-bit codes with packed block scales along K (see
     include/coda.h)."""
-    _shape(A, (K, M) if a_mn_major else (M, K), "A")
-    _shape(B, (K, N) if b_mn_major else (N, K), "B")
-    _shape(C, (M, N), "C")
-    _scales(sA, M, K, "sA")
-    _scales(sB, N, K, "sB")
-    _together(C, A, sA, B, sB)
-    _check(load_library().coda_gemm_fp8_block(
-        _h(C), _ptr(A, U8, "A"), int(a_mn_major), int(a_format), _ptr(sA, U8, "sA"), _ptr(B, U8, "B"),
-        int(b_mn_major), int(b_format), _ptr(sB, U8, "sB"), _ptr(C, BF, "C"), M, N, K, _stream_on(C, stream)),
-        "coda_gemm_fp8_block")
+    lib, h, dev, st = _on(C, stream)
+    st = lib.coda_gemm_fp8_block(
+        h, _arg(A, U8, (K, M) if a_mn_major else (M, K), "A", dev), bool(a_mn_major), a_format,
+        _arg(sA, U8, _packed(M, K), "sA", dev), _arg(B, U8, (K, N) if b_mn_major else (N, K), "B", dev),
+        bool(b_mn_major), b_format, _arg(sB, U8, _packed(N, K), "sB", dev), _arg(C, BF, (M, N), "C", dev), M, N, K,
+        st)
+    if st:
+        _check(st, "coda_gemm_fp8_block")
 
 
 def coda_lmhead_ce_workspace_bytes(M: int, d: int, V: int, with_grads: bool) -> int:
@@ -984,26 +989,20 @@ def coda_lmhead_policy(Hs, Wt, labels, advantage, weight, logp_old, logp_ref, cl
                        kl_coef: float, temperature: float, stats, logp, dHs, dWt, ws, stream=None):
     """Clipped policy loss with a KL term on the LM head; weight, logp_old,
     logp_ref and the gradients dHs, dWt may be None (see include/coda.h)."""
-    M, d = Hs.shape
-    V = Wt.shape[0]
-    _shape(Wt, (V, d), "Wt")
-    for t, n in ((labels, "labels"), (advantage, "advantage"), (weight, "weight"), (logp_old, "logp_old"),
-                 (logp_ref, "logp_ref"), (logp, "logp")):
-        if t is not None:
-            _shape(t, (M,), n)
-    _shape(stats, (4,), "stats")
     if (dHs is None) != (dWt is None):
         raise ValueError("dHs and dWt come together")
-    if dHs is not None:
-        _shape(dHs, (M, d), "dHs")
-        _shape(dWt, (V, d), "dWt")
-    _together(Hs, Wt, labels, advantage, weight, logp_old, logp_ref, stats, logp, dHs, dWt, ws)
-    _check(load_library().coda_lmhead_policy(
-        _h(Hs), _ptr(Hs, BF, "Hs"), _ptr(Wt, BF, "Wt"), _ptr(labels, I32, "labels"),
-        _ptr(advantage, F32, "advantage"), _ptr(weight, F32, "weight"), _ptr(logp_old, F32, "logp_old"),
-        _ptr(logp_ref, F32, "logp_ref"), clip_low, clip_high, kl_coef, temperature, _ptr(stats, F32, "stats"),
-        _ptr(logp, F32, "logp"), _ptr(dHs, BF, "dHs"), _ptr(dWt, BF, "dWt"), _ptr(ws, None, "ws"),
-        ws.numel() * ws.element_size(), M, d, V, _stream_on(Hs, stream)), "coda_lmhead_policy")
+    lib, h, dev, st = _on(Hs, stream)
+    hs, wt = Hs.shape, Wt.shape
+    (M, d), V = hs, wt[0]
+    row = (M,)
+    st = lib.coda_lmhead_policy(
+        h, _arg(Hs, BF, hs, "Hs", dev), _arg(Wt, BF, (V, d), "Wt", dev), _arg(labels, I32, row, "labels", dev),
+        _arg(advantage, F32, row, "advantage", dev), _opt(weight, F32, row, "weight", dev),
+        _opt(logp_old, F32, row, "logp_old", dev), _opt(logp_ref, F32, row, "logp_ref", dev), clip_low, clip_high,
+        kl_coef, temperature, _arg(stats, F32, (4,), "stats", dev), _arg(logp, F32, row, "logp", dev),
+        _opt(dHs, BF, hs, "dHs", dev), _opt(dWt, BF, wt, "dWt", dev), *_bytes(ws, dev, "ws"), M, d, V, st)
+    if st:
+        _check(st, "coda_lmhead_policy")
 
 
 def coda_unfused_workspace_bytes(M: int, d: int, N2: int) -> int:

@@ -80,6 +80,19 @@ cudaError_t launch_chained(const LaunchCtx& c, void (*kern)(KArgs...), dim3 grid
   return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
+// Dynamic shared memory above 48 KB is granted per kernel and device; asking
+// again on every call costs more than a launch.
+template <class Kern>
+inline cudaError_t allow_smem(Kern kern, int bytes, bool (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  done[dev] = e == cudaSuccess;
+  return e;
+}
+
 // Handle accessors (api.cu), for translation units that only see the
 // opaque coda_handle_t.
 LaunchCtx launch_ctx_of_handle(void* handle, void* stream);

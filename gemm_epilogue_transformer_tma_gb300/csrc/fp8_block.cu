@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kThreads = 256;
+constexpr int kCtas = 3;              // quantiser CTAs per SM
 constexpr uint32_t kScaleOne = 127;   // 2^0
 constexpr uint32_t kScaleNan = 255;
 
@@ -56,30 +57,47 @@ __device__ __forceinline__ int64_t scale_offset(int64_t r, int64_t b, int64_t kq
   return ((r >> 7) * kq + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3);
 }
 
-// A block (row i of the tile, or column) stores its scale; the CTA of the
-// last k-block also fills the word's unused bytes, so that every byte of the
-// packed array is written.
-__device__ __forceinline__ void store_scale(uint8_t* s, int64_t r, int64_t b, int64_t nb, int64_t kq, uint32_t byte) {
+// Stores the scale of operand row r, k-block b; the last k-block also fills
+// the word's unused bytes, so that every byte of the packed array is written.
+__device__ __forceinline__ void store_scale(uint8_t* s, int64_t r, int64_t b, int64_t nb, uint32_t byte) {
+  const int64_t kq = (nb + 3) >> 2;
   uint8_t* p = s + scale_offset(r, b, kq);
   *p = static_cast<uint8_t>(byte);
   if (b == nb - 1)
     for (int64_t i = b + 1; i < kq * 4; ++i) p[i - b] = static_cast<uint8_t>(kScaleOne);
 }
 
+// eight codes of f * inv (inv per value when they differ), packed in order
+template <bool E5M2>
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], const float (&inv)[8]) {
+  return make_uint2(codes4<E5M2>(f[0] * inv[0], f[1] * inv[1], f[2] * inv[2], f[3] * inv[3]),
+                    codes4<E5M2>(f[4] * inv[4], f[5] * inv[5], f[6] * inv[6], f[7] * inv[7]));
+}
+template <bool E5M2>
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], uint32_t byte) {
+  if (byte == kScaleNan) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  const float s = inv_scale(byte);
+  return make_uint2(codes4<E5M2>(f[0] * s, f[1] * s, f[2] * s, f[3] * s),
+                    codes4<E5M2>(f[4] * s, f[5] * s, f[6] * s, f[7] * s));
+}
+
 // One CTA per 128 x 128 tile of src [rows][cols] bf16.  Thread t holds the
 // 8-column chunk t % 16 of rows t / 16 + 16 i, i < 8: half a warp covers a
 // 256-byte row segment, all eight loads are issued before the first use, and
 // the tile stays in registers until its codes are written, so src is read
-// once however many block directions are asked for.  Memory-bound.
+// once however many block directions are asked for.  Scales go through shared
+// memory and leave as one byte per thread.  Memory-bound: what counts is
+// loads in flight, hence the register limit that lets kCtas CTAs share an SM.
 template <bool E5M2, bool ROW, bool COL, bool TILE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtas)
     block_quantize_kernel(const __nv_bfloat16* __restrict__ src, uint8_t* __restrict__ q_row,
                           uint8_t* __restrict__ s_row, uint8_t* __restrict__ q_col, uint8_t* __restrict__ s_col,
                           int64_t rows, int64_t cols, int64_t tiles_c) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ uint32_t red[8][kTile / 2];  // per warp: two columns' maxima in a word
-  __shared__ uint32_t col_max[kTile / 2];
+  __shared__ uint32_t red[8][kTile / 2];    // per warp: two columns' maxima in a word
+  __shared__ uint32_t col_max[kTile / 2];   // the tile's column maxima
+  __shared__ uint8_t row_scale[kTile];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int64_t rb = blockIdx.x / tiles_c, cb = blockIdx.x - rb * tiles_c;
   const int64_t nrb = (rows + kTile - 1) / kTile;
@@ -87,27 +105,17 @@ __global__ void __launch_bounds__(kThreads)
   const int cc = (t & 15) * 8;  // this thread's first column in the tile
   const int rr = t >> 4;        // its first row
   const bool col_ok = c0 + cc < cols;
+  const int nr = static_cast<int>(rows - r0 < kTile ? rows - r0 : kTile);  // rows of the tile
+  const int64_t base = (r0 + rr) * cols + c0 + cc;
   uint4 v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int64_t r = r0 + rr + 16 * i;
     v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (col_ok && r < rows) v[i] = __ldg(reinterpret_cast<const uint4*>(src + r * cols + c0 + cc));
+    if (col_ok && rr + 16 * i < nr) v[i] = __ldg(reinterpret_cast<const uint4*>(src + base + 16 * i * cols));
   }
-  uint32_t row_byte[8];
-  if (ROW) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t m = hi_lo_max(__vmaxu2(__vmaxu2(abs2(v[i].x), abs2(v[i].y)), __vmaxu2(abs2(v[i].z), abs2(v[i].w))));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      row_byte[i] = scale_byte<E5M2>(m);
-    }
-    // lane 0 of each half warp owns the rows' scales
-    if ((t & 15) == 0)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) store_scale(s_row, r0 + rr + 16 * i, cb, tiles_c, (tiles_c + 3) / 4, row_byte[i]);
-  }
+  float inv[8];                     // COL: this thread's columns
+  uint2 nan = make_uint2(0u, 0u);   // COL: 0x7F in the bytes of poisoned columns
+  uint32_t tile_byte = 0;
   if (COL || TILE) {
     uint32_t m[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -131,81 +139,58 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncthreads();
   }
-  if (ROW && col_ok) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t r = r0 + rr + 16 * i;
-      if (r < rows) {
-        float f[8];
-        unpack_bf16x8(v[i], f);
-        const float inv = inv_scale(row_byte[i]);
-        uint2 q = make_uint2(codes4<E5M2>(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                             codes4<E5M2>(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
-        if (row_byte[i] == kScaleNan) q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-        *reinterpret_cast<uint2*>(q_row + r * cols + c0 + cc) = q;
-      }
-    }
-  }
   if (COL) {
-    uint32_t byte[8];
-    float inv[8];
-    uint2 nan = make_uint2(0u, 0u);  // 0x7F in the bytes of poisoned columns
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint32_t w = col_max[cc / 2 + j / 2];
-      byte[j] = scale_byte<E5M2>((j & 1) ? w >> 16 : w & 0xFFFFu);
-      inv[j] = inv_scale(byte[j]);
-      if (byte[j] == kScaleNan) (j < 4 ? nan.x : nan.y) |= 0x7Fu << (8 * (j & 3));
-    }
-    // columns past the tensor have no loads behind them: scale 1
-    if (rr == 0)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) store_scale(s_col, c0 + cc + j, rb, nrb, (nrb + 3) / 4, byte[j]);
-    if (col_ok) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t r = r0 + rr + 16 * i;
-        if (r < rows) {
-          float f[8];
-          unpack_bf16x8(v[i], f);
-          uint2 q = make_uint2(codes4<E5M2>(f[0] * inv[0], f[1] * inv[1], f[2] * inv[2], f[3] * inv[3]),
-                               codes4<E5M2>(f[4] * inv[4], f[5] * inv[5], f[6] * inv[6], f[7] * inv[7]));
-          if ((nan.x | nan.y) != 0u) {
-            // bytes 0x7F -> masks 0xFF
-            const uint32_t mx = nan.x | (nan.x << 1), my = nan.y | (nan.y << 1);
-            q.x = (q.x & ~mx) | nan.x;
-            q.y = (q.y & ~my) | nan.y;
-          }
-          *reinterpret_cast<uint2*>(q_col + r * cols + c0 + cc) = q;
-        }
-      }
+      const uint32_t byte = scale_byte<E5M2>((j & 1) ? w >> 16 : w & 0xFFFFu);
+      inv[j] = inv_scale(byte);
+      if (byte == kScaleNan) (j < 4 ? nan.x : nan.y) |= 0x7Fu << (8 * (j & 3));
     }
   }
-  if (TILE) {
-    // one scale for the whole tile: every thread reduces the 64 words
+  if (TILE) {  // one scale for the whole tile: every warp reduces the 64 words
     uint32_t m = __vmaxu2(col_max[lane], col_max[lane + 32]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const uint32_t byte = scale_byte<E5M2>(hi_lo_max(m));
-    const float inv = inv_scale(byte);
-    if (t < kTile) {
-      store_scale(s_row, r0 + t, cb, tiles_c, (tiles_c + 3) / 4, byte);
-      store_scale(s_col, c0 + t, rb, nrb, (nrb + 3) / 4, byte);
-    }
-    if (col_ok) {
+    tile_byte = scale_byte<E5M2>(hi_lo_max(m));
+  }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int64_t r = r0 + rr + 16 * i;
-        if (r < rows) {
-          float f[8];
-          unpack_bf16x8(v[i], f);
-          uint2 q = make_uint2(codes4<E5M2>(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                               codes4<E5M2>(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
-          if (byte == kScaleNan) q = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-          *reinterpret_cast<uint2*>(q_row + r * cols + c0 + cc) = q;
-        }
-      }
+  for (int i = 0; i < 8; ++i) {
+    const bool ok = col_ok && rr + 16 * i < nr;
+    float f[8];
+    unpack_bf16x8(v[i], f);
+    const int64_t o = base + 16 * i * cols;
+    if (ROW) {
+      uint32_t m = hi_lo_max(__vmaxu2(__vmaxu2(abs2(v[i].x), abs2(v[i].y)), __vmaxu2(abs2(v[i].z), abs2(v[i].w))));
+#pragma unroll
+      for (int s = 8; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+      const uint32_t byte = scale_byte<E5M2>(m);
+      if ((t & 15) == 0) row_scale[rr + 16 * i] = static_cast<uint8_t>(byte);
+      if (ok) *reinterpret_cast<uint2*>(q_row + o) = codes8<E5M2>(f, byte);
     }
+    if (COL && ok) {
+      uint2 q = codes8<E5M2>(f, inv);
+      if ((nan.x | nan.y) != 0u) {  // bytes 0x7F -> masks 0xFF
+        q.x = (q.x & ~(nan.x | (nan.x << 1))) | nan.x;
+        q.y = (q.y & ~(nan.y | (nan.y << 1))) | nan.y;
+      }
+      *reinterpret_cast<uint2*>(q_col + o) = q;
+    }
+    if (TILE && ok) *reinterpret_cast<uint2*>(q_row + o) = codes8<E5M2>(f, tile_byte);
+  }
+  // threads 0-127: the scales of the tile's rows; 128-255: of its columns
+  // (rows and columns past the tensor hold zeros: scale 1)
+  if (ROW) __syncthreads();
+  if (t < kTile) {
+    if (ROW) store_scale(s_row, r0 + t, cb, tiles_c, row_scale[t]);
+    if (TILE) store_scale(s_row, r0 + t, cb, tiles_c, tile_byte);
+  } else {
+    const int c = t - kTile;
+    if (COL) {
+      const uint32_t w = col_max[c >> 1];
+      store_scale(s_col, c0 + c, rb, nrb, scale_byte<E5M2>((c & 1) ? w >> 16 : w & 0xFFFFu));
+    }
+    if (TILE) store_scale(s_col, c0 + c, rb, nrb, tile_byte);
   }
 }
 

@@ -371,4 +371,239 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockPairSmem::THREA
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few tokens: C^T = W X^T, the weight rows as the MMA's M = 128 and the tokens
+// as its N (BN = 16 to 128), one SM per tile.  The product is bound by reading
+// the weight once, so what counts is bytes in flight on every SM: a cluster of
+// S CTAs shares a tile, each streaming its own range of K (whole scale chunks
+// of 512), and the S fp32 partial tiles are summed through distributed shared
+// memory in rank order.  Beyond a launch's fixed 4 us, one token takes 5 us at
+// K = 4096, N = 6144 (25 MB: 5 TB/s) and 17 at N = 28672 (6.9 TB/s).
+//   warp 0 TMA, warp 1 TMEM and MMA, warps 2-5 epilogue; one tile per cluster.
+// ---------------------------------------------------------------------------
+template <int BN>
+struct BlockFewSmem {
+  static constexpr int W_BYTES = 128 * 128;
+  static constexpr int X_BYTES = BN * 128;
+  static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
+  static constexpr int SF_BYTES = 2 * kScaleChunk;  // weight rows, tokens
+  // two CTAs per SM up to 64 tokens, one above (the ring is what is in flight)
+  static constexpr int CTAS = BN <= 64 ? 2 : 1;
+  static constexpr int STAGES = BN <= 32 ? 5 : BN == 64 ? 4 : 6;
+  static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+  static constexpr int BAR_BYTES = 256;
+  static constexpr int TOTAL = RING_BYTES + STAGES * SF_BYTES + BAR_BYTES + 1024;
+  static_assert(CTAS * (TOTAL + 1024) <= 233472, "shared memory of an SM");
+  static_assert(BN * 128 * 4 <= RING_BYTES, "the partial tile takes the ring's place");
+  static constexpr int THREADS = 192;
+  static constexpr int SF_COL = BN < 32 ? 32 : BN;  // two buffers of 4 + 4 columns
+  static constexpr int TMEM_COLS = BN <= 32 ? 64 : BN == 64 ? 128 : 256;
+};
+
+constexpr int kFewMaxParts = 8;  // CTAs per cluster (K ranges)
+
+struct BlockFewArgs {
+  CUtensorMap W, X;    // codes: the weight's rows, the tokens
+  CUtensorMap sW, sX;  // packed scales, rows of 512 bytes
+  __nv_bfloat16* C;    // [M][N]
+  int M, N;            // tokens, weight rows
+  int num_kb;
+  uint32_t f8_fmt;     // format bits with the weight as A
+};
+
+template <int BN, bool W_MN>
+__global__ void __launch_bounds__(BlockFewSmem<BN>::THREADS, BlockFewSmem<BN>::CTAS)
+    gemm_block_few_kernel(const __grid_constant__ BlockFewArgs g, const KernelCtl ctl) {
+  using L = BlockFewSmem<BN>;
+  constexpr int STAGES = L::STAGES;
+  constexpr uint32_t IDESC0 = idesc_mxf8(128, BN, W_MN, false);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sf_ring = smem + L::RING_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sf_ring + STAGES * L::SF_BYTES);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int parts = static_cast<int>(cluster_nctarank());
+  const int n0 = static_cast<int>(blockIdx.x / parts) * 128;  // weight rows
+  const int m0 = static_cast<int>(blockIdx.y) * BN;           // tokens
+  const int groups = (g.num_kb + 3) >> 2;                     // scale chunks along K
+  const int kb0 = static_cast<int>(static_cast<int64_t>(groups) * rank / parts) * 4;
+  const int kb1 = min(static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / parts) * 4, g.num_kb);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&g.W);
+    tma_prefetch_desc(&g.X);
+    tma_prefetch_desc(&g.sW);
+    tma_prefetch_desc(&g.sX);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, L::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, pending = 0, parity = 0;
+      bool ok = true;
+      bool skip = ctl.skip_first_stage != 0 && blockIdx.x == 0 && blockIdx.y == 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, ctl.timeout_ns)) {
+          if (!*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_PRODUCER);
+          ok = false;
+          break;
+        }
+        if (skip) {
+          skip = false;  // test hook: leave this stage unfilled
+        } else {
+          uint8_t* sw = smem + stage * L::STAGE_BYTES;
+          uint8_t* sf = sf_ring + stage * L::SF_BYTES;
+          const bool with_sf = (kb & 3) == 0;
+          mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(L::STAGE_BYTES + (with_sf ? L::SF_BYTES : 0)));
+          if (!W_MN)
+            tma_load_2d(sw, &g.W, &full[stage], kb * 128, n0);
+          else
+            tma_load_2d(sw, &g.W, &full[stage], n0, kb * 128);
+          tma_load_2d(sw + L::W_BYTES, &g.X, &full[stage], kb * 128, m0);
+          if (with_sf) {
+            tma_load_2d(sf, &g.sW, &full[stage], 0, (n0 >> 7) * groups + (kb >> 2));
+            tma_load_2d(sf + kScaleChunk, &g.sX, &full[stage], 0, (m0 >> 7) * groups + (kb >> 2));
+          }
+          pending |= 1u << stage;
+          parity = (parity & ~(1u << stage)) | (phase << stage);
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) {
+        // let every copy this thread started land before shared memory is released
+        for (int st = 0; st < STAGES; ++st)
+          if ((pending >> st) & 1u)
+            if (!mbar_wait_timeout(&full[st], (parity >> st) & 1u, ctl.timeout_ns))
+              atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = IDESC0 | g.f8_fmt;
+      int stage = 0;
+      uint32_t phase = 0, sfa = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait_bounded(&full[stage], phase, abort_flag, ctl.timeout_ns)) {
+          if (!*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_MMA);
+          break;
+        }
+        tc_fence_after();
+        if ((kb & 3) == 0) {
+          const uint32_t sf = smem_u32(sf_ring + stage * L::SF_BYTES);
+          sfa = tmem_base + static_cast<uint32_t>(L::SF_COL) + (static_cast<uint32_t>(kb >> 2) & 1u) * 8u;
+          tmem_cp_scales(sfa, sdesc_scales(sf));
+          tmem_cp_scales(sfa + 4, sdesc_scales(sf + kScaleChunk));
+        }
+        const uint32_t id = idesc | idesc_scale_id(static_cast<uint32_t>(kb) & 3u);
+        const uint32_t sw = smem_u32(smem + stage * L::STAGE_BYTES);
+        const uint32_t sx = sw + L::W_BYTES;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t wd = W_MN ? sdesc_sw128(sw + k * 4096, 128 * 128, 1024) : sdesc_sw128(sw + k * 32, 16, 1024);
+          umma_mxf8(tmem_base, wd, sdesc_sw128(sx + k * 32, 16, 1024), id, sfa, sfa + 4, (kb != kb0 || k != 0) ? 1u : 0u);
+        }
+        umma_commit(&empty[stage]);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      // arrives when every MMA this thread issued has completed
+      umma_commit(tfull);
+    }
+  } else {
+    const int quad = warp & 3;
+    const int row = quad * 32 + lane;
+    // ignores the abort flag: TMEM and the ring are free only after the MMAs
+    const bool ok = mbar_wait_timeout(tfull, 0, 2 * ctl.timeout_ns);
+    if (!ok && lane == 0) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_EPILOGUE);
+    tc_fence_after();
+    const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+    const int tokens = min(BN, g.M - m0);
+    float* part = reinterpret_cast<float*>(smem);  // [token][row]
+    const bool row_ok = n0 + row < g.N;
+    __nv_bfloat16* out = g.C + static_cast<int64_t>(m0) * g.N + n0 + row;
+#pragma unroll 1
+    for (int c = 0; c < tokens; c += 16) {
+      float v[16];
+      tmem_ld16(taddr + static_cast<uint32_t>(c), v);
+      if (parts == 1) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (row_ok && c + j < tokens) out[static_cast<int64_t>(c + j) * g.N] = __float2bfloat16_rn(v[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c + j) * 128 + row] = v[j];
+      }
+    }
+    tc_fence_before();
+  }
+  if (parts > 1) {
+    __syncwarp();
+    cluster_sync_all();  // every CTA's partial tile is in its shared memory
+    if (warp >= 2) {
+      // rank r sums tokens r, r + S, ...; a warp takes one token at a time, a
+      // lane four of its 128 rows
+      const int tokens = min(BN, g.M - m0);
+      const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(lane) * 16u;
+      const bool ok = n0 + 4 * lane < g.N;  // N is a multiple of 8: four rows or none
+      __nv_bfloat16* out = g.C + static_cast<int64_t>(m0) * g.N + n0 + 4 * lane;
+#pragma unroll 2
+      for (int j = rank + (warp - 2) * parts; j < tokens; j += 4 * parts) {
+        const uint32_t at = mine + static_cast<uint32_t>(j) * 512u;
+        float4 s = ld_cluster_f4(mapa_shared(at, 0));
+#pragma unroll
+        for (int p = 1; p < kFewMaxParts; ++p) {
+          if (p < parts) {
+            const float4 x = ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(p)));
+            s.x += x.x;
+            s.y += x.y;
+            s.z += x.z;
+            s.w += x.w;
+          }
+        }
+        if (ok)
+          *reinterpret_cast<uint2*>(out + static_cast<int64_t>(j) * g.N) =
+              make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // nobody leaves while its partial tile is being read
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, L::TMEM_COLS);
+  }
+}
+
 }  // namespace coda

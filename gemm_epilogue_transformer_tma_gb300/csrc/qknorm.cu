@@ -27,6 +27,9 @@ namespace coda {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kBwdCtas = 2;        // CTAs of the backward per SM
+constexpr int kBwdHeads = 2;       // its heads per lane
+constexpr int kStages = 2;         // rows of a backward warp in flight
 constexpr int kMaxParts = 1024;  // CTAs of the backward, one pair of dg partials each
 
 struct HeadArgs {
@@ -40,6 +43,7 @@ struct HeadArgs {
   const int32_t* pos;       // position of every row, or null: row mod S
   float* part;              // backward: [CTA][2][D] partial sums of dgq, dgk
   int* status;
+  uint64_t timeout_ns;
   int64_t M, S;
   int n_q, n_kv, D;
   int chunks_q, chunks_k, chunks;  // per row: q, k, all (with v when it has to be copied)
@@ -71,11 +75,6 @@ __device__ __forceinline__ Chunk chunk_of(const HeadArgs& a, int64_t m, int c, i
   return k;
 }
 
-__device__ __forceinline__ uint4 pack8f(const float* f) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
-}
-
 template <int G>
 __device__ __forceinline__ float head_sum(float v) {
 #pragma unroll
@@ -83,32 +82,34 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// cos / sin of the row's position for pairs [8 l, 8 l + 8).  A position
-// outside the table raises the status bit and leaves the row unrotated.
-__device__ __forceinline__ void load_angles(const HeadArgs& a, int64_t m, int l, bool active, float (&cs)[8],
-                                            float (&sn)[8]) {
+// cos / sin of the row's position for pairs [8 l, 8 l + 8), two to a word.  A
+// position outside the table raises the status bit and leaves the row
+// unrotated.
+__device__ __forceinline__ void load_angles(const HeadArgs& a, int64_t m, int l, bool active, f32x2 (&cs)[4],
+                                            f32x2 (&sn)[4]) {
   const int64_t p = a.pos != nullptr ? static_cast<int64_t>(a.pos[m]) : m % a.S;
   const bool ok = p >= 0 && p < a.S;
   if (!ok && l == 0) atomicOr(a.status, DEV_ERR_POSITION_RANGE);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    cs[j] = 1.f;
-    sn[j] = 0.f;
-  }
   if (ok && active) {
     const int64_t o = p * (a.D / 2) + 8 * l;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float4 c4 = __ldg(reinterpret_cast<const float4*>(a.cos_t + o) + h);
       const float4 s4 = __ldg(reinterpret_cast<const float4*>(a.sin_t + o) + h);
-      cs[4 * h] = c4.x, cs[4 * h + 1] = c4.y, cs[4 * h + 2] = c4.z, cs[4 * h + 3] = c4.w;
-      sn[4 * h] = s4.x, sn[4 * h + 1] = s4.y, sn[4 * h + 2] = s4.z, sn[4 * h + 3] = s4.w;
+      cs[2 * h] = make_f32x2(c4.x, c4.y), cs[2 * h + 1] = make_f32x2(c4.z, c4.w);
+      sn[2 * h] = make_f32x2(s4.x, s4.y), sn[2 * h + 1] = make_f32x2(s4.z, s4.w);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      cs[j] = splat2(1.f);
+      sn[j] = splat2(0.f);
     }
   }
 }
 
 template <int G, int U>
-__global__ void __launch_bounds__(32 * kWarps) qknorm_rope_kernel(const HeadArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 4) qknorm_rope_kernel(const HeadArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr int HW = 32 / G;  // heads side by side
@@ -132,36 +133,39 @@ __global__ void __launch_bounds__(32 * kWarps) qknorm_rope_kernel(const HeadArgs
       hi[u] = *reinterpret_cast<const uint4*>(p + half);
     }
   }
-  float cs[8], sn[8], g1[8], g2[8];
+  f32x2 cs[4], sn[4], g1[4], g2[4];
   if (k.kind < 2) {
     load_angles(a, m, l, active, cs, sn);
-    const __nv_bfloat16* g = (k.kind == 0 ? a.gq : a.gk) + 8 * l;
-    uint4 q1 = make_uint4(0u, 0u, 0u, 0u), q2 = q1;
-    if (active) {
-      q1 = __ldg(reinterpret_cast<const uint4*>(g));
-      q2 = __ldg(reinterpret_cast<const uint4*>(g + half));
+    const uint32_t* g = reinterpret_cast<const uint32_t*>((k.kind == 0 ? a.gq : a.gk) + 8 * l);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      g1[j] = unpack_bf16x2(active ? __ldg(g + j) : 0u);
+      g2[j] = unpack_bf16x2(active ? __ldg(g + half / 2 + j) : 0u);
     }
-    unpack_bf16x8(q1, g1);
-    unpack_bf16x8(q2, g2);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int h = u * HW + hg;
     if (k.kind < 2) {
-      float x1[8], x2[8], ss = 0.f;
-      unpack_bf16x8(lo[u], x1);
-      unpack_bf16x8(hi[u], x2);
+      const uint32_t w1[4] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w}, w2[4] = {hi[u].x, hi[u].y, hi[u].z, hi[u].w};
+      f32x2 x1[4], x2[4], ss = splat2(0.f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(x1[j], x1[j], fmaf(x2[j], x2[j], ss));
-      const float r = 1.0f / sqrtf(head_sum<G>(ss) * a.inv_d + a.eps);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float n1 = x1[j] * r * g1[j], n2 = x2[j] * r * g2[j];
-        x1[j] = fmaf(n1, cs[j], -n2 * sn[j]);
-        x2[j] = fmaf(n2, cs[j], n1 * sn[j]);
+      for (int j = 0; j < 4; ++j) {
+        x1[j] = unpack_bf16x2(w1[j]);
+        x2[j] = unpack_bf16x2(w2[j]);
+        ss = fma2(x1[j], x1[j], fma2(x2[j], x2[j], ss));
       }
-      lo[u] = pack8f(x1);
-      hi[u] = pack8f(x2);
+      const float2 s2 = split2(ss);
+      const f32x2 r = splat2(rsqrtf(head_sum<G>(s2.x + s2.y) * a.inv_d + a.eps));
+      uint32_t y1[4], y2[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x2 n1 = mul2(mul2(x1[j], r), g1[j]), n2 = mul2(mul2(x2[j], r), g2[j]);
+        y1[j] = pack_bf16x2(fma2(n1, cs[j], neg2(mul2(n2, sn[j]))));
+        y2[j] = pack_bf16x2(fma2(n2, cs[j], mul2(n1, sn[j])));
+      }
+      lo[u] = make_uint4(y1[0], y1[1], y1[2], y1[3]);
+      hi[u] = make_uint4(y2[0], y2[1], y2[2], y2[3]);
     }
     if (active && h < k.heads) {
       __nv_bfloat16* p = a.out + row + static_cast<int64_t>(k.first + h) * a.D + 8 * l;
@@ -174,117 +178,162 @@ __global__ void __launch_bounds__(32 * kWarps) qknorm_rope_kernel(const HeadArgs
 // The grid's warps stride over the tasks by a multiple of the chunks per row,
 // so a warp sees one chunk of every row it visits, hence one kind of head,
 // and its lanes' sums of dg stay in 16 registers until the end: then over the
-// warp's head groups, the CTA's warps of that kind, and (col_sums_kernel) the
-// CTAs, in a fixed order.
+// warp's head groups, the CTA's warps of that kind, and (dg_sums_kernel) the
+// CTAs, in a fixed order.  A chunk of x and of dy is one contiguous piece, so
+// each warp keeps kStages rows of them in flight with bulk copies into its
+// own shared-memory ring.  Two CTAs per SM: the 128 registers a thread needs
+// leave no room for a third (84 us with spills against 58, at 8192 rows of 48
+// heads of 128; 302 MB).  Plain loads into registers took 70 us there; the
+// packed fp32 arithmetic (two values per instruction) 58 against 61.
 template <int G, int U>
-__global__ void __launch_bounds__(32 * kWarps) qknorm_rope_bwd_kernel(const HeadArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(const HeadArgs a) {
   griddep_wait();
   griddep_launch_dependents();
+  constexpr int P = 8, W = P / 2;  // pairs per lane, in words of two
   constexpr int HW = 32 / G;
-  __shared__ float red[kWarps][G * 16];
+  constexpr int CHUNK = U * 32 * 2 * P * 2;  // bytes of U heads per lane, at most
+  extern __shared__ __align__(128) uint8_t ring[];  // [warp][stage][x, dy]
+  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
+  __shared__ float red[kWarps][G * 2 * P];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane & (G - 1), hg = lane / G;
-  const bool active = 16 * l < a.D;
+  const bool active = 2 * P * l < a.D;
   const int half = a.D / 2;
   const int64_t first = blockIdx.x * static_cast<int64_t>(kWarps) + warp;
   const int64_t m_step = static_cast<int64_t>(gridDim.x) * kWarps / a.chunks;
   const int64_t m0 = first / a.chunks;
-  Chunk k = chunk_of(a, m0, static_cast<int>(first - m0 * a.chunks), U * HW);
-  float g1[8], g2[8], d1[8], d2[8];
-  {
-    const __nv_bfloat16* g = (k.kind == 0 ? a.gq : a.gk) + 8 * l;
-    uint4 q1 = make_uint4(0u, 0u, 0u, 0u), q2 = q1;
-    if (active && k.kind < 2) {
-      q1 = __ldg(reinterpret_cast<const uint4*>(g));
-      q2 = __ldg(reinterpret_cast<const uint4*>(g + half));
-    }
-    unpack_bf16x8(q1, g1);
-    unpack_bf16x8(q2, g2);
+  const Chunk k = chunk_of(a, m0, static_cast<int>(first - m0 * a.chunks), U * HW);
+  const int64_t width = static_cast<int64_t>(a.n_q + 2 * a.n_kv) * a.D;
+  const int64_t head0 = static_cast<int64_t>(k.first) * a.D;
+  uint8_t* mine = ring + warp * (kStages * 2 * CHUNK);
+  // lane 0 fetches the chunk of row m into a stage (v heads need dy alone)
+  const uint32_t bytes = static_cast<uint32_t>(k.heads * a.D * 2);
+  auto fetch = [&](int64_t m, int s) {
+    uint8_t* dst = mine + s * (2 * CHUNK);
+    mbar_arrive_expect_tx(&bars[warp][s], k.kind < 2 ? 2 * bytes : bytes);
+    if (k.kind < 2) bulk_load(dst, a.x + m * width + head0, bytes, &bars[warp][s]);
+    bulk_load(dst + CHUNK, a.dy + m * width + head0, bytes, &bars[warp][s]);
+  };
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&bars[warp][s], 1);
+    fence_mbar_init();
+    for (int s = 0; s < kStages; ++s)
+      if (m0 + s * m_step < a.M) fetch(m0 + s * m_step, s);
   }
+  __syncwarp();
+  const f32x2 zero = splat2(0.f);
+  f32x2 g1[W], g2[W], d1[W], d2[W];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) d1[j] = d2[j] = 0.f;
+  for (int j = 0; j < W; ++j) g1[j] = g2[j] = d1[j] = d2[j] = zero;
+  if (active && k.kind < 2) {
+    const uint32_t* g = reinterpret_cast<const uint32_t*>((k.kind == 0 ? a.gq : a.gk) + P * l);
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      g1[j] = unpack_bf16x2(__ldg(g + j));
+      g2[j] = unpack_bf16x2(__ldg(g + half / 2 + j));
+    }
+  }
+  int s = 0;
+  uint32_t phase = 0;
   for (int64_t m = m0; m < a.M; m += m_step) {
-    const int64_t row = m * (static_cast<int64_t>(a.n_q + 2 * a.n_kv) * a.D);
-    uint4 lo[U], hi[U], ylo[U], yhi[U];
-#pragma unroll
+    f32x2 cs[W], sn[W];
+    if (k.kind < 2) load_angles(a, m, l, active, cs, sn);
+    // the copies are this warp's own: they land, or the device has failed
+    const bool landed = mbar_wait_timeout(&bars[warp][s], phase, a.timeout_ns);
+    if (!__all_sync(0xffffffffu, landed)) {
+      if (lane == 0) atomicOr(a.status, DEV_ERR_TIMEOUT_PRODUCER);
+      break;
+    }
+    const uint8_t* px = mine + s * (2 * CHUNK) + 2 * P * l;
+#pragma unroll 1
     for (int u = 0; u < U; ++u) {
-      lo[u] = hi[u] = ylo[u] = yhi[u] = make_uint4(0u, 0u, 0u, 0u);
       const int h = u * HW + hg;
-      if (active && h < k.heads) {
-        const int64_t o = row + static_cast<int64_t>(k.first + h) * a.D + 8 * l;
-        ylo[u] = *reinterpret_cast<const uint4*>(a.dy + o);
-        yhi[u] = *reinterpret_cast<const uint4*>(a.dy + o + half);
-        if (k.kind < 2) {
-          lo[u] = *reinterpret_cast<const uint4*>(a.x + o);
-          hi[u] = *reinterpret_cast<const uint4*>(a.x + o + half);
+      const bool ok = active && h < k.heads;
+      const uint8_t* p = px + h * a.D * 2;
+      union {
+        uint4 v;
+        uint32_t w[W];
+      } o1, o2, v1, v2;
+#pragma unroll
+      for (int j = 0; j < W; ++j) o1.w[j] = o2.w[j] = v1.w[j] = v2.w[j] = 0u;
+      if (ok) {
+        o1.v = *reinterpret_cast<const uint4*>(p + CHUNK);
+        o2.v = *reinterpret_cast<const uint4*>(p + CHUNK + a.D);
+      }
+      if (k.kind < 2) {
+        if (ok) {
+          v1.v = *reinterpret_cast<const uint4*>(p);
+          v2.v = *reinterpret_cast<const uint4*>(p + a.D);
         }
+        f32x2 x1[W], x2[W], n1[W], n2[W], p1[W], p2[W], ss = zero, dot = zero;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const f32x2 y1 = unpack_bf16x2(o1.w[j]), y2 = unpack_bf16x2(o2.w[j]);
+          x1[j] = unpack_bf16x2(v1.w[j]);
+          x2[j] = unpack_bf16x2(v2.w[j]);
+          n1[j] = fma2(y1, cs[j], mul2(y2, sn[j]));
+          n2[j] = fma2(y2, cs[j], neg2(mul2(y1, sn[j])));
+          p1[j] = mul2(n1[j], g1[j]);
+          p2[j] = mul2(n2[j], g2[j]);
+          ss = fma2(x1[j], x1[j], fma2(x2[j], x2[j], ss));
+          dot = fma2(p1[j], x1[j], fma2(p2[j], x2[j], dot));
+        }
+        const float2 s2 = split2(ss), t2 = split2(dot);
+        // a slot past the chunk's heads holds zeros: no share of dg, also at eps = 0
+        const float rs = rsqrtf(head_sum<G>(s2.x + s2.y) * a.inv_d + a.eps);
+        const float r = h < k.heads ? rs : 0.f;
+        const float coef = r * r * a.inv_d * head_sum<G>(t2.x + t2.y);
+        const f32x2 rr = splat2(r), nc = splat2(-coef);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          x1[j] = mul2(x1[j], rr);  // x r
+          x2[j] = mul2(x2[j], rr);
+          d1[j] = fma2(n1[j], x1[j], d1[j]);
+          d2[j] = fma2(n2[j], x2[j], d2[j]);
+          o1.w[j] = pack_bf16x2(fma2(p1[j], rr, mul2(x1[j], nc)));
+          o2.w[j] = pack_bf16x2(fma2(p2[j], rr, mul2(x2[j], nc)));
+        }
+      }
+      if (ok) {
+        __nv_bfloat16* y = a.out + m * width + head0 + h * a.D + P * l;
+        *reinterpret_cast<uint4*>(y) = o1.v;
+        *reinterpret_cast<uint4*>(y + half) = o2.v;
       }
     }
-    float cs[8], sn[8];
-    if (k.kind < 2) load_angles(a, m, l, active, cs, sn);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = u * HW + hg;
-      if (k.kind < 2) {
-        float x1[8], x2[8], y1[8], y2[8], ss = 0.f, dot = 0.f;
-        unpack_bf16x8(lo[u], x1);
-        unpack_bf16x8(hi[u], x2);
-        unpack_bf16x8(ylo[u], y1);
-        unpack_bf16x8(yhi[u], y2);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float n1 = fmaf(y1[j], cs[j], y2[j] * sn[j]), n2 = fmaf(y2[j], cs[j], -y1[j] * sn[j]);
-          ss = fmaf(x1[j], x1[j], fmaf(x2[j], x2[j], ss));
-          dot = fmaf(n1 * g1[j], x1[j], fmaf(n2 * g2[j], x2[j], dot));
-          y1[j] = n1;
-          y2[j] = n2;
-        }
-        const float r = 1.0f / sqrtf(head_sum<G>(ss) * a.inv_d + a.eps);
-        const float coef = r * r * a.inv_d * head_sum<G>(dot);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          d1[j] = fmaf(y1[j], x1[j] * r, d1[j]);
-          d2[j] = fmaf(y2[j], x2[j] * r, d2[j]);
-          x1[j] = r * fmaf(y1[j], g1[j], -x1[j] * coef);
-          x2[j] = r * fmaf(y2[j], g2[j], -x2[j] * coef);
-        }
-        ylo[u] = pack8f(x1);
-        yhi[u] = pack8f(x2);
-      }
-      if (active && h < k.heads) {
-        __nv_bfloat16* p = a.out + row + static_cast<int64_t>(k.first + h) * a.D + 8 * l;
-        *reinterpret_cast<uint4*>(p) = ylo[u];
-        *reinterpret_cast<uint4*>(p + half) = yhi[u];
-      }
+    __syncwarp();  // every lane has read the stage
+    if (lane == 0 && m + kStages * m_step < a.M) fetch(m + kStages * m_step, s);
+    if (++s == kStages) {
+      s = 0;
+      phase ^= 1u;
     }
   }
   // over the warp's head groups
 #pragma unroll
-  for (int o = G; o < 32; o <<= 1) {
+  for (int j = 0; j < W; ++j) {
+    float2 u1 = split2(d1[j]), u2 = split2(d2[j]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      d1[j] += __shfl_xor_sync(0xffffffffu, d1[j], o);
-      d2[j] += __shfl_xor_sync(0xffffffffu, d2[j], o);
+    for (int o = G; o < 32; o <<= 1) {
+      u1.x += __shfl_xor_sync(0xffffffffu, u1.x, o);
+      u1.y += __shfl_xor_sync(0xffffffffu, u1.y, o);
+      u2.x += __shfl_xor_sync(0xffffffffu, u2.x, o);
+      u2.y += __shfl_xor_sync(0xffffffffu, u2.y, o);
     }
-  }
-  if (hg == 0 && active) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      red[warp][8 * l + j] = d1[j];
-      red[warp][half + 8 * l + j] = d2[j];
+    if (hg == 0 && active) {
+      *reinterpret_cast<float2*>(&red[warp][P * l + 2 * j]) = u1;
+      *reinterpret_cast<float2*>(&red[warp][half + P * l + 2 * j]) = u2;
     }
   }
   __syncthreads();
   // over the CTA's warps, by kind
   for (int i = threadIdx.x; i < 2 * a.D; i += 32 * kWarps) {
     const int kind = i >= a.D, col = i - kind * a.D;
-    float s = 0.f;
+    float t = 0.f;
     for (int w = 0; w < kWarps; ++w) {
       const int c = static_cast<int>((blockIdx.x * static_cast<int64_t>(kWarps) + w) % a.chunks);
       const int wk = c < a.chunks_q ? 0 : c < a.chunks_q + a.chunks_k ? 1 : 2;
-      if (wk == kind) s += red[w][col];
+      if (wk == kind) t += red[w][col];
     }
-    a.part[blockIdx.x * static_cast<int64_t>(2 * a.D) + i] = s;
+    a.part[blockIdx.x * static_cast<int64_t>(2 * a.D) + i] = t;
   }
 }
 
@@ -352,6 +401,7 @@ HeadArgs head_args(const LaunchCtx& c, const __nv_bfloat16* x, const __nv_bfloat
   a.sin_t = sin_t;
   a.pos = pos;
   a.status = c.status;
+  a.timeout_ns = c.timeout_ns;
   a.M = M;
   a.S = S;
   a.n_q = n_q;
@@ -395,13 +445,18 @@ cudaError_t launch_qknorm_rope_bwd(const LaunchCtx& c, const __nv_bfloat16* dy, 
   const int G = lanes_per_head(D);
   return by_lanes(G, [&](auto g) {
     constexpr int GC = decltype(g)::value;
-    set_chunks<2>(a, G, dy != dx);
+    set_chunks<kBwdHeads>(a, G, dy != dx);
     if (a.chunks > kMaxParts) return cudaErrorNotSupported;
-    // one wave of three CTAs per SM, rounded to whole rows of chunks
-    const int64_t want = std::min<int64_t>({(M * a.chunks + kWarps - 1) / kWarps, int64_t(c.num_sms) * 3, kMaxParts});
+    // one wave, rounded to whole rows of chunks
+    const int64_t want =
+        std::min<int64_t>({(M * a.chunks + kWarps - 1) / kWarps, int64_t(c.num_sms) * kBwdCtas, kMaxParts});
     int64_t blocks = std::max<int64_t>(1, want / a.chunks) * a.chunks;
-    const cudaError_t e = launch_chained(c, qknorm_rope_bwd_kernel<GC, 2>, dim3(static_cast<unsigned>(blocks)),
-                                         dim3(32 * kWarps), 0, a);
+    auto kern = qknorm_rope_bwd_kernel<GC, kBwdHeads>;
+    constexpr int smem = kWarps * kStages * 2 * (kBwdHeads * 32 * 16 * 2);  // a lane holds 16 values of a head
+    static bool smem_ok[64] = {};
+    cudaError_t e = allow_smem(kern, smem, smem_ok);
+    if (e != cudaSuccess) return e;
+    e = launch_chained(c, kern, dim3(static_cast<unsigned>(blocks)), dim3(32 * kWarps), smem, a);
     if (e != cudaSuccess) return e;
     return launch_chained(c, dg_sums_kernel, dim3(static_cast<unsigned>((n_kv > 0 ? 2 : 1) * D / 8)), dim3(256), 0,
                           static_cast<const float*>(part), static_cast<int>(blocks), D, dgq, dgk);

@@ -149,6 +149,16 @@ def test_zero_rows_and_no_kv_heads():
     assert np.allclose(f64(dgq), rq, rtol=1e-5, atol=1e-5)
 
 
+def test_eps_zero_with_heads_that_fill_no_chunk():
+    pb = Problem(37, 3, 1, 64, 16, False)
+    dx, dgq, dgk = pb.backward(eps=0.0)
+    rx, rq, rk = S.qknorm_rope_backward(f64(pb.qkv), f64(pb.dout), f64(pb.gq), f64(pb.gk), pb.positions, 3, 1, 64,
+                                        0.0)
+    assert np.allclose(f64(dgq), rq, rtol=1e-4, atol=1e-5) and np.allclose(f64(dgk), rk, rtol=1e-4, atol=1e-5)
+    assert np.linalg.norm(f64(dx) - rx) <= 2.0 ** -8 * np.linalg.norm(rx)
+    assert_device_ok()
+
+
 def test_nan_row_stays_in_its_head():
     pb = Problem(8, 2, 1, 64, 16, False)
     pb.qkv[3, 70] = float("nan")       # head 1 of row 3
