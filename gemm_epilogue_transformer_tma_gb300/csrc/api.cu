@@ -1281,8 +1281,7 @@ coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt
   CODA_CUDA(launch_policy_labels(cx, labels, weight, M, V, w.labels, w.ce.zy));
   LaunchCtx cl = cx;  // the logits carry 1 / temperature
   cl.scale_host = 1.0f / temperature;
-  CODA_CUDA(gemm_ce_stats(cl, Hb, Wb, w.labels, w.ce.pmax, w.ce.psum, w.ce.parg, w.ce.zy, int(M), int(d), int(V),
-                          int(T)));
+  CODA_CUDA(gemm_logit_stats(cl, Hb, Wb, w.labels, w.ce.pmax, w.ce.psum, w.ce.zy, int(M), int(d), int(V), int(T)));
   PolicyRows r{};
   r.labels_in = w.labels;
   r.adv = advantage;
@@ -1298,6 +1297,7 @@ coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt
   r.logp = logp;
   r.row_scale = w.row_scale;
   r.terms = w.terms;
+  r.status = cx.status;
   CODA_CUDA(launch_policy_rows(cx, w.ce.pmax, w.ce.psum, w.ce.zy, r, M, T, V, stats));
   if (!grads) return CODA_OK;
   const int64_t chunk = h->ce_chunk;

@@ -150,6 +150,12 @@ cudaError_t gemm_dgrad_swiglu_bwd(const LaunchCtx& c, const __nv_bfloat16* dYb, 
 cudaError_t gemm_ce_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt, const int32_t* labels,
                           float* pmax, float* psum, int32_t* parg, float* zy, int M, int d, int V, int T);
 
+// per (row, 128-column block) max / sum-exp of c.scale_host H Wt^T, and the
+// label's logit where the label lies in [0, V); the contraction summed in
+// pieces (gemm_logits.cuh)
+cudaError_t gemm_logit_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt,
+                             const int32_t* labels, float* pmax, float* psum, float* zy, int M, int d, int V, int T);
+
 // dL chunk = (softmax - onehot) / M for vocabulary rows [v0, v0 + Vc), or
 // row_scale[m] (softmax - onehot) with row_scale != null.  The logits are
 // c.scale_host H Wt^T, as in gemm_ce_stats.
@@ -300,6 +306,7 @@ struct PolicyRows {
   float* logp;
   float* row_scale;          // factor of (softmax - onehot), or null
   float4* terms;
+  int* status;
 };
 cudaError_t launch_policy_labels(const LaunchCtx& c, const int32_t* labels, const float* weight, int64_t M, int64_t V,
                                  int32_t* out, float* zy);

@@ -21,7 +21,6 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kThreads = 256;
-constexpr int kCtas = 3;              // quantiser CTAs per SM
 constexpr uint32_t kScaleOne = 127;   // 2^0
 constexpr uint32_t kScaleNan = 255;
 
@@ -36,13 +35,35 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
 // 2^-k of a scale byte k + 127 (at most 247 for a finite block)
 __device__ __forceinline__ float inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 
-// four codes of v[0..3] * inv, packed in order
+// codes of two values (the lower one in the lower byte), saturating, round to
+// nearest even
 template <bool E5M2>
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-  constexpr __nv_fp8_interpretation_t kind = E5M2 ? __NV_E5M2 : __NV_E4M3;
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, kind);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, kind);
-  return (lo & 0xFFFFu) | (hi << 16);
+__device__ __forceinline__ uint16_t codes2(f32x2 v) {
+  const float2 f = split2(v);
+  uint16_t c;
+  if (E5M2)
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(c) : "f"(f.y), "f"(f.x));
+  else
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(f.y), "f"(f.x));
+  return c;
+}
+
+// eight codes of f[j] * s[j], packed in order
+template <bool E5M2>
+__device__ __forceinline__ uint2 codes8(const f32x2 (&f)[4], const f32x2 (&s)[4]) {
+  uint2 q;
+  asm("mov.b32 %0, {%1, %2};" : "=r"(q.x) : "h"(codes2<E5M2>(mul2(f[0], s[0]))), "h"(codes2<E5M2>(mul2(f[1], s[1]))));
+  asm("mov.b32 %0, {%1, %2};" : "=r"(q.y) : "h"(codes2<E5M2>(mul2(f[2], s[2]))), "h"(codes2<E5M2>(mul2(f[3], s[3]))));
+  return q;
+}
+
+// the same with one scale byte for all
+template <bool E5M2>
+__device__ __forceinline__ uint2 codes8(const f32x2 (&f)[4], uint32_t byte) {
+  if (byte == kScaleNan) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  const f32x2 s = splat2(inv_scale(byte));
+  const f32x2 s4[4] = {s, s, s, s};
+  return codes8<E5M2>(f, s4);
 }
 
 __device__ __forceinline__ uint32_t abs2(uint32_t v) { return v & 0x7FFF7FFFu; }
@@ -67,29 +88,20 @@ __device__ __forceinline__ void store_scale(uint8_t* s, int64_t r, int64_t b, in
     for (int64_t i = b + 1; i < kq * 4; ++i) p[i - b] = static_cast<uint8_t>(kScaleOne);
 }
 
-// eight codes of f * inv (inv per value when they differ), packed in order
-template <bool E5M2>
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], const float (&inv)[8]) {
-  return make_uint2(codes4<E5M2>(f[0] * inv[0], f[1] * inv[1], f[2] * inv[2], f[3] * inv[3]),
-                    codes4<E5M2>(f[4] * inv[4], f[5] * inv[5], f[6] * inv[6], f[7] * inv[7]));
-}
-template <bool E5M2>
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], uint32_t byte) {
-  if (byte == kScaleNan) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  const float s = inv_scale(byte);
-  return make_uint2(codes4<E5M2>(f[0] * s, f[1] * s, f[2] * s, f[3] * s),
-                    codes4<E5M2>(f[4] * s, f[5] * s, f[6] * s, f[7] * s));
-}
-
 // One CTA per 128 x 128 tile of src [rows][cols] bf16.  Thread t holds the
 // 8-column chunk t % 16 of rows t / 16 + 16 i, i < 8: half a warp covers a
 // 256-byte row segment, all eight loads are issued before the first use, and
 // the tile stays in registers until its codes are written, so src is read
 // once however many block directions are asked for.  Scales go through shared
-// memory and leave as one byte per thread.  Memory-bound: what counts is
-// loads in flight, hence the register limit that lets kCtas CTAs share an SM.
+// memory and leave as one byte per thread.  Close to DRAM and to the SM's
+// issue rate at once (a first form ran at 50 % and 61 % of them), so what
+// counts is warps in flight, hence the register limit that lets 3 CTAs (both
+// directions) or 4 share an SM, and few instructions: packed fp32 products,
+// one redux per row maximum, column scales computed once per column.  8192 x
+// 8192, both directions: 49 us, 5.5 TB/s (first form 56 us under the profiler, 49
+// with 2 CTAs 59); one direction or tiles 29 to 31 us.
 template <bool E5M2, bool ROW, bool COL, bool TILE>
-__global__ void __launch_bounds__(kThreads, kCtas)
+__global__ void __launch_bounds__(kThreads, ROW && COL ? 3 : 4)
     block_quantize_kernel(const __nv_bfloat16* __restrict__ src, uint8_t* __restrict__ q_row,
                           uint8_t* __restrict__ s_row, uint8_t* __restrict__ q_col, uint8_t* __restrict__ s_col,
                           int64_t rows, int64_t cols, int64_t tiles_c) {
@@ -97,7 +109,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   griddep_launch_dependents();
   __shared__ uint32_t red[8][kTile / 2];    // per warp: two columns' maxima in a word
   __shared__ uint32_t col_max[kTile / 2];   // the tile's column maxima
-  __shared__ uint8_t row_scale[kTile];
+  __shared__ uint8_t row_scale[kTile], col_scale[kTile];
+  __shared__ __align__(16) float col_inv[kTile];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int64_t rb = blockIdx.x / tiles_c, cb = blockIdx.x - rb * tiles_c;
   const int64_t nrb = (rows + kTile - 1) / kTile;
@@ -106,15 +119,19 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   const int rr = t >> 4;        // its first row
   const bool col_ok = c0 + cc < cols;
   const int nr = static_cast<int>(rows - r0 < kTile ? rows - r0 : kTile);  // rows of the tile
-  const int64_t base = (r0 + rr) * cols + c0 + cc;
+  int64_t o = (r0 + rr) * cols + c0 + cc;
+  const int64_t step = 16 * cols;
   uint4 v[8];
+  {
+    const __nv_bfloat16* p = src + o;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (col_ok && rr + 16 * i < nr) v[i] = __ldg(reinterpret_cast<const uint4*>(src + base + 16 * i * cols));
+    for (int i = 0; i < 8; ++i, p += step) {
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (col_ok && rr + 16 * i < nr) v[i] = __ldg(reinterpret_cast<const uint4*>(p));
+    }
   }
-  float inv[8];                     // COL: this thread's columns
-  uint2 nan = make_uint2(0u, 0u);   // COL: 0x7F in the bytes of poisoned columns
+  f32x2 inv[4];               // COL: this thread's columns
+  bool poisoned = false;      // COL: one of the tile's columns holds an infinity or a NaN
   uint32_t tile_byte = 0;
   if (COL || TILE) {
     uint32_t m[4] = {0u, 0u, 0u, 0u};
@@ -131,22 +148,26 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll
       for (int j = 0; j < 4; ++j) red[warp][lane * 4 + j] = m[j];
     __syncthreads();
+    bool nan = false;
     if (t < kTile / 2) {
       uint32_t x = red[0][t];
 #pragma unroll
       for (int w = 1; w < 8; ++w) x = __vmaxu2(x, red[w][t]);
       col_max[t] = x;
+      if (COL) {
+        const uint32_t b0 = scale_byte<E5M2>(x & 0xFFFFu), b1 = scale_byte<E5M2>(x >> 16);
+        *reinterpret_cast<uint16_t*>(&col_scale[2 * t]) = static_cast<uint16_t>(b0 | (b1 << 8));
+        *reinterpret_cast<float2*>(&col_inv[2 * t]) = make_float2(inv_scale(b0), inv_scale(b1));
+        nan = b0 == kScaleNan || b1 == kScaleNan;
+      }
     }
-    __syncthreads();
+    poisoned = __syncthreads_or(nan);
   }
   if (COL) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t w = col_max[cc / 2 + j / 2];
-      const uint32_t byte = scale_byte<E5M2>((j & 1) ? w >> 16 : w & 0xFFFFu);
-      inv[j] = inv_scale(byte);
-      if (byte == kScaleNan) (j < 4 ? nan.x : nan.y) |= 0x7Fu << (8 * (j & 3));
-    }
+    const float4 a = *reinterpret_cast<const float4*>(&col_inv[cc]);
+    const float4 b = *reinterpret_cast<const float4*>(&col_inv[cc + 4]);
+    inv[0] = make_f32x2(a.x, a.y), inv[1] = make_f32x2(a.z, a.w);
+    inv[2] = make_f32x2(b.x, b.y), inv[3] = make_f32x2(b.z, b.w);
   }
   if (TILE) {  // one scale for the whole tile: every warp reduces the 64 words
     uint32_t m = __vmaxu2(col_max[lane], col_max[lane + 32]);
@@ -155,24 +176,24 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     tile_byte = scale_byte<E5M2>(hi_lo_max(m));
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 8; ++i, o += step) {
     const bool ok = col_ok && rr + 16 * i < nr;
-    float f[8];
-    unpack_bf16x8(v[i], f);
-    const int64_t o = base + 16 * i * cols;
+    const f32x2 f[4] = {unpack_bf16x2(v[i].x), unpack_bf16x2(v[i].y), unpack_bf16x2(v[i].z), unpack_bf16x2(v[i].w)};
     if (ROW) {
       uint32_t m = hi_lo_max(__vmaxu2(__vmaxu2(abs2(v[i].x), abs2(v[i].y)), __vmaxu2(abs2(v[i].z), abs2(v[i].w))));
-#pragma unroll
-      for (int s = 8; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+      m = __reduce_max_sync(lane < 16 ? 0x0000FFFFu : 0xFFFF0000u, m);
       const uint32_t byte = scale_byte<E5M2>(m);
       if ((t & 15) == 0) row_scale[rr + 16 * i] = static_cast<uint8_t>(byte);
       if (ok) *reinterpret_cast<uint2*>(q_row + o) = codes8<E5M2>(f, byte);
     }
     if (COL && ok) {
       uint2 q = codes8<E5M2>(f, inv);
-      if ((nan.x | nan.y) != 0u) {  // bytes 0x7F -> masks 0xFF
-        q.x = (q.x & ~(nan.x | (nan.x << 1))) | nan.x;
-        q.y = (q.y & ~(nan.y | (nan.y << 1))) | nan.y;
+      if (poisoned) {  // the codes of poisoned columns become 0x7F
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint32_t& w = j < 4 ? q.x : q.y;
+          if (col_scale[cc + j] == kScaleNan) w = (w & ~(0xFFu << (8 * (j & 3)))) | (0x7Fu << (8 * (j & 3)));
+        }
       }
       *reinterpret_cast<uint2*>(q_col + o) = q;
     }
@@ -186,10 +207,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     if (TILE) store_scale(s_row, r0 + t, cb, tiles_c, tile_byte);
   } else {
     const int c = t - kTile;
-    if (COL) {
-      const uint32_t w = col_max[c >> 1];
-      store_scale(s_col, c0 + c, rb, nrb, scale_byte<E5M2>((c & 1) ? w >> 16 : w & 0xFFFFu));
-    }
+    if (COL) store_scale(s_col, c0 + c, rb, nrb, col_scale[c]);
     if (TILE) store_scale(s_col, c0 + c, rb, nrb, tile_byte);
   }
 }

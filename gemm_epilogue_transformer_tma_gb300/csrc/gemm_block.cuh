@@ -176,59 +176,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockPairSmem::THREA
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA
-    if (lane == 0) {
-      const uint32_t leader_full = mapa_shared(smem_u32(full), 0);
-      const int groups = (g.num_kb + 3) >> 2;  // scale chunks per 128 rows
-      int stage = 0;
-      uint32_t phase = 0;
-      int issued = 0, skipped = -1;
-      bool ok = true;
-      bool skip = ctl.skip_first_stage == 1 && cluster_id == 0 && leader;
-      if (ctl.skip_first_stage == 2 && cluster_id == 0 && !leader) ok = false;
-      for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
-        int tm, tn;
-        tile_coords(t, sh, tm, tn);
-        const int m0 = tm * BM2 + static_cast<int>(rank) * 128;
-        const int n0 = tn * BN + static_cast<int>(rank) * 128;
-        for (int kb = 0; kb < g.num_kb; ++kb) {
-          if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, ctl.timeout_ns)) {
-            if (!*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_PRODUCER);
-            ok = false;
-            break;
-          }
-          if (skip) {
-            skip = false;  // test hook: the leader never arms this stage
-            skipped = issued;
-          } else {
-            uint8_t* sa = smem + stage * L::STAGE_BYTES;
-            uint8_t* sb = sa + L::A_BYTES;
-            uint8_t* sf = sf_ring + stage * L::SF_BYTES;
-            const uint32_t bar = leader_full + static_cast<uint32_t>(stage * 8);
-            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * L::fill_bytes(kb));
-            if (!A_MN)
-              tma_load_2d_pair(sa, &g.A, bar, kb * 128, m0);
-            else
-              tma_load_2d_pair(sa, &g.A, bar, m0, kb * 128);
-            if (!B_MN)
-              tma_load_2d_pair(sb, &g.B, bar, kb * 128, n0);
-            else
-              tma_load_2d_pair(sb, &g.B, bar, n0, kb * 128);
-            if ((kb & 3) == 0) {
-              const int q = kb >> 2;
-              tma_load_2d_pair(sf, &g.sA, bar, 0, (m0 >> 7) * groups + q);
-              tma_load_2d_pair(sf + kScaleChunk, &g.sB, bar, 0, (2 * tn) * groups + q);
-              tma_load_2d_pair(sf + 2 * kScaleChunk, &g.sB, bar, 0, (2 * tn + 1) * groups + q);
-            }
-          }
-          ++issued;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
+    // the whole warp, converged (elect_one)
+    const uint32_t leader_full = mapa_shared(smem_u32(full), 0);
+    const int groups = (g.num_kb + 3) >> 2;  // scale chunks per 128 rows
+    int stage = 0;
+    uint32_t phase = 0;
+    int issued = 0, skipped = -1;
+    bool ok = true;
+    bool skip = ctl.skip_first_stage == 1 && cluster_id == 0 && leader;
+    if (ctl.skip_first_stage == 2 && cluster_id == 0 && !leader) ok = false;
+    for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
+      int tm, tn;
+      tile_coords(t, sh, tm, tn);
+      const int m0 = tm * BM2 + static_cast<int>(rank) * 128;
+      const int n0 = tn * BN + static_cast<int>(rank) * 128;
+      for (int kb = 0; kb < g.num_kb; ++kb) {
+        ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, ctl.timeout_ns);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          if (lane == 0 && !*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_PRODUCER);
+          break;
+        }
+        if (skip) {
+          skip = false;  // test hook: the leader never arms this stage
+          skipped = issued;
+        } else if (elect_one()) {
+          uint8_t* sa = smem + stage * L::STAGE_BYTES;
+          uint8_t* sb = sa + L::A_BYTES;
+          uint8_t* sf = sf_ring + stage * L::SF_BYTES;
+          const uint32_t bar = leader_full + static_cast<uint32_t>(stage * 8);
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * L::fill_bytes(kb));
+          if (!A_MN)
+            tma_load_2d_pair(sa, &g.A, bar, kb * 128, m0);
+          else
+            tma_load_2d_pair(sa, &g.A, bar, m0, kb * 128);
+          if (!B_MN)
+            tma_load_2d_pair(sb, &g.B, bar, kb * 128, n0);
+          else
+            tma_load_2d_pair(sb, &g.B, bar, n0, kb * 128);
+          if ((kb & 3) == 0) {
+            const int q = kb >> 2;
+            tma_load_2d_pair(sf, &g.sA, bar, 0, (m0 >> 7) * groups + q);
+            tma_load_2d_pair(sf + kScaleChunk, &g.sB, bar, 0, (2 * tn) * groups + q);
+            tma_load_2d_pair(sf + 2 * kScaleChunk, &g.sB, bar, 0, (2 * tn + 1) * groups + q);
           }
         }
+        __syncwarp();
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      // every fill of both CTAs observed landed before shared memory can be
-      // released; fill i of the ring is k-block i mod num_kb of its tile
+    }
+    // every fill of both CTAs observed landed before shared memory can be
+    // released; fill i of the ring is k-block i mod num_kb of its tile
+    if (lane == 0) {
       bool landed = true;
       if (!leader) {
         st_release_cluster_u32(mapa_shared(smem_u32(fill_report), 0), static_cast<uint32_t>(issued) + 1u);
@@ -248,8 +251,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockPairSmem::THREA
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA
-    if (lane == 0 && leader) {
+    if (leader) {  // the whole warp, converged
       const uint32_t idesc = IDESC0 | g.f8_fmt;
+      // descriptors of stage 0, advanced by address / 16
+      const uint64_t adesc0 = sdesc_sw128(smem_u32(smem), A_MN ? 128 * 128 : 16, 1024);
+      const uint64_t bdesc0 = sdesc_sw128(smem_u32(smem) + L::A_BYTES, B_MN ? 128 * 128 : 16, 1024);
+      const uint64_t sfdesc0 = sdesc_scales(smem_u32(sf_ring));
       int stage = 0;
       uint32_t phase = 0;
       int it = 0;
@@ -257,55 +264,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockPairSmem::THREA
       bool ok = true;
       bool issued_any = false;
       for (int t = cluster_id; t < num_tiles && ok; t += num_clusters, ++it) {
-        // the previous tile's shared columns have been read, and with them
-        // all of the tile before it, whose accumulator this one takes
-        if (it > 0 && !mbar_wait_bounded_cluster(tempty, static_cast<uint32_t>(it - 1) & 1u, abort_flag,
-                                                 ctl.timeout_ns)) {
-          if (!*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_MMA);
-          ok = false;
-          break;
-        }
-        tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((it & 1) * L::ACC_STEP);
         uint32_t sfa = 0;
         for (int kb = 0; kb < g.num_kb; ++kb) {
-          if (!mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, ctl.timeout_ns)) {
-            if (!*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_MMA);
+          // the previous tile's shared columns have been read, and with them
+          // all of the tile before it, whose accumulator this one takes
+          if (kb == 0 && it > 0)
+            ok = mbar_wait_bounded_cluster(tempty, static_cast<uint32_t>(it - 1) & 1u, abort_flag, ctl.timeout_ns);
+          ok = ok && mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, ctl.timeout_ns);
+          if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
+            if (lane == 0 && !*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_MMA);
             break;
           }
           tc_fence_after();
           if ((kb & 3) == 0) {
-            const uint32_t sf = smem_u32(sf_ring + stage * L::SF_BYTES);
             sfa = tmem_base + static_cast<uint32_t>(L::SF_COL) + sf_buf * 12u;
             sf_buf ^= 1u;
-            tmem_cp_scales_pair(sfa, sdesc_scales(sf));
-            tmem_cp_scales_pair(sfa + 4, sdesc_scales(sf + kScaleChunk));
-            tmem_cp_scales_pair(sfa + 8, sdesc_scales(sf + 2 * kScaleChunk));
           }
-          const uint32_t id = idesc | idesc_scale_id(static_cast<uint32_t>(kb) & 3u);
-          const uint32_t sa = smem_u32(smem + stage * L::STAGE_BYTES);
-          const uint32_t sb = sa + L::A_BYTES;
+          if (elect_one()) {
+            if ((kb & 3) == 0) {
+              const uint64_t sf = sfdesc0 + static_cast<uint32_t>(stage * (L::SF_BYTES >> 4));
+              tmem_cp_scales_pair(sfa, sf);
+              tmem_cp_scales_pair(sfa + 4, sf + (kScaleChunk >> 4));
+              tmem_cp_scales_pair(sfa + 8, sf + 2 * (kScaleChunk >> 4));
+            }
+            const uint32_t id = idesc | idesc_scale_id(static_cast<uint32_t>(kb) & 3u);
+            const uint64_t ad = adesc0 + static_cast<uint32_t>(stage * (L::STAGE_BYTES >> 4));
+            const uint64_t bd = bdesc0 + static_cast<uint32_t>(stage * (L::STAGE_BYTES >> 4));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t ad = A_MN ? sdesc_sw128(sa + k * 4096, 128 * 128, 1024) : sdesc_sw128(sa + k * 32, 16, 1024);
-            const uint64_t bd = B_MN ? sdesc_sw128(sb + k * 4096, 128 * 128, 1024) : sdesc_sw128(sb + k * 32, 16, 1024);
-            umma_mxf8_pair(d_tmem, ad, bd, id, sfa, sfa + 4, (kb | k) != 0 ? 1u : 0u);
+            for (int k = 0; k < 4; ++k)
+              umma_mxf8_pair(d_tmem, ad + k * ((A_MN ? 4096 : 32) >> 4), bd + k * ((B_MN ? 4096 : 32) >> 4), id, sfa,
+                             sfa + 4, (kb | k) != 0 ? 1u : 0u);
+            umma_commit_pair_multicast(&empty[stage], 0x3);
+            if (kb == g.num_kb - 1) umma_commit_pair_multicast(&tfull[it & 1], 0x3);
           }
+          __syncwarp();
           issued_any = true;
-          umma_commit_pair_multicast(&empty[stage], 0x3);
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (!ok) break;
-        umma_commit_pair_multicast(&tfull[it & 1], 0x3);
       }
-      // every MMA this thread issued has completed before TMEM is freed
+      // every MMA this warp issued has completed before TMEM is freed
       if (issued_any) {
-        umma_commit_pair_local(drain);
-        if (!mbar_wait_timeout(drain, 0, ctl.timeout_ns)) atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
+        if (elect_one()) umma_commit_pair_local(drain);
+        __syncwarp();
+        if (!mbar_wait_timeout(drain, 0, ctl.timeout_ns) && lane == 0) atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
       }
     }
   } else {
@@ -339,7 +345,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockPairSmem::THREA
         if (j == 0) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(leader_tempty);
+          if (lane == 0) mbar_arrive_cluster_relaxed(leader_tempty);
         }
         const int n0 = tn * BN + blk * 32;
         if (n0 < g.N && m0 < g.M) {
@@ -461,20 +467,22 @@ __global__ void __launch_bounds__(BlockFewSmem<BN>::THREADS, BlockFewSmem<BN>::C
   griddep_wait();
 
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, pending = 0, parity = 0;
-      bool ok = true;
-      bool skip = ctl.skip_first_stage != 0 && blockIdx.x == 0 && blockIdx.y == 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, ctl.timeout_ns)) {
-          if (!*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_PRODUCER);
-          ok = false;
-          break;
-        }
-        if (skip) {
-          skip = false;  // test hook: leave this stage unfilled
-        } else {
+    // the whole warp, converged (elect_one)
+    int stage = 0;
+    uint32_t phase = 0, pending = 0, parity = 0;
+    bool ok = true;
+    bool skip = ctl.skip_first_stage != 0 && blockIdx.x == 0 && blockIdx.y == 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, ctl.timeout_ns);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        if (lane == 0 && !*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_PRODUCER);
+        break;
+      }
+      if (skip) {
+        skip = false;  // test hook: leave this stage unfilled
+      } else {
+        if (elect_one()) {
           uint8_t* sw = smem + stage * L::STAGE_BYTES;
           uint8_t* sf = sf_ring + stage * L::SF_BYTES;
           const bool with_sf = (kb & 3) == 0;
@@ -488,56 +496,62 @@ __global__ void __launch_bounds__(BlockFewSmem<BN>::THREADS, BlockFewSmem<BN>::C
             tma_load_2d(sf, &g.sW, &full[stage], 0, (n0 >> 7) * groups + (kb >> 2));
             tma_load_2d(sf + kScaleChunk, &g.sX, &full[stage], 0, (m0 >> 7) * groups + (kb >> 2));
           }
-          pending |= 1u << stage;
-          parity = (parity & ~(1u << stage)) | (phase << stage);
         }
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        __syncwarp();
+        pending |= 1u << stage;
+        parity = (parity & ~(1u << stage)) | (phase << stage);
       }
-      if (!ok) {
-        // let every copy this thread started land before shared memory is released
-        for (int st = 0; st < STAGES; ++st)
-          if ((pending >> st) & 1u)
-            if (!mbar_wait_timeout(&full[st], (parity >> st) & 1u, ctl.timeout_ns))
-              atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
       }
+    }
+    if (!ok && lane == 0) {
+      // let every copy this warp started land before shared memory is released
+      for (int st = 0; st < STAGES; ++st)
+        if ((pending >> st) & 1u)
+          if (!mbar_wait_timeout(&full[st], (parity >> st) & 1u, ctl.timeout_ns))
+            atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = IDESC0 | g.f8_fmt;
-      int stage = 0;
-      uint32_t phase = 0, sfa = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded(&full[stage], phase, abort_flag, ctl.timeout_ns)) {
-          if (!*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_MMA);
-          break;
-        }
-        tc_fence_after();
+    const uint32_t idesc = IDESC0 | g.f8_fmt;
+    const uint64_t wdesc0 = sdesc_sw128(smem_u32(smem), W_MN ? 128 * 128 : 16, 1024);
+    const uint64_t xdesc0 = sdesc_sw128(smem_u32(smem) + L::W_BYTES, 16, 1024);
+    const uint64_t sfdesc0 = sdesc_scales(smem_u32(sf_ring));
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const bool ok = mbar_wait_bounded(&full[stage], phase, abort_flag, ctl.timeout_ns);
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (lane == 0 && !*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_MMA);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t sfa = tmem_base + static_cast<uint32_t>(L::SF_COL) + (static_cast<uint32_t>(kb >> 2) & 1u) * 8u;
+      if (elect_one()) {
         if ((kb & 3) == 0) {
-          const uint32_t sf = smem_u32(sf_ring + stage * L::SF_BYTES);
-          sfa = tmem_base + static_cast<uint32_t>(L::SF_COL) + (static_cast<uint32_t>(kb >> 2) & 1u) * 8u;
-          tmem_cp_scales(sfa, sdesc_scales(sf));
-          tmem_cp_scales(sfa + 4, sdesc_scales(sf + kScaleChunk));
+          const uint64_t sf = sfdesc0 + static_cast<uint32_t>(stage * (L::SF_BYTES >> 4));
+          tmem_cp_scales(sfa, sf);
+          tmem_cp_scales(sfa + 4, sf + (kScaleChunk >> 4));
         }
         const uint32_t id = idesc | idesc_scale_id(static_cast<uint32_t>(kb) & 3u);
-        const uint32_t sw = smem_u32(smem + stage * L::STAGE_BYTES);
-        const uint32_t sx = sw + L::W_BYTES;
+        const uint64_t wd = wdesc0 + static_cast<uint32_t>(stage * (L::STAGE_BYTES >> 4));
+        const uint64_t xd = xdesc0 + static_cast<uint32_t>(stage * (L::STAGE_BYTES >> 4));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t wd = W_MN ? sdesc_sw128(sw + k * 4096, 128 * 128, 1024) : sdesc_sw128(sw + k * 32, 16, 1024);
-          umma_mxf8(tmem_base, wd, sdesc_sw128(sx + k * 32, 16, 1024), id, sfa, sfa + 4, (kb != kb0 || k != 0) ? 1u : 0u);
-        }
+        for (int k = 0; k < 4; ++k)
+          umma_mxf8(tmem_base, wd + k * ((W_MN ? 4096 : 32) >> 4), xd + k * 2, id, sfa, sfa + 4,
+                    (kb != kb0 || k != 0) ? 1u : 0u);
         umma_commit(&empty[stage]);
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
       }
-      // arrives when every MMA this thread issued has completed
-      umma_commit(tfull);
+      __syncwarp();
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
+    // arrives when every MMA this warp issued has completed
+    if (elect_one()) umma_commit(tfull);
+    __syncwarp();
   } else {
     const int quad = warp & 3;
     const int row = quad * 32 + lane;

@@ -1,6 +1,7 @@
 // LM-head GEMM instantiations: blocked log-sum-exp statistics epilogue and the
 // softmax-gradient epilogue (logits never leave the chip).
 #include "gemm_launch.cuh"
+#include "gemm_logits.cuh"
 
 namespace coda {
 
@@ -16,6 +17,35 @@ cudaError_t gemm_ce_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv
   if (!make_operand_maps(&ta, &tb, H, false, Wt, false, M, V, d, b_box_rows(c))) return cudaErrorInvalidValue;
   EpiCeStats::Params ep{labels, pmax, psum, parg, zy, T, c.status};
   return run_gemm<false, false, false, EpiCeStats>(c, ta, tb, tb, M, V, d, (V + kBN - 1) / kBN, ep);
+}
+
+cudaError_t gemm_logit_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt,
+                             const int32_t* labels, float* pmax, float* psum, float* zy, int M, int d, int V, int T) {
+  using L = LogitsSmem;
+  LogitsArgs g{};
+  if (!make_operand_maps(&g.H, &g.W, H, false, Wt, false, M, V, d, 128)) return cudaErrorInvalidValue;
+  g.labels = labels;
+  g.pmax = pmax;
+  g.psum = psum;
+  g.zy = zy;
+  g.M = M;
+  g.V = V;
+  g.T = T;
+  g.tiles_m = (M + BM2 - 1) / BM2;
+  g.tiles_n = (V + kBN - 1) / kBN;
+  g.num_kb = (d + BK - 1) / BK;
+  g.group_m = 8;
+  g.scale = c.scale_host;
+  static bool smem_ok[64] = {};
+  cudaError_t e = allow_smem(gemm_logits_kernel, L::TOTAL, smem_ok);
+  if (e != cudaSuccess) return e;
+  static int cap[64] = {};
+  int pairs = 0;
+  e = pair_capacity(reinterpret_cast<const void*>(gemm_logits_kernel), L::THREADS, L::TOTAL, c.num_sms, cap, &pairs);
+  if (e != cudaSuccess) return e;
+  KernelCtl ctl{c.status, c.timeout_ns, c.skip_first_stage};
+  const int clusters = std::max(1, std::min(g.tiles_m * g.tiles_n, pairs));
+  return launch_chained(c, gemm_logits_kernel, dim3(2 * clusters), dim3(L::THREADS), L::TOTAL, g, ctl);
 }
 
 cudaError_t gemm_ce_grad(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt_chunk,

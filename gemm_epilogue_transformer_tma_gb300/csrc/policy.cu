@@ -58,6 +58,7 @@ __global__ void policy_rows_kernel(const float* __restrict__ pmax, const float* 
   const float w = p.weight != nullptr ? p.weight[m] : p.uniform;
   const int32_t y = p.labels_in[m];
   const bool in_range = y >= 0 && y < V;
+  if (!in_range) atomicOr(p.status, DEV_ERR_LABEL_RANGE);
   const float lp = in_range ? zy[m] - lse : 0.f;
   p.logp[m] = lp;
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -355,6 +355,20 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// True in one lane of a converged warp.  A warp that stays together around
+// its elected lane's instructions keeps addresses and descriptors in uniform
+// registers, where the MMA wants them; a loop run by lane 0 alone has to move
+// them there for every MMA.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 // ---------------------------------------------------------------------------
 // CTA pairs (clusters of 2) and the 2-SM forms of the tcgen05 instructions
 // ---------------------------------------------------------------------------
@@ -404,6 +418,13 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 // Arrive on an mbarrier of another CTA of the cluster (release at cluster scope).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// The same without release: for hand-overs of tensor memory that this thread
+// has read (the loads have completed and tc_fence_before orders them).  A
+// release would also wait for the thread's earlier global stores.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // Whole-cluster barrier (every thread of both CTAs).

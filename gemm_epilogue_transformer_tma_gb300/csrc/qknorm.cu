@@ -82,12 +82,19 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// cos / sin of the row's position for pairs [8 l, 8 l + 8), two to a word.  A
+// a / b and a % b; a 64-bit division takes several times the instructions of
+// a 32-bit one
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+__device__ __forceinline__ int64_t rem(int64_t a, int64_t b) { return a - quot(a, b) * b; }
+
+// cos / sin of position p for pairs [8 l, 8 l + 8), two to a word.  A
 // position outside the table raises the status bit and leaves the row
 // unrotated.
-__device__ __forceinline__ void load_angles(const HeadArgs& a, int64_t m, int l, bool active, f32x2 (&cs)[4],
+__device__ __forceinline__ void load_angles(const HeadArgs& a, int64_t p, int l, bool active, f32x2 (&cs)[4],
                                             f32x2 (&sn)[4]) {
-  const int64_t p = a.pos != nullptr ? static_cast<int64_t>(a.pos[m]) : m % a.S;
   const bool ok = p >= 0 && p < a.S;
   if (!ok && l == 0) atomicOr(a.status, DEV_ERR_POSITION_RANGE);
   if (ok && active) {
@@ -118,7 +125,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) qknorm_rope_kernel(const HeadA
   const bool active = 16 * l < a.D;  // lanes past D / 16 hold nothing
   const int half = a.D / 2;
   const int64_t task = blockIdx.x * static_cast<int64_t>(kWarps) + (threadIdx.x >> 5);
-  const int64_t m = task / a.chunks;
+  const int64_t m = quot(task, a.chunks);
   if (m >= a.M) return;  // warp-uniform
   const Chunk k = chunk_of(a, m, static_cast<int>(task - m * a.chunks), U * HW);
   const int64_t row = m * (static_cast<int64_t>(a.n_q + 2 * a.n_kv) * a.D);
@@ -135,7 +142,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) qknorm_rope_kernel(const HeadA
   }
   f32x2 cs[4], sn[4], g1[4], g2[4];
   if (k.kind < 2) {
-    load_angles(a, m, l, active, cs, sn);
+    load_angles(a, a.pos != nullptr ? static_cast<int64_t>(a.pos[m]) : rem(m, a.S), l, active, cs, sn);
     const uint32_t* g = reinterpret_cast<const uint32_t*>((k.kind == 0 ? a.gq : a.gk) + 8 * l);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -201,7 +208,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(
   const int half = a.D / 2;
   const int64_t first = blockIdx.x * static_cast<int64_t>(kWarps) + warp;
   const int64_t m_step = static_cast<int64_t>(gridDim.x) * kWarps / a.chunks;
-  const int64_t m0 = first / a.chunks;
+  const int64_t m0 = quot(first, a.chunks);
   const Chunk k = chunk_of(a, m0, static_cast<int>(first - m0 * a.chunks), U * HW);
   const int64_t width = static_cast<int64_t>(a.n_q + 2 * a.n_kv) * a.D;
   const int64_t head0 = static_cast<int64_t>(k.first) * a.D;
@@ -235,9 +242,13 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(
   }
   int s = 0;
   uint32_t phase = 0;
+  int64_t pos = rem(m0, a.S);  // of row m when there are no positions
+  const int64_t pos_step = rem(m_step, a.S);
   for (int64_t m = m0; m < a.M; m += m_step) {
     f32x2 cs[W], sn[W];
-    if (k.kind < 2) load_angles(a, m, l, active, cs, sn);
+    if (k.kind < 2) load_angles(a, a.pos != nullptr ? static_cast<int64_t>(a.pos[m]) : pos, l, active, cs, sn);
+    pos += pos_step;
+    if (pos >= a.S) pos -= a.S;
     // the copies are this warp's own: they land, or the device has failed
     const bool landed = mbar_wait_timeout(&bars[warp][s], phase, a.timeout_ns);
     if (!__all_sync(0xffffffffu, landed)) {
