@@ -177,38 +177,26 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
-# The calls below that serve single tokens are as short as a kernel launch, so
-# their marshalling counts: one test per tensor on the way through (_arg), the
-# raw stream of the tensors' device (0.1 us; the Stream object's 2 us), and
-# the library object without its lock.
-def _on(t: torch.Tensor, stream):
-    """(library, handle, device index, stream) for a call on t's device."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError("the tensors of a call must be CUDA tensors")
-    lib = _lib or load_library()
-    h = _handles.get(dev) or handle(dev)
-    return lib, h, dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+# The block-scaled, head-norm and policy calls marshal their arguments in C++
+# (binding/marshal.cpp): they serve single tokens, where the same tests in Python
+# took longer than the kernels.
+_bound = None
 
 
-def _arg(t: torch.Tensor, dtype, shape: tuple, name: str, dev: int) -> int:
-    """The address of t, a contiguous tensor of that type and shape on device
-    dev."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    _ptr(t, dtype, name)
-    _shape(t, shape, name)
-    raise ValueError(f"{name} is on {t.device}, other tensors of the call on cuda:{dev}")
-
-
-def _opt(t, dtype, shape, name, dev):
-    return None if t is None else _arg(t, dtype, shape, name, dev)
-
-
-def _bytes(t: torch.Tensor, dev: int, name: str):
-    """(address, size in bytes) of a workspace on device dev."""
-    n = t.numel() * t.element_size()
-    return _arg(t, t.dtype, t.shape, name, dev), n
+def _bind():
+    """The marshalling module, bound to the loaded library's entry points."""
+    global _bound
+    if _bound is None:
+        lib = load_library()
+        try:
+            from . import _marshal as mod
+        except ImportError as e:
+            raise ImportError(f"{e}: build it with `python -m gemm_epilogue_transformer_tma_gb300.build`") from e
+        mod.bind(handle, *(ctypes.cast(getattr(lib, n), _P).value for n in (
+            "coda_fp8_block_quantize", "coda_fp8_block_quantize_weight", "coda_fp8_block_dequantize",
+            "coda_gemm_fp8_block", "coda_qknorm_rope", "coda_qknorm_rope_bwd", "coda_lmhead_policy")))
+        _bound = mod
+    return _bound
 
 
 def _ptr(t: torch.Tensor | None, dtype=None, name="tensor") -> int | None:
@@ -680,14 +668,8 @@ def coda_qknorm_rope(qkv, gq, gk, cos_t, sin_t, out, n_q_heads, n_kv_heads, head
                      positions=None, stream=None):
     """RMSNorm of the q and k heads (weights gq, gk), then RoPE, in one pass;
     out may be qkv (see include/coda.h)."""
-    lib, h, dev, st = _on(qkv, stream)
-    M, S = qkv.shape[0], cos_t.shape[0]
-    full, g, tab = (M, (n_q_heads + 2 * n_kv_heads) * head_dim), (head_dim,), (S, head_dim // 2)
-    st = lib.coda_qknorm_rope(
-        h, _arg(qkv, BF, full, "qkv", dev), _arg(gq, BF, g, "gq", dev), _opt(gk, BF, g, "gk", dev),
-        _arg(cos_t, F32, tab, "cos_t", dev), _arg(sin_t, F32, tab, "sin_t", dev),
-        _opt(positions, I32, (M,), "positions", dev), _arg(out, BF, full, "out", dev), M, n_q_heads, n_kv_heads,
-        head_dim, S, eps, st)
+    st = (_bound or _bind()).qknorm(qkv, gq, gk, cos_t, sin_t, out, n_q_heads, n_kv_heads, head_dim, eps, positions,
+                                    stream)
     if st:
         _check(st, "coda_qknorm_rope")
 
@@ -700,15 +682,8 @@ def coda_qknorm_rope_bwd(dout, qkv, gq, gk, cos_t, sin_t, dqkv, dgq, dgk, ws, n_
                          eps=1e-6, positions=None, stream=None):
     """Backward of coda_qknorm_rope from dout and its input qkv; dqkv may be
     dout or qkv (see include/coda.h)."""
-    lib, h, dev, st = _on(dgq, stream)
-    M, S = qkv.shape[0], cos_t.shape[0]
-    full, g, tab = (M, (n_q_heads + 2 * n_kv_heads) * head_dim), (head_dim,), (S, head_dim // 2)
-    st = lib.coda_qknorm_rope_bwd(
-        h, _arg(dout, BF, full, "dout", dev), _arg(qkv, BF, full, "qkv", dev), _arg(gq, BF, g, "gq", dev),
-        _opt(gk, BF, g, "gk", dev), _arg(cos_t, F32, tab, "cos_t", dev), _arg(sin_t, F32, tab, "sin_t", dev),
-        _opt(positions, I32, (M,), "positions", dev), _arg(dqkv, BF, full, "dqkv", dev),
-        _arg(dgq, F32, g, "dgq", dev), _opt(dgk, F32, g, "dgk", dev), *_bytes(ws, dev, "ws"), M, n_q_heads,
-        n_kv_heads, head_dim, S, eps, st)
+    st = (_bound or _bind()).qknorm_bwd(dout, qkv, gq, gk, cos_t, sin_t, dqkv, dgq, dgk, ws, n_q_heads, n_kv_heads,
+                                        head_dim, eps, positions, stream)
     if st:
         _check(st, "coda_qknorm_rope_bwd")
 
@@ -857,24 +832,11 @@ def coda_fp8_block_scale_bytes(rows: int, K: int) -> int:
     return load_library().coda_fp8_block_scale_bytes(rows, K)
 
 
-def _packed(rows: int, K: int) -> tuple:
-    """The shape of packed block scales (coda_fp8_block_scale_bytes)."""
-    return (-(-rows // 128) * -(-K // 512) * 512,)
-
-
 def coda_fp8_block_quantize(src, q_row, s_row, q_col, s_col, fmt: int = E4M3, stream=None):
     """Codes of src with a scale for each 1 x 128 block (q_row, s_row) and /
     or each 128 x 1 block (q_col, s_col); a pair may be None (see
     include/coda.h)."""
-    if (q_row is None) != (s_row is None) or (q_col is None) != (s_col is None):
-        raise ValueError("codes and their scales come together")
-    lib, h, dev, st = _on(src, stream)
-    shape = src.shape
-    rows, cols = shape
-    st = lib.coda_fp8_block_quantize(
-        h, _arg(src, BF, shape, "src", dev), fmt, _opt(q_row, U8, shape, "q_row", dev),
-        _opt(s_row, U8, _packed(rows, cols), "s_row", dev), _opt(q_col, U8, shape, "q_col", dev),
-        _opt(s_col, U8, _packed(cols, rows), "s_col", dev), rows, cols, st)
+    st = (_bound or _bind()).quantize(src, q_row, s_row, q_col, s_col, fmt, stream)
     if st:
         _check(st, "coda_fp8_block_quantize")
 
@@ -882,12 +844,7 @@ def coda_fp8_block_quantize(src, q_row, s_row, q_col, s_col, fmt: int = E4M3, st
 def coda_fp8_block_quantize_weight(W, q, s, s_t, fmt: int = E4M3, stream=None):
     """Codes of W [N, K] with a scale for each 128 x 128 block; s for the
     product over K, s_t for the one over N (see include/coda.h)."""
-    lib, h, dev, st = _on(W, stream)
-    shape = W.shape
-    N, K = shape
-    st = lib.coda_fp8_block_quantize_weight(
-        h, _arg(W, BF, shape, "W", dev), fmt, _arg(q, U8, shape, "q", dev), _arg(s, U8, _packed(N, K), "s", dev),
-        _arg(s_t, U8, _packed(K, N), "s_t", dev), N, K, st)
+    st = (_bound or _bind()).quantize_weight(W, q, s, s_t, fmt, stream)
     if st:
         _check(st, "coda_fp8_block_quantize_weight")
 
@@ -895,13 +852,7 @@ def coda_fp8_block_quantize_weight(W, q, s, s_t, fmt: int = E4M3, stream=None):
 def coda_fp8_block_dequantize(q, s, col_blocks: bool, dst, fmt: int = E4M3, stream=None):
     """dst = the bf16 values of codes q with packed scales s of blocks along
     the rows, or along the columns with col_blocks (see include/coda.h)."""
-    lib, h, dev, st = _on(q, stream)
-    shape = q.shape
-    rows, cols = shape
-    st = lib.coda_fp8_block_dequantize(
-        h, _arg(q, U8, shape, "q", dev),
-        _arg(s, U8, _packed(cols, rows) if col_blocks else _packed(rows, cols), "s", dev), bool(col_blocks), fmt,
-        _arg(dst, BF, shape, "dst", dev), rows, cols, st)
+    st = (_bound or _bind()).dequantize(q, s, col_blocks, dst, fmt, stream)
     if st:
         _check(st, "coda_fp8_block_dequantize")
 
@@ -910,12 +861,7 @@ def coda_gemm_fp8_block(A, a_mn_major: bool, a_format: int, sA, B, b_mn_major: b
                         M: int, N: int, K: int, stream=None):
     """C[M,N] = A B on 8-bit codes with packed block scales along K (see
     include/coda.h)."""
-    lib, h, dev, st = _on(C, stream)
-    st = lib.coda_gemm_fp8_block(
-        h, _arg(A, U8, (K, M) if a_mn_major else (M, K), "A", dev), bool(a_mn_major), a_format,
-        _arg(sA, U8, _packed(M, K), "sA", dev), _arg(B, U8, (K, N) if b_mn_major else (N, K), "B", dev),
-        bool(b_mn_major), b_format, _arg(sB, U8, _packed(N, K), "sB", dev), _arg(C, BF, (M, N), "C", dev), M, N, K,
-        st)
+    st = (_bound or _bind()).gemm(A, a_mn_major, a_format, sA, B, b_mn_major, b_format, sB, C, M, N, K, stream)
     if st:
         _check(st, "coda_gemm_fp8_block")
 
@@ -989,18 +935,8 @@ def coda_lmhead_policy(Hs, Wt, labels, advantage, weight, logp_old, logp_ref, cl
                        kl_coef: float, temperature: float, stats, logp, dHs, dWt, ws, stream=None):
     """Clipped policy loss with a KL term on the LM head; weight, logp_old,
     logp_ref and the gradients dHs, dWt may be None (see include/coda.h)."""
-    if (dHs is None) != (dWt is None):
-        raise ValueError("dHs and dWt come together")
-    lib, h, dev, st = _on(Hs, stream)
-    hs, wt = Hs.shape, Wt.shape
-    (M, d), V = hs, wt[0]
-    row = (M,)
-    st = lib.coda_lmhead_policy(
-        h, _arg(Hs, BF, hs, "Hs", dev), _arg(Wt, BF, (V, d), "Wt", dev), _arg(labels, I32, row, "labels", dev),
-        _arg(advantage, F32, row, "advantage", dev), _opt(weight, F32, row, "weight", dev),
-        _opt(logp_old, F32, row, "logp_old", dev), _opt(logp_ref, F32, row, "logp_ref", dev), clip_low, clip_high,
-        kl_coef, temperature, _arg(stats, F32, (4,), "stats", dev), _arg(logp, F32, row, "logp", dev),
-        _opt(dHs, BF, hs, "dHs", dev), _opt(dWt, BF, wt, "dWt", dev), *_bytes(ws, dev, "ws"), M, d, V, st)
+    st = (_bound or _bind()).policy(Hs, Wt, labels, advantage, weight, logp_old, logp_ref, clip_low, clip_high,
+                                    kl_coef, temperature, stats, logp, dHs, dWt, ws, stream)
     if st:
         _check(st, "coda_lmhead_policy")
 

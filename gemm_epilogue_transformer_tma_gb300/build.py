@@ -1,6 +1,7 @@
 """Build libcoda.so in-tree for sm_103a with nvcc (no cmake, no torch build
-machinery).  Translation units compile in parallel; the shared library lands
-next to this file and is rebuilt only when a source is newer."""
+machinery), and the binding's marshalling module _marshal.so with the host
+compiler.  Translation units compile in parallel; the libraries land next to
+this file and are rebuilt only when a source is newer."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -14,6 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libcoda.so")
+MARSHAL_SRC = os.path.join(HERE, "binding", "marshal.cpp")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -34,14 +37,33 @@ def sources():
 
 def _deps():
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
+        glob.glob(os.path.join(INCLUDE, "*.h")) + [MARSHAL_SRC, __file__]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _build_marshal() -> None:
+    """_marshal.so: a CPython module on torch's tensor headers."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    inc = [sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    tmp = MARSHAL + ".tmp"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{i}" for i in inc), MARSHAL_SRC,
+           "-o", tmp, f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the host compiler failed on {os.path.basename(MARSHAL_SRC)}:\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -61,8 +83,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        marshal = ex.submit(_build_marshal)
         objs = list(ex.map(compile_one, srcs))
+        marshal.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

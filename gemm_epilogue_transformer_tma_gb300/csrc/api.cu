@@ -1212,12 +1212,22 @@ namespace {
 // the cross-entropy's workspace, then the policy loss's per-row arrays
 struct PolicyWs {
   CeWs ce;
-  int32_t* labels;
   float* lse;
   float* row_scale;
   float4* terms;
+  float* dH_parts;  // fp32 [dh_parts()][M rounded up to 256][d], when the data gradient is split
   size_t bytes;
 };
+
+// K ranges of the data gradient dH = dL W over a vocabulary chunk of Vc: its
+// 256 x 256 output tiles are spread over kDhUnits SM pairs by cutting K, each
+// range at least 16 k-blocks (1024 of K); 1 leaves it to the grouped launch,
+// which runs the weight gradient's tiles beside it.
+constexpr int64_t kDhUnits = 76;
+int64_t dh_parts(int64_t M, int64_t d, int64_t Vc) {
+  const int64_t tiles = cdiv(M, 256) * cdiv(d, 256);
+  return std::max<int64_t>(1, std::min(kDhUnits / tiles, Vc / 1024));
+}
 
 PolicyWs policy_layout(uint8_t* base, int64_t M, int64_t d, int64_t V, bool grads) {
   PolicyWs w{};
@@ -1228,10 +1238,13 @@ PolicyWs policy_layout(uint8_t* base, int64_t M, int64_t d, int64_t V, bool grad
     off += align256(b);
     return p;
   };
-  w.labels = reinterpret_cast<int32_t*>(take(size_t(M) * 4));
   w.lse = reinterpret_cast<float*>(take(size_t(M) * 4));
   w.terms = reinterpret_cast<float4*>(take(size_t(M) * 16));
-  if (grads) w.row_scale = reinterpret_cast<float*>(take(size_t(M) * 4));
+  if (grads) {
+    w.row_scale = reinterpret_cast<float*>(take(size_t(M) * 4));
+    const int64_t parts = dh_parts(M, d, std::min<int64_t>(V, kCeChunk));
+    if (parts > 1) w.dH_parts = reinterpret_cast<float*>(take(size_t(parts) * cdiv(M, 256) * 256 * d * 4));
+  }
   w.bytes = off;
   return w;
 }
@@ -1278,12 +1291,11 @@ coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt
   LaunchCtx cx = ctx_of(h, stream);
   const bf16* Hb = static_cast<const bf16*>(Hs);
   const bf16* Wb = static_cast<const bf16*>(Wt);
-  CODA_CUDA(launch_policy_labels(cx, labels, weight, M, V, w.labels, w.ce.zy));
   LaunchCtx cl = cx;  // the logits carry 1 / temperature
   cl.scale_host = 1.0f / temperature;
-  CODA_CUDA(gemm_logit_stats(cl, Hb, Wb, w.labels, w.ce.pmax, w.ce.psum, w.ce.zy, int(M), int(d), int(V), int(T)));
+  CODA_CUDA(gemm_logit_stats(cl, Hb, Wb, labels, w.ce.pmax, w.ce.psum, w.ce.zy, int(M), int(d), int(V), int(T)));
   PolicyRows r{};
-  r.labels_in = w.labels;
+  r.labels = labels;
   r.adv = advantage;
   r.weight = weight;
   r.old = logp_old;
@@ -1300,15 +1312,26 @@ coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt
   r.status = cx.status;
   CODA_CUDA(launch_policy_rows(cx, w.ce.pmax, w.ce.psum, w.ce.zy, r, M, T, V, stats));
   if (!grads) return CODA_OK;
+  // the first chunk sets the number of ranges (never more than the workspace
+  // has slices); a short last chunk adds to as many slices as it has k-blocks
   const int64_t chunk = h->ce_chunk;
+  const int64_t parts = dh_parts(M, d, std::min(chunk, V));
   for (int64_t v0 = 0; v0 < V; v0 += chunk) {
     const int64_t Vc = std::min<int64_t>(chunk, V - v0);
     const bf16* Wc = Wb + v0 * d;
-    CODA_CUDA(gemm_ce_grad(cl, Hb, Wc, w.labels, w.lse, w.ce.dL, int(M), int(d), int(Vc), int(v0), 0.f, w.row_scale));
-    CODA_CUDA(gemm_group_ce_bwd(cx, w.ce.dL, Wc, Hb, w.ce.dH32, v0 > 0, static_cast<bf16*>(dWt) + v0 * d, int(M),
-                                int(d), int(Vc)));
+    bf16* dWc = static_cast<bf16*>(dWt) + v0 * d;
+    CODA_CUDA(gemm_ce_grad(cl, Hb, Wc, labels, w.lse, w.ce.dL, int(M), int(d), int(Vc), int(v0), 0.f, w.row_scale));
+    if (parts == 1) {
+      CODA_CUDA(gemm_group_ce_bwd(cx, w.ce.dL, Wc, Hb, w.ce.dH32, v0 > 0, dWc, int(M), int(d), int(Vc)));
+    } else {
+      CODA_CUDA(gemm_splitk(cx, w.ce.dL, Wc, w.dH_parts, int(std::min(parts, cdiv(Vc, 64))), v0 > 0, int(M), int(d), int(Vc)));
+      CODA_CUDA(gemm_store(cx, w.ce.dL, true, Hb, true, dWc, int(Vc), int(d), int(M), nullptr, nullptr));
+    }
   }
-  CODA_CUDA(launch_f32_to_bf16(cx, w.ce.dH32, static_cast<bf16*>(dHs), M * d));
+  if (parts == 1)
+    CODA_CUDA(launch_f32_to_bf16(cx, w.ce.dH32, static_cast<bf16*>(dHs), M * d));
+  else
+    CODA_CUDA(launch_sum_parts(cx, w.dH_parts, int(parts), cdiv(M, 256) * 256 * d, static_cast<bf16*>(dHs), M * d));
   return CODA_OK;
 }
 

@@ -156,6 +156,11 @@ cudaError_t gemm_ce_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv
 cudaError_t gemm_logit_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt,
                              const int32_t* labels, float* pmax, float* psum, float* zy, int M, int d, int V, int T);
 
+// parts_buf [parts][M rounded up to 256][N] fp32 (+)= the K ranges of A B, A
+// [M][K], B [K][N] (gemm_splitk.cuh); parts <= the k-blocks of 64 in K
+cudaError_t gemm_splitk(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_bfloat16* B, float* parts_buf, int parts,
+                        bool accumulate, int M, int N, int K);
+
 // dL chunk = (softmax - onehot) / M for vocabulary rows [v0, v0 + Vc), or
 // row_scale[m] (softmax - onehot) with row_scale != null.  The logits are
 // c.scale_host H Wt^T, as in gemm_ce_stats.
@@ -295,7 +300,7 @@ cudaError_t launch_qknorm_rope_bwd(const LaunchCtx& c, const __nv_bfloat16* dy, 
 int qknorm_max_parts();
 // the policy loss's row kernels (policy.cu)
 struct PolicyRows {
-  const int32_t* labels_in;  // from launch_policy_labels
+  const int32_t* labels;
   const float* adv;
   const float* weight;       // or null: uniform
   const float* old;          // or null: the current log-probabilities (ratio 1)
@@ -308,8 +313,9 @@ struct PolicyRows {
   float4* terms;
   int* status;
 };
-cudaError_t launch_policy_labels(const LaunchCtx& c, const int32_t* labels, const float* weight, int64_t M, int64_t V,
-                                 int32_t* out, float* zy);
+// out = bf16(sum_p parts[p]), n values per part at a distance of `stride` values
+cudaError_t launch_sum_parts(const LaunchCtx& c, const float* parts, int num, int64_t stride, __nv_bfloat16* out,
+                             int64_t n);
 cudaError_t launch_policy_rows(const LaunchCtx& c, const float* pmax, const float* psum, const float* zy,
                                const PolicyRows& p, int64_t M, int64_t T, int64_t V, float* stats);
 // unfused ablation kernels

@@ -2,6 +2,7 @@
 // softmax-gradient epilogue (logits never leave the chip).
 #include "gemm_launch.cuh"
 #include "gemm_logits.cuh"
+#include "gemm_splitk.cuh"
 
 namespace coda {
 
@@ -46,6 +47,29 @@ cudaError_t gemm_logit_stats(const LaunchCtx& c, const __nv_bfloat16* H, const _
   KernelCtl ctl{c.status, c.timeout_ns, c.skip_first_stage};
   const int clusters = std::max(1, std::min(g.tiles_m * g.tiles_n, pairs));
   return launch_chained(c, gemm_logits_kernel, dim3(2 * clusters), dim3(L::THREADS), L::TOTAL, g, ctl);
+}
+
+cudaError_t gemm_splitk(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_bfloat16* B, float* parts_buf, int parts,
+                        bool accumulate, int M, int N, int K) {
+  using L = SplitKSmem;
+  SplitKArgs g{};
+  g.M = M;
+  g.N = N;
+  g.num_kb = (K + BK - 1) / BK;
+  g.tiles_m = (M + BM2 - 1) / BM2;
+  g.tiles_n = (N + kBN - 1) / kBN;
+  g.parts = parts;
+  g.rows = g.tiles_m * BM2;
+  g.beta = accumulate ? 1 : 0;
+  if (parts < 1 || parts > g.num_kb || !make_operand_maps(&g.A, &g.B, A, false, B, true, M, N, K, 128) ||
+      !make_tmap_store_f32(&g.out, parts_buf, N, uint64_t(parts) * g.rows, N))
+    return cudaErrorInvalidValue;
+  static bool smem_ok[64] = {};
+  const cudaError_t e = allow_smem(gemm_splitk_kernel, L::TOTAL, smem_ok);
+  if (e != cudaSuccess) return e;
+  KernelCtl ctl{c.status, c.timeout_ns, c.skip_first_stage};
+  return launch_chained(c, gemm_splitk_kernel, dim3(2 * g.tiles_m * g.tiles_n * parts), dim3(L::THREADS), L::TOTAL, g,
+                        ctl);
 }
 
 cudaError_t gemm_ce_grad(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt_chunk,

@@ -250,7 +250,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
           v[c][i] = c * 32 + i < nv ? v[c][i] * g.scale : -INFINITY;
           mx = fmaxf(mx, v[c][i]);
         }
-      const int y = g.labels[m] - n0;
+      const int64_t y = static_cast<int64_t>(g.labels[m]) - n0;
       if (y >= 0 && y < BN / 2 && y < nv) {
         float z = 0.f;
 #pragma unroll

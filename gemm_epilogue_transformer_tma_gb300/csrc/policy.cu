@@ -19,20 +19,6 @@ namespace coda {
 
 namespace {
 
-// Labels as the GEMM epilogues take them: a row without weight may carry any
-// label (padding) and stands for column 0; zy (the label logits) starts at 0.
-__global__ void policy_labels_kernel(const int32_t* __restrict__ labels, const float* __restrict__ weight, int64_t M,
-                                     int64_t V, int32_t* __restrict__ out, float* __restrict__ zy) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t m = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-  if (m >= M) return;
-  const int32_t y = labels[m];
-  const bool padding = weight != nullptr && weight[m] == 0.f && (y < 0 || y >= V);
-  out[m] = padding ? 0 : y;
-  zy[m] = 0.f;
-}
-
 // One warp per row: the log-sum-exp of the row's block statistics, then lane
 // 0's token terms.  terms [M][4]: the row's shares of the four statistics.
 __global__ void policy_rows_kernel(const float* __restrict__ pmax, const float* __restrict__ psum,
@@ -44,21 +30,30 @@ __global__ void policy_rows_kernel(const float* __restrict__ pmax, const float* 
   if (m >= M) return;
   const float* mx = pmax + m * T;
   const float* se = psum + m * T;
-  float best = -INFINITY;
-  for (int64_t j = lane; j < T; j += 32) best = fmaxf(best, mx[j]);
+  // one pass: the running maximum and the sum relative to it
+  float best = -INFINITY, s = 0.f;
+#pragma unroll 4
+  for (int64_t j = lane; j < T; j += 32) {
+    const float v = mx[j], e = se[j], top = fmaxf(best, v);
+    s = s * __expf(best - top) + e * __expf(v - top);
+    best = top;
+  }
+  // a lane without a block (T < 32) has s = 0 and must not meet inf - inf
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-  float s = 0.f;
-  for (int64_t j = lane; j < T; j += 32) s += se[j] * __expf(mx[j] - best);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    const float ob = __shfl_xor_sync(0xffffffffu, best, o), os = __shfl_xor_sync(0xffffffffu, s, o);
+    const float top = fmaxf(best, ob);
+    s = (s == 0.f ? 0.f : s * __expf(best - top)) + (os == 0.f ? 0.f : os * __expf(ob - top));
+    best = top;
+  }
   if (lane != 0) return;
   const float lse = best + logf(s);
   p.lse[m] = lse;
   const float w = p.weight != nullptr ? p.weight[m] : p.uniform;
-  const int32_t y = p.labels_in[m];
+  const int32_t y = p.labels[m];
   const bool in_range = y >= 0 && y < V;
-  if (!in_range) atomicOr(p.status, DEV_ERR_LABEL_RANGE);
+  // padding, a row without weight, may carry any label
+  if (!in_range && w != 0.f) atomicOr(p.status, DEV_ERR_LABEL_RANGE);
   const float lp = in_range ? zy[m] - lse : 0.f;
   p.logp[m] = lp;
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -83,43 +78,82 @@ __global__ void policy_rows_kernel(const float* __restrict__ pmax, const float* 
   if (p.row_scale != nullptr) p.row_scale[m] = -g * p.inv_temp;
 }
 
-// stats[i] = sum_m terms[m][i], i < 4, in a fixed order; the sums of signed
-// terms nearly cancel, so they are taken in fp64 (one CTA, M / 1024 rows per
-// thread)
+// a + b and its rounding error, added to lo: sums that nearly cancel keep the
+// digits fp32 drops (fp64 units are scarce on this GPU: the same kernel in
+// fp64 took 10 us for 136 rows)
+__device__ __forceinline__ void add_exact(float& hi, float& lo, float b, float b_lo) {
+  const float s = hi + b;
+  const float t = s - hi;
+  lo += ((hi - (s - t)) + (b - t)) + b_lo;
+  hi = s;
+}
+
+// stats[i] = sum_m terms[m][i], i < 4, in a fixed order (one CTA)
 __global__ void __launch_bounds__(1024) policy_stats_kernel(const float4* __restrict__ terms, int64_t M,
                                                             float* __restrict__ stats) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ double red[32][4];
-  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  __shared__ float2 red[32][4];
+  float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
   for (int64_t i = threadIdx.x; i < M; i += 1024) {
     const float4 t = terms[i];
-    s[0] += t.x;
-    s[1] += t.y;
-    s[2] += t.z;
-    s[3] += t.w;
+    add_exact(hi[0], lo[0], t.x, 0.f);
+    add_exact(hi[1], lo[1], t.y, 0.f);
+    add_exact(hi[2], lo[2], t.z, 0.f);
+    add_exact(hi[3], lo[3], t.w, 0.f);
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s[j] += __shfl_xor_sync(0xffffffffu, s[j], o);
+    for (int j = 0; j < 4; ++j) {
+      const float h = __shfl_xor_sync(0xffffffffu, hi[j], o), l = __shfl_xor_sync(0xffffffffu, lo[j], o);
+      add_exact(hi[j], lo[j], h, l);
+    }
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) red[threadIdx.x >> 5][j] = s[j];
+    for (int j = 0; j < 4; ++j) red[threadIdx.x >> 5][j] = make_float2(hi[j], lo[j]);
   __syncthreads();
-  if (threadIdx.x < 4) {
-    double t = 0.0;
-    for (int w = 0; w < 32; ++w) t += red[w][threadIdx.x];
-    stats[threadIdx.x] = static_cast<float>(t);
+  if (threadIdx.x < 32) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float h = red[threadIdx.x][j].x, l = red[threadIdx.x][j].y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float h2 = __shfl_xor_sync(0xffffffffu, h, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+        add_exact(h, l, h2, l2);
+      }
+      if (threadIdx.x == 0) stats[j] = h + l;
+    }
+  }
+}
+
+// four values per thread: the parts in order
+__global__ void sum_parts_kernel(const float4* __restrict__ parts, int num, int64_t stride4, uint2* __restrict__ out,
+                                 int64_t n4) {
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n4;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    float4 s = parts[i];
+#pragma unroll 4
+    for (int p = 1; p < num; ++p) {
+      const float4 x = parts[p * stride4 + i];
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
+    }
+    out[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
   }
 }
 
 }  // namespace
 
-cudaError_t launch_policy_labels(const LaunchCtx& c, const int32_t* labels, const float* weight, int64_t M, int64_t V,
-                                 int32_t* out, float* zy) {
-  return launch_chained(c, policy_labels_kernel, dim3(static_cast<unsigned>((M + 255) / 256)), dim3(256), 0, labels,
-                        weight, M, V, out, zy);
+cudaError_t launch_sum_parts(const LaunchCtx& c, const float* parts, int num, int64_t stride, __nv_bfloat16* out,
+                             int64_t n) {
+  const int64_t blocks = std::min<int64_t>((n / 4 + 127) / 128, int64_t(c.num_sms) * 16);
+  return launch_chained(c, sum_parts_kernel, dim3(static_cast<unsigned>(blocks)), dim3(128), 0,
+                        reinterpret_cast<const float4*>(parts), num, stride / 4, reinterpret_cast<uint2*>(out), n / 4);
 }
 
 cudaError_t launch_policy_rows(const LaunchCtx& c, const float* pmax, const float* psum, const float* zy,

@@ -751,8 +751,9 @@ coda_status_t coda_lmhead_ce_fp8(coda_handle_t h, const void* Hq, const float* s
                                  void* dWt, void* ws, size_t ws_bytes, int64_t M, int64_t d, int64_t V,
                                  void* stream);
 
-/* Workspace of coda_lmhead_policy: that of coda_lmhead_ce and 28 bytes per
- * row. */
+/* Workspace of coda_lmhead_policy: that of coda_lmhead_ce, 24 bytes per row,
+ * and, with gradients of few tokens (M d below some 2.5 million), up to 20 MB
+ * of fp32 partial sums of dHs. */
 size_t coda_lmhead_policy_workspace_bytes(int64_t M, int64_t d, int64_t V, int with_grads);
 
 /* Clipped policy loss with a KL term on the LM head, without ever writing an
@@ -769,7 +770,7 @@ size_t coda_lmhead_policy_workspace_bytes(int64_t M, int64_t d, int64_t V, int w
  * stats fp32 [4] = {loss, sum -w s, sum w kl, sum of w where clipped}; logp
  * fp32 [M] = lp.  A row of weight 0 (prompt, padding) adds nothing to stats
  * and its dHs row is 0, whatever its advantage, logp_old and logp_ref hold;
- * its label may be anything (one outside [0, V) gives the lp of column 0).
+ * its label may be anything (its logp is 0 for one outside [0, V)).
  * Its Hs row must still be finite (it meets dL = 0 in dWt's contraction).
  * For a row with weight, a label outside [0, V) sets CODA_ERR_LABEL_RANGE in
  * the status word; the row then adds nothing, and its logp is 0.

@@ -119,7 +119,6 @@ def policy_loss(H, Wt, labels, adv, w, old, ref, clip_low, clip_high, beta, temp
     V = Wt.shape[0]
     w = np.full(M, 1.0 / M) if w is None else np.asarray(w, np.float64)
     y = np.asarray(labels, np.int64)
-    y = np.where((w == 0) & ((y < 0) | (y >= V)), 0, y)
     good = (y >= 0) & (y < V)
     L = H @ Wt.T / temperature
     lse = lse_rows(L)
