@@ -1215,7 +1215,7 @@ struct PolicyWs {
   float* lse;
   float* row_scale;
   float4* terms;
-  float* dH_parts;  // fp32 [dh_parts()][M rounded up to 256][d], when the data gradient is split
+  float* dH_parts;  // the data gradient's K ranges: fp32 [dh_parts()][M rounded up to 256][d]
   size_t bytes;
 };
 
@@ -1227,6 +1227,17 @@ constexpr int64_t kDhUnits = 76;
 int64_t dh_parts(int64_t M, int64_t d, int64_t Vc) {
   const int64_t tiles = cdiv(M, 256) * cdiv(d, 256);
   return std::max<int64_t>(1, std::min(kDhUnits / tiles, Vc / 1024));
+}
+
+// Bytes of the ranges' fp32 slices, enough for any number of tokens up to M:
+// a workspace sized for M serves smaller batches too.
+size_t dh_parts_bytes(int64_t M, int64_t d, int64_t Vc) {
+  int64_t most = 0;
+  for (int64_t r = 1; r <= std::min<int64_t>(cdiv(M, 256), kDhUnits); ++r) {
+    const int64_t parts = dh_parts(r * 256, d, Vc);
+    if (parts > 1) most = std::max(most, parts * r);
+  }
+  return size_t(most) * 256 * d * 4;
 }
 
 PolicyWs policy_layout(uint8_t* base, int64_t M, int64_t d, int64_t V, bool grads) {
@@ -1242,8 +1253,7 @@ PolicyWs policy_layout(uint8_t* base, int64_t M, int64_t d, int64_t V, bool grad
   w.terms = reinterpret_cast<float4*>(take(size_t(M) * 16));
   if (grads) {
     w.row_scale = reinterpret_cast<float*>(take(size_t(M) * 4));
-    const int64_t parts = dh_parts(M, d, std::min<int64_t>(V, kCeChunk));
-    if (parts > 1) w.dH_parts = reinterpret_cast<float*>(take(size_t(parts) * cdiv(M, 256) * 256 * d * 4));
+    w.dH_parts = reinterpret_cast<float*>(take(dh_parts_bytes(M, d, std::min<int64_t>(V, kCeChunk))));
   }
   w.bytes = off;
   return w;

@@ -242,13 +242,18 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(
   }
   int s = 0;
   uint32_t phase = 0;
-  int64_t pos = rem(m0, a.S);  // of row m when there are no positions
-  const int64_t pos_step = rem(m_step, a.S);
+  // the position of row m, read one row ahead: the table load waits for it
+  int64_t pos = a.pos == nullptr ? rem(m0, a.S) : m0 < a.M ? a.pos[m0] : 0;
+  const int64_t pos_step = a.pos == nullptr ? rem(m_step, a.S) : 0;
   for (int64_t m = m0; m < a.M; m += m_step) {
     f32x2 cs[W], sn[W];
-    if (k.kind < 2) load_angles(a, a.pos != nullptr ? static_cast<int64_t>(a.pos[m]) : pos, l, active, cs, sn);
-    pos += pos_step;
-    if (pos >= a.S) pos -= a.S;
+    if (k.kind < 2) load_angles(a, pos, l, active, cs, sn);
+    if (a.pos == nullptr) {
+      pos += pos_step;
+      if (pos >= a.S) pos -= a.S;
+    } else if (m + m_step < a.M) {
+      pos = a.pos[m + m_step];
+    }
     // the copies are this warp's own: they land, or the device has failed
     const bool landed = mbar_wait_timeout(&bars[warp][s], phase, a.timeout_ns);
     if (!__all_sync(0xffffffffu, landed)) {

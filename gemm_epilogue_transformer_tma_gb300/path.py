@@ -18,6 +18,9 @@ from . import (CODA_EPI_PLAIN, CODA_EPI_SWIGLU, E4M3, E5M2, coda_bwd_workspace_b
                coda_gemm_res_prms_bwd, coda_gemm_rowscale_swiglu, coda_gemm_rowscale_swiglu_bwd,
                coda_gemm_wgrad_gscale, coda_prms_num_tiles, coda_rstd_combine, coda_swiglu_bwd, coda_swiglu_bwd_fp8,
                coda_unfused_bwd, coda_unfused_fwd, coda_unfused_workspace_bytes)
+from . import (coda_fp8_block_quantize, coda_fp8_block_quantize_weight, coda_fp8_block_scale_bytes,
+               coda_gemm_fp8_block, coda_lmhead_policy, coda_lmhead_policy_workspace_bytes, coda_qknorm_rope,
+               coda_qknorm_rope_bwd, coda_qknorm_rope_bwd_workspace_bytes, coda_rope_table)
 from . import (CODA_BLOCK_BACKWARD, CODA_BLOCK_FP8, CODA_BLOCK_FP8_DELAYED, coda_block_arena_bytes,
                coda_block_create, coda_block_destroy, coda_block_quantize_weights, coda_block_step_host,
                coda_block_stream, coda_block_sync, coda_block_wait_step, STATUS_NAMES)
@@ -371,3 +374,127 @@ class HostBlockStepper:
             self.close()
         except Exception:
             pass
+
+
+class BlockScaledLinear:
+    """A linear layer Y = X W^T on 8-bit codes with a scale for each block of
+    128: weights and activations e4m3, gradients e5m2.
+
+    W [N, K] bf16 stays the caller's; quantize_weight() makes its codes, once
+    for a served model and after every update in training.  M is the largest
+    number of tokens of a call; forward and backward take any up to it and
+    return views of the layer's buffers.
+    """
+
+    def __init__(self, W: torch.Tensor, M: int, backward: bool = True):
+        self.W, self.M, self.with_backward = W, M, backward
+        N, K = W.shape
+        self.N, self.K = N, K
+
+        def u8(*shape):
+            return torch.empty(*shape, dtype=torch.uint8, device=W.device)
+
+        def scales(rows, k):
+            return u8(coda_fp8_block_scale_bytes(max(rows, 1), max(k, 1)))
+
+        self.Wq, self.sW, self.sWt = u8(N, K), scales(N, K), scales(K, N)
+        self.Xq, self.sX, self.Y = u8(M, K), scales(M, K), torch.empty(M, N, dtype=BF, device=W.device)
+        if backward:
+            self.Xc, self.sXc = u8(M, K), scales(K, M)
+            self.Gq, self.sG, self.Gc, self.sGc = u8(M, N), scales(M, N), u8(M, N), scales(N, M)
+            self.dX = torch.empty(M, K, dtype=BF, device=W.device)
+            self.dW = torch.empty(N, K, dtype=BF, device=W.device)
+        self.quantize_weight()
+
+    def quantize_weight(self):
+        coda_fp8_block_quantize_weight(self.W, self.Wq, self.sW, self.sWt)
+
+    @staticmethod
+    def _packed(s, rows, k):
+        return s[:coda_fp8_block_scale_bytes(rows, k)]
+
+    def forward(self, X):
+        """Y [m, N] of X [m, K]; keeps X's codes for the backward."""
+        m, N, K = X.shape[0], self.N, self.K
+        if m == 0:
+            self.m = 0
+            return self.Y[:0]
+        self.m = m
+        Xq, sX = self.Xq[:m], self._packed(self.sX, m, K)
+        if self.with_backward:
+            coda_fp8_block_quantize(X, Xq, sX, self.Xc[:m], self._packed(self.sXc, K, m))
+        else:
+            coda_fp8_block_quantize(X, Xq, sX, None, None)
+        coda_gemm_fp8_block(Xq, False, E4M3, sX, self.Wq, False, E4M3, self.sW, self.Y[:m], m, N, K)
+        return self.Y[:m]
+
+    def backward(self, dY):
+        """(dX, dW) of the last forward from dY [m, N]."""
+        m, N, K = self.m, self.N, self.K
+        if m == 0:
+            self.dW.zero_()
+            return self.dX[:0], self.dW
+        Gq, sG, Gc, sGc = self.Gq[:m], self._packed(self.sG, m, N), self.Gc[:m], self._packed(self.sGc, N, m)
+        coda_fp8_block_quantize(dY, Gq, sG, Gc, sGc, E5M2)
+        coda_gemm_fp8_block(Gq, False, E5M2, sG, self.Wq, True, E4M3, self.sWt, self.dX[:m], m, K, N)
+        coda_gemm_fp8_block(Gc, True, E5M2, sGc, self.Xc[:m], True, E4M3, self._packed(self.sXc, K, m), self.dW, N, K,
+                            m)
+        return self.dX[:m], self.dW
+
+
+class QKVProjection:
+    """The attention input of a block: a BlockScaledLinear to the packed qkv,
+    then the norm of the q and k heads and RoPE, with the backward of both.
+    gq, gk bf16 [head_dim]; positions up to S."""
+
+    def __init__(self, Wqkv, gq, gk, n_q_heads: int, n_kv_heads: int, M: int, S: int, backward: bool = True,
+                 eps: float = 1e-6, base: float = 10000.0):
+        self.linear = BlockScaledLinear(Wqkv, M, backward)
+        self.gq, self.gk, self.eps = gq, gk, eps
+        self.heads = (n_q_heads, n_kv_heads, gq.shape[0])
+        D, dev = gq.shape[0], Wqkv.device
+        self.cos_t, self.sin_t = torch.empty(S, D // 2, device=dev), torch.empty(S, D // 2, device=dev)
+        coda_rope_table(self.cos_t, self.sin_t, base)
+        self.out = torch.empty_like(self.linear.Y)
+        if backward:
+            self.dqkv = torch.empty_like(self.linear.Y)
+            self.dgq, self.dgk = torch.empty(D, device=dev), torch.empty(D, device=dev)
+            self.ws = torch.empty(coda_qknorm_rope_bwd_workspace_bytes(max(M, 1), D), dtype=torch.uint8, device=dev)
+
+    def forward(self, X, positions=None):
+        """The normalised and rotated qkv [m, ...] of X [m, d]."""
+        qkv, self.positions = self.linear.forward(X), positions
+        out = self.out[:qkv.shape[0]]
+        coda_qknorm_rope(qkv, self.gq, self.gk, self.cos_t, self.sin_t, out, *self.heads, self.eps, positions)
+        return out
+
+    def backward(self, dout):
+        """(dX, dWqkv, dgq, dgk) of the last forward."""
+        m = dout.shape[0]
+        coda_qknorm_rope_bwd(dout, self.linear.Y[:m], self.gq, self.gk, self.cos_t, self.sin_t, self.dqkv[:m],
+                             self.dgq, self.dgk, self.ws, *self.heads, self.eps, self.positions)
+        dX, dW = self.linear.backward(self.dqkv[:m])
+        return dX, dW, self.dgq, self.dgk
+
+
+class PolicyHead:
+    """The LM head of a policy update on up to M tokens: loss statistics,
+    log-probabilities and the gradients of the hidden states and of Wt."""
+
+    def __init__(self, Wt, M: int, clip=(0.2, 0.2), kl_coef: float = 0.0, temperature: float = 1.0,
+                 backward: bool = True):
+        self.Wt, self.clip, self.kl_coef, self.temperature = Wt, clip, kl_coef, temperature
+        V, d = Wt.shape
+        e = dict(device=Wt.device)
+        self.ws = torch.empty(coda_lmhead_policy_workspace_bytes(M, d, V, backward), dtype=torch.uint8, **e)
+        self.stats, self.logp = torch.empty(4, **e), torch.empty(M, **e)
+        self.dH = torch.empty(M, d, dtype=BF, **e) if backward else None
+        self.dWt = torch.empty(V, d, dtype=BF, **e) if backward else None
+
+    def step(self, H, labels, advantage, weight=None, logp_old=None, logp_ref=None):
+        """(stats, logp, dH, dWt); the last two None without backward."""
+        m = H.shape[0]
+        dH = None if self.dH is None else self.dH[:m]
+        coda_lmhead_policy(H, self.Wt, labels, advantage, weight, logp_old, logp_ref, *self.clip, self.kl_coef,
+                           self.temperature, self.stats, self.logp[:m], dH, self.dWt, self.ws)
+        return self.stats, self.logp[:m], dH, self.dWt

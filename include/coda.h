@@ -752,8 +752,8 @@ coda_status_t coda_lmhead_ce_fp8(coda_handle_t h, const void* Hq, const float* s
                                  void* stream);
 
 /* Workspace of coda_lmhead_policy: that of coda_lmhead_ce, 24 bytes per row,
- * and, with gradients of few tokens (M d below some 2.5 million), up to 20 MB
- * of fp32 partial sums of dHs. */
+ * and, with gradients, up to 20 MB of fp32 partial sums of dHs (used for few
+ * tokens).  A workspace for M tokens also serves any smaller number. */
 size_t coda_lmhead_policy_workspace_bytes(int64_t M, int64_t d, int64_t V, int with_grads);
 
 /* Clipped policy loss with a KL term on the LM head, without ever writing an

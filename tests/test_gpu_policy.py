@@ -139,6 +139,21 @@ def test_narrow_chunks_give_the_same_gradients():
     assert torch.equal(dW, pb.dW)
 
 
+def test_a_workspace_serves_smaller_batches():
+    """The bytes grow with the tokens, also where the number of K ranges of
+    the data gradient falls."""
+    for d, V in ((64, 4096), (512, 8000), (4096, 4096), (2048, 128256)):
+        for grads in (False, True):
+            n = [C.coda_lmhead_policy_workspace_bytes(m, d, V, grads) for m in range(1, 12000, 85)]
+            assert n == sorted(n)
+
+
+@pytest.mark.parametrize("M,d,V", [(700, 512, 4096), (300, 264, 2056), (40, 2048, 2048)])
+def test_data_gradient_in_ranges_of_the_vocabulary(M, d, V):
+    pb = Problem(M, d, V)
+    pb.grade(pb.run())
+
+
 def test_captured_graph():
     pb = Problem(48, 64, 520)
     pb.run()
