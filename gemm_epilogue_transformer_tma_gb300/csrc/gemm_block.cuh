@@ -229,6 +229,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockPairSmem::THREA
         }
       }
     }
+    if (lane == 0 && (skipped >= 0 || (ctl.skip_first_stage == 2 && cluster_id == 0 && !leader))) hook_hold_back(ctl);
     // every fill of both CTAs observed landed before shared memory can be
     // released; fill i of the ring is k-block i mod num_kb of its tile
     if (lane == 0) {

@@ -124,6 +124,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SplitKSmem::THREADS,
         phase ^= 1u;
       }
     }
+    if (lane == 0 && (skipped >= 0 || (ctl.skip_first_stage == 2 && unit == 0 && !leader))) hook_hold_back(ctl);
     if (lane == 0 &&
         !pair_fills_landed(leader, issued, skipped, full, STAGES, L::STAGE_BYTES, fill_report, ctl.timeout_ns)) {
       atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);

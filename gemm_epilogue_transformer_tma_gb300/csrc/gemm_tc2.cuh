@@ -155,6 +155,15 @@ __device__ __forceinline__ bool pair_fills_landed(bool leader, int issued, int s
                           [peer_bytes](int, bool) { return peer_bytes; }, timeout_ns);
 }
 
+// Test hook: a producer that left a fill out (or stopped before its first)
+// holds back its hand-off until the waits on the missing fill have expired;
+// with fewer k-blocks than stages it would get there at once, and the
+// hand-off completes the phase.
+__device__ __forceinline__ void hook_hold_back(const KernelCtl& ctl) {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < ctl.timeout_ns + ctl.timeout_ns / 2) __nanosleep(1000);
+}
+
 // Wait (bounded, like the mbarrier waits) for a split partial's flag.
 __device__ __forceinline__ bool split_flag_wait(const int* f, const volatile int* abort_flag, uint64_t timeout_ns) {
   if (ld_acquire_gpu(f) != 0) return true;
