@@ -182,13 +182,16 @@ __global__ void __launch_bounds__(32 * kWarps, 4) qknorm_rope_kernel(const HeadA
   }
 }
 
+// bytes of a stage: U heads per lane of x and of dy, then cos and sin of a row
+constexpr int bwd_stage_bytes(int G, int U) { return 2 * (U * 32 * 16 * 2) + 2 * (G * 8 * 4); }
+
 // The grid's warps stride over the tasks by a multiple of the chunks per row,
 // so a warp sees one chunk of every row it visits, hence one kind of head,
 // and its lanes' sums of dg stay in 16 registers until the end: then over the
 // warp's head groups, the CTA's warps of that kind, and (dg_sums_kernel) the
 // CTAs, in a fixed order.  A chunk of x and of dy is one contiguous piece, so
-// each warp keeps kStages rows of them in flight with bulk copies into its
-// own shared-memory ring.  Two CTAs per SM: the 128 registers a thread needs
+// each warp keeps kStages rows of them, with their rows of the tables, in
+// flight with bulk copies into its own shared-memory ring.  Two CTAs per SM: the 128 registers a thread needs
 // leave no room for a third (84 us with spills against 58, at 8192 rows of 48
 // heads of 128; 302 MB).  Plain loads into registers took 70 us there; the
 // packed fp32 arithmetic (two values per instruction) 58 against 61.
@@ -199,6 +202,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(
   constexpr int P = 8, W = P / 2;  // pairs per lane, in words of two
   constexpr int HW = 32 / G;
   constexpr int CHUNK = U * 32 * 2 * P * 2;  // bytes of U heads per lane, at most
+  constexpr int STAGE = bwd_stage_bytes(G, U);
   extern __shared__ __align__(128) uint8_t ring[];  // [warp][stage][x, dy]
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   __shared__ float red[kWarps][G * 2 * P];
@@ -212,20 +216,37 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(
   const Chunk k = chunk_of(a, m0, static_cast<int>(first - m0 * a.chunks), U * HW);
   const int64_t width = static_cast<int64_t>(a.n_q + 2 * a.n_kv) * a.D;
   const int64_t head0 = static_cast<int64_t>(k.first) * a.D;
-  uint8_t* mine = ring + warp * (kStages * 2 * CHUNK);
-  // lane 0 fetches the chunk of row m into a stage (v heads need dy alone)
+  uint8_t* mine = ring + warp * (kStages * STAGE);
+  // Positions of the rows ahead: the next kStages rows' and one more, so that
+  // a row's position is here when its table row is fetched.
+  auto position = [&](int64_t m) -> int64_t {
+    return k.kind == 2 || m >= a.M ? 0 : a.pos != nullptr ? static_cast<int64_t>(a.pos[m]) : rem(m, a.S);
+  };
+  static_assert(kStages == 2, "positions are held for two rows in flight");
+  int64_t pos0 = position(m0), pos1 = position(m0 + m_step), pos2 = position(m0 + 2 * m_step);
+  const int64_t pos_step = a.pos == nullptr ? rem(m_step, a.S) : 0;
+  // lane 0 fetches the chunk of row m and its row of the tables into a stage
+  // (v heads need dy alone; a position outside the table has no row)
   const uint32_t bytes = static_cast<uint32_t>(k.heads * a.D * 2);
-  auto fetch = [&](int64_t m, int s) {
-    uint8_t* dst = mine + s * (2 * CHUNK);
-    mbar_arrive_expect_tx(&bars[warp][s], k.kind < 2 ? 2 * bytes : bytes);
-    if (k.kind < 2) bulk_load(dst, a.x + m * width + head0, bytes, &bars[warp][s]);
-    bulk_load(dst + CHUNK, a.dy + m * width + head0, bytes, &bars[warp][s]);
+  auto fetch = [&](int64_t m, int64_t pos, int s) {
+    uint8_t* dst = mine + s * STAGE;
+    uint64_t* bar = &bars[warp][s];
+    const uint32_t tab = pos >= 0 && pos < a.S ? static_cast<uint32_t>(a.D * 2) : 0u;  // D / 2 fp32
+    mbar_arrive_expect_tx(bar, k.kind < 2 ? 2 * bytes + 2 * tab : bytes);
+    if (k.kind < 2) {
+      bulk_load(dst, a.x + m * width + head0, bytes, bar);
+      if (tab != 0) {
+        bulk_load(dst + 2 * CHUNK, a.cos_t + pos * half, tab, bar);
+        bulk_load(dst + 2 * CHUNK + tab, a.sin_t + pos * half, tab, bar);
+      }
+    }
+    bulk_load(dst + CHUNK, a.dy + m * width + head0, bytes, bar);
   };
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&bars[warp][s], 1);
     fence_mbar_init();
-    for (int s = 0; s < kStages; ++s)
-      if (m0 + s * m_step < a.M) fetch(m0 + s * m_step, s);
+    if (m0 < a.M) fetch(m0, pos0, 0);
+    if (m0 + m_step < a.M) fetch(m0 + m_step, pos1, 1);
   }
   __syncwarp();
   const f32x2 zero = splat2(0.f);
@@ -242,25 +263,32 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(
   }
   int s = 0;
   uint32_t phase = 0;
-  // the position of row m, read one row ahead: the table load waits for it
-  int64_t pos = a.pos == nullptr ? rem(m0, a.S) : m0 < a.M ? a.pos[m0] : 0;
-  const int64_t pos_step = a.pos == nullptr ? rem(m_step, a.S) : 0;
   for (int64_t m = m0; m < a.M; m += m_step) {
-    f32x2 cs[W], sn[W];
-    if (k.kind < 2) load_angles(a, pos, l, active, cs, sn);
-    if (a.pos == nullptr) {
-      pos += pos_step;
-      if (pos >= a.S) pos -= a.S;
-    } else if (m + m_step < a.M) {
-      pos = a.pos[m + m_step];
-    }
+    int64_t pos3 = pos2 + pos_step;
+    if (a.pos != nullptr)
+      pos3 = position(m + 3 * m_step);
+    else if (pos3 >= a.S)
+      pos3 -= a.S;
     // the copies are this warp's own: they land, or the device has failed
     const bool landed = mbar_wait_timeout(&bars[warp][s], phase, a.timeout_ns);
     if (!__all_sync(0xffffffffu, landed)) {
       if (lane == 0) atomicOr(a.status, DEV_ERR_TIMEOUT_PRODUCER);
       break;
     }
-    const uint8_t* px = mine + s * (2 * CHUNK) + 2 * P * l;
+    const uint8_t* px = mine + s * STAGE + 2 * P * l;
+    f32x2 cs[W], sn[W];
+    if (k.kind < 2) {
+      const bool known = pos0 >= 0 && pos0 < a.S;
+      if (!known && l == 0) atomicOr(a.status, DEV_ERR_POSITION_RANGE);
+      const float* tab = reinterpret_cast<const float*>(mine + s * STAGE + 2 * CHUNK) + P * l;
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const float2 c2 = known && active ? *reinterpret_cast<const float2*>(tab + 2 * j) : make_float2(1.f, 1.f);
+        const float2 s2 = known && active ? *reinterpret_cast<const float2*>(tab + half + 2 * j) : make_float2(0.f, 0.f);
+        cs[j] = make_f32x2(c2.x, c2.y);
+        sn[j] = make_f32x2(s2.x, s2.y);
+      }
+    }
 #pragma unroll 1
     for (int u = 0; u < U; ++u) {
       const int h = u * HW + hg;
@@ -317,7 +345,10 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(
       }
     }
     __syncwarp();  // every lane has read the stage
-    if (lane == 0 && m + kStages * m_step < a.M) fetch(m + kStages * m_step, s);
+    if (lane == 0 && m + 2 * m_step < a.M) fetch(m + 2 * m_step, pos2, s);
+    pos0 = pos1;
+    pos1 = pos2;
+    pos2 = pos3;
     if (++s == kStages) {
       s = 0;
       phase ^= 1u;
@@ -354,21 +385,28 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(
 }
 
 // out[i] = sum over parts of part[p][i], i < 2 D: dgq then dgk.  A CTA sums 8
-// columns with 32 row lanes (1024 parts: 32 loads per thread, all
-// independent), then across the lanes in a fixed order.
-__global__ void __launch_bounds__(256) dg_sums_kernel(const float* __restrict__ part, int parts, int D,
-                                                      float* __restrict__ dgq, float* __restrict__ dgk) {
+// columns with 128 row lanes (at most 8 loads per thread, all in flight at
+// once), then across the lanes in a fixed order.
+__global__ void __launch_bounds__(1024) dg_sums_kernel(const float* __restrict__ part, int parts, int D,
+                                                       float* __restrict__ dgq, float* __restrict__ dgk) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ float red[32][9];
+  __shared__ float red[32][8];
   const int col = threadIdx.x & 7, rl = threadIdx.x >> 3;
   const int i = blockIdx.x * 8 + col;
-  float s = 0.f;
-#pragma unroll 4
-  for (int p = rl; p < parts; p += 32) s += part[static_cast<int64_t>(p) * 2 * D + i];
-  red[rl][col] = s;
+  float v[kMaxParts / 128], s = 0.f;
+#pragma unroll
+  for (int j = 0; j < kMaxParts / 128; ++j) {
+    const int p = rl + 128 * j;
+    v[j] = p < parts ? part[static_cast<int64_t>(p) * 2 * D + i] : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < kMaxParts / 128; ++j) s += v[j];
+  s += __shfl_xor_sync(0xffffffffu, s, 8);
+  s += __shfl_xor_sync(0xffffffffu, s, 16);
+  if ((threadIdx.x & 31) < 8) red[threadIdx.x >> 5][col] = s;
   __syncthreads();
-  if (rl == 0) {
+  if (threadIdx.x < 8) {
     float t = 0.f;
 #pragma unroll
     for (int r = 0; r < 32; ++r) t += red[r][col];
@@ -468,13 +506,13 @@ cudaError_t launch_qknorm_rope_bwd(const LaunchCtx& c, const __nv_bfloat16* dy, 
         std::min<int64_t>({(M * a.chunks + kWarps - 1) / kWarps, int64_t(c.num_sms) * kBwdCtas, kMaxParts});
     int64_t blocks = std::max<int64_t>(1, want / a.chunks) * a.chunks;
     auto kern = qknorm_rope_bwd_kernel<GC, kBwdHeads>;
-    constexpr int smem = kWarps * kStages * 2 * (kBwdHeads * 32 * 16 * 2);  // a lane holds 16 values of a head
+    constexpr int smem = kWarps * kStages * bwd_stage_bytes(GC, kBwdHeads);
     static bool smem_ok[64] = {};
     cudaError_t e = allow_smem(kern, smem, smem_ok);
     if (e != cudaSuccess) return e;
     e = launch_chained(c, kern, dim3(static_cast<unsigned>(blocks)), dim3(32 * kWarps), smem, a);
     if (e != cudaSuccess) return e;
-    return launch_chained(c, dg_sums_kernel, dim3(static_cast<unsigned>((n_kv > 0 ? 2 : 1) * D / 8)), dim3(256), 0,
+    return launch_chained(c, dg_sums_kernel, dim3(static_cast<unsigned>((n_kv > 0 ? 2 : 1) * D / 8)), dim3(1024), 0,
                           static_cast<const float*>(part), static_cast<int>(blocks), D, dgq, dgk);
   });
 }
