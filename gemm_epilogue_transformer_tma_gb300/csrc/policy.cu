@@ -19,15 +19,21 @@ namespace coda {
 
 namespace {
 
-// One warp per row: the log-sum-exp of the row's block statistics, then lane
-// 0's token terms.  terms [M][4]: the row's shares of the four statistics.
-__global__ void policy_rows_kernel(const float* __restrict__ pmax, const float* __restrict__ psum,
-                                   const float* __restrict__ zy, const PolicyRows p, int64_t M, int64_t T, int64_t V) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t m = blockIdx.x * static_cast<int64_t>(blockDim.x / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (m >= M) return;
+// a + b and its rounding error, added to lo: sums that nearly cancel keep the
+// digits fp32 drops (fp64 units are scarce on this GPU: the same kernel in
+// fp64 took 10 us for 136 rows)
+__device__ __forceinline__ void add_exact(float& hi, float& lo, float b, float b_lo) {
+  const float s = hi + b;
+  const float t = s - hi;
+  lo += ((hi - (s - t)) + (b - t)) + b_lo;
+  hi = s;
+}
+
+// A warp's row: the log-sum-exp of its block statistics, then the token terms
+// (in every lane): the row's shares of the four statistics.
+__device__ __forceinline__ float4 policy_row(const float* __restrict__ pmax, const float* __restrict__ psum,
+                                             const float* __restrict__ zy, const PolicyRows& p, int64_t m, int64_t T,
+                                             int64_t V, int lane) {
   const float* mx = pmax + m * T;
   const float* se = psum + m * T;
   // one pass: the running maximum and the sum relative to it
@@ -46,16 +52,11 @@ __global__ void policy_rows_kernel(const float* __restrict__ pmax, const float* 
     s = (s == 0.f ? 0.f : s * __expf(best - top)) + (os == 0.f ? 0.f : os * __expf(ob - top));
     best = top;
   }
-  if (lane != 0) return;
   const float lse = best + logf(s);
-  p.lse[m] = lse;
   const float w = p.weight != nullptr ? p.weight[m] : p.uniform;
   const int32_t y = p.labels[m];
   const bool in_range = y >= 0 && y < V;
-  // padding, a row without weight, may carry any label
-  if (!in_range && w != 0.f) atomicOr(p.status, DEV_ERR_LABEL_RANGE);
   const float lp = in_range ? zy[m] - lse : 0.f;
-  p.logp[m] = lp;
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
   float g = 0.f;  // d loss / d lp
   if (in_range && w != 0.f) {
@@ -74,18 +75,70 @@ __global__ void policy_rows_kernel(const float* __restrict__ pmax, const float* 
     t = make_float4(w * (p.beta * kl + pg), w * pg, w * kl, free ? 0.f : w);
     g = w * (p.beta * dkl - (free ? ra : 0.f));
   }
-  p.terms[m] = t;
-  if (p.row_scale != nullptr) p.row_scale[m] = -g * p.inv_temp;
+  if (lane == 0) {
+    // padding, a row without weight, may carry any label
+    if (!in_range && w != 0.f) atomicOr(p.status, DEV_ERR_LABEL_RANGE);
+    p.lse[m] = lse;
+    p.logp[m] = lp;
+    if (p.row_scale != nullptr) p.row_scale[m] = -g * p.inv_temp;
+  }
+  return t;
 }
 
-// a + b and its rounding error, added to lo: sums that nearly cancel keep the
-// digits fp32 drops (fp64 units are scarce on this GPU: the same kernel in
-// fp64 took 10 us for 136 rows)
-__device__ __forceinline__ void add_exact(float& hi, float& lo, float b, float b_lo) {
-  const float s = hi + b;
-  const float t = s - hi;
-  lo += ((hi - (s - t)) + (b - t)) + b_lo;
-  hi = s;
+// Many rows: one warp per row, terms [M][4] to memory.
+__global__ void policy_rows_kernel(const float* __restrict__ pmax, const float* __restrict__ psum,
+                                   const float* __restrict__ zy, const PolicyRows p, int64_t M, int64_t T, int64_t V) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t m = blockIdx.x * static_cast<int64_t>(blockDim.x / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (m >= M) return;
+  const float4 t = policy_row(pmax, psum, zy, p, m, T, V, lane);
+  if (lane == 0) p.terms[m] = t;
+}
+
+// Few rows: a cluster of 8 CTAs takes them all, a warp every 256th, and sums
+// the statistics through shared memory: one launch instead of two.
+constexpr int kRowCtas = 8;
+constexpr int kFewRows = 512;  // two rows to a warp
+__global__ void __cluster_dims__(kRowCtas, 1, 1) __launch_bounds__(1024)
+    policy_rows_stats_kernel(const float* __restrict__ pmax, const float* __restrict__ psum,
+                             const float* __restrict__ zy, const PolicyRows p, int64_t M, int64_t T, int64_t V,
+                             float* __restrict__ stats) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ float2 red[32][4];   // per warp: sum and its low part
+  __shared__ float2 total[kRowCtas][4];  // CTA 0: per CTA
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t rank = cluster_ctarank();
+  float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int64_t m = rank * 32 + warp; m < M; m += kRowCtas * 32) {
+    const float4 t = policy_row(pmax, psum, zy, p, m, T, V, lane);
+    add_exact(hi[0], lo[0], t.x, 0.f);
+    add_exact(hi[1], lo[1], t.y, 0.f);
+    add_exact(hi[2], lo[2], t.z, 0.f);
+    add_exact(hi[3], lo[3], t.w, 0.f);
+  }
+  if (lane == 0)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) red[warp][j] = make_float2(hi[j], lo[j]);
+  __syncthreads();
+  if (warp < 4) {  // warp j: statistic j over the CTA's warps
+    float h = red[lane][warp].x, l = red[lane][warp].y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float h2 = __shfl_xor_sync(0xffffffffu, h, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+      add_exact(h, l, h2, l2);
+    }
+    if (lane == 0) st_cluster_f2(mapa_shared(smem_u32(&total[rank][warp]), 0), make_float2(h, l));
+  }
+  cluster_sync_all();
+  if (rank == 0 && threadIdx.x < 4) {
+    float h = 0.f, l = 0.f;
+#pragma unroll
+    for (int c = 0; c < kRowCtas; ++c) add_exact(h, l, total[c][threadIdx.x].x, total[c][threadIdx.x].y);
+    stats[threadIdx.x] = h + l;
+  }
 }
 
 // stats[i] = sum_m terms[m][i], i < 4, in a fixed order (one CTA)
@@ -158,6 +211,9 @@ cudaError_t launch_sum_parts(const LaunchCtx& c, const float* parts, int num, in
 
 cudaError_t launch_policy_rows(const LaunchCtx& c, const float* pmax, const float* psum, const float* zy,
                                const PolicyRows& p, int64_t M, int64_t T, int64_t V, float* stats) {
+  if (M <= kFewRows)
+    return launch_chained(c, policy_rows_stats_kernel, dim3(kRowCtas), dim3(1024), 0, pmax, psum, zy, p, M, T, V,
+                          stats);
   const cudaError_t e = launch_chained(c, policy_rows_kernel, dim3(static_cast<unsigned>((M + 7) / 8)), dim3(256), 0,
                                        pmax, psum, zy, p, M, T, V);
   if (e != cudaSuccess) return e;

@@ -394,6 +394,12 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t cluster_addr) {
   return v;
 }
 
+// A store to shared memory of any CTA of the cluster, ordered by the next
+// cluster barrier.
+__device__ __forceinline__ void st_cluster_f2(uint32_t cluster_addr, float2 v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_addr), "f"(v.x), "f"(v.y) : "memory");
+}
+
 // Shared::cluster address of the variable at local address `addr` in CTA `rank`.
 // A 32-bit store to shared memory of another CTA of the cluster (address
 // from mapa_shared), ordered after this thread's earlier memory operations.
