@@ -97,9 +97,9 @@ __device__ __forceinline__ void store_scale(uint8_t* s, int64_t r, int64_t b, in
 // issue rate at once (a first form ran at 50 % and 61 % of them), so what
 // counts is warps in flight, hence the register limit that lets 3 CTAs (both
 // directions) or 4 share an SM, and few instructions: packed fp32 products,
-// one redux per row maximum, column scales computed once per column.  8192 x
-// 8192, both directions: 49 us, 5.5 TB/s (first form 56 us under the profiler, 49
-// with 2 CTAs 59); one direction or tiles 29 to 31 us.
+// two rows' maxima per shuffle, column scales computed once per column.
+// 8192 x 28672, both directions: 150 us, 6.3 TB/s (168 with a redux per row,
+// 184 with scalar products); one direction or tiles 97 to 98 us, 7.2 TB/s.
 template <bool E5M2, bool ROW, bool COL, bool TILE>
 __global__ void __launch_bounds__(kThreads, ROW && COL ? 3 : 4)
     block_quantize_kernel(const __nv_bfloat16* __restrict__ src, uint8_t* __restrict__ q_row,
@@ -175,14 +175,21 @@ __global__ void __launch_bounds__(kThreads, ROW && COL ? 3 : 4)
     for (int o = 16; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
     tile_byte = scale_byte<E5M2>(hi_lo_max(m));
   }
+  uint32_t pair_max = 0;  // ROW: the maxima of rows i and i + 1 of an even i
 #pragma unroll
   for (int i = 0; i < 8; ++i, o += step) {
     const bool ok = col_ok && rr + 16 * i < nr;
     const f32x2 f[4] = {unpack_bf16x2(v[i].x), unpack_bf16x2(v[i].y), unpack_bf16x2(v[i].z), unpack_bf16x2(v[i].w)};
     if (ROW) {
-      uint32_t m = hi_lo_max(__vmaxu2(__vmaxu2(abs2(v[i].x), abs2(v[i].y)), __vmaxu2(abs2(v[i].z), abs2(v[i].w))));
-      m = __reduce_max_sync(lane < 16 ? 0x0000FFFFu : 0xFFFF0000u, m);
-      const uint32_t byte = scale_byte<E5M2>(m);
+      if (i % 2 == 0) {
+        auto eight = [](const uint4& w) {
+          return hi_lo_max(__vmaxu2(__vmaxu2(abs2(w.x), abs2(w.y)), __vmaxu2(abs2(w.z), abs2(w.w))));
+        };
+        pair_max = eight(v[i]) | (eight(v[i + 1]) << 16);
+#pragma unroll
+        for (int s = 8; s > 0; s >>= 1) pair_max = __vmaxu2(pair_max, __shfl_xor_sync(0xffffffffu, pair_max, s));
+      }
+      const uint32_t byte = scale_byte<E5M2>(i % 2 == 0 ? pair_max & 0xFFFFu : pair_max >> 16);
       if ((t & 15) == 0) row_scale[rr + 16 * i] = static_cast<uint8_t>(byte);
       if (ok) *reinterpret_cast<uint2*>(q_row + o) = codes8<E5M2>(f, byte);
     }

@@ -379,6 +379,279 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockPairSmem::THREA
 }
 
 // ---------------------------------------------------------------------------
+// Few tiles, long K: a cluster of `parts` SM pairs shares a 256 x 256 tile,
+// each pair taking a range of K (whole scale chunks of 512).  Every CTA then
+// puts its 128 x 256 fp32 accumulator into the ring's shared memory, and each
+// pair sums 256 / parts of the tile's columns over all of them through
+// distributed shared memory, in the order of the ranges.  One tile per
+// cluster; roles as in the pair kernel.
+// ---------------------------------------------------------------------------
+template <int PARTS>
+__device__ __forceinline__ float4 sum_parts(const float4 (&x)[PARTS]) {
+  float4 s = x[0];
+#pragma unroll
+  for (int p = 1; p < PARTS; ++p) {
+    s.x += x[p].x;
+    s.y += x[p].y;
+    s.z += x[p].z;
+    s.w += x[p].w;
+  }
+  return s;
+}
+
+constexpr int kSplitPitch = 260;  // floats per row of a partial tile: 16-byte rows, no bank conflicts
+static_assert(128 * kSplitPitch * 4 <= BlockPairSmem::RING_BYTES, "the partial tile takes the ring's place");
+
+struct BlockSplitArgs {
+  CUtensorMap A, B;    // codes
+  CUtensorMap sA, sB;  // packed scales as rows of 512 bytes, one per chunk
+  __nv_bfloat16* C;    // [M][N]
+  int M, N;
+  int tiles_m, num_kb;
+  uint32_t f8_fmt;
+};
+
+template <bool A_MN, bool B_MN, int PARTS>
+__global__ void __launch_bounds__(BlockPairSmem::THREADS, 1)
+    gemm_block_split_kernel(const __grid_constant__ BlockSplitArgs g, const KernelCtl ctl) {
+  using L = BlockPairSmem;
+  constexpr int STAGES = L::STAGES;
+  constexpr int BN = 256;
+  constexpr uint32_t IDESC0 = idesc_mxf8(BM2, BN, A_MN, B_MN);
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sf_ring = smem + L::RING_BYTES + L::STORE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sf_ring + L::SF_RING_BYTES);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* drain = tfull + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* fill_report = reinterpret_cast<uint32_t*>(tmem_slot + 2);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_ctarank();
+  const uint32_t rank = crank & 1u;         // in its pair
+  const uint32_t lead_rank = crank & ~1u;   // the pair's leader
+  const bool leader = rank == 0;
+  const int part = static_cast<int>(crank >> 1);
+  const int tile = static_cast<int>(blockIdx.x) / (2 * PARTS);
+  const int tm = tile % g.tiles_m, tn = tile / g.tiles_m;
+  const int groups = (g.num_kb + 3) >> 2;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(groups) * part / PARTS) * 4;
+  const int kb1 = min(static_cast<int>(static_cast<int64_t>(groups) * (part + 1) / PARTS) * 4, g.num_kb);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *fill_report = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&g.A);
+    tma_prefetch_desc(&g.B);
+    tma_prefetch_desc(&g.sA);
+    tma_prefetch_desc(&g.sB);
+  }
+  cluster_sync_all();
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  if (warp == 0) {
+    const uint32_t leader_full = mapa_shared(smem_u32(full), lead_rank);
+    const int m0 = tm * BM2 + static_cast<int>(rank) * 128;
+    const int n0 = tn * BN + static_cast<int>(rank) * 128;
+    int stage = 0;
+    uint32_t phase = 0;
+    int issued = 0, skipped = -1;
+    bool ok = !(ctl.skip_first_stage == 2 && tile == 0 && part == 0 && !leader);
+    bool skip = ctl.skip_first_stage == 1 && tile == 0 && part == 0 && leader;
+    for (int kb = kb0; kb < kb1 && ok; ++kb) {
+      ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, ctl.timeout_ns);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        if (lane == 0 && !*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_PRODUCER);
+        break;
+      }
+      if (skip) {
+        skip = false;  // test hook: the leader never arms this stage
+        skipped = issued;
+      } else if (elect_one()) {
+        uint8_t* sa = smem + stage * L::STAGE_BYTES;
+        uint8_t* sb = sa + L::A_BYTES;
+        uint8_t* sf = sf_ring + stage * L::SF_BYTES;
+        const uint32_t bar = leader_full + static_cast<uint32_t>(stage * 8);
+        if (leader) mbar_arrive_expect_tx(&full[stage], 2 * L::fill_bytes(kb));
+        if (!A_MN)
+          tma_load_2d_pair(sa, &g.A, bar, kb * 128, m0);
+        else
+          tma_load_2d_pair(sa, &g.A, bar, m0, kb * 128);
+        if (!B_MN)
+          tma_load_2d_pair(sb, &g.B, bar, kb * 128, n0);
+        else
+          tma_load_2d_pair(sb, &g.B, bar, n0, kb * 128);
+        if ((kb & 3) == 0) {
+          const int q = kb >> 2;
+          tma_load_2d_pair(sf, &g.sA, bar, 0, (m0 >> 7) * groups + q);
+          tma_load_2d_pair(sf + kScaleChunk, &g.sB, bar, 0, (2 * tn) * groups + q);
+          tma_load_2d_pair(sf + 2 * kScaleChunk, &g.sB, bar, 0, (2 * tn + 1) * groups + q);
+        }
+      }
+      __syncwarp();
+      ++issued;
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (lane == 0) {
+      if (skipped >= 0 || (ctl.skip_first_stage == 2 && tile == 0 && part == 0 && !leader)) hook_hold_back(ctl);
+      // fill i of the ring is k-block kb0 + i, and kb0 a multiple of 4
+      bool landed = true;
+      if (!leader) {
+        st_release_cluster_u32(mapa_shared(smem_u32(fill_report), lead_rank), static_cast<uint32_t>(issued) + 1u);
+      } else {
+        uint32_t r;
+        landed = pair_report_wait(fill_report, ctl.timeout_ns, r) &&
+                 pair_ring_landed(issued, skipped, static_cast<int>(r) - 1, full, STAGES,
+                                  [](int i, bool) { return L::fill_bytes(i); }, ctl.timeout_ns);
+      }
+      if (!landed) {
+        atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
+        // far longer than any copy's latency, as in gemm_tc2_kernel
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (leader) {
+      const uint32_t idesc = IDESC0 | g.f8_fmt;
+      const uint16_t pair_mask = static_cast<uint16_t>(0x3u << lead_rank);
+      const uint64_t adesc0 = sdesc_sw128(smem_u32(smem), A_MN ? 128 * 128 : 16, 1024);
+      const uint64_t bdesc0 = sdesc_sw128(smem_u32(smem) + L::A_BYTES, B_MN ? 128 * 128 : 16, 1024);
+      const uint64_t sfdesc0 = sdesc_scales(smem_u32(sf_ring));
+      int stage = 0;
+      uint32_t phase = 0;
+      bool issued_any = false;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const bool ok = mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, ctl.timeout_ns);
+        if (!__all_sync(0xffffffffu, ok)) {
+          if (lane == 0 && !*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_MMA);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sfa =
+            tmem_base + static_cast<uint32_t>(L::SF_COL) + (static_cast<uint32_t>(kb >> 2) & 1u) * 12u;
+        if (elect_one()) {
+          if ((kb & 3) == 0) {
+            const uint64_t sf = sfdesc0 + static_cast<uint32_t>(stage * (L::SF_BYTES >> 4));
+            tmem_cp_scales_pair(sfa, sf);
+            tmem_cp_scales_pair(sfa + 4, sf + (kScaleChunk >> 4));
+            tmem_cp_scales_pair(sfa + 8, sf + 2 * (kScaleChunk >> 4));
+          }
+          const uint32_t id = idesc | idesc_scale_id(static_cast<uint32_t>(kb) & 3u);
+          const uint64_t ad = adesc0 + static_cast<uint32_t>(stage * (L::STAGE_BYTES >> 4));
+          const uint64_t bd = bdesc0 + static_cast<uint32_t>(stage * (L::STAGE_BYTES >> 4));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_mxf8_pair(tmem_base, ad + k * ((A_MN ? 4096 : 32) >> 4), bd + k * ((B_MN ? 4096 : 32) >> 4), id, sfa,
+                           sfa + 4, (kb != kb0 || k != 0) ? 1u : 0u);
+          umma_commit_pair_multicast(&empty[stage], pair_mask);
+          if (kb == kb1 - 1) umma_commit_pair_multicast(tfull, pair_mask);
+        }
+        __syncwarp();
+        issued_any = true;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (issued_any) {
+        if (elect_one()) umma_commit_pair_local(drain);
+        __syncwarp();
+        if (!mbar_wait_timeout(drain, 0, ctl.timeout_ns) && lane == 0) atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
+      }
+    }
+  } else {
+    // the accumulator to shared memory: every load of the ring was consumed
+    // by an MMA that tfull says is complete (on a failure nothing is written)
+    const int row = (warp & 3) * 32 + lane;
+    bool ok = mbar_wait_bounded(tfull, 0, abort_flag, ctl.timeout_ns);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) {
+      if (lane == 0 && !*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_EPILOGUE);
+    } else {
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      float* mine = reinterpret_cast<float*>(smem) + row * kSplitPitch;
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 32) {
+        float v[32];
+        tmem_ld32(taddr + static_cast<uint32_t>(c), v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<float4*>(mine + c + 4 * j) =
+              make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      }
+      tc_fence_before();
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();  // every CTA's partial tile is in its shared memory
+  {
+    // this pair's columns [part * share, + share) of its rank's 128 rows: a
+    // lane takes four columns, a warp 128 / share rows at a time
+    constexpr int share = BN / PARTS, lanes = share / 4, rows_at_once = 32 / lanes;
+    constexpr int step = L::THREADS / 32 * rows_at_once;
+    const int c4 = (lane % lanes) * 4, n = tn * BN + part * share + c4;
+    const int m0 = tm * BM2 + static_cast<int>(rank) * 128;
+    const uint32_t base = smem_u32(smem) + static_cast<uint32_t>(part * share + c4) * 4u;
+    uint32_t from[PARTS];
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) from[p] = mapa_shared(base, static_cast<uint32_t>(2 * p) + rank);
+    // two rows at a time, every part's load issued before the first sum: a
+    // load from another SM takes some 250 ns
+    for (int r = warp * rows_at_once + lane / lanes; r < 128; r += 2 * step) {
+      float4 x[2][PARTS];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p)
+          x[h][p] = ld_cluster_f4(from[p] + static_cast<uint32_t>(min(r + h * step, 127) * kSplitPitch) * 4u);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 s = sum_parts<PARTS>(x[h]);
+        const int m = m0 + r + h * step;
+        if (r + h * step < 128 && m < g.M && n < g.N)  // N is a multiple of 8: four columns or none
+          *reinterpret_cast<uint2*>(g.C + static_cast<int64_t>(m) * g.N + n) =
+              make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();  // nobody leaves while its partial tile is being read
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Few tokens: C^T = W X^T, the weight rows as the MMA's M = 128 and the tokens
 // as its N (BN = 16 to 128), one SM per tile.  The product is bound by reading
 // the weight once, so what counts is bytes in flight on every SM: a cluster of
@@ -407,8 +680,6 @@ struct BlockFewSmem {
   static constexpr int TMEM_COLS = BN <= 32 ? 64 : BN == 64 ? 128 : 256;
 };
 
-constexpr int kFewMaxParts = 8;  // CTAs per cluster (K ranges)
-
 struct BlockFewArgs {
   CUtensorMap W, X;    // codes: the weight's rows, the tokens
   CUtensorMap sW, sX;  // packed scales, rows of 512 bytes
@@ -418,7 +689,7 @@ struct BlockFewArgs {
   uint32_t f8_fmt;     // format bits with the weight as A
 };
 
-template <int BN, bool W_MN>
+template <int BN, bool W_MN, int PARTS>
 __global__ void __launch_bounds__(BlockFewSmem<BN>::THREADS, BlockFewSmem<BN>::CTAS)
     gemm_block_few_kernel(const __grid_constant__ BlockFewArgs g, const KernelCtl ctl) {
   using L = BlockFewSmem<BN>;
@@ -436,12 +707,11 @@ __global__ void __launch_bounds__(BlockFewSmem<BN>::THREADS, BlockFewSmem<BN>::C
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
-  const int parts = static_cast<int>(cluster_nctarank());
-  const int n0 = static_cast<int>(blockIdx.x / parts) * 128;  // weight rows
+  const int n0 = static_cast<int>(blockIdx.x) / PARTS * 128;  // weight rows
   const int m0 = static_cast<int>(blockIdx.y) * BN;           // tokens
   const int groups = (g.num_kb + 3) >> 2;                     // scale chunks along K
-  const int kb0 = static_cast<int>(static_cast<int64_t>(groups) * rank / parts) * 4;
-  const int kb1 = min(static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / parts) * 4, g.num_kb);
+  const int kb0 = static_cast<int>(static_cast<int64_t>(groups) * rank / PARTS) * 4;
+  const int kb1 = min(static_cast<int>(static_cast<int64_t>(groups) * (rank + 1) / PARTS) * 4, g.num_kb);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -569,7 +839,7 @@ __global__ void __launch_bounds__(BlockFewSmem<BN>::THREADS, BlockFewSmem<BN>::C
     for (int c = 0; c < tokens; c += 16) {
       float v[16];
       tmem_ld16(taddr + static_cast<uint32_t>(c), v);
-      if (parts == 1) {
+      if (PARTS == 1) {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           if (row_ok && c + j < tokens) out[static_cast<int64_t>(c + j) * g.N] = __float2bfloat16_rn(v[j]);
@@ -580,7 +850,7 @@ __global__ void __launch_bounds__(BlockFewSmem<BN>::THREADS, BlockFewSmem<BN>::C
     }
     tc_fence_before();
   }
-  if (parts > 1) {
+  if constexpr (PARTS > 1) {
     __syncwarp();
     cluster_sync_all();  // every CTA's partial tile is in its shared memory
     if (warp >= 2) {
@@ -590,20 +860,14 @@ __global__ void __launch_bounds__(BlockFewSmem<BN>::THREADS, BlockFewSmem<BN>::C
       const uint32_t mine = smem_u32(smem) + static_cast<uint32_t>(lane) * 16u;
       const bool ok = n0 + 4 * lane < g.N;  // N is a multiple of 8: four rows or none
       __nv_bfloat16* out = g.C + static_cast<int64_t>(m0) * g.N + n0 + 4 * lane;
-#pragma unroll 2
-      for (int j = rank + (warp - 2) * parts; j < tokens; j += 4 * parts) {
-        const uint32_t at = mine + static_cast<uint32_t>(j) * 512u;
-        float4 s = ld_cluster_f4(mapa_shared(at, 0));
+      uint32_t from[PARTS];
 #pragma unroll
-        for (int p = 1; p < kFewMaxParts; ++p) {
-          if (p < parts) {
-            const float4 x = ld_cluster_f4(mapa_shared(at, static_cast<uint32_t>(p)));
-            s.x += x.x;
-            s.y += x.y;
-            s.z += x.z;
-            s.w += x.w;
-          }
-        }
+      for (int p = 0; p < PARTS; ++p) from[p] = mapa_shared(mine, static_cast<uint32_t>(p));
+      for (int j = rank + (warp - 2) * PARTS; j < tokens; j += 4 * PARTS) {
+        float4 x[PARTS];
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) x[p] = ld_cluster_f4(from[p] + static_cast<uint32_t>(j) * 512u);
+        const float4 s = sum_parts<PARTS>(x);
         if (ok)
           *reinterpret_cast<uint2*>(out + static_cast<int64_t>(j) * g.N) =
               make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));

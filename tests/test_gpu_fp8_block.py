@@ -170,6 +170,18 @@ def test_gemm_known_answer(M, N, K, layout):
 
 
 @pytest.mark.parametrize("layout", LAYOUTS, ids=["kk", "km", "mm"])
+@pytest.mark.parametrize("M,N,K", [(5008, 272, 2080), (272, 528, 9008), (3008, 2064, 2576), (272, 5200, 4112),
+                                   (1040, 1296, 4112), (2000, 1040, 8704)])
+def test_gemm_long_contractions(M, N, K, layout):
+    """Few output tiles and a long K: ranges of K on their own SMs."""
+    a_mn, b_mn = layout
+    if a_mn:
+        K -= 5
+    out, a, b = _int_gemm(np.random.default_rng(K), M, N, K, a_mn, b_mn, "e4m3", "e4m3")
+    assert torch.equal(out, _bf((torch.from_numpy(a).cuda() @ torch.from_numpy(b).cuda().t()).cpu().numpy()))
+
+
+@pytest.mark.parametrize("layout", LAYOUTS, ids=["kk", "km", "mm"])
 def test_gemm_many_tiles_per_pair(layout):
     """Several tiles per SM pair: the accumulators that share columns, ragged
     edges in both extents, a K of several scale chunks and a tail."""

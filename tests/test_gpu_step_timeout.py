@@ -31,8 +31,8 @@ def _expire(call, mode):
 
 
 @pytest.mark.parametrize("mode", [1, 2])
-@pytest.mark.parametrize("M,N,K", [(8, 512, 4096), (64, 256, 1024), (3000, 4608, 1664)],
-                         ids=["few_split", "few", "pairs"])
+@pytest.mark.parametrize("M,N,K", [(8, 512, 4096), (64, 256, 1024), (3000, 4608, 1664), (1536, 2816, 4608)],
+                         ids=["few_split", "few", "pairs", "pairs_split"])
 def test_block_scaled_gemm(M, N, K, mode):
     g = torch.Generator(device="cuda").manual_seed(M)
     lin = BlockScaledLinear(torch.randn(N, K, device="cuda", generator=g).to(BF), M, backward=False)
