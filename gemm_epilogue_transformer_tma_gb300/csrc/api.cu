@@ -1215,6 +1215,9 @@ struct PolicyWs {
   float* lse;
   float* row_scale;
   float4* terms;
+  float* lost;        // [M]: what bf16 takes from dL's label entries
+  float* label_rows;  // [M][d]: lost H summed per label, at the label's first token
+  uint32_t* slot;     // [V]: that token
   float* dH_parts;  // the data gradient's K ranges: fp32 [dh_parts()][M rounded up to 256][d]
   size_t bytes;
 };
@@ -1253,6 +1256,9 @@ PolicyWs policy_layout(uint8_t* base, int64_t M, int64_t d, int64_t V, bool grad
   w.terms = reinterpret_cast<float4*>(take(size_t(M) * 16));
   if (grads) {
     w.row_scale = reinterpret_cast<float*>(take(size_t(M) * 4));
+    w.lost = reinterpret_cast<float*>(take(size_t(M) * 4));
+    w.label_rows = reinterpret_cast<float*>(take(size_t(M) * d * 4));
+    w.slot = reinterpret_cast<uint32_t*>(take(size_t(V) * 4));
     w.dH_parts = reinterpret_cast<float*>(take(dh_parts_bytes(M, d, std::min<int64_t>(V, kCeChunk))));
   }
   w.bytes = off;
@@ -1318,8 +1324,11 @@ coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt
   r.lse = w.lse;
   r.logp = logp;
   r.row_scale = w.row_scale;
+  r.lost = w.lost;
+  r.slot = w.slot;
   r.terms = w.terms;
   r.status = cx.status;
+  if (grads) CODA_CUDA(cudaMemsetAsync(w.slot, 0xFF, size_t(V) * 4, cx.stream));  // kNoSlot
   CODA_CUDA(launch_policy_rows(cx, w.ce.pmax, w.ce.psum, w.ce.zy, r, M, T, V, stats));
   if (!grads) return CODA_OK;
   // the first chunk sets the number of ranges (never more than the workspace
@@ -1330,19 +1339,20 @@ coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt
     const int64_t Vc = std::min<int64_t>(chunk, V - v0);
     const bf16* Wc = Wb + v0 * d;
     bf16* dWc = static_cast<bf16*>(dWt) + v0 * d;
-    CODA_CUDA(gemm_ce_grad(cl, Hb, Wc, labels, w.lse, w.ce.dL, int(M), int(d), int(Vc), int(v0), 0.f, w.row_scale));
+    CODA_CUDA(gemm_ce_grad(cl, Hb, Wc, labels, w.lse, w.ce.dL, int(M), int(d), int(Vc), int(v0), 0.f, w.row_scale,
+                           w.lost));
+    CODA_CUDA(launch_label_rows(cx, labels, w.slot, w.lost, Hb, w.label_rows, M, d, v0, Vc));
     if (parts == 1) {
-      CODA_CUDA(gemm_group_ce_bwd(cx, w.ce.dL, Wc, Hb, w.ce.dH32, v0 > 0, dWc, int(M), int(d), int(Vc)));
+      CODA_CUDA(gemm_group_policy_bwd(cx, w.ce.dL, Wc, Hb, w.ce.dH32, v0 > 0, dWc, w.slot + v0, w.label_rows, int(M),
+                                      int(d), int(Vc)));
     } else {
-      CODA_CUDA(gemm_splitk(cx, w.ce.dL, Wc, w.dH_parts, int(std::min(parts, cdiv(Vc, 64))), v0 > 0, int(M), int(d), int(Vc)));
-      CODA_CUDA(gemm_store(cx, w.ce.dL, true, Hb, true, dWc, int(Vc), int(d), int(M), nullptr, nullptr));
+      CODA_CUDA(gemm_splitk(cx, w.ce.dL, Wc, w.dH_parts, int(std::min(parts, cdiv(Vc, 64))), v0 > 0, int(M), int(d),
+                            int(Vc)));
+      CODA_CUDA(gemm_store_plus_rows(cx, w.ce.dL, Hb, dWc, w.slot + v0, w.label_rows, int(M), int(d), int(Vc)));
     }
   }
-  if (parts == 1)
-    CODA_CUDA(launch_f32_to_bf16(cx, w.ce.dH32, static_cast<bf16*>(dHs), M * d));
-  else
-    CODA_CUDA(launch_sum_parts(cx, w.dH_parts, int(parts), cdiv(M, 256) * 256 * d, static_cast<bf16*>(dHs), M * d));
-  return CODA_OK;
+  return from_cuda(launch_policy_dh(cx, parts == 1 ? w.ce.dH32 : w.dH_parts, int(parts), cdiv(M, 256) * 256 * d,
+                                    w.lost, labels, Wb, static_cast<bf16*>(dHs), M, d));
 }
 
 // ---------------------------------------------------------------------------

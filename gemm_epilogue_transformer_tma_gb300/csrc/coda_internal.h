@@ -163,10 +163,11 @@ cudaError_t gemm_splitk(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_b
 
 // dL chunk = (softmax - onehot) / M for vocabulary rows [v0, v0 + Vc), or
 // row_scale[m] (softmax - onehot) with row_scale != null.  The logits are
-// c.scale_host H Wt^T, as in gemm_ce_stats.
+// c.scale_host H Wt^T, as in gemm_ce_stats.  With lost != null, lost[m] = what
+// the bf16 rounding takes from the entry of a label in the chunk.
 cudaError_t gemm_ce_grad(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt_chunk,
                          const int32_t* labels, const float* lse, __nv_bfloat16* dL, int M, int d, int Vc, int v0,
-                         float inv_M, const float* row_scale = nullptr);
+                         float inv_M, const float* row_scale = nullptr, float* lost = nullptr);
 
 // qkv = X Wqkv with RoPE (head_dim 128) on the first rot_cols columns.
 cudaError_t gemm_qkv_rope(const LaunchCtx& c, const __nv_bfloat16* X, const __nv_bfloat16* Wqkv_t,
@@ -192,6 +193,13 @@ cudaError_t gemm_group_store(const LaunchCtx& c, const __nv_bfloat16* dH, const 
 cudaError_t gemm_group_ce_bwd(const LaunchCtx& c, const __nv_bfloat16* dL, const __nv_bfloat16* Wc,
                               const __nv_bfloat16* H, float* dH32, bool accumulate, __nv_bfloat16* dWc, int M, int d,
                               int Vc);
+//   the same with rows[slot[v]] (fp32, d wide) added to row v of dWc before
+//   it is rounded, where slot[v] != kNoSlot; and the dW GEMM of it alone
+cudaError_t gemm_group_policy_bwd(const LaunchCtx& c, const __nv_bfloat16* dL, const __nv_bfloat16* Wc,
+                                  const __nv_bfloat16* H, float* dH32, bool accumulate, __nv_bfloat16* dWc,
+                                  const uint32_t* slot, const float* rows, int M, int d, int Vc);
+cudaError_t gemm_store_plus_rows(const LaunchCtx& c, const __nv_bfloat16* dL, const __nv_bfloat16* H,
+                                 __nv_bfloat16* dWc, const uint32_t* slot, const float* rows, int M, int d, int Vc);
 //   the same first-layer pair on 8-bit codes: dX = sdH sW1 dHq W1q and
 //   dW1t = sdH sX dHq^T Xq (dH format dh_fmt; W1 and X in w_fmt); two
 //   launches when pairing is off.
@@ -310,12 +318,19 @@ struct PolicyRows {
   float* lse;
   float* logp;
   float* row_scale;          // factor of (softmax - onehot), or null
+  float* lost;               // set to 0, with row_scale
+  uint32_t* slot;            // [V], with row_scale: minimum of the tokens that carry the label and a weight
   float4* terms;
   int* status;
 };
-// out = bf16(sum_p parts[p]), n values per part at a distance of `stride` values
-cudaError_t launch_sum_parts(const LaunchCtx& c, const float* parts, int num, int64_t stride, __nv_bfloat16* out,
-                             int64_t n);
+// rows[m] = sum of lost[t] H[t] over the tokens t with m's label, for every m
+// that is the first token of a label in [v0, v0 + Vc) (slot[label] == m)
+cudaError_t launch_label_rows(const LaunchCtx& c, const int32_t* labels, const uint32_t* slot, const float* lost,
+                              const __nv_bfloat16* H, float* rows, int64_t M, int64_t d, int64_t v0, int64_t Vc);
+// dH[m] = bf16(sum_p parts[p][m] + lost[m] Wt[labels[m]]), `stride` values
+// between parts
+cudaError_t launch_policy_dh(const LaunchCtx& c, const float* parts, int num, int64_t stride, const float* lost,
+                             const int32_t* labels, const __nv_bfloat16* Wt, __nv_bfloat16* dH, int64_t M, int64_t d);
 cudaError_t launch_policy_rows(const LaunchCtx& c, const float* pmax, const float* psum, const float* zy,
                                const PolicyRows& p, int64_t M, int64_t T, int64_t V, float* stats);
 // unfused ablation kernels

@@ -1,5 +1,6 @@
 // LM-head GEMM instantiations: blocked log-sum-exp statistics epilogue and the
 // softmax-gradient epilogue (logits never leave the chip).
+#include "gemm_dw.cuh"
 #include "gemm_launch.cuh"
 #include "gemm_logits.cuh"
 #include "gemm_splitk.cuh"
@@ -72,9 +73,34 @@ cudaError_t gemm_splitk(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_b
                         ctl);
 }
 
+cudaError_t gemm_store_plus_rows(const LaunchCtx& c, const __nv_bfloat16* dL, const __nv_bfloat16* H,
+                                 __nv_bfloat16* dWc, const uint32_t* slot, const float* rows, int M, int d, int Vc) {
+  using L = DwSmem;
+  DwArgs g{};
+  if (!make_operand_maps(&g.A, &g.B, dL, true, H, true, Vc, d, M, 128) || !make_tmap_bf16(&g.out, dWc, d, Vc, d, 64, 32))
+    return cudaErrorInvalidValue;
+  g.slot = slot;
+  g.rows = rows;
+  g.M = Vc;
+  g.N = d;
+  g.tiles_m = (Vc + BM2 - 1) / BM2;
+  g.tiles_n = (d + kBN - 1) / kBN;
+  g.num_kb = (M + BK - 1) / BK;
+  static bool smem_ok[64] = {};
+  cudaError_t e = allow_smem(gemm_dw_kernel, L::TOTAL, smem_ok);
+  if (e != cudaSuccess) return e;
+  static int cap[64] = {};
+  int pairs = 0;
+  e = pair_capacity(reinterpret_cast<const void*>(gemm_dw_kernel), L::THREADS, L::TOTAL, c.num_sms, cap, &pairs);
+  if (e != cudaSuccess) return e;
+  KernelCtl ctl{c.status, c.timeout_ns, c.skip_first_stage};
+  const int clusters = std::max(1, std::min(g.tiles_m * g.tiles_n, pairs));
+  return launch_chained(c, gemm_dw_kernel, dim3(2 * clusters), dim3(L::THREADS), L::TOTAL, g, ctl);
+}
+
 cudaError_t gemm_ce_grad(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt_chunk,
                          const int32_t* labels, const float* lse, __nv_bfloat16* dL, int M, int d, int Vc, int v0,
-                         float inv_M, const float* row_scale) {
+                         float inv_M, const float* row_scale, float* lost) {
   CUtensorMap ta, tb;
   if (!make_operand_maps(&ta, &tb, H, false, Wt_chunk, false, M, Vc, d, b_box_rows(c))) return cudaErrorInvalidValue;
   EpiCeGrad::Params ep{};
@@ -84,6 +110,7 @@ cudaError_t gemm_ce_grad(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_
   ep.inv_M = inv_M;
   ep.v0 = v0;
   ep.row_scale = row_scale;
+  ep.lost = lost;
   return run_gemm<false, false, false, EpiCeGrad>(c, ta, tb, tb, M, Vc, d, (Vc + kBN - 1) / kBN, ep);
 }
 

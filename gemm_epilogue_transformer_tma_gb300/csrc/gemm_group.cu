@@ -158,6 +158,28 @@ cudaError_t gemm_group_ce_bwd(const LaunchCtx& c, const __nv_bfloat16* dL, const
   return launch_group<false, true, true, true, EpiStoreF32, EpiStore>(c, ga);
 }
 
+cudaError_t gemm_group_policy_bwd(const LaunchCtx& c, const __nv_bfloat16* dL, const __nv_bfloat16* Wc,
+                                  const __nv_bfloat16* H, float* dH32, bool accumulate, __nv_bfloat16* dWc,
+                                  const uint32_t* slot, const float* rows, int M, int d, int Vc) {
+  if (!c.pair) {
+    cudaError_t e = gemm_store_f32(c, dL, false, Wc, true, dH32, M, d, Vc, accumulate);
+    if (e != cudaSuccess) return e;
+    return gemm_store_plus_rows(c, dL, H, dWc, slot, rows, M, d, Vc);
+  }
+  GroupArgs<EpiStoreF32, EpiStorePlusRows> ga{};
+  if (!make_operand_maps(&ga.tmA0, &ga.tmB0, dL, false, Wc, true, M, d, Vc, b_box_rows(c)) ||
+      !make_operand_maps(&ga.tmA1, &ga.tmB1, dL, true, H, true, Vc, d, M, b_box_rows(c)))
+    return cudaErrorInvalidValue;
+  ga.sh0 = pair_shape(M, d, Vc);
+  ga.sh1 = pair_shape(Vc, d, M);
+  if (!make_tmap_store_f32(&ga.ep0.out, dH32, d, M, d)) return cudaErrorInvalidValue;
+  ga.ep0.beta = accumulate ? 1 : 0;
+  if (!make_tmap_store_bf16(&ga.ep1.out, dWc, d, Vc, d)) return cudaErrorInvalidValue;
+  ga.ep1.slot = slot;
+  ga.ep1.rows = rows;
+  return launch_group<false, true, true, true, EpiStoreF32, EpiStorePlusRows>(c, ga);
+}
+
 cudaError_t gemm_group_ce_bwd_fp8(const LaunchCtx& c0, const uint8_t* dLq, float s_dL, const uint8_t* Wq_chunk,
                                   const float* sW, const uint8_t* Hq, const float* sH, float* dH32, bool accumulate,
                                   __nv_bfloat16* dWc, int M, int d, int Vc) {

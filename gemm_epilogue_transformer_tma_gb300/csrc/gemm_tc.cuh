@@ -628,6 +628,54 @@ struct EpiStore {
   }
 };
 
+// C = bf16(acc + rows[slot[m]]): an fp32 row added where row m has a slot
+// (slot[m] != kNoSlot).  The weight gradient of the policy loss: what the bf16
+// label entries of dL lost, summed over a vocabulary row's tokens.
+constexpr uint32_t kNoSlot = 0xFFFFFFFFu;
+struct EpiStorePlusRows {
+  static constexpr int kEpiWarps = 4;
+  static constexpr int kStoreSlots = 2;  // two slots used alternately
+  static constexpr bool kAccScale = false;  // bf16 operands only
+  struct Params {
+    CUtensorMap out;       // [M][N] bf16
+    const uint32_t* slot;  // [M]
+    const float* rows;     // [slots][N]
+  };
+  template <int BN>
+  static __device__ __forceinline__ void run(const Params& p, const EpiCtx& c) {
+    const uint32_t s = c.m < c.M ? p.slot[c.m] : kNoSlot;
+    const float* add = p.rows + static_cast<int64_t>(s == kNoSlot ? 0u : s) * c.N;
+#pragma unroll 1
+    for (int cc = c.c0; cc < c.c1; cc += 32) {
+      float v[32];
+      acc_ld32(c, cc, v);
+      const int n0 = c.tn * BN + cc;
+      if (n0 < c.N && c.m0 < c.M) {
+        if (s != kNoSlot) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            if (n0 + 4 * q < c.N) {  // N is a multiple of 8
+              const float4 x = __ldg(reinterpret_cast<const float4*>(add + n0) + q);
+              v[4 * q] += x.x;
+              v[4 * q + 1] += x.y;
+              v[4 * q + 2] += x.z;
+              v[4 * q + 3] += x.w;
+            }
+          }
+        }
+        const int slot = ((cc - c.c0) >> 5) & 1;
+        slots_acquire_db(c.lane, cc == c.c0);
+        stage_bf16x32(slot_addr(c, slot), c.lane, v);
+        slots_publish();
+        if (c.lane == 0) {
+          tma_store_2d(&p.out, slot_addr(c, slot), n0, c.m0);
+          bulk_commit_group();
+        }
+      }
+    }
+  }
+};
+
 // fp32 output, overwrite (beta = 0) or accumulate (beta = 1, a TMA
 // reduce-add: each element receives one add per launch).
 struct EpiStoreF32 {
@@ -1110,6 +1158,8 @@ struct EpiCeGrad {
     int codes;
     float code_inv;  // the inverse of the codes' power-of-two scale
     const float* row_scale;  // [M], or null: inv_M for every row
+    float* lost;             // [M], or null: what the label's entry loses to bf16 (written by the chunk
+                             // that holds the label)
   };
   template <int BN>
   static __device__ __forceinline__ void run(const Params& p, const EpiCtx& c) {
@@ -1127,6 +1177,11 @@ struct EpiCeGrad {
         for (int i = 0; i < 32; ++i) {
           const float e = __expf(v[i] * c.acc_scale - l) - ((n0 + i == y) ? 1.f : 0.f);
           v[i] = s == 0.f ? 0.f : e * s;
+        }
+        if (p.lost != nullptr && y >= n0 && y < n0 + 32) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (n0 + i == y) p.lost[c.m] = v[i] - bf16_round(v[i]);
         }
         slots_acquire(c.lane);
         if (p.codes)

@@ -80,7 +80,11 @@ __device__ __forceinline__ float4 policy_row(const float* __restrict__ pmax, con
     if (!in_range && w != 0.f) atomicOr(p.status, DEV_ERR_LABEL_RANGE);
     p.lse[m] = lse;
     p.logp[m] = lp;
-    if (p.row_scale != nullptr) p.row_scale[m] = -g * p.inv_temp;
+    if (p.row_scale != nullptr) {
+      p.row_scale[m] = -g * p.inv_temp;
+      p.lost[m] = 0.f;
+      if (in_range && w != 0.f) atomicMin(&p.slot[y], static_cast<uint32_t>(m));  // the order does not matter
+    }
   }
   return t;
 }
@@ -180,15 +184,76 @@ __global__ void __launch_bounds__(1024) policy_stats_kernel(const float4* __rest
   }
 }
 
-// four values per thread: the parts in order
-__global__ void sum_parts_kernel(const float4* __restrict__ parts, int num, int64_t stride4, uint2* __restrict__ out,
-                                 int64_t n4) {
+// The label's entry of dL, g (p_y - 1), outweighs its row (the other entries
+// are the p_v of thousands of columns), so its rounding to bf16 would be most
+// of the gradients' error: a factor 1.4 to 1.7 over a single rounding of the
+// results.  The GEMMs take the rounded entry; what it lost is added in fp32,
+// lost[m] W[y_m] to dH[m] and lost[m] H[m] to dW[y_m].
+//
+// dW's part, per label: CTA m works when m is the label's first token, finds
+// the label's other tokens by a scan of the labels behind it, and adds their
+// rows in token order.
+__global__ void __launch_bounds__(256) label_rows_kernel(const int32_t* __restrict__ labels,
+                                                         const uint32_t* __restrict__ slot,
+                                                         const float* __restrict__ lost,
+                                                         const __nv_bfloat16* __restrict__ H, float* __restrict__ rows,
+                                                         int64_t M, int64_t d, int64_t v0, int64_t Vc) {
   griddep_wait();
   griddep_launch_dependents();
+  __shared__ int list[256];       // this tile's tokens of the label, in order
+  __shared__ int warp_count[8];
+  const int64_t m = blockIdx.x;
+  const int64_t y = labels[m];
+  if (y < v0 || y >= v0 + Vc || slot[y] != static_cast<uint32_t>(m)) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int64_t c0 = 0; c0 < d; c0 += 2048) {  // 8 columns per thread
+    const int64_t col = c0 + tid * 8;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int64_t t0 = m; t0 < M; t0 += 256) {
+      const bool hit = t0 + tid < M && labels[t0 + tid] == y;
+      const unsigned mask = __ballot_sync(0xffffffffu, hit);
+      if (lane == 0) warp_count[warp] = __popc(mask);
+      __syncthreads();
+      int before = 0, n = 0;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        before += w < warp ? warp_count[w] : 0;
+        n += warp_count[w];
+      }
+      if (hit) list[before + __popc(mask & ((1u << lane) - 1u))] = static_cast<int>(t0 - m) + tid;
+      __syncthreads();
+      if (col < d) {
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+          const int64_t t = m + list[i];
+          const float r = lost[t];
+          float h[8];
+          unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(H + t * d + col)), h);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] = fmaf(r, h[j], acc[j]);
+        }
+      }
+      __syncthreads();
+    }
+    if (col < d) {
+      float4* o = reinterpret_cast<float4*>(rows + m * d + col);
+      o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    }
+  }
+}
+
+// dH: the parts in order, then the label's lost share; four columns per thread.
+__global__ void policy_dh_kernel(const float4* __restrict__ parts, int num, int64_t stride4,
+                                 const float* __restrict__ lost, const int32_t* __restrict__ labels,
+                                 const uint2* __restrict__ Wt, uint2* __restrict__ out, int64_t M, int64_t d4) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t n4 = M * d4;
   for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n4;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     float4 s = parts[i];
-#pragma unroll 4
+#pragma unroll 8
     for (int p = 1; p < num; ++p) {
       const float4 x = parts[p * stride4 + i];
       s.x += x.x;
@@ -196,17 +261,34 @@ __global__ void sum_parts_kernel(const float4* __restrict__ parts, int num, int6
       s.z += x.z;
       s.w += x.w;
     }
+    const int64_t m = i / d4;
+    const float r = lost[m];
+    if (r != 0.f) {  // only a row whose label was in range has lost anything
+      const uint2 q = __ldg(Wt + static_cast<int64_t>(labels[m]) * d4 + (i - m * d4));
+      const float2 a = split2(unpack_bf16x2(q.x)), b = split2(unpack_bf16x2(q.y));
+      s.x = fmaf(r, a.x, s.x);
+      s.y = fmaf(r, a.y, s.y);
+      s.z = fmaf(r, b.x, s.z);
+      s.w = fmaf(r, b.y, s.w);
+    }
     out[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
   }
 }
 
 }  // namespace
 
-cudaError_t launch_sum_parts(const LaunchCtx& c, const float* parts, int num, int64_t stride, __nv_bfloat16* out,
-                             int64_t n) {
-  const int64_t blocks = std::min<int64_t>((n / 4 + 127) / 128, int64_t(c.num_sms) * 16);
-  return launch_chained(c, sum_parts_kernel, dim3(static_cast<unsigned>(blocks)), dim3(128), 0,
-                        reinterpret_cast<const float4*>(parts), num, stride / 4, reinterpret_cast<uint2*>(out), n / 4);
+cudaError_t launch_label_rows(const LaunchCtx& c, const int32_t* labels, const uint32_t* slot, const float* lost,
+                              const __nv_bfloat16* H, float* rows, int64_t M, int64_t d, int64_t v0, int64_t Vc) {
+  return launch_chained(c, label_rows_kernel, dim3(static_cast<unsigned>(M)), dim3(256), 0, labels, slot, lost, H, rows,
+                        M, d, v0, Vc);
+}
+
+cudaError_t launch_policy_dh(const LaunchCtx& c, const float* parts, int num, int64_t stride, const float* lost,
+                             const int32_t* labels, const __nv_bfloat16* Wt, __nv_bfloat16* dH, int64_t M, int64_t d) {
+  const int64_t blocks = std::min<int64_t>((M * d / 4 + 127) / 128, int64_t(c.num_sms) * 16);
+  return launch_chained(c, policy_dh_kernel, dim3(static_cast<unsigned>(blocks)), dim3(128), 0,
+                        reinterpret_cast<const float4*>(parts), num, stride / 4, lost, labels,
+                        reinterpret_cast<const uint2*>(Wt), reinterpret_cast<uint2*>(dH), M, d / 4);
 }
 
 cudaError_t launch_policy_rows(const LaunchCtx& c, const float* pmax, const float* psum, const float* zy,

@@ -752,7 +752,7 @@ coda_status_t coda_lmhead_ce_fp8(coda_handle_t h, const void* Hq, const float* s
                                  void* stream);
 
 /* Workspace of coda_lmhead_policy: that of coda_lmhead_ce, 24 bytes per row,
- * and, with gradients, up to 20 MB of fp32 partial sums of dHs (used for few
+ * and, with gradients, 4 (M d + M + V) bytes and up to 20 MB of fp32 partial sums of dHs (used for few
  * tokens).  A workspace for M tokens also serves any smaller number. */
 size_t coda_lmhead_policy_workspace_bytes(int64_t M, int64_t d, int64_t V, int with_grads);
 
@@ -775,7 +775,8 @@ size_t coda_lmhead_policy_workspace_bytes(int64_t M, int64_t d, int64_t V, int w
  * For a row with weight, a label outside [0, V) sets CODA_ERR_LABEL_RANGE in
  * the status word; the row then adds nothing, and its logp is 0.
  * If dHs is not NULL the gradients of loss are produced as coda_lmhead_ce
- * does: dHs = dL Wt, dWt = dL^T Hs.
+ * does: dHs = dL Wt, dWt = dL^T Hs, dL in bf16, but with the labels' entries,
+ * which outweigh their rows, in fp32.
  * Hs bf16 [M][d], Wt bf16 [V][d], labels int32 [M], advantage, weight,
  * logp_old, logp_ref fp32 [M] (these, stats and logp 4-byte aligned), dHs bf16
  * [M][d] or NULL, dWt bf16 [V][d] (required iff dHs != NULL).  clip_low in
