@@ -12,6 +12,7 @@
 
 #include <c10/cuda/CUDAStream.h>
 
+#include <exception>
 #include <initializer_list>
 
 #include "../../include/coda.h"
@@ -334,7 +335,20 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
-#define CODA_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr}
+// A method as Python calls it: a C++ exception (a tensor without storage, a
+// sparse one) becomes a Python one instead of crossing the C boundary.
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  try {
+    return F(self, a, n);
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_ValueError, e.what());
+    return nullptr;
+  }
+}
+
+#define CODA_METHOD(f) \
+  {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(guarded<f>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {CODA_METHOD(bind),       CODA_METHOD(quantize), CODA_METHOD(quantize_weight),
                            CODA_METHOD(dequantize), CODA_METHOD(gemm),     CODA_METHOD(qknorm),
                            CODA_METHOD(qknorm_bwd), CODA_METHOD(policy),   {nullptr, nullptr, 0, nullptr}};

@@ -35,6 +35,9 @@
  *     not CODA_OK.  Conditions detected on the device (a bounded wait that
  *     expired, a label out of range) are recorded in the handle's device
  *     status word and reported by coda_sync_status.
+ *   - A workspace (arena) belongs to one call until that call has completed
+ *     on its stream: calls, or replays of captured graphs, that may run at the
+ *     same time need a workspace each.
  *   - A handle may be used from one host thread at a time.
  */
 #ifndef CODA_H_

@@ -258,6 +258,14 @@ def test_empty_problems_and_refusals():
         C.coda_fp8_block_quantize(x, q, torch.empty(16, dtype=U8, device="cuda"), None, None)
     with pytest.raises(ValueError):
         C.coda_fp8_block_quantize(x, q, None, None, None)
+    with pytest.raises(ValueError):
+        C.coda_fp8_block_quantize(x.to_sparse(), q, _scales(4, 128), None, None)
+    with pytest.raises(ValueError):
+        C.coda_fp8_block_quantize(x.cpu(), q, _scales(4, 128), None, None)
+    with pytest.raises(ValueError):
+        C.coda_fp8_block_quantize(x[:, ::2], q, _scales(4, 128), None, None)
+    with pytest.raises(TypeError):
+        C.coda_fp8_block_quantize(None, q, _scales(4, 128), None, None)
     with pytest.raises(TypeError):
         C.coda_fp8_block_quantize(x.float(), q, _scales(4, 128), None, None)
     assert_device_ok()

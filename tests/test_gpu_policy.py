@@ -148,10 +148,49 @@ def test_a_workspace_serves_smaller_batches():
             assert n == sorted(n)
 
 
-@pytest.mark.parametrize("M,d,V", [(700, 512, 4096), (300, 264, 2056), (40, 2048, 2048)])
+@pytest.mark.parametrize("M,d,V", [(700, 512, 4096), (300, 264, 2056), (40, 2048, 2048), (2600, 1024, 264)])
 def test_data_gradient_in_ranges_of_the_vocabulary(M, d, V):
     pb = Problem(M, d, V)
     pb.grade(pb.run())
+
+
+def _one_rounding(got, ref, what):
+    """Relative Frobenius error against that of the reference itself rounded
+    to bf16: the label entries of dL, the bulk of both gradients, are kept in
+    fp32, so the rounding of the results is nearly all there is (a factor 1.1
+    leaves room for the bf16 of the other entries and fp32 accumulation)."""
+    r = torch.from_numpy(ref)
+    own = (r.to(BF).double() - r).norm()
+    assert (got.cpu().double() - r).norm() <= 1.1 * own, what
+
+
+@pytest.mark.parametrize("M,d,V", [(60, 256, 1000), (2600, 1024, 520)])
+@pytest.mark.parametrize("pairing", [True, False], ids=["sm_pair", "single_sm"])
+def test_gradients_carry_one_rounding(M, d, V, pairing):
+    """Advantages whose gradient factors sit just above a power of two, where
+    bf16 is coarsest; V = 520 makes labels repeat (the sums per label), M =
+    2600 takes the grouped launch."""
+    pb = Problem(M, d, V, seed=11)
+    pb.w[:] = 1.0 / 64
+    pb.adv = np.where(pb.adv > 0, 1.01, -1.01).astype(np.float32)
+    C.coda_set_sm_pairing(pairing)
+    try:
+        r = pb.run(old=False, ref=False)
+    finally:
+        C.coda_set_sm_pairing(True)
+    assert_device_ok()
+    _one_rounding(pb.dH, r["dH"], "dH")
+    _one_rounding(pb.dW, r["dWt"], "dWt")
+
+
+def test_every_token_has_the_same_label():
+    pb = Problem(700, 64, 264)
+    pb.y[:] = 77
+    r = pb.run()
+    pb.grade(r)
+    a = pb.dW.clone()
+    pb.run()
+    assert torch.equal(a, pb.dW)               # the sum per label has a fixed order
 
 
 def test_captured_graph():
