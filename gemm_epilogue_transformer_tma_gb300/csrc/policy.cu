@@ -113,6 +113,7 @@ __global__ void __cluster_dims__(kRowCtas, 1, 1) __launch_bounds__(1024)
   griddep_launch_dependents();
   __shared__ float2 red[32][4];   // per warp: sum and its low part
   __shared__ float2 total[kRowCtas][4];  // CTA 0: per CTA
+  cluster_arrive();  // CTA 0 has started before anyone writes to its shared memory
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = cluster_ctarank();
   float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
@@ -127,6 +128,7 @@ __global__ void __cluster_dims__(kRowCtas, 1, 1) __launch_bounds__(1024)
 #pragma unroll
     for (int j = 0; j < 4; ++j) red[warp][j] = make_float2(hi[j], lo[j]);
   __syncthreads();
+  cluster_wait();
   if (warp < 4) {  // warp j: statistic j over the CTA's warps
     float h = red[lane][warp].x, l = red[lane][warp].y;
 #pragma unroll
