@@ -28,6 +28,8 @@ __device__ __forceinline__ void add_exact(float& hi, float& lo, float b, float b
   lo += ((hi - (s - t)) + (b - t)) + b_lo;
   hi = s;
 }
+// the pair as one number; an infinite sum has no rounding error to add
+__device__ __forceinline__ float exact_value(float hi, float lo) { return isinf(hi) ? hi : hi + lo; }
 
 // A warp's row: the log-sum-exp of its block statistics, then the token terms
 // (in every lane): the row's shares of the four statistics.
@@ -60,10 +62,11 @@ __device__ __forceinline__ float4 policy_row(const float* __restrict__ pmax, con
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
   float g = 0.f;  // d loss / d lp
   if (in_range && w != 0.f) {
+    // exp overflows fp32 past 88, where the formula's products with 0 are still 0
     const float A = p.adv[m];
     const float r = p.old != nullptr ? expf(lp - p.old[m]) : 1.f;
-    const float ra = r * A;
-    const float ca = fminf(fmaxf(r, p.lo), p.hi) * A;
+    const float ra = A != 0.f ? r * A : 0.f;
+    const float ca = A != 0.f ? fminf(fmaxf(r, p.lo), p.hi) * A : 0.f;
     const bool free = ra <= ca;
     float kl = 0.f, dkl = 0.f;
     if (p.ref != nullptr) {
@@ -72,8 +75,9 @@ __device__ __forceinline__ float4 policy_row(const float* __restrict__ pmax, con
       dkl = -em;
     }
     const float pg = -(free ? ra : ca);
-    t = make_float4(w * (p.beta * kl + pg), w * pg, w * kl, free ? 0.f : w);
-    g = w * (p.beta * dkl - (free ? ra : 0.f));
+    const bool with_kl = p.beta != 0.f;
+    t = make_float4(w * ((with_kl ? p.beta * kl : 0.f) + pg), w * pg, w * kl, free ? 0.f : w);
+    g = w * ((with_kl ? p.beta * dkl : 0.f) - (free ? ra : 0.f));
   }
   if (lane == 0) {
     // padding, a row without weight, may carry any label
@@ -143,7 +147,7 @@ __global__ void __cluster_dims__(kRowCtas, 1, 1) __launch_bounds__(1024)
     float h = 0.f, l = 0.f;
 #pragma unroll
     for (int c = 0; c < kRowCtas; ++c) add_exact(h, l, total[c][threadIdx.x].x, total[c][threadIdx.x].y);
-    stats[threadIdx.x] = h + l;
+    stats[threadIdx.x] = exact_value(h, l);
   }
 }
 
@@ -181,7 +185,7 @@ __global__ void __launch_bounds__(1024) policy_stats_kernel(const float4* __rest
         const float h2 = __shfl_xor_sync(0xffffffffu, h, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
         add_exact(h, l, h2, l2);
       }
-      if (threadIdx.x == 0) stats[j] = h + l;
+      if (threadIdx.x == 0) stats[j] = exact_value(h, l);
     }
   }
 }

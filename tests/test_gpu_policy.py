@@ -230,3 +230,23 @@ def test_refusals():
     assert call(T=0.0) == 1 and call(T=inf) == 1 and call(T=nan) == 1
     assert call(M=0) == 1 and call(V=0) == 1 and call(d=12) == 2 and call(adv=odd) == 2 and call(n=n - 1) == 4
     assert_device_ok()
+
+
+@pytest.mark.parametrize("M", [40, 700])
+def test_exponentials_past_fp32(M):
+    """A ratio or a KL term that overflows fp32 stays out of what it is
+    multiplied by zero in: tokens without advantage, kl_coef = 0.  The KL
+    statistic itself is then an infinity, not a NaN."""
+    pb = Problem(M, 64, 264)
+    pb.adv[::3] = 0.0
+    pb.old[::3] -= 200.0                       # r = inf at A = 0
+    pb.ref[1::4] += 100.0                      # kl = e^100
+    r = pb.run(beta=0.0)
+    assert pb.stats[2].item() == np.inf
+    pb.stats[2], r["stats"][2] = 0.0, 0.0
+    pb.grade(r)
+    pb = Problem(M, 64, 264)
+    pb.old[5], pb.adv[5] = pb.old[5] - 200.0, -1.0   # unclipped: the loss itself overflows
+    pb.run()
+    assert pb.stats[0].item() == np.inf and pb.stats[1].item() == np.inf and np.isfinite(pb.stats[2].item())
+    assert_device_ok()
