@@ -1296,7 +1296,8 @@ coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt
                .st);
   if (M == 0) return CODA_ERR_INVALID_ARG;  // as coda_lmhead_ce
   if (!(clip_low >= 0.f && clip_low <= 1.f) || !(clip_high >= 0.f)) return CODA_ERR_INVALID_ARG;
-  if (!(kl_coef >= 0.f) || std::isinf(kl_coef) || !(temperature > 0.f) || std::isinf(temperature))
+  if (!(kl_coef >= 0.f) || std::isinf(kl_coef) || !(temperature > 0.f) || std::isinf(temperature) ||
+      std::isinf(1.0f / temperature))
     return CODA_ERR_INVALID_ARG;
   const bool grads = dHs != nullptr;
   if (grads != (dWt != nullptr)) return CODA_ERR_INVALID_ARG;

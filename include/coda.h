@@ -754,9 +754,10 @@ coda_status_t coda_lmhead_ce_fp8(coda_handle_t h, const void* Hq, const float* s
                                  void* dWt, void* ws, size_t ws_bytes, int64_t M, int64_t d, int64_t V,
                                  void* stream);
 
-/* Workspace of coda_lmhead_policy: that of coda_lmhead_ce, 24 bytes per row,
- * and, with gradients, 4 (M d + M + V) bytes and up to 20 MB of fp32 partial sums of dHs (used for few
- * tokens).  A workspace for M tokens also serves any smaller number. */
+/* Workspace of coda_lmhead_policy: that of coda_lmhead_ce, 20 bytes per row,
+ * and, with gradients, 4 (M d + 2 M + V) bytes and up to 20 MB of fp32 partial
+ * sums of dHs (used for few tokens).  A workspace for M tokens also serves any
+ * smaller number. */
 size_t coda_lmhead_policy_workspace_bytes(int64_t M, int64_t d, int64_t V, int with_grads);
 
 /* Clipped policy loss with a KL term on the LM head, without ever writing an
@@ -784,7 +785,7 @@ size_t coda_lmhead_policy_workspace_bytes(int64_t M, int64_t d, int64_t V, int w
  * logp_old, logp_ref fp32 [M] (these, stats and logp 4-byte aligned), dHs bf16
  * [M][d] or NULL, dWt bf16 [V][d] (required iff dHs != NULL).  clip_low in
  * [0, 1], clip_high >= 0 (infinity: no upper bound), kl_coef >= 0,
- * temperature > 0, M >= 1. */
+ * temperature > 0 with a finite fp32 reciprocal, M >= 1. */
 coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt, const int32_t* labels,
                                  const float* advantage, const float* weight, const float* logp_old,
                                  const float* logp_ref, float clip_low, float clip_high, float kl_coef,

@@ -250,3 +250,20 @@ def test_exponentials_past_fp32(M):
     pb.run()
     assert pb.stats[0].item() == np.inf and pb.stats[1].item() == np.inf and np.isfinite(pb.stats[2].item())
     assert_device_ok()
+
+
+def test_a_temperature_without_a_reciprocal_is_refused():
+    pb = Problem(4, 64, 136)
+    pb.T = 1e-39
+    with pytest.raises(C.CodaError):
+        C.coda_lmhead_policy(*pb_args(pb))
+    assert_device_ok()
+
+
+def pb_args(pb):
+    def e(*s):
+        return torch.zeros(*s, device="cuda")
+
+    n = C.coda_lmhead_policy_workspace_bytes(pb.M, pb.d, pb.V, False)
+    return (pb.H, pb.W, torch.from_numpy(pb.y).cuda(), e(pb.M), None, None, None, 0.2, 0.2, 0.0, pb.T, e(4), e(pb.M),
+            None, None, torch.empty(n, dtype=torch.uint8, device="cuda"))
