@@ -4,7 +4,7 @@
 // whole tiles would leave to as many SM pairs (136 tokens, d = 1024: 4 of 76,
 // 503 us).  Each unit (tile, range) has its own SM pair and its own slice of a
 // [parts][rows][N] fp32 buffer; the slices are added in a fixed order by the
-// pass that rounds the result (sum_parts_kernel), so results do not depend on
+// pass that rounds the result (policy_dh_kernel), so results do not depend on
 // timing.
 //
 // A K-major [M][K] bf16, B MN-major [K][N] bf16.  One unit per cluster of two

@@ -191,10 +191,13 @@ constexpr int bwd_stage_bytes(int G, int U) { return 2 * (U * 32 * 16 * 2) + 2 *
 // warp's head groups, the CTA's warps of that kind, and (dg_sums_kernel) the
 // CTAs, in a fixed order.  A chunk of x and of dy is one contiguous piece, so
 // each warp keeps kStages rows of them, with their rows of the tables, in
-// flight with bulk copies into its own shared-memory ring.  Two CTAs per SM: the 128 registers a thread needs
-// leave no room for a third (84 us with spills against 58, at 8192 rows of 48
-// heads of 128; 302 MB).  Plain loads into registers took 70 us there; the
-// packed fp32 arithmetic (two values per instruction) 58 against 61.
+// flight with bulk copies into its own shared-memory ring.  8192 rows of 48
+// heads of 128 (302 MB): 48 us, 6.3 TB/s, and 3 for dg_sums_kernel.  What it
+// took on the way there: plain loads into registers 70; bulk copies of x and dy
+// alone 61, with packed fp32 arithmetic (two values per instruction) 58; the
+// tables' rows copied too, the present form.  Two CTAs per SM: the 128
+// registers a thread needs leave no room for a third (84 with spills against
+// 58).
 template <int G, int U>
 __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(const HeadArgs a) {
   griddep_wait();
