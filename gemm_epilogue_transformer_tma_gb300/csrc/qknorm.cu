@@ -16,7 +16,8 @@
 // before the first use.  A warp's task is a chunk of U * 32 / G heads of one
 // kind (q, k or v) of one row: cos, sin and g are loaded once per chunk, and
 // neighbouring warps take the chunks of the same row, which find the table
-// row in L1.  Memory-bound: x (and dy) read once, one result written.
+// row in L1.  Memory-bound: x (and dy) read once, one result written; forward
+// of 8192 rows of 48 heads of 128 (201 MB) 33 us, 6.1 TB/s.
 #include <algorithm>
 
 #include "coda_internal.h"
