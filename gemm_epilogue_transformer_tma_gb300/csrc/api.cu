@@ -1217,7 +1217,7 @@ struct PolicyWs {
   float4* terms;
   float* lost;        // [M]: what bf16 takes from dL's label entries
   float* label_rows;  // [M][d]: lost H summed per label, at the label's first token
-  uint32_t* slot;     // [V]: that token
+  uint32_t* slot;     // [2][V]: that token, and the complement of the label's last
   float* dH_parts;  // the data gradient's K ranges: fp32 [dh_parts()][M rounded up to 256][d]
   size_t bytes;
 };
@@ -1258,7 +1258,7 @@ PolicyWs policy_layout(uint8_t* base, int64_t M, int64_t d, int64_t V, bool grad
     w.row_scale = reinterpret_cast<float*>(take(size_t(M) * 4));
     w.lost = reinterpret_cast<float*>(take(size_t(M) * 4));
     w.label_rows = reinterpret_cast<float*>(take(size_t(M) * d * 4));
-    w.slot = reinterpret_cast<uint32_t*>(take(size_t(V) * 4));
+    w.slot = reinterpret_cast<uint32_t*>(take(size_t(V) * 8));
     w.dH_parts = reinterpret_cast<float*>(take(dh_parts_bytes(M, d, std::min<int64_t>(V, kCeChunk))));
   }
   w.bytes = off;
@@ -1329,7 +1329,7 @@ coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt
   r.slot = w.slot;
   r.terms = w.terms;
   r.status = cx.status;
-  if (grads) CODA_CUDA(cudaMemsetAsync(w.slot, 0xFF, size_t(V) * 4, cx.stream));  // kNoSlot
+  if (grads) CODA_CUDA(cudaMemsetAsync(w.slot, 0xFF, size_t(V) * 8, cx.stream));  // kNoSlot
   CODA_CUDA(launch_policy_rows(cx, w.ce.pmax, w.ce.psum, w.ce.zy, r, M, T, V, stats));
   if (!grads) return CODA_OK;
   // the first chunk sets the number of ranges (never more than the workspace
@@ -1342,7 +1342,7 @@ coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt
     bf16* dWc = static_cast<bf16*>(dWt) + v0 * d;
     CODA_CUDA(gemm_ce_grad(cl, Hb, Wc, labels, w.lse, w.ce.dL, int(M), int(d), int(Vc), int(v0), 0.f, w.row_scale,
                            w.lost));
-    CODA_CUDA(launch_label_rows(cx, labels, w.slot, w.lost, Hb, w.label_rows, M, d, v0, Vc));
+    CODA_CUDA(launch_label_rows(cx, labels, w.slot, w.slot + V, w.lost, Hb, w.label_rows, M, d, v0, Vc));
     if (parts == 1) {
       CODA_CUDA(gemm_group_policy_bwd(cx, w.ce.dL, Wc, Hb, w.ce.dH32, v0 > 0, dWc, w.slot + v0, w.label_rows, int(M),
                                       int(d), int(Vc)));

@@ -319,14 +319,17 @@ struct PolicyRows {
   float* logp;
   float* row_scale;          // factor of (softmax - onehot), or null
   float* lost;               // set to 0, with row_scale
-  uint32_t* slot;            // [V], with row_scale: minimum of the tokens that carry the label and a weight
+  uint32_t* slot;            // [2][V], with row_scale: the first of the tokens that carry the label and a
+                             // weight, and the complement of the last (so both are minima)
   float4* terms;
   int* status;
 };
 // rows[m] = sum of lost[t] H[t] over the tokens t with m's label, for every m
-// that is the first token of a label in [v0, v0 + Vc) (slot[label] == m)
-cudaError_t launch_label_rows(const LaunchCtx& c, const int32_t* labels, const uint32_t* slot, const float* lost,
-                              const __nv_bfloat16* H, float* rows, int64_t M, int64_t d, int64_t v0, int64_t Vc);
+// that is the first token of a label in [v0, v0 + Vc) (slot[label] == m;
+// ~not_last[label] is its last)
+cudaError_t launch_label_rows(const LaunchCtx& c, const int32_t* labels, const uint32_t* slot,
+                              const uint32_t* not_last, const float* lost, const __nv_bfloat16* H, float* rows,
+                              int64_t M, int64_t d, int64_t v0, int64_t Vc);
 // dH[m] = bf16(sum_p parts[p][m] + lost[m] Wt[labels[m]]), `stride` values
 // between parts
 cudaError_t launch_policy_dh(const LaunchCtx& c, const float* parts, int num, int64_t stride, const float* lost,

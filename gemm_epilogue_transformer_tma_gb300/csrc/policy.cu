@@ -87,7 +87,10 @@ __device__ __forceinline__ float4 policy_row(const float* __restrict__ pmax, con
     if (p.row_scale != nullptr) {
       p.row_scale[m] = -g * p.inv_temp;
       p.lost[m] = 0.f;
-      if (in_range && w != 0.f) atomicMin(&p.slot[y], static_cast<uint32_t>(m));  // the order does not matter
+      if (in_range && w != 0.f) {  // the order does not matter
+        atomicMin(&p.slot[y], static_cast<uint32_t>(m));
+        atomicMin(&p.slot[V + y], ~static_cast<uint32_t>(m));
+      }
     }
   }
   return t;
@@ -200,17 +203,18 @@ constexpr int kLabelTile = 1024;  // labels it looks at in one step: four to a t
 // lost[m] W[y_m] to dH[m] and lost[m] H[m] to dW[y_m].
 //
 // dW's part, per label: CTA (m, c) works when m is the label's first token,
-// finds the label's other tokens by a scan of the labels behind it, and adds
-// 1024 columns c of their rows in token order, eight rows in flight.  Tokens
-// without weight have lost nothing and are passed over (padding may repeat one
-// label thousands of times).  A whole update of 8192 tokens, d = 2048, V =
+// finds the label's other tokens by a scan of the labels up to its last one,
+// and adds 1024 columns c of their rows in token order, eight rows in flight.
+// Tokens without weight have lost nothing and are passed over (padding may
+// repeat one label thousands of times).  A whole update of 8192 tokens, d = 2048, V =
 // 32000: labels all different or random 2.4 ms, half of them padding 2.4 (3.9
 // with the padding's rows added in), all the same 3.4 (5.6 one row at a time).
 __global__ void __launch_bounds__(256) label_rows_kernel(const int32_t* __restrict__ labels,
                                                          const uint32_t* __restrict__ slot,
+                                                         const uint32_t* __restrict__ not_last,
                                                          const float* __restrict__ lost,
                                                          const __nv_bfloat16* __restrict__ H, float* __restrict__ rows,
-                                                         int64_t M, int64_t d, int64_t v0, int64_t Vc) {
+                                                         int64_t d, int64_t v0, int64_t Vc) {
   griddep_wait();
   griddep_launch_dependents();
   __shared__ int list[kLabelTile];  // this tile's tokens of the label, in order
@@ -218,16 +222,27 @@ __global__ void __launch_bounds__(256) label_rows_kernel(const int32_t* __restri
   __shared__ int warp_count[8];
   const int64_t m = blockIdx.x;
   const int64_t y = labels[m];
-  if (y < v0 || y >= v0 + Vc || slot[y] != static_cast<uint32_t>(m)) return;
+  if (y < v0 || y >= v0 + Vc) return;
+  const uint32_t first = slot[y];
+  const int64_t end = int64_t(~not_last[y]) + 1;
+  if (first != static_cast<uint32_t>(m)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t col = blockIdx.y * static_cast<int64_t>(kLabelCols) + tid * 4;
   f32x2 a0 = splat2(0.f), a1 = splat2(0.f);
-  for (int64_t t0 = m; t0 < M; t0 += kLabelTile) {
+  if (end == m + 1) {  // most labels have one token
+    if (col < d) {
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(H + m * d + col));
+      const f32x2 s = splat2(lost[m]);
+      a0 = mul2(s, unpack_bf16x2(q.x));
+      a1 = mul2(s, unpack_bf16x2(q.y));
+    }
+  }
+  for (int64_t t0 = end > m + 1 ? m : end; t0 < end; t0 += kLabelTile) {
     const int64_t t = t0 + tid * 4;  // four tokens per thread
     bool hit[4];
     float r[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) hit[j] = t + j < M && labels[t + j] == y;
+    for (int j = 0; j < 4; ++j) hit[j] = t + j < end && labels[t + j] == y;
     int own = 0, below = 0, warp_n = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -313,10 +328,12 @@ __global__ void policy_dh_kernel(const float4* __restrict__ parts, int num, int6
 
 }  // namespace
 
-cudaError_t launch_label_rows(const LaunchCtx& c, const int32_t* labels, const uint32_t* slot, const float* lost,
-                              const __nv_bfloat16* H, float* rows, int64_t M, int64_t d, int64_t v0, int64_t Vc) {
-  return launch_chained(c, label_rows_kernel, dim3(static_cast<unsigned>(M), static_cast<unsigned>((d + kLabelCols - 1) / kLabelCols)),
-                        dim3(256), 0, labels, slot, lost, H, rows, M, d, v0, Vc);
+cudaError_t launch_label_rows(const LaunchCtx& c, const int32_t* labels, const uint32_t* slot,
+                              const uint32_t* not_last, const float* lost, const __nv_bfloat16* H, float* rows,
+                              int64_t M, int64_t d, int64_t v0, int64_t Vc) {
+  return launch_chained(c, label_rows_kernel,
+                        dim3(static_cast<unsigned>(M), static_cast<unsigned>((d + kLabelCols - 1) / kLabelCols)),
+                        dim3(256), 0, labels, slot, not_last, lost, H, rows, d, v0, Vc);
 }
 
 cudaError_t launch_policy_dh(const LaunchCtx& c, const float* parts, int num, int64_t stride, const float* lost,

@@ -755,7 +755,7 @@ coda_status_t coda_lmhead_ce_fp8(coda_handle_t h, const void* Hq, const float* s
                                  void* stream);
 
 /* Workspace of coda_lmhead_policy: that of coda_lmhead_ce, 20 bytes per row,
- * and, with gradients, 4 (M d + 2 M + V) bytes and up to 20 MB of fp32 partial
+ * and, with gradients, 4 (M d + 2 M + 2 V) bytes and up to 20 MB of fp32 partial
  * sums of dHs (used for few tokens).  A workspace for M tokens also serves any
  * smaller number. */
 size_t coda_lmhead_policy_workspace_bytes(int64_t M, int64_t d, int64_t V, int with_grads);
