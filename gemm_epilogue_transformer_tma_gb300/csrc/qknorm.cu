@@ -17,7 +17,7 @@
 // kind (q, k or v) of one row: cos, sin and g are loaded once per chunk, and
 // neighbouring warps take the chunks of the same row, which find the table
 // row in L1.  Memory-bound: x (and dy) read once, one result written; forward
-// of 8192 rows of 48 heads of 128 (201 MB) 33 us, 6.1 TB/s.
+// of 8192 rows of 48 heads of 128 (201 MB) 32 us, 6.3 TB/s.
 #include <algorithm>
 
 #include "coda_internal.h"
@@ -27,11 +27,11 @@ namespace coda {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kBwdCtas = 2;        // CTAs of the backward per SM
-constexpr int kBwdHeads = 2;       // its heads per lane
-constexpr int kStages = 2;         // rows of a backward warp in flight
-constexpr int kMaxParts = 1024;  // CTAs of the backward, one pair of dg partials each
+constexpr int kWarps = 4;            // per CTA: with 8, 300 rows take 6.9 us instead of 5.2 in the backward
+constexpr int kFwdCtas = 8;            // CTAs of the forward per SM
+constexpr int kBwdCtas = 4;            // of the backward
+constexpr int kStages = 2;             // rows of a backward warp in flight
+constexpr int kMaxParts = 1024;        // CTAs of the backward, one pair of dg partials each
 
 struct HeadArgs {
   const __nv_bfloat16* x;   // qkv before the norm
@@ -117,7 +117,7 @@ __device__ __forceinline__ void load_angles(const HeadArgs& a, int64_t p, int l,
 }
 
 template <int G, int U>
-__global__ void __launch_bounds__(32 * kWarps, 4) qknorm_rope_kernel(const HeadArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, kFwdCtas) qknorm_rope_kernel(const HeadArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr int HW = 32 / G;  // heads side by side
@@ -193,12 +193,11 @@ constexpr int bwd_stage_bytes(int G, int U) { return 2 * (U * 32 * 16 * 2) + 2 *
 // CTAs, in a fixed order.  A chunk of x and of dy is one contiguous piece, so
 // each warp keeps kStages rows of them, with their rows of the tables, in
 // flight with bulk copies into its own shared-memory ring.  8192 rows of 48
-// heads of 128 (302 MB): 48 us, 6.3 TB/s, and 3 for dg_sums_kernel.  What it
+// heads of 128 (302 MB): 47 us, 6.4 TB/s, and 3 for dg_sums_kernel.  What it
 // took on the way there: plain loads into registers 70; bulk copies of x and dy
 // alone 61, with packed fp32 arithmetic (two values per instruction) 58; the
-// tables' rows copied too, the present form.  Two CTAs per SM: the 128
-// registers a thread needs leave no room for a third (84 with spills against
-// 58).
+// tables' rows copied too 49.  16 warps per SM: the 128 registers a thread
+// needs leave no room for more (84 with spills against 58).
 template <int G, int U>
 __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(const HeadArgs a) {
   griddep_wait();
@@ -210,6 +209,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(
   extern __shared__ __align__(128) uint8_t ring[];  // [warp][stage][x, dy]
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   __shared__ float red[kWarps][G * 2 * P];
+  __shared__ int kinds[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane & (G - 1), hg = lane / G;
   const bool active = 2 * P * l < a.D;
@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(
     bulk_load(dst + CHUNK, a.dy + m * width + head0, bytes, bar);
   };
   if (lane == 0) {
+    kinds[warp] = k.kind;
     for (int s = 0; s < kStages; ++s) mbar_init(&bars[warp][s], 1);
     fence_mbar_init();
     if (m0 < a.M) fetch(m0, pos0, 0);
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(
       }
     }
 #pragma unroll 1
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u * HW < k.heads; ++u) {
       const int h = u * HW + hg;
       const bool ok = active && h < k.heads;
       const uint8_t* p = px + h * a.D * 2;
@@ -379,11 +380,9 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(
   for (int i = threadIdx.x; i < 2 * a.D; i += 32 * kWarps) {
     const int kind = i >= a.D, col = i - kind * a.D;
     float t = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      const int c = static_cast<int>((blockIdx.x * static_cast<int64_t>(kWarps) + w) % a.chunks);
-      const int wk = c < a.chunks_q ? 0 : c < a.chunks_q + a.chunks_k ? 1 : 2;
-      if (wk == kind) t += red[w][col];
-    }
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      if (kinds[w] == kind) t += red[w][col];
     a.part[blockIdx.x * static_cast<int64_t>(2 * a.D) + i] = t;
   }
 }
@@ -486,9 +485,16 @@ cudaError_t launch_qknorm_rope(const LaunchCtx& c, const __nv_bfloat16* x, const
       if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
       return launch_chained(c, kern, dim3(static_cast<unsigned>(blocks)), dim3(32 * kWarps), 0, a);
     };
+    // Two heads per lane or one?  A chunk costs its heads per lane and as much
+    // again for the tables and the weights, so what counts is how well the
+    // heads fill the chunks (1777 rows of 12 heads of 80: one 3.9 us, two 4.7;
+    // 300 rows of 48 heads of 128: two 2.7, one 2.9); and no SM is left
+    // without warps.
+    set_chunks<1>(a, G, x != out);
+    const int one = a.chunks;
     set_chunks<2>(a, G, x != out);
-    // two heads per lane, unless that leaves SMs without a warp
-    if (M * a.chunks >= static_cast<int64_t>(c.num_sms) * kWarps) return go(qknorm_rope_kernel<GC, 2>);
+    if (2 * one >= 3 * a.chunks && M * a.chunks >= static_cast<int64_t>(c.num_sms) * 8)
+      return go(qknorm_rope_kernel<GC, 2>);
     set_chunks<1>(a, G, x != out);
     return go(qknorm_rope_kernel<GC, 1>);
   });
@@ -503,18 +509,37 @@ cudaError_t launch_qknorm_rope_bwd(const LaunchCtx& c, const __nv_bfloat16* dy, 
   const int G = lanes_per_head(D);
   return by_lanes(G, [&](auto g) {
     constexpr int GC = decltype(g)::value;
-    set_chunks<kBwdHeads>(a, G, dy != dx);
+    int64_t blocks = 0;
+    auto go = [&](auto heads) {
+      constexpr int U = decltype(heads)::value;
+      // one wave, rounded to whole rows of chunks
+      const int64_t want =
+          std::min<int64_t>({(M * a.chunks + kWarps - 1) / kWarps, int64_t(c.num_sms) * kBwdCtas, kMaxParts});
+      blocks = std::max<int64_t>(1, want / a.chunks) * a.chunks;
+      auto kern = qknorm_rope_bwd_kernel<GC, U>;
+      constexpr int smem = kWarps * kStages * bwd_stage_bytes(GC, U);
+      static bool smem_ok[64] = {};
+      const cudaError_t e = allow_smem(kern, smem, smem_ok);
+      if (e != cudaSuccess) return e;
+      return launch_chained(c, kern, dim3(static_cast<unsigned>(blocks)), dim3(32 * kWarps), smem, a);
+    };
+    // A warp's time goes with its rounds of rows, and a round's with the heads
+    // per lane and as much again for the wait and the table's row (1777 rows of
+    // 12 heads of 80: one head per lane 10.6 us, two 14.9; of 48 heads of 128:
+    // two 14.5, one 17.3).
+    auto rounds = [&] { return (M * a.chunks - 1) / (int64_t(c.num_sms) * kBwdCtas * kWarps) + 1; };
+    set_chunks<1>(a, G, dy != dx);
+    const int64_t one = 2 * rounds();
+    const bool fits = a.chunks <= kMaxParts;
+    set_chunks<2>(a, G, dy != dx);
     if (a.chunks > kMaxParts) return cudaErrorNotSupported;
-    // one wave, rounded to whole rows of chunks
-    const int64_t want =
-        std::min<int64_t>({(M * a.chunks + kWarps - 1) / kWarps, int64_t(c.num_sms) * kBwdCtas, kMaxParts});
-    int64_t blocks = std::max<int64_t>(1, want / a.chunks) * a.chunks;
-    auto kern = qknorm_rope_bwd_kernel<GC, kBwdHeads>;
-    constexpr int smem = kWarps * kStages * bwd_stage_bytes(GC, kBwdHeads);
-    static bool smem_ok[64] = {};
-    cudaError_t e = allow_smem(kern, smem, smem_ok);
-    if (e != cudaSuccess) return e;
-    e = launch_chained(c, kern, dim3(static_cast<unsigned>(blocks)), dim3(32 * kWarps), smem, a);
+    cudaError_t e;
+    if (fits && one < 3 * rounds()) {
+      set_chunks<1>(a, G, dy != dx);
+      e = go(std::integral_constant<int, 1>{});
+    } else {
+      e = go(std::integral_constant<int, 2>{});
+    }
     if (e != cudaSuccess) return e;
     return launch_chained(c, dg_sums_kernel, dim3(static_cast<unsigned>((n_kv > 0 ? 2 : 1) * D / 8)), dim3(1024), 0,
                           static_cast<const float*>(part), static_cast<int>(blocks), D, dgq, dgk);
