@@ -927,7 +927,9 @@ def coda_lmhead_ce_fp8(Hq, sH, Wq, sW, labels, loss, lse, argmax, dHs, dWt, ws, 
         _stream(stream)), "coda_lmhead_ce_fp8")
 
 
-def coda_lmhead_policy_workspace_bytes(M: int, d: int, V: int, with_grads: bool) -> int:
+def coda_lmhead_policy_workspace_bytes(M: int, d: int, V: int, with_grads: int) -> int:
+    """with_grads False or 0 without gradients, True or 1 with them, 2 with
+    them in the least memory (see include/coda.h)."""
     return load_library().coda_lmhead_policy_workspace_bytes(M, d, V, int(with_grads))
 
 

@@ -152,9 +152,12 @@ cudaError_t gemm_ce_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv
 
 // per (row, 128-column block) max / sum-exp of c.scale_host H Wt^T, and the
 // label's logit where the label lies in [0, V); the contraction summed in
-// pieces (gemm_logits.cuh)
+// pieces (gemm_logits.cuh).  kept: exp(logit - its block's max) in bf16 of the
+// first kept_cols columns (whole chunks, V or 0), vocabulary chunk c of `chunk`
+// columns [M][its columns] from kept + c * chunk * (M rounded up to 32)
 cudaError_t gemm_logit_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt,
-                             const int32_t* labels, float* pmax, float* psum, float* zy, int M, int d, int V, int T);
+                             const int32_t* labels, float* pmax, float* psum, float* zy, __nv_bfloat16* kept, int chunk,
+                             int kept_cols, int M, int d, int V, int T);
 
 // parts_buf [parts][M rounded up to 256][N] fp32 (+)= the K ranges of A B, A
 // [M][K], B [K][N] (gemm_splitk.cuh); parts <= the k-blocks of 64 in K
@@ -324,6 +327,11 @@ struct PolicyRows {
   float4* terms;
   int* status;
 };
+// dL of a vocabulary chunk in place of its kept exponentials [M][Vc], and
+// lost, as gemm_ce_grad; pmax [M][T]
+cudaError_t launch_policy_dl(const LaunchCtx& c, __nv_bfloat16* dL, const float* pmax, const int32_t* labels,
+                             const float* lse, const float* logp, const float* row_scale, float* lost, int64_t M,
+                             int64_t T, int64_t v0, int64_t Vc);
 // rows[m] = sum of lost[t] H[t] over the tokens t with m's label, for every m
 // that is the first token of a label in [v0, v0 + Vc) (slot[label] == m;
 // ~not_last[label] is its last)

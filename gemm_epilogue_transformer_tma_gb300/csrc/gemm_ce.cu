@@ -22,7 +22,8 @@ cudaError_t gemm_ce_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv
 }
 
 cudaError_t gemm_logit_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt,
-                             const int32_t* labels, float* pmax, float* psum, float* zy, int M, int d, int V, int T) {
+                             const int32_t* labels, float* pmax, float* psum, float* zy, __nv_bfloat16* kept, int chunk,
+                             int kept_cols, int M, int d, int V, int T) {
   using L = LogitsSmem;
   LogitsArgs g{};
   if (!make_operand_maps(&g.H, &g.W, H, false, Wt, false, M, V, d, 128)) return cudaErrorInvalidValue;
@@ -30,6 +31,15 @@ cudaError_t gemm_logit_stats(const LaunchCtx& c, const __nv_bfloat16* H, const _
   g.pmax = pmax;
   g.psum = psum;
   g.zy = zy;
+  g.kept_cols = kept_cols;
+  if (kept_cols > 0) {
+    g.chunk = chunk;
+    g.rows = (M + 31) / 32 * 32;
+    const int whole = kept_cols / chunk, rest = kept_cols - whole * chunk;
+    if ((whole > 0 && !make_tmap_store_bf16(&g.whole, kept, chunk, uint64_t(whole) * g.rows, chunk)) ||
+        (rest > 0 && !make_tmap_store_bf16(&g.rest, kept + int64_t(whole) * g.rows * chunk, rest, M, rest)))
+      return cudaErrorInvalidValue;
+  }
   g.M = M;
   g.V = V;
   g.T = T;

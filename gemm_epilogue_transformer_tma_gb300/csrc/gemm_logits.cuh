@@ -1,6 +1,9 @@
 // The LM head's blocked log-sum-exp statistics with the contraction summed in
 // pieces: per (row, 128-column vocabulary block) the maximum and the sum of
-// exp(L - max), and the label's logit, L = scale * H Wt^T.
+// exp(L - max), and the label's logit, L = scale * H Wt^T.  The exponentials of
+// the first `kept_cols` columns are kept too, in bf16, for the gradients:
+// vocabulary chunks of `chunk` columns one after the other, each [rows][its
+// columns].
 //
 // The tensor core drops the bits of a product that fall below the running
 // sum, so a logit loses about half a unit in the last place of that sum at
@@ -29,8 +32,10 @@ struct LogitsSmem {
   static constexpr int A_BYTES = 128 * BK * 2;
   static constexpr int STAGE_BYTES = 2 * A_BYTES;
   static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+  static constexpr int STORE_BYTES = EPI_WARPS * 2 * STORE_SLOT_BYTES;
   static constexpr int BAR_BYTES = 512;
-  static constexpr int TOTAL = RING_BYTES + BAR_BYTES + 1024;
+  static constexpr int TOTAL = RING_BYTES + STORE_BYTES + BAR_BYTES + 1024;
+  static_assert(TOTAL <= MAX_DYN_SMEM, "shared memory budget");
 };
 
 struct LogitsArgs {
@@ -39,6 +44,11 @@ struct LogitsArgs {
   float* pmax;            // [M][T], T = ceil(V / 128)
   float* psum;            // [M][T]
   float* zy;              // [M], written where the label is found
+  // the kept exponentials, 32 x 32 boxes: the whole chunks below each other
+  // (`chunk` columns wide, chunk c from row c * rows), and the last, narrower one
+  CUtensorMap whole, rest;
+  int kept_cols;          // whole chunks, or V
+  int chunk, rows;        // rows: M rounded up to 32
   int M, V, T;
   int tiles_m, tiles_n, num_kb, group_m;
   float scale;
@@ -53,7 +63,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::RING_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::RING_BYTES + L::STORE_BYTES);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;  // leader only
@@ -205,6 +215,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
     const int quad = warp & 3;
     const int half = (warp - 2) >> 2;
     const uint32_t leader_tempty = mapa_shared(smem_u32(tempty), 0);
+    const uint32_t slot = smem_u32(smem + L::RING_BYTES) + static_cast<uint32_t>((warp - 2) * 2 * STORE_SLOT_BYTES);
     const int pieces = (g.num_kb + kPieceKb - 1) / kPieceKb;
     int it = 0;
     bool ok = true;
@@ -239,9 +250,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
         if (lane == 0) mbar_arrive_cluster_relaxed(leader_tempty + static_cast<uint32_t>(acc * 8));
       }
       if (!ok) break;
-      const int m = (tm * 2 + static_cast<int>(rank)) * 128 + quad * 32 + lane;
+      const int m0 = (tm * 2 + static_cast<int>(rank)) * 128 + quad * 32;
+      const int m = m0 + lane;
       const int n0 = tn * BN + half * (BN / 2);
-      if (m >= g.M || n0 >= g.V) continue;
+      if (m0 >= g.M || n0 >= g.V) continue;
       const int nv = g.V - n0;  // columns of this half tile that exist
       float mx = -INFINITY;
 #pragma unroll
@@ -251,7 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
           v[c][i] = c * 32 + i < nv ? v[c][i] * g.scale : -INFINITY;
           mx = fmaxf(mx, v[c][i]);
         }
-      const int64_t y = static_cast<int64_t>(g.labels[m]) - n0;
+      const int64_t y = m < g.M ? static_cast<int64_t>(g.labels[m]) - n0 : -1;
       if (y >= 0 && y < BN / 2 && y < nv) {
         float z = 0.f;
 #pragma unroll
@@ -265,11 +277,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s4[i & 3] += __expf(v[c][i] - mx);
+        for (int i = 0; i < 32; ++i) s4[i & 3] += v[c][i] = __expf(v[c][i] - mx);
+      if (n0 < g.kept_cols) {
+        const int ch = n0 / g.chunk;
+        const bool whole = (ch + 1) * static_cast<int64_t>(g.chunk) <= g.kept_cols;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c * 32 >= nv) break;
+          const uint32_t at = slot + (c & 1) * STORE_SLOT_BYTES;
+          if (lane == 0) bulk_wait_group_read1();
+          __syncwarp();
+          stage_bf16x32(at, lane, v[c]);
+          slots_publish();
+          if (lane == 0) {
+            tma_store_2d(whole ? &g.whole : &g.rest, at, n0 - ch * g.chunk + c * 32, (whole ? ch * g.rows : 0) + m0);
+            bulk_commit_group();
+          }
+        }
+      }
+      if (m >= g.M) continue;
       const int64_t o = static_cast<int64_t>(m) * g.T + tn * 2 + half;
       g.pmax[o] = mx;
       g.psum[o] = (s4[0] + s4[1]) + (s4[2] + s4[3]);
     }
+    __syncwarp();
+    if (lane == 0) bulk_wait_group0();
+    __syncwarp();
   }
 
   __syncwarp();

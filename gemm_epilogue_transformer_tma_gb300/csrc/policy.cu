@@ -193,6 +193,42 @@ __global__ void __launch_bounds__(1024) policy_stats_kernel(const float4* __rest
   }
 }
 
+// dL of a vocabulary chunk in place of the exponentials e = exp(L - block max)
+// that the forward kept in bf16: row_scale (e exp(block max - lse) - onehot),
+// eight columns per thread, which lie in one block of 128.  Kept values are
+// rounded twice, once more than a second product would: 2^-9 of each p_v, whose
+// sum is below 1, beside the rounding of dL itself.  The label's entry, which
+// outweighs its row, comes from the fp32 log-probability.
+__global__ void __launch_bounds__(256) policy_dl_kernel(__nv_bfloat16* __restrict__ dL,
+                                                        const float* __restrict__ pmax,
+                                                        const int32_t* __restrict__ labels,
+                                                        const float* __restrict__ lse,
+                                                        const float* __restrict__ logp,
+                                                        const float* __restrict__ row_scale,
+                                                        float* __restrict__ lost, uint32_t n8, int64_t T, int64_t v0,
+                                                        uint32_t Vc) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= n8) return;
+  const uint32_t m = i * 8u / Vc, col = i * 8u - m * Vc;  // at most 2^29 values are kept
+  uint4* at = reinterpret_cast<uint4*>(dL) + i;
+  float v[8];
+  unpack_bf16x8(*at, v);
+  const float s = row_scale[m], f = __expf(pmax[int64_t(m) * T + ((v0 + col) >> 7)] - lse[m]) * s;
+  const int64_t y = labels[m] - v0 - col;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = s == 0.f ? 0.f : v[j] * f;
+    if (j == y) {
+      v[j] = s == 0.f ? 0.f : (__expf(logp[m]) - 1.f) * s;
+      lost[m] = v[j] - bf16_round(v[j]);
+    }
+  }
+  *at = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                   pack_bf16x2(v[6], v[7]));
+}
+
 constexpr int kLabelCols = 1024;  // per CTA of label_rows_kernel: four to a thread
 constexpr int kLabelTile = 1024;  // labels it looks at in one step: four to a thread
 
@@ -327,6 +363,14 @@ __global__ void policy_dh_kernel(const float4* __restrict__ parts, int num, int6
 }
 
 }  // namespace
+
+cudaError_t launch_policy_dl(const LaunchCtx& c, __nv_bfloat16* dL, const float* pmax, const int32_t* labels,
+                             const float* lse, const float* logp, const float* row_scale, float* lost, int64_t M,
+                             int64_t T, int64_t v0, int64_t Vc) {
+  const uint32_t n8 = static_cast<uint32_t>(M * Vc / 8);
+  return launch_chained(c, policy_dl_kernel, dim3((n8 + 255) / 256), dim3(256), 0, dL, pmax, labels, lse, logp,
+                        row_scale, lost, n8, T, v0, static_cast<uint32_t>(Vc));
+}
 
 cudaError_t launch_label_rows(const LaunchCtx& c, const int32_t* labels, const uint32_t* slot,
                               const uint32_t* not_last, const float* lost, const __nv_bfloat16* H, float* rows,

@@ -479,14 +479,17 @@ class QKVProjection:
 
 class PolicyHead:
     """The LM head of a policy update on up to M tokens: loss statistics,
-    log-probabilities and the gradients of the hidden states and of Wt."""
+    log-probabilities and the gradients of the hidden states and of Wt.
+    least_memory computes the logits a second time for the gradients instead of
+    keeping up to 1 GB of the forward's exponentials."""
 
     def __init__(self, Wt, M: int, clip=(0.2, 0.2), kl_coef: float = 0.0, temperature: float = 1.0,
-                 backward: bool = True):
+                 backward: bool = True, least_memory: bool = False):
         self.Wt, self.clip, self.kl_coef, self.temperature = Wt, clip, kl_coef, temperature
         V, d = Wt.shape
         e = dict(device=Wt.device)
-        self.ws = torch.empty(coda_lmhead_policy_workspace_bytes(M, d, V, backward), dtype=torch.uint8, **e)
+        form = 2 if backward and least_memory else int(backward)
+        self.ws = torch.empty(coda_lmhead_policy_workspace_bytes(M, d, V, form), dtype=torch.uint8, **e)
         self.stats, self.logp = torch.empty(4, **e), torch.empty(M, **e)
         self.dH = torch.empty(M, d, dtype=BF, **e) if backward else None
         self.dWt = torch.empty(V, d, dtype=BF, **e) if backward else None

@@ -756,12 +756,15 @@ coda_status_t coda_lmhead_ce_fp8(coda_handle_t h, const void* Hq, const float* s
 
 /* Workspace of coda_lmhead_policy: that of coda_lmhead_ce, 20 bytes per row,
  * and, with gradients, 4 (M d + 2 M + 2 V) bytes and up to 20 MB of fp32 partial
- * sums of dHs (used for few tokens).  A workspace for M tokens also serves any
- * smaller number. */
+ * sums of dHs (used for few tokens).  With with_grads = 1 it also has room for
+ * the forward's exponentials in bf16, up to 1 GB of them: the gradients of as
+ * many vocabulary chunks as that holds start from there, the others, and all of
+ * them in the least workspace (with_grads = 2), from logits computed a second
+ * time.  A workspace for M tokens also serves any smaller number. */
 size_t coda_lmhead_policy_workspace_bytes(int64_t M, int64_t d, int64_t V, int with_grads);
 
-/* Clipped policy loss with a KL term on the LM head, without ever writing an
- * [M][V] logits tensor.  With L = Hs Wt^T / temperature, per token m
+/* Clipped policy loss with a KL term on the LM head, without an [M][V] logits
+ * tensor in memory (see the workspace for what the gradients keep).  With L = Hs Wt^T / temperature, per token m
  *   lp = log softmax(L[m])[labels[m]]
  *   r  = exp(lp - logp_old[m]),  A = advantage[m],  w = weight[m]
  *   s  = min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)

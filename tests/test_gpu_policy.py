@@ -22,6 +22,8 @@ BF, F32 = torch.bfloat16, torch.float32
 
 
 class Problem:
+    least = False   # the gradients' least workspace: the logits computed twice
+
     def __init__(self, M, d, V, T=1.0, seed=0, weighted=True):
         rng = np.random.default_rng(seed)
         self.M, self.d, self.V, self.T = M, d, V, T
@@ -42,7 +44,8 @@ class Problem:
         self.stats, self.logp = gd.new((4,), F32), gd.new((self.M,), F32)
         self.dH = gd.like(self.H) if grads else None
         self.dW = gd.like(self.W) if grads else None
-        ws = gd.new((C.coda_lmhead_policy_workspace_bytes(self.M, self.d, self.V, grads),), torch.uint8)
+        form = 2 if grads and self.least else int(grads)
+        ws = gd.new((C.coda_lmhead_policy_workspace_bytes(self.M, self.d, self.V, form),), torch.uint8)
         self.args = (self.H, self.W, dev(self.y), dev(self.adv), dev(self.w), dev(self.old) if old else None,
                      dev(self.ref) if ref else None, lo, hi, beta, self.T, self.stats, self.logp, self.dH, self.dW, ws)
         C.coda_lmhead_policy(*self.args, stream=stream)
@@ -228,7 +231,9 @@ def test_refusals():
     assert call(lo=-0.1) == 1 and call(lo=1.1) == 1 and call(lo=nan) == 1 and call(hi=-0.1) == 1 and call(hi=nan) == 1
     assert call(beta=-1.0) == 1 and call(beta=nan) == 1 and call(beta=inf) == 1
     assert call(T=0.0) == 1 and call(T=inf) == 1 and call(T=nan) == 1
-    assert call(M=0) == 1 and call(V=0) == 1 and call(d=12) == 2 and call(adv=odd) == 2 and call(n=n - 1) == 4
+    least = C.coda_lmhead_policy_workspace_bytes(M, d, V, 2)
+    assert call(M=0) == 1 and call(V=0) == 1 and call(d=12) == 2 and call(adv=odd) == 2 and call(n=least - 1) == 4
+    assert C.coda_lmhead_policy_workspace_bytes(M, d, V, 3) == 0
     assert_device_ok()
 
 
@@ -267,3 +272,77 @@ def pb_args(pb):
     n = C.coda_lmhead_policy_workspace_bytes(pb.M, pb.d, pb.V, False)
     return (pb.H, pb.W, torch.from_numpy(pb.y).cuda(), e(pb.M), None, None, None, 0.2, 0.2, 0.0, pb.T, e(4), e(pb.M),
             None, None, torch.empty(n, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("M,d,V,T", [(1, 8, 8, 1.0), (136, 72, 1000, 1.3), (300, 128, 520, 1.0), (129, 256, 33000, 1.0),
+                                     (2600, 1024, 264, 1.0)])
+def test_least_workspace(M, d, V, T):
+    """The logits computed a second time: the same statistics, and gradients
+    within the same bounds."""
+    pb = Problem(M, d, V, T, seed=M)
+    pb.run()
+    a = (pb.stats.clone(), pb.logp.clone())
+    pb.least = True
+    need = [C.coda_lmhead_policy_workspace_bytes(M, d, V, k) for k in (0, 2, 1)]
+    assert need == sorted(need)
+    pb.grade(pb.run())
+    assert torch.equal(a[0], pb.stats) and torch.equal(a[1], pb.logp)
+    C.coda_set_lmhead_chunk(256)
+    try:
+        pb.grade(pb.run())
+    finally:
+        C.coda_set_lmhead_chunk(0)
+
+
+@pytest.mark.parametrize("pairing", [True, False], ids=["sm_pair", "single_sm"])
+def test_least_workspace_carries_one_rounding(pairing):
+    pb = Problem(60, 256, 1000, seed=11)
+    pb.least = True
+    pb.w[:] = 1.0 / 64
+    pb.adv = np.where(pb.adv > 0, 1.01, -1.01).astype(np.float32)
+    C.coda_set_sm_pairing(pairing)
+    try:
+        r = pb.run(old=False, ref=False)
+    finally:
+        C.coda_set_sm_pairing(True)
+    assert_device_ok()
+    _one_rounding(pb.dH, r["dH"], "dH")
+    _one_rounding(pb.dW, r["dWt"], "dWt")
+
+
+def test_confident_policy():
+    """Probabilities near one half on the label and on another token: the
+    entries beside the label's count as much as it, and are rounded twice when
+    they are kept (3 2^-8 with the result's rounding bounds each element's
+    terms; a third of it in the mean square)."""
+    pb = Problem(96, 64, 520, seed=8)
+    pb.W.zero_()
+    rows = torch.randn(520, 64, generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    pb.W.copy_(rows)
+    a, b = torch.from_numpy(pb.y.astype(np.int64)).cuda(), (torch.from_numpy(pb.y.astype(np.int64)).cuda() + 7) % 520
+    pb.H.copy_((rows[a].float() + rows[b].float()).to(BF) * 0.5)
+    for least in (False, True):
+        pb.least = least
+        r = pb.run(old=False, ref=False)
+        assert_device_ok()
+        assert_frob(pb.dH, r["dH"], "dH")
+        assert_frob(pb.dW, r["dWt"], "dWt")
+
+
+def test_narrow_kept_chunks():
+    """Whole chunks and a last one of 232 columns, tokens not a multiple of 32."""
+    pb = Problem(77, 64, 1000)
+    C.coda_set_lmhead_chunk(256)
+    try:
+        pb.grade(pb.run())
+    finally:
+        C.coda_set_lmhead_chunk(0)
+    dW = pb.dW.clone()
+    pb.grade(pb.run())
+    assert torch.equal(dW, pb.dW)
+    pb = Problem(64, 64, 512)
+    C.coda_set_lmhead_chunk(512)
+    try:
+        pb.grade(pb.run())
+    finally:
+        C.coda_set_lmhead_chunk(0)

@@ -104,10 +104,14 @@ def test_head_norm_and_backward():
     assert_device_ok()
 
 
-def test_policy_rows():
-    R, d, V, k = 600, 64, 33000, 115           # the chunk of dL holds 2.26e9 elements
+@pytest.mark.parametrize("k,form", [(30, 1), (115, 1), (115, 2)],
+                         ids=["one_narrow_chunk_kept", "narrow_chunks_kept", "computed_twice"])
+def test_policy_rows(k, form):
+    """115 repetitions: a chunk of dL holds 2.26e9 elements.  Kept are 29696
+    and 7680 of the columns."""
+    R, d, V = 600, 64, 33000
     M = R * k
-    assert M * min(V, 32768) > 2 ** 31
+    assert M * min(V, 32768) > 2 ** (31 if k == 115 else 29)
     pb = PolicyProblem(R, d, V, seed=6)
     r = pb.run()
     pb.grade(r)
@@ -118,7 +122,7 @@ def test_policy_rows():
         a[i] = a[i].repeat(k)
     logp, dH, dW, stats = (torch.empty(M, device="cuda"), torch.empty(M, d, dtype=BF, device="cuda"),
                            torch.empty_like(pb.W), torch.empty(4, device="cuda"))
-    a[11:16] = [stats, logp, dH, dW, _u8(C.coda_lmhead_policy_workspace_bytes(M, d, V, True))]
+    a[11:16] = [stats, logp, dH, dW, _u8(C.coda_lmhead_policy_workspace_bytes(M, d, V, form))]
     C.coda_lmhead_policy(*a)
     assert (logp.view(k, R) == small[1]).all()
     # the statistics: one fp32 rounding each of a sum carried in two words
