@@ -21,10 +21,25 @@ cudaError_t gemm_ce_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv
   return run_gemm<false, false, false, EpiCeStats>(c, ta, tb, tb, M, V, d, (V + kBN - 1) / kBN, ep);
 }
 
+template <bool KEEP>
+static cudaError_t launch_logits(const LaunchCtx& c, const LogitsArgs& g) {
+  using L = LogitsSmem;
+  auto kern = gemm_logits_kernel<KEEP>;
+  static bool smem_ok[64] = {};
+  cudaError_t e = allow_smem(kern, L::TOTAL, smem_ok);
+  if (e != cudaSuccess) return e;
+  static int cap[64] = {};
+  int pairs = 0;
+  e = pair_capacity(reinterpret_cast<const void*>(kern), L::THREADS, L::TOTAL, c.num_sms, cap, &pairs);
+  if (e != cudaSuccess) return e;
+  KernelCtl ctl{c.status, c.timeout_ns, c.skip_first_stage};
+  const int clusters = std::max(1, std::min(g.tiles_m * g.tiles_n, pairs));
+  return launch_chained(c, kern, dim3(2 * clusters), dim3(L::THREADS), L::TOTAL, g, ctl);
+}
+
 cudaError_t gemm_logit_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt,
                              const int32_t* labels, float* pmax, float* psum, float* zy, __nv_bfloat16* kept, int chunk,
                              int kept_cols, int M, int d, int V, int T) {
-  using L = LogitsSmem;
   LogitsArgs g{};
   if (!make_operand_maps(&g.H, &g.W, H, false, Wt, false, M, V, d, 128)) return cudaErrorInvalidValue;
   g.labels = labels;
@@ -48,16 +63,7 @@ cudaError_t gemm_logit_stats(const LaunchCtx& c, const __nv_bfloat16* H, const _
   g.num_kb = (d + BK - 1) / BK;
   g.group_m = 8;
   g.scale = c.scale_host;
-  static bool smem_ok[64] = {};
-  cudaError_t e = allow_smem(gemm_logits_kernel, L::TOTAL, smem_ok);
-  if (e != cudaSuccess) return e;
-  static int cap[64] = {};
-  int pairs = 0;
-  e = pair_capacity(reinterpret_cast<const void*>(gemm_logits_kernel), L::THREADS, L::TOTAL, c.num_sms, cap, &pairs);
-  if (e != cudaSuccess) return e;
-  KernelCtl ctl{c.status, c.timeout_ns, c.skip_first_stage};
-  const int clusters = std::max(1, std::min(g.tiles_m * g.tiles_n, pairs));
-  return launch_chained(c, gemm_logits_kernel, dim3(2 * clusters), dim3(L::THREADS), L::TOTAL, g, ctl);
+  return kept_cols > 0 ? launch_logits<true>(c, g) : launch_logits<false>(c, g);
 }
 
 cudaError_t gemm_splitk(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_bfloat16* B, float* parts_buf, int parts,

@@ -16,7 +16,10 @@
 // running sums start at zero, which divides the loss by the number of pieces.
 //
 // SM-pair schedule of gemm_tc2.cuh on 256 x 256 tiles; 8 epilogue warps, so
-// that a thread keeps one row's 128 sums of a half tile in registers.
+// that a thread keeps one row's 128 sums of a half tile in registers.  2048
+// tokens, V = 65536, d = 2048 under the profiler: 278 us, 92 % of the tensor
+// pipe; with all exponentials kept 317, 78 % (their way through shared memory;
+// stores from the registers, a row per lane, made a whole update 5 % slower).
 #pragma once
 
 #include "gemm_tc2.cuh"
@@ -54,6 +57,8 @@ struct LogitsArgs {
   float scale;
 };
 
+// KEEP: kept_cols > 0; scoring runs without the stores' code
+template <bool KEEP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS, 1)
     gemm_logits_kernel(const __grid_constant__ LogitsArgs g, const KernelCtl ctl) {
   using L = LogitsSmem;
@@ -277,8 +282,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s4[i & 3] += v[c][i] = __expf(v[c][i] - mx);
-      if (n0 < g.kept_cols) {
+        for (int i = 0; i < 32; ++i) {
+          const float e = __expf(v[c][i] - mx);
+          s4[i & 3] += e;
+          if (KEEP) v[c][i] = e;
+        }
+      if (KEEP && n0 < g.kept_cols) {
         const int ch = n0 / g.chunk;
         const bool whole = (ch + 1) * static_cast<int64_t>(g.chunk) <= g.kept_cols;
 #pragma unroll
@@ -300,9 +309,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
       g.pmax[o] = mx;
       g.psum[o] = (s4[0] + s4[1]) + (s4[2] + s4[3]);
     }
-    __syncwarp();
-    if (lane == 0) bulk_wait_group0();
-    __syncwarp();
+    if (KEEP) {
+      __syncwarp();
+      if (lane == 0) bulk_wait_group0();
+      __syncwarp();
+    }
   }
 
   __syncwarp();
