@@ -680,6 +680,8 @@ struct BlockFewSmem {
   static constexpr int TMEM_COLS = BN <= 32 ? 64 : BN == 64 ? 128 : 256;
 };
 
+constexpr int kFewAhead = 8;  // k-blocks of the weight fetched ahead
+
 struct BlockFewArgs {
   CUtensorMap W, X;    // codes: the weight's rows, the tokens
   CUtensorMap sW, sX;  // packed scales, rows of 512 bytes
@@ -735,6 +737,15 @@ __global__ void __launch_bounds__(BlockFewSmem<BN>::THREADS, BlockFewSmem<BN>::C
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   griddep_launch_dependents();
+  // while the kernel before this one runs (it quantises the tokens): the first
+  // of the weight into L2
+  if (warp == 0 && elect_one())
+    for (int kb = kb0; kb < min(kb1, kb0 + kFewAhead); ++kb) {
+      if (!W_MN)
+        tma_prefetch_2d(&g.W, kb * 128, n0);
+      else
+        tma_prefetch_2d(&g.W, n0, kb * 128);
+    }
   griddep_wait();
 
   if (warp == 0) {
