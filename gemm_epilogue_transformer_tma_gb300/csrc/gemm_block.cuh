@@ -103,6 +103,11 @@ struct BlockPairSmem {
   }
 };
 
+// k-blocks of B fetched into L2 while the kernel before this one, A's
+// quantiser, ends (512 tokens of 4096 x 6144 with their quantisation 18.5 to
+// 18.0 us; 32 k-blocks 19.2)
+constexpr int kPairAhead = 4;
+
 struct BlockGemmArgs {
   CUtensorMap A, B;    // codes
   CUtensorMap sA, sB;  // packed scales as rows of 512 bytes, one per chunk
@@ -172,6 +177,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BlockPairSmem::THREA
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   griddep_launch_dependents();
+  if (warp == 0 && cluster_id < num_tiles && elect_one()) {
+    int tm, tn;
+    tile_coords(cluster_id, sh, tm, tn);
+    for (int kb = 0; kb < min(g.num_kb, kPairAhead); ++kb) {
+      const int n0 = tn * BN + static_cast<int>(rank) * 128;
+      if (!B_MN)
+        tma_prefetch_2d(&g.B, kb * 128, n0);
+      else
+        tma_prefetch_2d(&g.B, n0, kb * 128);
+    }
+  }
   griddep_wait();
 
   if (warp == 0) {

@@ -27,6 +27,9 @@
 namespace coda {
 
 constexpr int kPieceKb = 8;  // k-blocks of 64 per piece
+// k-blocks of W fetched into L2 while the kernel before this one ends (136
+// tokens, V = 32000, d = 1024 22.9 to 22.4 us, 16 tokens at d = 4096 53.8 to 53.4)
+constexpr int kAheadKb = 8;
 
 struct LogitsSmem {
   static constexpr int STAGES = 6;
@@ -115,6 +118,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   griddep_launch_dependents();
+  if (warp == 0 && cluster_id < num_tiles && elect_one()) {
+    int tm, tn;
+    tile_coords(cluster_id, sh, tm, tn);
+    for (int kb = 0; kb < min(g.num_kb, kAheadKb); ++kb)
+      tma_prefetch_2d(&g.W, kb * BK, tn * BN + static_cast<int>(rank) * 128);
+  }
   griddep_wait();
 
   if (warp == 0) {
