@@ -782,8 +782,9 @@ size_t coda_lmhead_policy_workspace_bytes(int64_t M, int64_t d, int64_t V, int w
  * For a row with weight, a label outside [0, V) sets CODA_ERR_LABEL_RANGE in
  * the status word; the row then adds nothing, and its logp is 0.
  * If dHs is not NULL the gradients of loss are produced as coda_lmhead_ce
- * does: dHs = dL Wt, dWt = dL^T Hs, dL in bf16, but with the labels' entries,
- * which outweigh their rows, in fp32.
+ * does: dHs = dL Wt, dWt = dL^T Hs, dL in bf16 (an entry that starts from a
+ * kept exponential rounded twice), but with the labels' entries, which outweigh
+ * their rows, in fp32.
  * Hs bf16 [M][d], Wt bf16 [V][d], labels int32 [M], advantage, weight,
  * logp_old, logp_ref fp32 [M] (these, stats and logp 4-byte aligned), dHs bf16
  * [M][d] or NULL, dWt bf16 [V][d] (required iff dHs != NULL).  clip_low in
