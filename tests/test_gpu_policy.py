@@ -346,3 +346,27 @@ def test_narrow_kept_chunks():
         pb.grade(pb.run())
     finally:
         C.coda_set_lmhead_chunk(0)
+
+
+def test_a_head_takes_any_number_of_tokens_up_to_its_own():
+    from gemm_epilogue_transformer_tma_gb300.path import PolicyHead
+    pb = Problem(700, 128, 1000, T=0.9)
+    big = PolicyHead(pb.W, 700, clip=(0.2, 0.28), kl_coef=0.05, temperature=0.9)
+    least = PolicyHead(pb.W, 700, clip=(0.2, 0.28), kl_coef=0.05, temperature=0.9, least_memory=True)
+    assert least.ws.numel() < big.ws.numel()
+
+    def cut(a, m):
+        return torch.from_numpy(a[:m].copy()).cuda()
+
+    for m in (40, 700, 1, 333):
+        w = (pb.w[:m] * 700 / m).astype(np.float32)
+        args = (pb.H[:m].contiguous(), cut(pb.y, m), cut(pb.adv, m), cut(w, m), cut(pb.old, m), cut(pb.ref, m))
+        own = PolicyHead(pb.W, m, clip=(0.2, 0.28), kl_coef=0.05, temperature=0.9)
+        for u, v in zip(big.step(*args), own.step(*args)):
+            assert torch.equal(u, v)
+        ref = S.policy_loss(f64(args[0]), f64(pb.W), pb.y[:m], pb.adv[:m], w, pb.old[:m], pb.ref[:m], 0.2, 0.28, 0.05,
+                            0.9)
+        _, _, dH, dW = least.step(*args)
+        assert_frob(dH, ref["dH"], "dH")
+        assert_frob(dW, ref["dWt"], "dWt")
+    assert_device_ok()
