@@ -302,9 +302,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           if (c * 32 >= nv) break;
+          // a ragged last tile stores 1 or 3 blocks, so the tile after it starts
+          // in the slot of the last store: its first block waits for all of them
           const uint32_t at = slot + (c & 1) * STORE_SLOT_BYTES;
-          if (lane == 0) bulk_wait_group_read1();
-          __syncwarp();
+          slots_acquire_db(lane, c == 0);
           stage_bf16x32(at, lane, v[c]);
           slots_publish();
           if (lane == 0) {
