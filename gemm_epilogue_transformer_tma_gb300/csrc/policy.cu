@@ -62,12 +62,14 @@ __device__ __forceinline__ float4 policy_row(const float* __restrict__ pmax, con
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
   float g = 0.f;  // d loss / d lp
   if (in_range && w != 0.f) {
-    // exp overflows fp32 past 88, where the formula's products with 0 are still 0
+    // exp overflows fp32 past 88, where the formula's products with 0 are still
+    // 0.  A NaN ratio stays one: the minimum and maximum of the clip would drop
+    // it, so a NaN product counts as not clipped and goes into loss and gradient.
     const float A = p.adv[m];
-    const float r = p.old != nullptr ? expf(lp - p.old[m]) : 1.f;
-    const float ra = A != 0.f ? r * A : 0.f;
+    const float r = p.old != nullptr ? expf(lp - p.old[m]) : isnan(lp) ? lp : 1.f;
+    const float ra = A != 0.f || isnan(r) ? r * A : 0.f;
     const float ca = A != 0.f ? fminf(fmaxf(r, p.lo), p.hi) * A : 0.f;
-    const bool free = ra <= ca;
+    const bool free = !(ra > ca);
     float kl = 0.f, dkl = 0.f;
     if (p.ref != nullptr) {
       const float x = p.ref[m] - lp, em = expm1f(x);

@@ -770,10 +770,12 @@ size_t coda_lmhead_policy_workspace_bytes(int64_t M, int64_t d, int64_t V, int w
  *   s  = min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
  *   x  = logp_ref[m] - lp,       kl = exp(x) - x - 1
  *   loss = sum_m w (kl_coef kl - s)
- * logp_old NULL: r = 1, its gradient that of exp(lp - stop(lp)) (the first
+ * logp_old NULL: r = exp(lp - stop(lp)) = 1, with its gradient (the first
  * update on fresh samples).  logp_ref NULL: no KL term.  weight NULL: 1 / M.
  * The gradient flows through r where r A <= clip(r) A (inside the clip range
- * and on its border) and through kl everywhere.
+ * and on its border) and through kl everywhere.  A NaN ratio (logp_old, or the
+ * logits of a diverged model) or advantage of a row with weight is not clipped:
+ * it makes the loss, the row's dHs and dWt NaN.
  * stats fp32 [4] = {loss, sum -w s, sum w kl, sum of w where clipped}; logp
  * fp32 [M] = lp.  A row of weight 0 (prompt, padding) adds nothing to stats
  * and its dHs row is 0, whatever its advantage, logp_old and logp_ref hold;

@@ -1,5 +1,5 @@
 """The policy loss where its epilogues, row kernels and roundings meet their
-limits: ragged vocabularies behind many tiles."""
+limits: ragged vocabularies behind many tiles, NaN in weighted tokens."""
 import numpy as np
 import pytest
 import torch
@@ -32,3 +32,41 @@ def test_tiles_behind_a_ragged_vocabulary(V):
     want = (pb.dH.clone(), pb.dW.clone())
     pb.run(old=False, ref=False)
     assert torch.equal(want[0], pb.dH) and torch.equal(want[1], pb.dW)
+
+
+@pytest.mark.parametrize("M", [40, 700])
+@pytest.mark.parametrize("least", [False, True], ids=["kept", "least"])
+@pytest.mark.parametrize("what", ["old", "old_without_advantage", "advantage", "logits", "logits_without_old"])
+def test_a_nan_of_a_weighted_token_is_not_clipped(M, what, least):
+    """It reaches the loss, the token's row of dH and every row of dW (its row
+    of dL meets them all); the other tokens' dH keep their bits, and the KL
+    statistic is NaN only where the log-probability is."""
+    pb = Problem(M, 64, 264, seed=3)
+    pb.least = least
+    old = what != "logits_without_old"
+    pb.run(old=old)
+    clean = pb.dH.clone()
+    t = M // 2
+    if what == "advantage":
+        pb.adv[t] = np.nan
+    elif what.startswith("logits"):
+        pb.H[t] = float("nan")
+    else:
+        pb.old[t] = np.nan
+        pb.adv[t] = 0.0 if what == "old_without_advantage" else -0.7
+    pb.run(old=old)
+    assert torch.isnan(pb.stats[:2]).all()
+    assert torch.isnan(pb.logp[t]).item() == torch.isnan(pb.stats[2]).item() == what.startswith("logits")
+    assert torch.isfinite(pb.stats[3]).item()
+    assert torch.isnan(pb.dH[t]).all() and torch.isnan(pb.dW).all()
+    rest = torch.arange(M, device="cuda") != t
+    assert torch.equal(pb.dH[rest], clean[rest])
+    assert_device_ok()
+
+
+def test_the_open_clip_and_a_finite_ratio_are_as_before():
+    """r A on the border of the clip and an infinite upper bound pass the
+    gradient; a token outside does not."""
+    pb = Problem(30, 64, 264, seed=4)
+    for kw in (dict(lo=1.0, hi=float("inf")), dict(lo=0.0, hi=0.0), dict(lo=0.2, hi=0.28, old=False)):
+        pb.grade(pb.run(**kw))
