@@ -768,12 +768,10 @@ __global__ void __launch_bounds__(BlockFewSmem<BN>::THREADS, BlockFewSmem<BN>::C
     // the whole warp, converged (elect_one)
     int stage = 0;
     uint32_t phase = 0, pending = 0, parity = 0;
-    bool ok = true;
     bool skip = ctl.skip_first_stage != 0 && blockIdx.x == 0 && blockIdx.y == 0;
     for (int kb = kb0; kb < kb1; ++kb) {
-      ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, ctl.timeout_ns);
+      const bool ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, ctl.timeout_ns);
       if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
         if (lane == 0 && !*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_PRODUCER);
         break;
       }
@@ -804,12 +802,20 @@ __global__ void __launch_bounds__(BlockFewSmem<BN>::THREADS, BlockFewSmem<BN>::C
         phase ^= 1u;
       }
     }
-    if (!ok && lane == 0) {
-      // let every copy this warp started land before shared memory is released
+    if (lane == 0) {
+      // every copy this warp started has landed before shared memory is
+      // released, also when the loop ended well: with no more k-blocks than
+      // stages it never waits, and the MMA warp may have given up on a fill
+      bool landed = true;
       for (int st = 0; st < STAGES; ++st)
-        if ((pending >> st) & 1u)
-          if (!mbar_wait_timeout(&full[st], (parity >> st) & 1u, ctl.timeout_ns))
-            atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
+        if ((pending >> st) & 1u) landed = mbar_wait_timeout(&full[st], (parity >> st) & 1u, ctl.timeout_ns) && landed;
+      if (!landed) {
+        atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
+        // far longer than any copy's latency, as in gemm_tc2_kernel
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+      }
     }
   } else if (warp == 1) {
     const uint32_t idesc = IDESC0 | g.f8_fmt;
