@@ -274,10 +274,23 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) qknorm_rope_bwd_kernel(
       pos3 = position(m + 3 * m_step);
     else if (pos3 >= a.S)
       pos3 -= a.S;
-    // the copies are this warp's own: they land, or the device has failed
     const bool landed = mbar_wait_timeout(&bars[warp][s], phase, a.timeout_ns);
     if (!__all_sync(0xffffffffu, landed)) {
-      if (lane == 0) atomicOr(a.status, DEV_ERR_TIMEOUT_PRODUCER);
+      if (lane == 0) {
+        atomicOr(a.status, DEV_ERR_TIMEOUT_PRODUCER);
+        // both stages' copies have landed before shared memory is released:
+        // this one's, and the next row's, whose phase is the other one if its
+        // stage comes round to 0
+        bool drained = mbar_wait_timeout(&bars[warp][s], phase, a.timeout_ns);
+        if (m + m_step < a.M) drained = mbar_wait_timeout(&bars[warp][s ^ 1], phase ^ (s == 1), a.timeout_ns) && drained;
+        if (!drained) {
+          atomicOr(a.status, DEV_ERR_TIMEOUT_DRAIN);
+          // far longer than any copy's latency, as in gemm_tc2_kernel
+          const uint64_t t0 = globaltimer_ns();
+          while (globaltimer_ns() - t0 < 2000000ull) {
+          }
+        }
+      }
       break;
     }
     const uint8_t* px = mine + s * STAGE + 2 * P * l;

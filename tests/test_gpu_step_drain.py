@@ -30,3 +30,35 @@ def test_no_more_k_blocks_than_stages(M, N, K):
         _expire(lambda: lin.forward(x), 1)
         assert torch.equal(lin.forward(x), want)
         assert_device_ok()
+
+
+@pytest.mark.parametrize("M,nq,nk,D", [(5000, 32, 8, 128), (777, 6, 3, 80), (3, 2, 1, 64)])
+def test_head_norm_backward_with_the_least_wait_limit(M, nq, nk, D):
+    """A limit of 1 ns: every wait either meets its copies or reports that it
+    gave up, and the call after has its usual bits."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    width = (nq + 2 * nk) * D
+    qkv, dout = (torch.randn(M, width, device="cuda", generator=g).to(BF) for _ in range(2))
+    gain = torch.ones(D, dtype=BF, device="cuda")
+    cos, sin = torch.empty(1000, D // 2, device="cuda"), torch.empty(1000, D // 2, device="cuda")
+    C.coda_rope_table(cos, sin)
+    ws = torch.empty(C.coda_qknorm_rope_bwd_workspace_bytes(M, D), dtype=torch.uint8, device="cuda")
+    out = [torch.empty_like(qkv), torch.empty(D, device="cuda"), torch.empty(D, device="cuda")]
+
+    def call():
+        C.coda_qknorm_rope_bwd(dout, qkv, gain, gain, cos, sin, *out, ws, nq, nk, D)
+        return [t.clone() for t in out]
+
+    want = call()
+    assert_device_ok()
+    C.coda_set_wait_timeout_ns(1)
+    try:
+        for _ in range(10):
+            got = call()
+            st, bits = C.coda_sync_status()
+            assert st in (0, 6), bits
+            assert st == 6 or all(torch.equal(a, b) for a, b in zip(got, want))
+    finally:
+        C.coda_set_wait_timeout_ns(0)
+    assert all(torch.equal(a, b) for a, b in zip(call(), want))
+    assert_device_ok()
