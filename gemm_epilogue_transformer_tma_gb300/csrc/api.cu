@@ -1368,8 +1368,8 @@ coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt
     if (kept)
       CODA_CUDA(launch_policy_dl(cx, dL, w.ce.pmax, labels, w.lse, logp, w.row_scale, w.lost, M, T, v0, Vc));
     else
-      CODA_CUDA(gemm_ce_grad(cl, Hb, Wc, labels, w.lse, dL, int(M), int(d), int(Vc), int(v0), 0.f, w.row_scale,
-                             w.lost));
+      CODA_CUDA(gemm_policy_grad(cl, Hb, Wc, labels, w.lse, dL, int(M), int(d), int(Vc), int(v0), w.row_scale,
+                                 w.lost));
     CODA_CUDA(launch_label_rows(cx, labels, w.slot, w.slot + V, w.lost, Hb, w.label_rows, M, d, v0, Vc));
     if (parts == 1) {
       CODA_CUDA(gemm_group_policy_bwd(cx, dL, Wc, Hb, w.ce.dH32, v0 > 0, dWc, w.slot + v0, w.label_rows, int(M),

@@ -164,13 +164,15 @@ cudaError_t gemm_logit_stats(const LaunchCtx& c, const __nv_bfloat16* H, const _
 cudaError_t gemm_splitk(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_bfloat16* B, float* parts_buf, int parts,
                         bool accumulate, int M, int N, int K);
 
-// dL chunk = (softmax - onehot) / M for vocabulary rows [v0, v0 + Vc), or
-// row_scale[m] (softmax - onehot) with row_scale != null.  The logits are
-// c.scale_host H Wt^T, as in gemm_ce_stats.  With lost != null, lost[m] = what
-// the bf16 rounding takes from the entry of a label in the chunk.
+// dL chunk = (softmax - onehot) / M for vocabulary rows [v0, v0 + Vc).
 cudaError_t gemm_ce_grad(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt_chunk,
                          const int32_t* labels, const float* lse, __nv_bfloat16* dL, int M, int d, int Vc, int v0,
-                         float inv_M, const float* row_scale = nullptr, float* lost = nullptr);
+                         float inv_M);
+// The same as row_scale[m] (softmax - onehot) of the logits c.scale_host H Wt^T;
+// lost[m] = what the bf16 rounding takes from the entry of a label in the chunk.
+cudaError_t gemm_policy_grad(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt_chunk,
+                             const int32_t* labels, const float* lse, __nv_bfloat16* dL, int M, int d, int Vc, int v0,
+                             const float* row_scale, float* lost);
 
 // qkv = X Wqkv with RoPE (head_dim 128) on the first rot_cols columns.
 cudaError_t gemm_qkv_rope(const LaunchCtx& c, const __nv_bfloat16* X, const __nv_bfloat16* Wqkv_t,
@@ -328,7 +330,7 @@ struct PolicyRows {
   int* status;
 };
 // dL of a vocabulary chunk in place of its kept exponentials [M][Vc], and
-// lost, as gemm_ce_grad; pmax [M][T]
+// lost, as gemm_policy_grad; pmax [M][T]
 cudaError_t launch_policy_dl(const LaunchCtx& c, __nv_bfloat16* dL, const float* pmax, const int32_t* labels,
                              const float* lse, const float* logp, const float* row_scale, float* lost, int64_t M,
                              int64_t T, int64_t v0, int64_t Vc);

@@ -114,20 +114,36 @@ cudaError_t gemm_store_plus_rows(const LaunchCtx& c, const __nv_bfloat16* dL, co
   return launch_chained(c, gemm_dw_kernel, dim3(2 * clusters), dim3(L::THREADS), L::TOTAL, g, ctl);
 }
 
-cudaError_t gemm_ce_grad(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt_chunk,
-                         const int32_t* labels, const float* lse, __nv_bfloat16* dL, int M, int d, int Vc, int v0,
-                         float inv_M, const float* row_scale, float* lost) {
+// dL of a chunk by either epilogue: ep holds what is its own
+template <class Epi>
+static cudaError_t softmax_grad(const LaunchCtx& c, typename Epi::Params& ep, const __nv_bfloat16* H,
+                                const __nv_bfloat16* Wt_chunk, const int32_t* labels, const float* lse,
+                                __nv_bfloat16* dL, int M, int d, int Vc, int v0) {
   CUtensorMap ta, tb;
-  if (!make_operand_maps(&ta, &tb, H, false, Wt_chunk, false, M, Vc, d, b_box_rows(c))) return cudaErrorInvalidValue;
-  EpiCeGrad::Params ep{};
-  if (!make_tmap_store_bf16(&ep.dL, dL, Vc, M, Vc)) return cudaErrorInvalidValue;
+  if (!make_operand_maps(&ta, &tb, H, false, Wt_chunk, false, M, Vc, d, b_box_rows(c)) ||
+      !make_tmap_store_bf16(&ep.dL, dL, Vc, M, Vc))
+    return cudaErrorInvalidValue;
   ep.labels = labels;
   ep.lse = lse;
-  ep.inv_M = inv_M;
   ep.v0 = v0;
+  return run_gemm<false, false, false, Epi>(c, ta, tb, tb, M, Vc, d, (Vc + kBN - 1) / kBN, ep);
+}
+
+cudaError_t gemm_ce_grad(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt_chunk,
+                         const int32_t* labels, const float* lse, __nv_bfloat16* dL, int M, int d, int Vc, int v0,
+                         float inv_M) {
+  EpiCeGrad::Params ep{};
+  ep.inv_M = inv_M;
+  return softmax_grad<EpiCeGrad>(c, ep, H, Wt_chunk, labels, lse, dL, M, d, Vc, v0);
+}
+
+cudaError_t gemm_policy_grad(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt_chunk,
+                             const int32_t* labels, const float* lse, __nv_bfloat16* dL, int M, int d, int Vc, int v0,
+                             const float* row_scale, float* lost) {
+  EpiPolicyGrad::Params ep{};
   ep.row_scale = row_scale;
   ep.lost = lost;
-  return run_gemm<false, false, false, EpiCeGrad>(c, ta, tb, tb, M, Vc, d, (Vc + kBN - 1) / kBN, ep);
+  return softmax_grad<EpiPolicyGrad>(c, ep, H, Wt_chunk, labels, lse, dL, M, d, Vc, v0);
 }
 
 }  // namespace coda

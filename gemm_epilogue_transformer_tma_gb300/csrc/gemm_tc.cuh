@@ -1139,13 +1139,16 @@ struct EpiCeStats {
   }
 };
 
-// LM-head backward epilogue: dL = s (exp(L - lse[m]) - [n == y_m]), s = 1 / M
-// (the mean cross-entropy) or a factor per row (row_scale: a weighted loss of
-// the label's log-probability; 0 gives an exact 0), into a vocabulary-chunk
-// buffer (column n of the chunk = vocabulary v0 + n), as bf16
-// or, with FP8 operands, as e5m2 codes of dL * code_inv (|dL| <= 1/M, so a
-// power-of-two scale fixed in advance never saturates).
-struct EpiCeGrad {
+// LM-head backward epilogue: dL = s (exp(L - lse[m]) - [n == y_m]) into a
+// vocabulary-chunk buffer (column n of the chunk = vocabulary v0 + n).  s = 1 / M
+// for the mean cross-entropy, as bf16 or, with FP8 operands, as e5m2 codes of
+// dL * code_inv (|dL| <= 1/M, so a power-of-two scale fixed in advance never
+// saturates).  PER_ROW: a factor per row (a weighted loss of the label's
+// log-probability; 0 gives an exact 0), as bf16, and what the label's entry
+// loses to bf16; a form of its own, so that the cross-entropy's keeps its
+// registers (82 in the SM-pair kernel, 96 with both in one).
+template <bool PER_ROW>
+struct EpiSoftmaxGrad {
   static constexpr int kEpiWarps = 4;
   static constexpr int kStoreSlots = 1;
   static constexpr bool kAccScale = true;  // multiplies by EpiCtx::acc_scale: usable on FP8 operands
@@ -1153,20 +1156,22 @@ struct EpiCeGrad {
     CUtensorMap dL;  // [M][Vc] bf16, or e5m2 codes when codes != 0
     const int32_t* labels;
     const float* lse;
-    float inv_M;
     int v0;
+    // the mean cross-entropy
+    float inv_M;
     int codes;
     float code_inv;  // the inverse of the codes' power-of-two scale
-    const float* row_scale;  // [M], or null: inv_M for every row
-    float* lost;             // [M], or null: what the label's entry loses to bf16 (written by the chunk
-                             // that holds the label)
+    // PER_ROW
+    const float* row_scale;  // [M]
+    float* lost;             // [M], written by the chunk that holds the label
   };
   template <int BN>
   static __device__ __forceinline__ void run(const Params& p, const EpiCtx& c) {
     const bool row_ok = c.m < c.M;
     const float l = row_ok ? p.lse[c.m] : 0.f;
     const int y = row_ok ? p.labels[c.m] - p.v0 : -1;
-    const float s = p.row_scale == nullptr ? p.inv_M : row_ok ? p.row_scale[c.m] : 0.f;
+    float s = 0.f;
+    if constexpr (PER_ROW) s = row_ok ? p.row_scale[c.m] : 0.f;
 #pragma unroll 1
     for (int cc = c.c0; cc < c.c1; cc += 32) {
       float v[32];
@@ -1176,15 +1181,20 @@ struct EpiCeGrad {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const float e = __expf(v[i] * c.acc_scale - l) - ((n0 + i == y) ? 1.f : 0.f);
-          v[i] = s == 0.f ? 0.f : e * s;
+          if constexpr (PER_ROW)
+            v[i] = s == 0.f ? 0.f : e * s;
+          else
+            v[i] = e * p.inv_M;
         }
-        if (p.lost != nullptr && y >= n0 && y < n0 + 32) {
+        if constexpr (PER_ROW) {
+          if (y >= n0 && y < n0 + 32) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (n0 + i == y) p.lost[c.m] = v[i] - bf16_round(v[i]);
+            for (int i = 0; i < 32; ++i)
+              if (n0 + i == y) p.lost[c.m] = v[i] - bf16_round(v[i]);
+          }
         }
         slots_acquire(c.lane);
-        if (p.codes)
+        if (!PER_ROW && p.codes)
           stage_e5m2x32(slot_addr(c, 0), c.lane, v, p.code_inv);
         else
           stage_bf16x32(slot_addr(c, 0), c.lane, v);
@@ -1197,5 +1207,7 @@ struct EpiCeGrad {
     }
   }
 };
+using EpiCeGrad = EpiSoftmaxGrad<false>;
+using EpiPolicyGrad = EpiSoftmaxGrad<true>;
 
 }  // namespace coda
