@@ -37,14 +37,19 @@ def sources():
 
 def _deps():
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h")) + [MARSHAL_SRC, __file__]
+        glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
+
+
+def _newer(target, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _newer(LIB, _deps()) and _newer(MARSHAL, _marshal_deps())
+
+
+def _marshal_deps():
+    return glob.glob(os.path.join(INCLUDE, "*.h")) + [MARSHAL_SRC, __file__]
 
 
 def _build_marshal() -> None:
@@ -66,9 +71,8 @@ def _build_marshal() -> None:
     os.replace(tmp, MARSHAL)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
+def _build_lib(verbose: bool) -> None:
+    """libcoda.so: every translation unit, in parallel, then the link."""
     nvcc = _nvcc()
     os.makedirs(OBJ, exist_ok=True)
     srcs = sources()
@@ -83,16 +87,28 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        marshal = ex.submit(_build_marshal)
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
         objs = list(ex.map(compile_one, srcs))
-        marshal.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Both libraries, side by side; each is made whether or not the other can
+    be: libcoda.so takes nvcc alone, _marshal.so torch's headers and a host
+    compiler."""
+    with cf.ThreadPoolExecutor(max_workers=2) as ex:
+        made = []
+        if force or not _newer(LIB, _deps()):
+            made.append(ex.submit(_build_lib, verbose))
+        if force or not _newer(MARSHAL, _marshal_deps()):
+            made.append(ex.submit(_build_marshal))
+    for m in made:
+        m.result()
     return LIB
 
 
