@@ -1207,7 +1207,7 @@ struct EpiSoftmaxGrad {
     }
   }
 };
-using EpiCeGrad = EpiSoftmaxGrad<false>;
-using EpiPolicyGrad = EpiSoftmaxGrad<true>;
+struct EpiCeGrad : EpiSoftmaxGrad<false> {};  // types of their own: kernels are named after them
+struct EpiPolicyGrad : EpiSoftmaxGrad<true> {};
 
 }  // namespace coda
