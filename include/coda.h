@@ -786,7 +786,11 @@ size_t coda_lmhead_policy_workspace_bytes(int64_t M, int64_t d, int64_t V, int w
  * If dHs is not NULL the gradients of loss are produced as coda_lmhead_ce
  * does: dHs = dL Wt, dWt = dL^T Hs, dL in bf16 (an entry that starts from a
  * kept exponential rounded twice), but with the labels' entries, which outweigh
- * their rows, in fp32.
+ * their rows, in fp32.  Against fp64 their error is that of rounding the results
+ * to bf16 where the softmax is flat, and grows with the probability beside the
+ * labels: 1.1 times it at a mean label probability of 0.4, 1.13 to 1.17 at 0.6,
+ * and at most 1.25 where the label and one other token have a half each.  The
+ * least workspace rounds an entry once; the difference is below 0.02.
  * Hs bf16 [M][d], Wt bf16 [V][d], labels int32 [M], advantage, weight,
  * logp_old, logp_ref fp32 [M] (these, stats and logp 4-byte aligned), dHs bf16
  * [M][d] or NULL, dWt bf16 [V][d] (required iff dHs != NULL).  clip_low in

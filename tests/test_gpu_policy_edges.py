@@ -1,5 +1,6 @@
 """The policy loss where its epilogues, row kernels and roundings meet their
-limits: ragged vocabularies behind many tiles, NaN in weighted tokens."""
+limits: ragged vocabularies behind many tiles, NaN in weighted tokens, and the
+roundings of confident policies."""
 import numpy as np
 import pytest
 import torch
@@ -70,3 +71,58 @@ def test_the_open_clip_and_a_finite_ratio_are_as_before():
     pb = Problem(30, 64, 264, seed=4)
     for kw in (dict(lo=1.0, hi=float("inf")), dict(lo=0.0, hi=0.0), dict(lo=0.2, hi=0.28, old=False)):
         pb.grade(pb.run(**kw))
+
+
+def _of_one_rounding(pb, r):
+    """dH's and dW's errors over that of the fp64 results rounded to bf16."""
+    out = []
+    for got, ref in ((pb.dH, r["dH"]), (pb.dW, r["dWt"])):
+        ref = torch.from_numpy(ref)
+        out.append(((got.cpu().double() - ref).norm() / (ref.to(got.dtype).double() - ref).norm()).item())
+    return out
+
+
+# dL's entries beside the label's are rounded to bf16 and the label's is not.
+# Rounding to nearest costs the same share of every value, so with `share` of
+# dL's square beside the label the error is sqrt(1 + share) of that of rounding
+# the results alone.  sum p_v = 1 - p_y over the others, hence sum p_v^2 <=
+# (1 - p_y)^2, the label's square: share <= 1/2.  Kept exponentials round those
+# that are not their block's largest once more, half of the share where two
+# tokens lead: sqrt(1 + 1/2 + 1/4) = 1.32, and 2 % for fp32 sums and for W rows
+# that are not orthogonal.  On a flat softmax the label is all of dL.
+ONE_ROUNDING = {0.9: 1.02, 5.0: 1.35, 8.0: 1.35}
+
+
+@pytest.mark.parametrize("spread", sorted(ONE_ROUNDING))
+@pytest.mark.parametrize("least", [False, True], ids=["kept", "least"])
+@pytest.mark.parametrize("M", [200, 2600])
+def test_rounding_of_the_gradients_by_confidence(M, least, spread):
+    """Labels drawn from the softmax of logits with this spread: a flat
+    policy, and mean label probabilities of 0.4 and 0.6."""
+    pb = Problem(M, 128, 1000, seed=int(spread))
+    g = torch.Generator().manual_seed(M)
+    pb.W.copy_((torch.randn(1000, 128, generator=g) * spread / 128 ** 0.5).to(pb.W.dtype))
+    L = f64(pb.H) @ f64(pb.W).T
+    p = np.exp(L - L.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    u = np.random.default_rng(M).random((M, 1))
+    pb.y = np.minimum((p.cumsum(1) < u).sum(1), 999).astype(np.int32)
+    pb.least = least
+    r = pb.run(old=False, ref=False)
+    assert_device_ok()
+    assert max(_of_one_rounding(pb, r)) <= ONE_ROUNDING[spread]
+
+
+@pytest.mark.parametrize("least", [False, True], ids=["kept", "least"])
+def test_two_tokens_of_one_half(least):
+    """The label and one other token share the probability: the largest share
+    beside the label that there is."""
+    pb = Problem(96, 64, 520, seed=8)
+    rows = torch.randn(520, 64, generator=torch.Generator().manual_seed(1)).to(pb.W.dtype).cuda()
+    pb.W.copy_(rows)
+    a = torch.from_numpy(pb.y.astype(np.int64)).cuda()
+    pb.H.copy_((rows[a].float() + rows[(a + 7) % 520].float()).to(pb.H.dtype) * 0.5)
+    pb.least = least
+    r = pb.run(old=False, ref=False)
+    assert_device_ok()
+    assert max(_of_one_rounding(pb, r)) <= 1.35
