@@ -1228,7 +1228,8 @@ struct PolicyWs {
 // K ranges of the data gradient dH = dL W over a vocabulary chunk of Vc: its
 // 256 x 256 output tiles are spread over kDhUnits SM pairs by cutting K, each
 // range at least 16 k-blocks (1024 of K); 1 leaves it to the grouped launch,
-// which runs the weight gradient's tiles beside it.
+// which runs the weight gradient's tiles beside it.  The pairs of a GB300's 152
+// SMs, as a constant: a workspace is sized without a device.
 constexpr int64_t kDhUnits = 76;
 int64_t dh_parts(int64_t M, int64_t d, int64_t Vc) {
   const int64_t tiles = cdiv(M, 256) * cdiv(d, 256);

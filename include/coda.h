@@ -100,7 +100,11 @@ coda_status_t coda_set_wait_timeout_ns(coda_handle_t h, uint64_t ns);
  * default): each 256 x 256 output tile is computed by a pair of SMs with the
  * 2-SM tcgen05 MMA, each SM loading half of the operands; enable = 0: one SM
  * per 128 x 256 tile.  Results are identical up to fp32 summation order
- * inside the tensor core; the choice only affects speed. */
+ * inside the tensor core; the choice only affects speed.
+ * Not affected, because they have one form: coda_gemm_fp8_block (its form
+ * follows from the sizes) and, in coda_lmhead_policy, the logits, dWt, and dHs
+ * where it is summed in ranges of the vocabulary (few tokens); its logits of
+ * the least workspace and dHs of many tokens follow the switch. */
 coda_status_t coda_set_sm_pairing(coda_handle_t h, int enable);
 
 /* Wide tiles for the long-K GEMMs of the backward (the RMSNorm-backward
@@ -123,8 +127,9 @@ coda_status_t coda_set_wide_tiles(coda_handle_t h, int lead_kblocks);
  * rows are computed from it.  Narrower chunks shrink the dL buffer that
  * passes between the two launches, at the price of more and smaller launches
  * (measured slower at every width below the default).  cols: a multiple of 256 in [256, 32768]; 0
- * restores the default, 32768.  The workspace size does not depend on it.  Results equal across widths up to fp32 summation order
- * of dH.  Returns CODA_ERR_INVALID_ARG otherwise. */
+ * restores the default, 32768.  The workspace size does not depend on it.
+ * Results equal across widths up to fp32 summation order of dH.  It is also the
+ * chunk width of coda_lmhead_policy's gradients.  Returns CODA_ERR_INVALID_ARG otherwise. */
 coda_status_t coda_set_lmhead_chunk(coda_handle_t h, int64_t cols);
 
 /* Scratch that lets this handle's SM-pair GEMMs keep every SM pair busy in
