@@ -249,9 +249,11 @@ constexpr int kLabelTile = 1024;  // labels it looks at in one step: four to a t
 // finds the label's other tokens by a scan of the labels up to its last one,
 // and adds 1024 columns c of their rows in token order, eight rows in flight.
 // Tokens without weight have lost nothing and are passed over (padding may
-// repeat one label thousands of times).  A whole update of 8192 tokens, d = 2048, V =
-// 32000: labels all different or random 2.4 ms, half of them padding 2.4 (3.9
+// repeat one label thousands of times).  A whole update of 8192 tokens, d = 2048,
+// V = 32000: labels all different or random 2.4 ms, half of them padding 2.4 (3.9
 // with the padding's rows added in), all the same 3.4 (5.6 one row at a time).
+// Where labels repeat far apart the searches grow with M^2: 65536 tokens, d =
+// 1024, V = 32000 11.9 ms, 11.0 with equal labels side by side (least workspace).
 __global__ void __launch_bounds__(256) label_rows_kernel(const int32_t* __restrict__ labels,
                                                          const uint32_t* __restrict__ slot,
                                                          const uint32_t* __restrict__ not_last,
