@@ -312,12 +312,18 @@ __global__ void __launch_bounds__(gemm_threads<Epi>(), 1)
           }
         }
       }
-      if (!ok) {
-        // let every copy this thread started land before shared memory is released
-        for (int st = 0; st < STAGES; ++st)
-          if ((pending >> st) & 1u)
-            if (!mbar_wait_timeout(&full[st], (parity >> st) & 1u, ctl.timeout_ns))
-              atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
+      // every copy this thread started has landed before shared memory is
+      // released, also when the loop ended well: with no more k-blocks than
+      // stages it never waits, and the MMA warp may have given up on a fill
+      bool landed = true;
+      for (int st = 0; st < STAGES; ++st)
+        if ((pending >> st) & 1u) landed = mbar_wait_timeout(&full[st], (parity >> st) & 1u, ctl.timeout_ns) && landed;
+      if (!landed) {
+        atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
+        // far longer than any copy's latency, as in gemm_tc2_kernel
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
       }
     }
   } else if (warp == 1) {

@@ -62,3 +62,26 @@ def test_head_norm_backward_with_the_least_wait_limit(M, nq, nk, D):
         C.coda_set_wait_timeout_ns(0)
     assert all(torch.equal(a, b) for a, b in zip(call(), want))
     assert_device_ok()
+
+
+@pytest.mark.parametrize("M,N,K", [(128, 256, 64), (130, 264, 256), (700, 1032, 136)])
+def test_one_sm_gemm_with_no_more_k_blocks_than_stages(M, N, K):
+    """The one-SM form of the bf16 GEMMs (4 stages of 64 of K), as above."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    a, b = (torch.randn(r, K, device="cuda", generator=g).to(BF) for r in (M, N))
+    out = torch.empty(M, N, dtype=BF, device="cuda")
+
+    def call():
+        C.coda_gemm(a, False, b, False, out, M, N, K)
+        return out
+
+    C.coda_set_sm_pairing(False)
+    try:
+        want = call().clone()
+        assert_device_ok()
+        for _ in range(2):
+            _expire(call, 1)
+            assert torch.equal(call(), want)
+            assert_device_ok()
+    finally:
+        C.coda_set_sm_pairing(True)
