@@ -109,6 +109,8 @@ SIGNATURES = {
     "coda_lmhead_policy_workspace_bytes": (_SZ, [_I64, _I64, _I64, _INT]),
     "coda_lmhead_policy": (_INT, [_P, _P, _P, _P, _P, _P, _P, _P, _F32, _F32, _F32, _F32, _P, _P, _P, _P, _P, _SZ,
                                   _I64, _I64, _I64, _P]),
+    "coda_lmhead_score_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
+    "coda_lmhead_score": (_INT, [_P, _P, _P, _P, _F32, _P, _P, _P, _P, _I64, _P, _SZ, _I64, _I64, _I64, _P]),
     "coda_fp8_quantize": (_INT, [_P, _P, _P, _P, _P, _I64, _I64, _P]),
     "coda_fp8_quantize_e5m2": (_INT, [_P, _P, _P, _P, _P, _I64, _I64, _P]),
     "coda_swiglu_bwd_fp8": (_INT, [_P, _P, _P, _P, _INT, _P, _P, _P, _I64, _I64, _I64, _P]),
@@ -194,7 +196,8 @@ def _bind():
             raise ImportError(f"{e}: build it with `python -m gemm_epilogue_transformer_tma_gb300.build`") from e
         mod.bind(handle, *(ctypes.cast(getattr(lib, n), _P).value for n in (
             "coda_fp8_block_quantize", "coda_fp8_block_quantize_weight", "coda_fp8_block_dequantize",
-            "coda_gemm_fp8_block", "coda_qknorm_rope", "coda_qknorm_rope_bwd", "coda_lmhead_policy")))
+            "coda_gemm_fp8_block", "coda_qknorm_rope", "coda_qknorm_rope_bwd", "coda_lmhead_policy",
+            "coda_lmhead_score")))
         _bound = mod
     return _bound
 
@@ -941,6 +944,19 @@ def coda_lmhead_policy(Hs, Wt, labels, advantage, weight, logp_old, logp_ref, cl
                                     kl_coef, temperature, stats, logp, dHs, dWt, ws, stream)
     if st:
         _check(st, "coda_lmhead_policy")
+
+
+def coda_lmhead_score_workspace_bytes(M: int, d: int, V: int, k: int) -> int:
+    return load_library().coda_lmhead_score_workspace_bytes(M, d, V, k)
+
+
+def coda_lmhead_score(Hs, Wt, labels, temperature: float, logp, entropy, top_ids, top_logp, ws, stream=None):
+    """Log-probabilities of labels, the entropy and the k most probable tokens
+    of every row (k: the columns of top_ids and top_logp).  labels and logp,
+    entropy, top_ids and top_logp may be None (see include/coda.h)."""
+    st = (_bound or _bind()).score(Hs, Wt, labels, temperature, logp, entropy, top_ids, top_logp, ws, stream)
+    if st:
+        _check(st, "coda_lmhead_score")
 
 
 def coda_unfused_workspace_bytes(M: int, d: int, N2: int) -> int:

@@ -26,6 +26,7 @@ decltype(&coda_gemm_fp8_block) p_gemm;
 decltype(&coda_qknorm_rope) p_qknorm;
 decltype(&coda_qknorm_rope_bwd) p_qknorm_bwd;
 decltype(&coda_lmhead_policy) p_policy;
+decltype(&coda_lmhead_score) p_score;
 
 constexpr int kMaxDevices = 64;
 coda_handle_t g_handles[kMaxDevices];
@@ -310,13 +311,39 @@ PyObject* policy(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// bind(make_handle, quantize, quantize_weight, dequantize, gemm, qknorm, qknorm_bwd, policy): the addresses of the
-// library's entry points
+// (Hs, Wt, labels, temperature, logp, entropy, top_ids, top_logp, ws, stream)
+PyObject* score(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Call c(a, n, 10);
+  c.on(0, "Hs", 9);
+  const int64_t M = c.extent(0, "Hs", 0, 2), d = c.extent(0, "Hs", 1, 2), V = c.extent(1, "Wt", 0, 2);
+  if (c.ok && ((a[2] == Py_None) != (a[4] == Py_None) || (a[6] == Py_None) != (a[7] == Py_None))) {
+    PyErr_SetString(PyExc_ValueError, "labels and logp, top_ids and top_logp come together");
+    c.ok = false;
+  }
+  const int64_t k = c.ok && a[6] != Py_None ? c.extent(6, "top_ids", 1, 2) : 0;
+  const float T = c.real(3);
+  size_t bytes = 0;
+  void* H = c.arg(0, "Hs", BF, {M, d});
+  void* W = c.arg(1, "Wt", BF, {V, d});
+  auto* y = static_cast<const int32_t*>(c.opt(2, "labels", I32, {M}));
+  auto* logp = static_cast<float*>(c.opt(4, "logp", F32, {M}));
+  auto* entropy = static_cast<float*>(c.opt(5, "entropy", F32, {M}));
+  auto* ids = static_cast<int32_t*>(c.opt(6, "top_ids", I32, {M, k}));
+  auto* top = static_cast<float*>(c.opt(7, "top_logp", F32, {M, k}));
+  void* ws = c.workspace(8, &bytes);
+  return finish(c, [&] {
+    return p_score(c.handle, H, W, y, T, logp, entropy, ids, top, k, ws, bytes, M, d, V, c.stream);
+  });
+}
+
+// bind(make_handle, quantize, quantize_weight, dequantize, gemm, qknorm, qknorm_bwd, policy, score): the addresses of
+// the library's entry points
+constexpr int kBound = 9;
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  Call c(a, n, 8);
+  Call c(a, n, kBound);
   if (!c.ok) return nullptr;
-  void* p[8] = {};
-  for (int i = 1; i < 8; ++i) {
+  void* p[kBound] = {};
+  for (int i = 1; i < kBound; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (p[i] == nullptr) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null entry point");
@@ -332,6 +359,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   p_qknorm = reinterpret_cast<decltype(p_qknorm)>(p[5]);
   p_qknorm_bwd = reinterpret_cast<decltype(p_qknorm_bwd)>(p[6]);
   p_policy = reinterpret_cast<decltype(p_policy)>(p[7]);
+  p_score = reinterpret_cast<decltype(p_score)>(p[8]);
   Py_RETURN_NONE;
 }
 
@@ -351,7 +379,8 @@ PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(guarded<f>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {CODA_METHOD(bind),       CODA_METHOD(quantize), CODA_METHOD(quantize_weight),
                            CODA_METHOD(dequantize), CODA_METHOD(gemm),     CODA_METHOD(qknorm),
-                           CODA_METHOD(qknorm_bwd), CODA_METHOD(policy),   {nullptr, nullptr, 0, nullptr}};
+                           CODA_METHOD(qknorm_bwd), CODA_METHOD(policy),   CODA_METHOD(score),
+                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", "Argument marshalling of libcoda calls.", -1, g_methods,
                         nullptr,               nullptr, nullptr,                                nullptr};
 

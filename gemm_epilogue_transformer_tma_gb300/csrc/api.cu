@@ -147,6 +147,9 @@ size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// the temperature of a softmax on the LM head
+bool temperature_ok(float t) { return t > 0.f && !std::isinf(t) && !std::isinf(1.0f / t); }
+
 }  // namespace
 
 bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t ld,
@@ -1312,9 +1315,7 @@ coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt
                .st);
   if (M == 0) return CODA_ERR_INVALID_ARG;  // as coda_lmhead_ce
   if (!(clip_low >= 0.f && clip_low <= 1.f) || !(clip_high >= 0.f)) return CODA_ERR_INVALID_ARG;
-  if (!(kl_coef >= 0.f) || std::isinf(kl_coef) || !(temperature > 0.f) || std::isinf(temperature) ||
-      std::isinf(1.0f / temperature))
-    return CODA_ERR_INVALID_ARG;
+  if (!(kl_coef >= 0.f) || std::isinf(kl_coef) || !temperature_ok(temperature)) return CODA_ERR_INVALID_ARG;
   const bool grads = dHs != nullptr;
   if (grads != (dWt != nullptr)) return CODA_ERR_INVALID_ARG;
   const bool room = ws_bytes >= coda_lmhead_policy_workspace_bytes(M, d, V, grads ? 1 : 0);
@@ -1383,6 +1384,97 @@ coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt
   }
   return from_cuda(launch_policy_dh(cx, parts == 1 ? w.ce.dH32 : w.dH_parts, int(parts), cdiv(M, 256) * 256 * d,
                                     w.lost, labels, Wb, static_cast<bf16*>(dHs), M, d));
+}
+
+// ---------------------------------------------------------------------------
+namespace {
+// Alternatives are chosen from fp32 logits in memory: as many rows at a time as
+// this many values (2 GB) hold, and 256 at least, a row of tiles.
+constexpr int64_t kScoreValues = int64_t(1) << 29;
+int64_t score_rows(int64_t M, int64_t V, int64_t k) {
+  return k == 0 ? M : std::min(M, std::max<int64_t>(256, kScoreValues / V / 256 * 256));
+}
+
+struct ScoreWs {
+  ScoreStats s;
+  size_t bytes;
+};
+
+ScoreWs score_layout(uint8_t* base, int64_t M, int64_t V, int64_t k) {
+  ScoreWs w{};
+  const int64_t R = score_rows(M, V, k), T = cdiv(V, ce_tile_cols());
+  size_t off = 0;
+  auto take = [&](size_t values) {
+    uint8_t* p = base ? base + off : nullptr;
+    off += align256(values * 4);
+    return reinterpret_cast<float*>(p);
+  };
+  w.s.T = static_cast<int>(T);
+  w.s.sub_cols = ce_tile_cols() / 4;
+  w.s.pmax = take(size_t(R) * T);
+  w.s.psum = take(size_t(R) * T);
+  w.s.pdot = take(size_t(R) * T);
+  w.s.zy = take(size_t(R));
+  if (k > 0) {
+    w.s.sub = take(size_t(R) * T * 4);
+    w.s.logits = take(size_t(R) * V);
+  }
+  w.bytes = off;
+  return w;
+}
+}  // namespace
+
+size_t coda_lmhead_score_workspace_bytes(int64_t M, int64_t d, int64_t V, int64_t k) {
+  if (M <= 0 || d <= 0 || V <= 0 || k < 0 || k > std::min<int64_t>(V, kScoreMaxTop)) return 0;
+  return score_layout(nullptr, M, V, k).bytes;
+}
+
+coda_status_t coda_lmhead_score(coda_handle_t h, const void* Hs, const void* Wt, const int32_t* labels,
+                                float temperature, float* logp, float* entropy, int32_t* top_ids, float* top_logp,
+                                int64_t k, void* ws, size_t ws_bytes, int64_t M, int64_t d, int64_t V, void* stream) {
+  CODA_TRY(Check()
+               .handle(h)
+               .mptr(Hs, M)
+               .ptr(Wt)
+               .opt_sptr(labels)
+               .opt_sptr(logp)
+               .opt_sptr(entropy)
+               .opt_sptr(top_ids)
+               .opt_sptr(top_logp)
+               .mptr(ws, M)
+               .rows(M)
+               .cols(d)
+               .cols(V)
+               .st);
+  if (!temperature_ok(temperature)) return CODA_ERR_INVALID_ARG;
+  if (k < 0 || k > std::min<int64_t>(V, kScoreMaxTop)) return CODA_ERR_INVALID_ARG;
+  if (M == 0) return CODA_OK;
+  if ((labels != nullptr) != (logp != nullptr) || (top_ids != nullptr) != (top_logp != nullptr) ||
+      (top_ids != nullptr) != (k > 0) || (logp == nullptr && entropy == nullptr && k == 0))
+    return CODA_ERR_INVALID_ARG;
+  if (ws_bytes < coda_lmhead_score_workspace_bytes(M, d, V, k)) return CODA_ERR_WORKSPACE_TOO_SMALL;
+  const OnDevice dev(h->device);
+  const LaunchCtx cx = ctx_of(h, stream);
+  const ScoreWs w = score_layout(static_cast<uint8_t*>(ws), M, V, k);
+  const float c = static_cast<float>(1.4426950408889634 / double(temperature));
+  const int64_t R = score_rows(M, V, k);
+  for (int64_t m0 = 0; m0 < M; m0 += R) {
+    const int64_t rows = std::min(R, M - m0);
+    ScoreOut o{};
+    o.labels = labels ? labels + m0 : nullptr;
+    o.logp = logp ? logp + m0 : nullptr;
+    o.entropy = entropy ? entropy + m0 : nullptr;
+    o.top_ids = top_ids ? top_ids + m0 * k : nullptr;
+    o.top_logp = top_logp ? top_logp + m0 * k : nullptr;
+    o.k = static_cast<int>(k);
+    o.temperature = temperature;
+    o.log2e_over_t = c;
+    o.status = cx.status;
+    CODA_CUDA(gemm_score(cx, static_cast<const bf16*>(Hs) + m0 * d, static_cast<const bf16*>(Wt), o.labels, w.s, c,
+                         int(rows), int(d), int(V)));
+    CODA_CUDA(launch_score_rows(cx, w.s, o, rows, V));
+  }
+  return CODA_OK;
 }
 
 // ---------------------------------------------------------------------------

@@ -159,6 +159,34 @@ cudaError_t gemm_logit_stats(const LaunchCtx& c, const __nv_bfloat16* H, const _
                              const int32_t* labels, float* pmax, float* psum, float* zy, __nv_bfloat16* kept, int chunk,
                              int kept_cols, int M, int d, int V, int T);
 
+// Scoring (logits_score.cuh): blocks of a row and what is kept of each.
+struct ScoreStats {
+  float* pmax;    // [M][T]: the block's largest logit
+  float* psum;    // [M][T]: sum of exp((L - pmax) / temperature), less 1
+  float* pdot;    // [M][T]: sum of (L - pmax) exp((L - pmax) / temperature)
+  float* zy;      // [M]: the logit of the row's token
+  float* logits;  // [M][V], or null: no alternatives
+  float* sub;     // [M][4 T]: maxima of sub_cols columns each, with logits
+  int T;          // blocks of a row
+  int sub_cols;   // a quarter of a block
+};
+cudaError_t gemm_score(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt, const int32_t* labels,
+                       const ScoreStats& s, float log2e_over_t, int M, int d, int V);
+// logp, entropy, the k highest logits' tokens and log-probabilities of M rows
+// (score.cu); any of the outputs may be null, top_ids and top_logp together
+constexpr int kScoreMaxTop = 256;
+struct ScoreOut {
+  const int32_t* labels;  // or null, with logp
+  float* logp;
+  float* entropy;
+  int32_t* top_ids;       // [M][k]
+  float* top_logp;
+  int k;
+  float temperature, log2e_over_t;
+  int* status;
+};
+cudaError_t launch_score_rows(const LaunchCtx& c, const ScoreStats& s, const ScoreOut& o, int64_t M, int64_t V);
+
 // parts_buf [parts][M rounded up to 256][N] fp32 (+)= the K ranges of A B, A
 // [M][K], B [K][N] (gemm_splitk.cuh); parts <= the k-blocks of 64 in K
 cudaError_t gemm_splitk(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_bfloat16* B, float* parts_buf, int parts,

@@ -2,7 +2,7 @@
 // softmax-gradient epilogue (logits never leave the chip).
 #include "gemm_dw.cuh"
 #include "gemm_launch.cuh"
-#include "gemm_logits.cuh"
+#include "gemm_logits_launch.cuh"
 #include "gemm_splitk.cuh"
 
 namespace coda {
@@ -21,49 +21,32 @@ cudaError_t gemm_ce_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv
   return run_gemm<false, false, false, EpiCeStats>(c, ta, tb, tb, M, V, d, (V + kBN - 1) / kBN, ep);
 }
 
-template <bool KEEP>
-static cudaError_t launch_logits(const LaunchCtx& c, const LogitsArgs& g) {
-  using L = LogitsSmem;
-  auto kern = gemm_logits_kernel<KEEP>;
-  static bool smem_ok[64] = {};
-  cudaError_t e = allow_smem(kern, L::TOTAL, smem_ok);
-  if (e != cudaSuccess) return e;
-  static int cap[64] = {};
-  int pairs = 0;
-  e = pair_capacity(reinterpret_cast<const void*>(kern), L::THREADS, L::TOTAL, c.num_sms, cap, &pairs);
-  if (e != cudaSuccess) return e;
-  KernelCtl ctl{c.status, c.timeout_ns, c.skip_first_stage};
-  const int clusters = std::max(1, std::min(g.tiles_m * g.tiles_n, pairs));
-  return launch_chained(c, kern, dim3(2 * clusters), dim3(L::THREADS), L::TOTAL, g, ctl);
-}
-
 cudaError_t gemm_logit_stats(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt,
                              const int32_t* labels, float* pmax, float* psum, float* zy, __nv_bfloat16* kept, int chunk,
                              int kept_cols, int M, int d, int V, int T) {
-  LogitsArgs g{};
-  if (!make_operand_maps(&g.H, &g.W, H, false, Wt, false, M, V, d, 128)) return cudaErrorInvalidValue;
-  g.labels = labels;
-  g.pmax = pmax;
-  g.psum = psum;
-  g.zy = zy;
-  g.kept_cols = kept_cols;
-  if (kept_cols > 0) {
-    g.chunk = chunk;
-    g.rows = (M + 31) / 32 * 32;
-    const int whole = kept_cols / chunk, rest = kept_cols - whole * chunk;
-    if ((whole > 0 && !make_tmap_store_bf16(&g.whole, kept, chunk, uint64_t(whole) * g.rows, chunk)) ||
-        (rest > 0 && !make_tmap_store_bf16(&g.rest, kept + int64_t(whole) * g.rows * chunk, rest, M, rest)))
-      return cudaErrorInvalidValue;
+  auto fill = [&](auto& p) {
+    p.labels = labels;
+    p.pmax = pmax;
+    p.psum = psum;
+    p.zy = zy;
+    p.T = T;
+    p.kept_cols = kept_cols;
+    p.scale = c.scale_host;
+  };
+  if (kept_cols == 0) {
+    LogitsPolicy<false>::Params p{};
+    fill(p);
+    return launch_logits<LogitsPolicy<false>>(c, H, Wt, p, M, d, V);
   }
-  g.M = M;
-  g.V = V;
-  g.T = T;
-  g.tiles_m = (M + BM2 - 1) / BM2;
-  g.tiles_n = (V + kBN - 1) / kBN;
-  g.num_kb = (d + BK - 1) / BK;
-  g.group_m = 8;
-  g.scale = c.scale_host;
-  return kept_cols > 0 ? launch_logits<true>(c, g) : launch_logits<false>(c, g);
+  LogitsPolicy<true>::Params p{};
+  fill(p);
+  p.chunk = chunk;
+  p.rows = (M + 31) / 32 * 32;
+  const int whole = kept_cols / chunk, rest = kept_cols - whole * chunk;
+  if ((whole > 0 && !make_tmap_store_bf16(&p.whole, kept, chunk, uint64_t(whole) * p.rows, chunk)) ||
+      (rest > 0 && !make_tmap_store_bf16(&p.rest, kept + int64_t(whole) * p.rows * chunk, rest, M, rest)))
+    return cudaErrorInvalidValue;
+  return launch_logits<LogitsPolicy<true>>(c, H, Wt, p, M, d, V);
 }
 
 cudaError_t gemm_splitk(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_bfloat16* B, float* parts_buf, int parts,

@@ -1,9 +1,7 @@
-// The LM head's blocked log-sum-exp statistics with the contraction summed in
-// pieces: per (row, 128-column vocabulary block) the maximum and the sum of
-// exp(L - max), and the label's logit, L = scale * H Wt^T.  The exponentials of
-// the first `kept_cols` columns are kept too, in bf16, for the gradients:
-// vocabulary chunks of `chunk` columns one after the other, each [rows][its
-// columns].
+// LM-head GEMMs whose epilogue works on whole logits: L = H Wt^T with the
+// contraction summed in pieces, and a program (LogitsPolicy below,
+// logits_score.cuh, logits_distill.cuh) that gets 128 columns of a row in the
+// registers of one thread.
 //
 // The tensor core drops the bits of a product that fall below the running
 // sum, so a logit loses about half a unit in the last place of that sum at
@@ -44,26 +42,106 @@ struct LogitsSmem {
   static_assert(TOTAL <= MAX_DYN_SMEM, "shared memory budget");
 };
 
-struct LogitsArgs {
-  CUtensorMap H, W;       // [M][d], [V][d] bf16
-  const int32_t* labels;  // [M]
-  float* pmax;            // [M][T], T = ceil(V / 128)
-  float* psum;            // [M][T]
-  float* zy;              // [M], written where the label is found
-  // the kept exponentials, 32 x 32 boxes: the whole chunks below each other
-  // (`chunk` columns wide, chunk c from row c * rows), and the last, narrower one
-  CUtensorMap whole, rest;
-  int kept_cols;          // whole chunks, or V
-  int chunk, rows;        // rows: M rounded up to 32
-  int M, V, T;
-  int tiles_m, tiles_n, num_kb, group_m;
-  float scale;
+// 128 columns [n0, n0 + nv) of the 32 rows from m0, a row to a lane
+struct LogitsTile {
+  int m0, n0, nv;  // nv >= 128 where all of them exist
+  int part;        // n0 / 128, the block
+  int lane;
+  uint32_t slot;   // this warp's two store slots in shared memory
 };
 
-// KEEP: kept_cols > 0; scoring runs without the stores' code
+// A program has Params, a State that ahead() loads while the tile's MMAs run
+// (kAhead), run(), which gets the raw products, and kStores: whether it leaves
+// bulk stores in flight.  Both are called for tiles with a row and a column only.
+template <class Prog>
+struct LogitsArgs {
+  CUtensorMap H, W;  // [M][d], [V][d] bf16
+  int M, V;
+  int tiles_m, tiles_n, num_kb, group_m;
+  typename Prog::Params p;
+};
+
+// The policy loss: per (row, 128-column vocabulary block) the maximum and the
+// sum of exp(L - max), and the label's logit, L = scale * H Wt^T.  KEEP: the
+// exponentials of the first `kept_cols` columns are kept too, in bf16, for the
+// gradients: vocabulary chunks of `chunk` columns one after the other, each
+// [rows][its columns].
 template <bool KEEP>
+struct LogitsPolicy {
+  static constexpr bool kAhead = false;
+  static constexpr bool kStores = KEEP;
+  struct Params {
+    const int32_t* labels;  // [M]
+    float* pmax;            // [M][T], T = ceil(V / 128)
+    float* psum;            // [M][T]
+    float* zy;              // [M], written where the label is found
+    // the kept exponentials, 32 x 32 boxes: the whole chunks below each other
+    // (`chunk` columns wide, chunk c from row c * rows), and the last, narrower one
+    CUtensorMap whole, rest;
+    int kept_cols;          // whole chunks, or V
+    int chunk, rows;        // rows: M rounded up to 32
+    int T;
+    float scale;
+  };
+  struct State {};
+  static __device__ __forceinline__ void run(const Params& g, const LogitsTile& t, const State&, int M,
+                                             float (&v)[4][32]) {
+    const int m = t.m0 + t.lane, n0 = t.n0, nv = t.nv, lane = t.lane;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        v[c][i] = c * 32 + i < nv ? v[c][i] * g.scale : -INFINITY;
+        mx = fmaxf(mx, v[c][i]);
+      }
+    const int64_t y = m < M ? static_cast<int64_t>(g.labels[m]) - n0 : -1;
+    if (y >= 0 && y < PART_COLS && y < nv) {
+      float z = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c * 32 + i == y) z = v[c][i];
+      g.zy[m] = z;
+    }
+    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float e = __expf(v[c][i] - mx);
+        s4[i & 3] += e;
+        if (KEEP) v[c][i] = e;
+      }
+    if (KEEP && n0 < g.kept_cols) {
+      const int ch = n0 / g.chunk;
+      const bool whole = (ch + 1) * static_cast<int64_t>(g.chunk) <= g.kept_cols;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c * 32 >= nv) break;
+        // a ragged last tile stores 1 or 3 blocks, so the tile after it starts
+        // in the slot of the last store: its first block waits for all of them
+        const uint32_t at = t.slot + (c & 1) * STORE_SLOT_BYTES;
+        slots_acquire_db(lane, c == 0);
+        stage_bf16x32(at, lane, v[c]);
+        slots_publish();
+        if (lane == 0) {
+          tma_store_2d(whole ? &g.whole : &g.rest, at, n0 - ch * g.chunk + c * 32, (whole ? ch * g.rows : 0) + t.m0);
+          bulk_commit_group();
+        }
+      }
+    }
+    if (m >= M) return;
+    const int64_t o = static_cast<int64_t>(m) * g.T + t.part;
+    g.pmax[o] = mx;
+    g.psum[o] = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+  }
+};
+
+template <class Prog>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS, 1)
-    gemm_logits_kernel(const __grid_constant__ LogitsArgs g, const KernelCtl ctl) {
+    gemm_logits_kernel(const __grid_constant__ LogitsArgs<Prog> g, const KernelCtl ctl) {
   using L = LogitsSmem;
   constexpr int STAGES = L::STAGES;
   constexpr int BN = 256;
@@ -231,11 +309,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
     const uint32_t leader_tempty = mapa_shared(smem_u32(tempty), 0);
     const uint32_t slot = smem_u32(smem + L::RING_BYTES) + static_cast<uint32_t>((warp - 2) * 2 * STORE_SLOT_BYTES);
     const int pieces = (g.num_kb + kPieceKb - 1) / kPieceKb;
+    auto tile_of = [&](int t) {
+      int tm, tn;
+      tile_coords(t, sh, tm, tn);
+      LogitsTile tile;
+      tile.m0 = (tm * 2 + static_cast<int>(rank)) * 128 + quad * 32;
+      tile.n0 = tn * BN + half * (BN / 2);
+      tile.nv = g.V - tile.n0;
+      tile.part = tn * 2 + half;
+      tile.lane = lane;
+      tile.slot = slot;
+      return tile;
+    };
     int it = 0;
     bool ok = true;
     for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
-      int tm, tn;
-      tile_coords(t, sh, tm, tn);
+      typename Prog::State st{};
+      if constexpr (Prog::kAhead) {
+        const LogitsTile tile = tile_of(t);
+        if (tile.m0 < g.M && tile.nv > 0) st = Prog::ahead(g.p, tile, g.M);
+      }
       float v[4][32];
       for (int p = 0; p < pieces; ++p, ++it) {
         const int acc = it & 1;
@@ -264,62 +357,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
         if (lane == 0) mbar_arrive_cluster_relaxed(leader_tempty + static_cast<uint32_t>(acc * 8));
       }
       if (!ok) break;
-      const int m0 = (tm * 2 + static_cast<int>(rank)) * 128 + quad * 32;
-      const int m = m0 + lane;
-      const int n0 = tn * BN + half * (BN / 2);
-      if (m0 >= g.M || n0 >= g.V) continue;
-      const int nv = g.V - n0;  // columns of this half tile that exist
-      float mx = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          v[c][i] = c * 32 + i < nv ? v[c][i] * g.scale : -INFINITY;
-          mx = fmaxf(mx, v[c][i]);
-        }
-      const int64_t y = m < g.M ? static_cast<int64_t>(g.labels[m]) - n0 : -1;
-      if (y >= 0 && y < BN / 2 && y < nv) {
-        float z = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c * 32 + i == y) z = v[c][i];
-        g.zy[m] = z;
-      }
-      float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float e = __expf(v[c][i] - mx);
-          s4[i & 3] += e;
-          if (KEEP) v[c][i] = e;
-        }
-      if (KEEP && n0 < g.kept_cols) {
-        const int ch = n0 / g.chunk;
-        const bool whole = (ch + 1) * static_cast<int64_t>(g.chunk) <= g.kept_cols;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c * 32 >= nv) break;
-          // a ragged last tile stores 1 or 3 blocks, so the tile after it starts
-          // in the slot of the last store: its first block waits for all of them
-          const uint32_t at = slot + (c & 1) * STORE_SLOT_BYTES;
-          slots_acquire_db(lane, c == 0);
-          stage_bf16x32(at, lane, v[c]);
-          slots_publish();
-          if (lane == 0) {
-            tma_store_2d(whole ? &g.whole : &g.rest, at, n0 - ch * g.chunk + c * 32, (whole ? ch * g.rows : 0) + m0);
-            bulk_commit_group();
-          }
-        }
-      }
-      if (m >= g.M) continue;
-      const int64_t o = static_cast<int64_t>(m) * g.T + tn * 2 + half;
-      g.pmax[o] = mx;
-      g.psum[o] = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+      const LogitsTile tile = tile_of(t);  // not held through the pieces: registers are short
+      if (tile.m0 < g.M && tile.nv > 0) Prog::run(g.p, tile, st, g.M, v);
     }
-    if (KEEP) {
+    if (Prog::kStores) {
       __syncwarp();
       if (lane == 0) bulk_wait_group0();
       __syncwarp();

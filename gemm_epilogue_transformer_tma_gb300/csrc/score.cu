@@ -1,0 +1,347 @@
+// Row kernels of scoring: from the block statistics of a row's logits
+// (logits_score.cuh) the log-probability of its token, the entropy and the k
+// most probable tokens.
+//
+// With x = L - max L over the row, s = sum exp(x / T) - 1 (the largest itself
+// left out) and u = sum x exp(x / T):
+//   log p_v = x_v / T - log(1 + s),   entropy = log(1 + s) - (u / T) / (1 + s)
+// Neither has a cancellation: x and u are never positive, s never negative, and
+// log1p keeps the digits of a row that is nearly certain.
+//
+// The k largest logits lie in sub-blocks whose maximum is at least the k-th
+// largest of those maxima, so nearly all of a row's logits are never read
+// again: 64 of 128256 read some 70 sub-blocks of 32.
+#include <algorithm>
+
+#include "coda_internal.h"
+#include "ptx.cuh"
+
+namespace coda {
+
+namespace {
+
+// the largest logit of some blocks, and psum and pdot relative to it
+struct RowSum {
+  float mx, s, u;
+};
+__device__ __forceinline__ void merge(RowSum& a, RowSum b, float c) {
+  if (b.mx == -INFINITY && b.s == 0.f) return;  // no block
+  if (a.mx == -INFINITY && a.s == 0.f) {
+    a = b;
+    return;
+  }
+  if (b.mx > a.mx) {
+    const RowSum t = a;
+    a = b;
+    b = t;
+  }
+  const float dx = b.mx - a.mx, f = ex2_f(dx * c), n = 1.f + b.s;
+  a.s = fmaf(f, n, a.s);
+  a.u += f * fmaf(dx, n, b.u);
+}
+
+__device__ __forceinline__ RowSum merge_warp(RowSum r, float c) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    // the lower lane's first on both sides: all lanes end with the same bits
+    RowSum x;
+    x.mx = __shfl_xor_sync(0xffffffffu, r.mx, o);
+    x.s = __shfl_xor_sync(0xffffffffu, r.s, o);
+    x.u = __shfl_xor_sync(0xffffffffu, r.u, o);
+    if (threadIdx.x & o) {
+      merge(x, r, c);
+      r = x;
+    } else {
+      merge(r, x, c);
+    }
+  }
+  return r;
+}
+
+__device__ __forceinline__ RowSum row_blocks(const ScoreStats& s, int64_t m, int first, int step, float c) {
+  RowSum r{-INFINITY, 0.f, 0.f};
+  const int64_t at = m * s.T;
+#pragma unroll 2
+  for (int j = first; j < s.T; j += step) merge(r, RowSum{s.pmax[at + j], s.psum[at + j], s.pdot[at + j]}, c);
+  return r;
+}
+
+__device__ __forceinline__ void write_row(const ScoreStats& s, const ScoreOut& o, const RowSum& r, int64_t m,
+                                          int64_t V) {
+  const float log_s = log1pf(r.s);
+  if (o.entropy != nullptr) o.entropy[m] = log_s - r.u / o.temperature / (1.f + r.s);
+  if (o.logp != nullptr) {
+    const int32_t y = o.labels[m];
+    const bool in_range = y >= 0 && y < V;
+    o.logp[m] = in_range ? (s.zy[m] - r.mx) / o.temperature - log_s : 0.f;
+    if (y >= V) atomicOr(o.status, DEV_ERR_LABEL_RANGE);  // a negative one is a position without a token
+  }
+}
+
+// Without alternatives: a warp to a row.
+__global__ void __launch_bounds__(128) score_rows_kernel(const ScoreStats s, const ScoreOut o, int64_t M, int64_t V) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t m = blockIdx.x * 4ll + (threadIdx.x >> 5);
+  if (m >= M) return;
+  const RowSum r = merge_warp(row_blocks(s, m, threadIdx.x & 31, 32, o.log2e_over_t), o.log2e_over_t);
+  if ((threadIdx.x & 31) == 0) write_row(s, o, r, m, V);
+}
+
+// A logit as an unsigned number of the same order; a NaN ranks with -infinity,
+// -0 with 0.
+__device__ __forceinline__ uint32_t rank_key(float v) {
+  const uint32_t b = __float_as_uint(__fadd_rn(v, 0.f));
+  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0x007FFFFFu;
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) != 0u ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+constexpr int kTopThreads = 128;
+constexpr int kTopWarps = kTopThreads / 32;
+constexpr int kTopList = 1024;            // candidates held in shared memory
+constexpr int kTopSlack = 64;             // ranked beside the k: selecting more exactly costs a pass over the list
+constexpr int kTopFinal = kScoreMaxTop + kTopSlack;
+
+struct TopSmem {
+  uint64_t list[kTopList];  // rank_key(logit) << 32 | ~token: the order of the answer, largest first
+  uint64_t best[kTopFinal];
+  int hist[256];
+  int pick[2];
+  int n, n_best;
+  RowSum part[kTopWarps];
+};
+
+// pick[0]: the largest digit with at least `need` counted at it and above,
+// pick[1]: how many were counted above it.  By warp 0; hist holds `need` or more.
+__device__ __forceinline__ void pick_digit(TopSmem& sm, int need, int lane) {
+  int h[8], sum = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    h[j] = sm.hist[255 - (lane * 8 + j)];
+    sum += h[j];
+  }
+  int upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  int above = upto - sum;
+  if (above < need && need <= upto) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (above < need && above + h[j] >= need) {
+        sm.pick[0] = 255 - (lane * 8 + j);
+        sm.pick[1] = above;
+        need = 0;  // found
+      }
+      above += h[j];
+    }
+  }
+}
+
+// Adds the warp's chosen values to the list in lane order (counting on past its end).
+__device__ __forceinline__ void append(TopSmem& sm, bool take, uint32_t key, uint32_t token, int lane) {
+  const unsigned who = __ballot_sync(0xffffffffu, take);
+  if (who == 0) return;
+  int at = 0;
+  if (lane == 0) at = atomicAdd(&sm.n, __popc(who));
+  at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1u));
+  if (take && at < kTopList) sm.list[at] = (static_cast<uint64_t>(key) << 32) | static_cast<uint32_t>(~token);
+}
+
+// f(logit's key, token) for the logits of sub-blocks with a key of at least
+// lo; all lanes of a warp call it, with `there` false past the end.  A warp
+// takes 32 sub-blocks at a time.
+template <class F>
+__device__ __forceinline__ void each_logit(const float* __restrict__ sub, const float* __restrict__ logits, int subs,
+                                           int cols, int64_t V, uint32_t lo, int warp, int warps, int lane, F&& f) {
+  for (int j0 = warp * 32; j0 < subs; j0 += warps * 32) {
+    const int j = j0 + lane;
+    unsigned hit = __ballot_sync(0xffffffffu, j < subs && rank_key(sub[j]) >= lo);
+    while (hit != 0) {
+      int64_t at[4];
+      bool there[4];
+      float v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {  // four sub-blocks in flight
+        const int b = hit != 0 ? __ffs(hit) - 1 : -1;
+        hit &= hit - 1;
+        at[q] = static_cast<int64_t>(j0 + b) * cols + lane;
+        there[q] = b >= 0 && lane < cols && at[q] < V;
+        v[q] = there[q] ? logits[at[q]] : 0.f;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f(there[q], rank_key(v[q]), static_cast<uint32_t>(at[q]));
+    }
+  }
+}
+
+// With alternatives: 128 threads to a row.
+__global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats s, const ScoreOut o, int64_t M,
+                                                                int64_t V) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ TopSmem sm;
+  const int64_t m = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = o.k;
+  const float c = o.log2e_over_t;
+  RowSum r = merge_warp(row_blocks(s, m, tid, kTopThreads, c), c);
+  if (lane == 0) sm.part[warp] = r;
+  const float* sub = s.sub + m * 4 * s.T;
+  const float* logits = s.logits + m * V;
+  const int cols = s.sub_cols, subs = static_cast<int>((V + cols - 1) / cols);
+  for (int i = tid; i < 256; i += kTopThreads) sm.hist[i] = 0;
+  if (tid == 0) sm.n = sm.n_best = 0;
+  __syncthreads();
+  r = sm.part[0];
+#pragma unroll
+  for (int w = 1; w < kTopWarps; ++w) merge(r, sm.part[w], c);
+  if (tid == 0) write_row(s, o, r, m, V);
+
+  // One step of a selection by digits of 8 bits, from the highest: counts the
+  // digit of the keys that share the digits found so far, then finds the
+  // largest digit that leaves `need` at or above it.  Returns how many keys
+  // of all are at least the new prefix.
+  auto step = [&](auto count_all, auto& prefix, int& need, int shift) {
+    count_all(shift);
+    __syncthreads();
+    if (warp == 0) pick_digit(sm, need, lane);
+    __syncthreads();
+    const int digit = sm.pick[0], above = sm.pick[1], here = sm.hist[digit];
+    __syncthreads();
+    for (int i = tid; i < 256; i += kTopThreads) sm.hist[i] = 0;
+    __syncthreads();
+    prefix |= static_cast<decltype(+prefix)>(digit) << shift;
+    need -= above;
+    return here;
+  };
+
+  // a bound on the k-th largest sub-block maximum from its upper 16 bits
+  uint32_t lo = 0;
+  if (subs > k) {
+    int need = k;
+#pragma unroll 1
+    for (int shift = 24; shift >= 16; shift -= 8)
+      step(
+          [&](int sh) {
+            for (int j = tid; j < subs; j += kTopThreads) {
+              const uint32_t key = rank_key(sub[j]);
+              if (sh == 24 || (key >> 24) == (lo >> 24)) atomicAdd(&sm.hist[(key >> sh) & 255u], 1);
+            }
+          },
+          lo, need, shift);
+  }
+  auto gather = [&](uint32_t least) {
+    each_logit(sub, logits, subs, cols, V, least, warp, kTopWarps, lane, [&](bool there, uint32_t key, uint32_t token) {
+      append(sm, there && key >= least, key, token, lane);
+    });
+    __syncthreads();
+  };
+  gather(lo);
+  int n = sm.n;
+  if (n > kTopList) {
+    // Many logits are near the k-th, or equal.  Equal ones are taken in token
+    // order by one warp, which ends as soon as it has them: a row of zeros
+    // after its first sub-blocks.
+    auto first_equal = [&](uint32_t key0, int want) {  // warp 0
+      int have = 0;
+      for (int j0 = 0; j0 < subs && have < want; j0 += 32) {
+        const int j = j0 + lane;
+        unsigned hit = __ballot_sync(0xffffffffu, j < subs && rank_key(sub[j]) >= key0);
+        while (hit != 0 && have < want) {
+          const int64_t at = static_cast<int64_t>(j0 + __ffs(hit) - 1) * cols + lane;
+          hit &= hit - 1;
+          const bool eq = lane < cols && at < V && rank_key(logits[at]) == key0;
+          const unsigned who = __ballot_sync(0xffffffffu, eq);
+          const int rank = have + __popc(who & ((1u << lane) - 1u));
+          append(sm, eq && rank < want, key0, static_cast<uint32_t>(at), lane);
+          have += __popc(who);
+        }
+      }
+      return min(have, want);
+    };
+    __syncthreads();
+    if (tid == 0) sm.n = 0;
+    __syncthreads();
+    if (warp == 0) {
+      const int have = first_equal(rank_key(r.mx), k);
+      if (lane == 0) sm.pick[0] = have;
+    }
+    __syncthreads();
+    n = sm.pick[0];
+    __syncthreads();
+    if (n < k) {  // by digits over all logits that can be among them
+      uint32_t key = 0;
+      int need = k, here = kTopList + 1;
+#pragma unroll 1
+      for (int shift = 24; shift >= 0 && k - need + here > kTopList; shift -= 8)
+        here = step(
+            [&](int sh) {
+              each_logit(sub, logits, subs, cols, V, lo, warp, kTopWarps, lane,
+                         [&](bool there, uint32_t x, uint32_t) {
+                           if (there && (sh == 24 || (x >> (sh + 8)) == (key >> (sh + 8))))
+                             atomicAdd(&sm.hist[(x >> sh) & 255u], 1);
+                         });
+            },
+            key, need, shift);
+      const bool ties = k - need + here > kTopList;  // key is the k-th, and too many equal it
+      if (tid == 0) sm.n = 0;
+      __syncthreads();
+      gather(ties ? key + 1 : key);
+      if (ties && warp == 0) first_equal(key, need);
+      __syncthreads();
+      n = sm.n;
+    }
+  }
+
+  // more than the k and some: by digits over the list
+  uint64_t least = 0;
+  if (n > k + kTopSlack) {
+    int need = k, here = n;
+#pragma unroll 1
+    for (int shift = 56; shift >= 0 && k - need + here > k + kTopSlack; shift -= 8)
+      here = step(
+          [&](int sh) {
+            for (int i = tid; i < n; i += kTopThreads) {
+              const uint64_t x = sm.list[i];
+              if (sh == 56 || (x >> (sh + 8)) == (least >> (sh + 8))) atomicAdd(&sm.hist[(x >> sh) & 255u], 1);
+            }
+          },
+          least, need, shift);
+    for (int i = tid; i < n; i += kTopThreads) {
+      const uint64_t x = sm.list[i];
+      if (x >= least) sm.best[atomicAdd(&sm.n_best, 1)] = x;
+    }
+    __syncthreads();
+    n = sm.n_best;
+  } else {
+    for (int i = tid; i < n; i += kTopThreads) sm.best[i] = sm.list[i];
+    __syncthreads();
+  }
+  // all different: each one's place is the number of larger ones
+  const float log_s = log1pf(r.s);
+  for (int i = tid; i < n; i += kTopThreads) {
+    const uint64_t x = sm.best[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += sm.best[j] > x;
+    if (rank < k) {
+      const int64_t at = m * k + rank;
+      o.top_ids[at] = static_cast<int32_t>(~static_cast<uint32_t>(x));
+      o.top_logp[at] = (key_value(static_cast<uint32_t>(x >> 32)) - r.mx) / o.temperature - log_s;
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_score_rows(const LaunchCtx& c, const ScoreStats& s, const ScoreOut& o, int64_t M, int64_t V) {
+  if (o.k == 0)
+    return launch_chained(c, score_rows_kernel, dim3(static_cast<unsigned>((M + 3) / 4)), dim3(128), 0, s, o, M, V);
+  return launch_chained(c, score_top_kernel, dim3(static_cast<unsigned>(M)), dim3(kTopThreads), 0, s, o, M, V);
+}
+
+}  // namespace coda

@@ -19,8 +19,9 @@ from . import (CODA_EPI_PLAIN, CODA_EPI_SWIGLU, E4M3, E5M2, coda_bwd_workspace_b
                coda_gemm_wgrad_gscale, coda_prms_num_tiles, coda_rstd_combine, coda_swiglu_bwd, coda_swiglu_bwd_fp8,
                coda_unfused_bwd, coda_unfused_fwd, coda_unfused_workspace_bytes)
 from . import (coda_fp8_block_quantize, coda_fp8_block_quantize_weight, coda_fp8_block_scale_bytes,
-               coda_gemm_fp8_block, coda_lmhead_policy, coda_lmhead_policy_workspace_bytes, coda_qknorm_rope,
-               coda_qknorm_rope_bwd, coda_qknorm_rope_bwd_workspace_bytes, coda_rope_table)
+               coda_gemm_fp8_block, coda_lmhead_policy, coda_lmhead_policy_workspace_bytes, coda_lmhead_score,
+               coda_lmhead_score_workspace_bytes, coda_qknorm_rope, coda_qknorm_rope_bwd,
+               coda_qknorm_rope_bwd_workspace_bytes, coda_rope_table)
 from . import (CODA_BLOCK_BACKWARD, CODA_BLOCK_FP8, CODA_BLOCK_FP8_DELAYED, coda_block_arena_bytes,
                coda_block_create, coda_block_destroy, coda_block_quantize_weights, coda_block_step_host,
                coda_block_stream, coda_block_sync, coda_block_wait_step, STATUS_NAMES)
@@ -501,3 +502,25 @@ class PolicyHead:
         coda_lmhead_policy(H, self.Wt, labels, advantage, weight, logp_old, logp_ref, *self.clip, self.kl_coef,
                            self.temperature, self.stats, self.logp[:m], dH, self.dWt, self.ws)
         return self.stats, self.logp[:m], dH, self.dWt
+
+
+class ScoringHead:
+    """The LM head as a scorer of up to M tokens: log-probabilities, entropy
+    and the k most probable tokens, from the caller's Wt [V, d]."""
+
+    def __init__(self, Wt, M: int, k: int = 0, temperature: float = 1.0):
+        self.Wt, self.k, self.temperature = Wt, k, temperature
+        V, d = Wt.shape
+        e = dict(device=Wt.device)
+        self.ws = torch.empty(coda_lmhead_score_workspace_bytes(M, d, V, k), dtype=torch.uint8, **e)
+        self.logp, self.entropy = torch.empty(M, **e), torch.empty(M, **e)
+        self.top_ids, self.top_logp = torch.empty(M, k, dtype=torch.int32, **e), torch.empty(M, k, **e)
+
+    def score(self, H, labels=None):
+        """(logp, entropy, top_ids, top_logp) of H [m, d]; logp None without
+        labels, the last two None with k = 0."""
+        m, k = H.shape[0], self.k
+        logp = None if labels is None else self.logp[:m]
+        ids, top = (self.top_ids[:m], self.top_logp[:m]) if k else (None, None)
+        coda_lmhead_score(H, self.Wt, labels, self.temperature, logp, self.entropy[:m], ids, top, self.ws)
+        return logp, self.entropy[:m], ids, top
