@@ -24,6 +24,10 @@ CODA_EPI_PLAIN = 1
 # columns covered by one block-reduction partial (psum, CE statistics, c
 # partials): partial j of a row covers columns [128 j, 128 j + 128)
 PARTIAL_COLS = 128
+# how a teacher's list is read (coda_lmhead_distill)
+CODA_DISTILL_LISTED = 0
+CODA_DISTILL_NORMALIZED = 1
+CODA_DISTILL_TAIL = 2
 
 STATUS_NAMES = {
     0: "CODA_OK", 1: "CODA_ERR_INVALID_ARG", 2: "CODA_ERR_ALIGNMENT", 3: "CODA_ERR_UNSUPPORTED",
@@ -111,6 +115,9 @@ SIGNATURES = {
                                   _I64, _I64, _I64, _P]),
     "coda_lmhead_score_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
     "coda_lmhead_score": (_INT, [_P, _P, _P, _P, _F32, _P, _P, _P, _P, _I64, _P, _SZ, _I64, _I64, _I64, _P]),
+    "coda_lmhead_distill_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _INT]),
+    "coda_lmhead_distill": (_INT, [_P, _P, _P, _P, _P, _P, _INT, _F32, _P, _P, _P, _P, _I64, _P, _SZ, _I64, _I64, _I64,
+                                   _P]),
     "coda_fp8_quantize": (_INT, [_P, _P, _P, _P, _P, _I64, _I64, _P]),
     "coda_fp8_quantize_e5m2": (_INT, [_P, _P, _P, _P, _P, _I64, _I64, _P]),
     "coda_swiglu_bwd_fp8": (_INT, [_P, _P, _P, _P, _INT, _P, _P, _P, _I64, _I64, _I64, _P]),
@@ -197,7 +204,7 @@ def _bind():
         mod.bind(handle, *(ctypes.cast(getattr(lib, n), _P).value for n in (
             "coda_fp8_block_quantize", "coda_fp8_block_quantize_weight", "coda_fp8_block_dequantize",
             "coda_gemm_fp8_block", "coda_qknorm_rope", "coda_qknorm_rope_bwd", "coda_lmhead_policy",
-            "coda_lmhead_score")))
+            "coda_lmhead_score", "coda_lmhead_distill")))
         _bound = mod
     return _bound
 
@@ -957,6 +964,20 @@ def coda_lmhead_score(Hs, Wt, labels, temperature: float, logp, entropy, top_ids
     st = (_bound or _bind()).score(Hs, Wt, labels, temperature, logp, entropy, top_ids, top_logp, ws, stream)
     if st:
         _check(st, "coda_lmhead_score")
+
+
+def coda_lmhead_distill_workspace_bytes(M: int, d: int, V: int, k: int, with_grads: bool) -> int:
+    return load_library().coda_lmhead_distill_workspace_bytes(M, d, V, k, int(with_grads))
+
+
+def coda_lmhead_distill(Hs, Wt, ids, val, weight, mode: int, temperature: float, stats, row_loss, dHs, dWt, ws,
+                        stream=None):
+    """Loss against a teacher's list of tokens (ids, val [M, k]) on the LM head
+    with its gradients; weight, row_loss and the gradients dHs, dWt may be None
+    (see include/coda.h)."""
+    st = (_bound or _bind()).distill(Hs, Wt, ids, val, weight, mode, temperature, stats, row_loss, dHs, dWt, ws, stream)
+    if st:
+        _check(st, "coda_lmhead_distill")
 
 
 def coda_unfused_workspace_bytes(M: int, d: int, N2: int) -> int:

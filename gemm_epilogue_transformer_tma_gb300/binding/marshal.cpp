@@ -27,6 +27,7 @@ decltype(&coda_qknorm_rope) p_qknorm;
 decltype(&coda_qknorm_rope_bwd) p_qknorm_bwd;
 decltype(&coda_lmhead_policy) p_policy;
 decltype(&coda_lmhead_score) p_score;
+decltype(&coda_lmhead_distill) p_distill;
 
 constexpr int kMaxDevices = 64;
 coda_handle_t g_handles[kMaxDevices];
@@ -336,9 +337,38 @@ PyObject* score(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// bind(make_handle, quantize, quantize_weight, dequantize, gemm, qknorm, qknorm_bwd, policy, score): the addresses of
-// the library's entry points
-constexpr int kBound = 9;
+// (Hs, Wt, ids, val, weight, mode, temperature, stats, row_loss, dHs, dWt, ws, stream)
+PyObject* distill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Call c(a, n, 13);
+  c.on(0, "Hs", 12);
+  const int64_t M = c.extent(0, "Hs", 0, 2), d = c.extent(0, "Hs", 1, 2), V = c.extent(1, "Wt", 0, 2);
+  const int64_t k = c.extent(2, "ids", 1, 2);
+  if (c.ok && (a[9] == Py_None) != (a[10] == Py_None)) {
+    PyErr_SetString(PyExc_ValueError, "dHs and dWt come together");
+    c.ok = false;
+  }
+  const int64_t mode = c.num(5);
+  const float T = c.real(6);
+  size_t bytes = 0;
+  void* H = c.arg(0, "Hs", BF, {M, d});
+  void* W = c.arg(1, "Wt", BF, {V, d});
+  auto* ids = static_cast<const int32_t*>(c.arg(2, "ids", I32, {M, k}));
+  auto* val = static_cast<const float*>(c.arg(3, "val", F32, {M, k}));
+  auto* w = static_cast<const float*>(c.opt(4, "weight", F32, {M}));
+  auto* stats = static_cast<float*>(c.arg(7, "stats", F32, {4}));
+  auto* loss = static_cast<float*>(c.opt(8, "row_loss", F32, {M}));
+  void* dH = c.opt(9, "dHs", BF, {M, d});
+  void* dW = c.opt(10, "dWt", BF, {V, d});
+  void* ws = c.workspace(11, &bytes);
+  return finish(c, [&] {
+    return p_distill(c.handle, H, W, ids, val, w, mode == static_cast<int>(mode) ? static_cast<int>(mode) : -1, T, stats,
+                     loss, dH, dW, k, ws, bytes, M, d, V, c.stream);
+  });
+}
+
+// bind(make_handle, quantize, quantize_weight, dequantize, gemm, qknorm, qknorm_bwd, policy, score, distill): the
+// addresses of the library's entry points
+constexpr int kBound = 10;
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Call c(a, n, kBound);
   if (!c.ok) return nullptr;
@@ -360,6 +390,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   p_qknorm_bwd = reinterpret_cast<decltype(p_qknorm_bwd)>(p[6]);
   p_policy = reinterpret_cast<decltype(p_policy)>(p[7]);
   p_score = reinterpret_cast<decltype(p_score)>(p[8]);
+  p_distill = reinterpret_cast<decltype(p_distill)>(p[9]);
   Py_RETURN_NONE;
 }
 
@@ -380,7 +411,7 @@ PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef g_methods[] = {CODA_METHOD(bind),       CODA_METHOD(quantize), CODA_METHOD(quantize_weight),
                            CODA_METHOD(dequantize), CODA_METHOD(gemm),     CODA_METHOD(qknorm),
                            CODA_METHOD(qknorm_bwd), CODA_METHOD(policy),   CODA_METHOD(score),
-                           {nullptr, nullptr, 0, nullptr}};
+                           CODA_METHOD(distill),    {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", "Argument marshalling of libcoda calls.", -1, g_methods,
                         nullptr,               nullptr, nullptr,                                nullptr};
 

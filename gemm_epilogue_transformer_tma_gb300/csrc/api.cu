@@ -9,6 +9,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/coda.h"
 #include "../../include/coda_testing.h"
@@ -1475,6 +1476,108 @@ coda_status_t coda_lmhead_score(coda_handle_t h, const void* Hs, const void* Wt,
     CODA_CUDA(launch_score_rows(cx, w.s, o, rows, V));
   }
   return CODA_OK;
+}
+
+// ---------------------------------------------------------------------------
+namespace {
+struct DistillWs {
+  DistillWork w;
+  float* dH_parts;  // as PolicyWs
+  size_t bytes;
+};
+
+DistillWs distill_layout(uint8_t* base, int64_t M, int64_t d, int64_t V, int64_t k, bool grads) {
+  DistillWs w{};
+  const int64_t T = cdiv(V, ce_tile_cols());
+  size_t off = 0;
+  auto take = [&](auto*& p, size_t values) {
+    p = base ? reinterpret_cast<std::remove_reference_t<decltype(p)>>(base + off) : nullptr;
+    off += align256(values * sizeof(*p));
+  };
+  w.w.k = static_cast<int>(k);
+  w.w.T = static_cast<int>(T);
+  take(w.w.done, 1);
+  take(w.w.terms, size_t(M));
+  take(w.w.mass, size_t(M));
+  take(w.w.count, size_t(M));
+  take(w.w.n, size_t(M));
+  take(w.w.ids, size_t(M) * k);
+  take(w.w.t, size_t(M) * k);
+  take(w.w.listed, size_t(M) * k);
+  take(w.w.at, size_t(M) * T);
+  take(w.w.pn, size_t(M) * T);
+  take(w.w.psum, size_t(M) * T);
+  if (grads) {
+    take(w.w.factor, size_t(M));
+    take(w.w.scaled, size_t(M) * d);
+    take(w.dH_parts, dh_parts_bytes(M, d, V) / 4);
+    take(w.w.kept, size_t(M) * V);
+  }
+  w.bytes = off;
+  return w;
+}
+}  // namespace
+
+size_t coda_lmhead_distill_workspace_bytes(int64_t M, int64_t d, int64_t V, int64_t k, int with_grads) {
+  if (M <= 0 || d <= 0 || V <= 0 || k <= 0 || k > kDistillMaxList) return 0;
+  return distill_layout(nullptr, M, d, V, k, with_grads != 0).bytes;
+}
+
+coda_status_t coda_lmhead_distill(coda_handle_t h, const void* Hs, const void* Wt, const int32_t* ids, const float* val,
+                                  const float* weight, int mode, float temperature, float* stats, float* row_loss,
+                                  void* dHs, void* dWt, int64_t k, void* ws, size_t ws_bytes, int64_t M, int64_t d,
+                                  int64_t V, void* stream) {
+  CODA_TRY(Check()
+               .handle(h)
+               .ptr(Hs)
+               .ptr(Wt)
+               .sptr(ids)
+               .sptr(val)
+               .opt_sptr(weight)
+               .sptr(stats)
+               .opt_sptr(row_loss)
+               .opt_ptr(dHs)
+               .opt_ptr(dWt)
+               .ptr(ws)
+               .rows(M)
+               .cols(d)
+               .cols(V)
+               .st);
+  if (M == 0 || k < 1 || k > kDistillMaxList || !temperature_ok(temperature)) return CODA_ERR_INVALID_ARG;
+  if (mode != CODA_DISTILL_LISTED && mode != CODA_DISTILL_NORMALIZED && mode != CODA_DISTILL_TAIL)
+    return CODA_ERR_INVALID_ARG;
+  const bool grads = dHs != nullptr;
+  if (grads != (dWt != nullptr)) return CODA_ERR_INVALID_ARG;
+  if (ws_bytes < coda_lmhead_distill_workspace_bytes(M, d, V, k, grads)) return CODA_ERR_WORKSPACE_TOO_SMALL;
+  const OnDevice dev(h->device);
+  const LaunchCtx cx = ctx_of(h, stream);
+  const DistillWs w = distill_layout(static_cast<uint8_t*>(ws), M, d, V, k, grads);
+  const bf16* Hb = static_cast<const bf16*>(Hs);
+  const bf16* Wb = static_cast<const bf16*>(Wt);
+  DistillIn in{};
+  in.ids = ids;
+  in.val = val;
+  in.weight = weight;
+  in.uniform = 1.0f / static_cast<float>(M);
+  in.mode = mode;
+  in.temperature = temperature;
+  in.log2e_over_t = static_cast<float>(1.4426950408889634 / double(temperature));
+  in.status = cx.status;
+  CODA_CUDA(launch_distill_list(cx, in, w.w, Hb, Wb, M, d, V));
+  CODA_CUDA(gemm_distill(cx, Hb, Wb, w.w, in.log2e_over_t, int(M), int(d), int(V)));
+  CODA_CUDA(launch_distill_rows(cx, in, w.w, DistillOut{stats, row_loss}, Hb, M, d, V));
+  if (!grads) return CODA_OK;
+  bf16* dH = static_cast<bf16*>(dHs);
+  bf16* dW = static_cast<bf16*>(dWt);
+  const int64_t parts = dh_parts(M, d, V);
+  if (parts == 1)
+    return from_cuda(
+        gemm_group_scaled_bwd(cx, w.w.kept, w.w.factor, Wb, w.w.scaled, dH, dW, int(M), int(d), int(V)));
+  // few tokens: dH in ranges of the vocabulary
+  CODA_CUDA(gemm_splitk(cx, w.w.kept, Wb, w.dH_parts, int(parts), false, int(M), int(d), int(V)));
+  CODA_CUDA(gemm_store_plus_rows(cx, w.w.kept, w.w.scaled, dW, nullptr, nullptr, int(M), int(d), int(V)));
+  return from_cuda(
+      launch_distill_dh(cx, w.dH_parts, int(parts), cdiv(M, 256) * 256 * d, w.w.factor, dH, M, d));
 }
 
 // ---------------------------------------------------------------------------

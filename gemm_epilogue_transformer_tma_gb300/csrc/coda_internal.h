@@ -187,6 +187,53 @@ struct ScoreOut {
 };
 cudaError_t launch_score_rows(const LaunchCtx& c, const ScoreStats& s, const ScoreOut& o, int64_t M, int64_t V);
 
+// Distillation from a teacher's list (distill.cu, logits_distill.cuh).
+constexpr int kDistillMaxList = 256;
+struct DistillIn {
+  const int32_t* ids;   // [M][k], an entry outside [0, V) is not used
+  const float* val;     // [M][k]
+  const float* weight;  // [M], or null: uniform
+  float uniform;
+  int mode;             // CODA_DISTILL_*
+  float temperature, log2e_over_t;
+  int* status;
+};
+struct DistillWork {
+  int k, T;             // entries of a list, 128-column blocks of the vocabulary
+  int32_t* ids;         // [M][k]: a row's distinct tokens, ascending
+  float* t;             // [M][k]: their targets
+  int32_t* count;       // [M]
+  uint16_t* at;         // [M][T]: a block's first entry | its entries << 8
+  float4* mass;         // [M]: P, r, P + r - 1
+  float* n;             // [M]: the exponent of the row's kept values, NaN: no weight
+  float* listed;        // [M][k]: the student's logits of those tokens
+  float* pn;            // [M][T]
+  float* psum;          // [M][T]
+  float4* terms;        // [M]: shares of the statistics
+  int* done;            // rows finished
+  // with gradients
+  __nv_bfloat16* kept;    // [M][V]: dL up to a factor per row
+  float* factor;          // [M]
+  __nv_bfloat16* scaled;  // [M][d]: factor H
+};
+struct DistillOut {
+  float* stats;
+  float* row_loss;  // or null
+};
+cudaError_t launch_distill_list(const LaunchCtx& c, const DistillIn& in, const DistillWork& w, const __nv_bfloat16* H,
+                                const __nv_bfloat16* Wt, int64_t M, int64_t d, int64_t V);
+cudaError_t gemm_distill(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt, const DistillWork& w,
+                         float log2e_over_t, int M, int d, int V);
+cudaError_t launch_distill_rows(const LaunchCtx& c, const DistillIn& in, const DistillWork& w, const DistillOut& o,
+                                const __nv_bfloat16* H, int64_t M, int64_t d, int64_t V);
+// dH[m] = bf16(factor[m] sum_p parts[p][m]), `stride` values between parts
+cudaError_t launch_distill_dh(const LaunchCtx& c, const float* parts, int num, int64_t stride, const float* factor,
+                              __nv_bfloat16* dH, int64_t M, int64_t d);
+// dH = diag(factor) E Wt and dW = E^T scaled (E [M][V], scaled [M][d]), one grouped launch
+cudaError_t gemm_group_scaled_bwd(const LaunchCtx& c, const __nv_bfloat16* E, const float* factor,
+                                  const __nv_bfloat16* Wt, const __nv_bfloat16* scaled, __nv_bfloat16* dH,
+                                  __nv_bfloat16* dW, int M, int d, int V);
+
 // parts_buf [parts][M rounded up to 256][N] fp32 (+)= the K ranges of A B, A
 // [M][K], B [K][N] (gemm_splitk.cuh); parts <= the k-blocks of 64 in K
 cudaError_t gemm_splitk(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_bfloat16* B, float* parts_buf, int parts,
@@ -231,6 +278,7 @@ cudaError_t gemm_group_ce_bwd(const LaunchCtx& c, const __nv_bfloat16* dL, const
 cudaError_t gemm_group_policy_bwd(const LaunchCtx& c, const __nv_bfloat16* dL, const __nv_bfloat16* Wc,
                                   const __nv_bfloat16* H, float* dH32, bool accumulate, __nv_bfloat16* dWc,
                                   const uint32_t* slot, const float* rows, int M, int d, int Vc);
+//   (slot null: dWc = dL^T H)
 cudaError_t gemm_store_plus_rows(const LaunchCtx& c, const __nv_bfloat16* dL, const __nv_bfloat16* H,
                                  __nv_bfloat16* dWc, const uint32_t* slot, const float* rows, int M, int d, int Vc);
 //   the same first-layer pair on 8-bit codes: dX = sdH sW1 dHq W1q and

@@ -8,7 +8,7 @@
 // rows while its MMAs run: 24 us, 20 without the rows.
 //
 // dL [M][Vc] and H [M][d] bf16 are both read MN-major.  rows fp32 [tokens][d]
-// and slot [Vc] as EpiStorePlusRows.
+// and slot [Vc] as EpiStorePlusRows; slot may be null: no rows (distillation).
 #pragma once
 
 #include "gemm_tc2.cuh"
@@ -197,7 +197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DwSmem::THREADS, 1)
     auto row0 = [&](int t) { return t / g.tiles_n * BM2 + static_cast<int>(rank) * 128 + quad * 32; };
     auto slot_of = [&](int t) {
       const int m = row0(t) + lane;
-      return t < num_tiles && m < g.M ? __ldg(g.slot + m) : kNoSlot;
+      return g.slot != nullptr && t < num_tiles && m < g.M ? __ldg(g.slot + m) : kNoSlot;
     };
     uint32_t s_next = slot_of(cluster_id);
     for (int t = cluster_id; t < num_tiles; t += num_clusters, ++it) {

@@ -19,18 +19,6 @@ namespace coda {
 
 namespace {
 
-// a + b and its rounding error, added to lo: sums that nearly cancel keep the
-// digits fp32 drops (fp64 units are scarce on this GPU: the same kernel in
-// fp64 took 10 us for 136 rows)
-__device__ __forceinline__ void add_exact(float& hi, float& lo, float b, float b_lo) {
-  const float s = hi + b;
-  const float t = s - hi;
-  lo += ((hi - (s - t)) + (b - t)) + b_lo;
-  hi = s;
-}
-// the pair as one number; an infinite sum has no rounding error to add
-__device__ __forceinline__ float exact_value(float hi, float lo) { return isinf(hi) ? hi : hi + lo; }
-
 // A warp's row: the log-sum-exp of its block statistics, then the token terms
 // (in every lane): the row's shares of the four statistics.
 __device__ __forceinline__ float4 policy_row(const float* __restrict__ pmax, const float* __restrict__ psum,

@@ -553,6 +553,18 @@ __device__ __forceinline__ float ex2_f(float x) {
   return y;
 }
 
+// a + b and its rounding error, added to lo: sums that nearly cancel keep the
+// digits fp32 drops (fp64 units are scarce on this GPU: the same kernel in
+// fp64 took 10 us for 136 rows)
+__device__ __forceinline__ void add_exact(float& hi, float& lo, float b, float b_lo) {
+  const float s = hi + b;
+  const float t = s - hi;
+  lo += ((hi - (s - t)) + (b - t)) + b_lo;
+  hi = s;
+}
+// the pair as one number; an infinite sum has no rounding error to add
+__device__ __forceinline__ float exact_value(float hi, float lo) { return isinf(hi) ? hi : hi + lo; }
+
 // 32 bytes to a 32-byte aligned address
 __device__ __forceinline__ void st_global_v8(float* p, const float* f) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]),

@@ -18,8 +18,8 @@ from . import (CODA_EPI_PLAIN, CODA_EPI_SWIGLU, E4M3, E5M2, coda_bwd_workspace_b
                coda_gemm_res_prms_bwd, coda_gemm_rowscale_swiglu, coda_gemm_rowscale_swiglu_bwd,
                coda_gemm_wgrad_gscale, coda_prms_num_tiles, coda_rstd_combine, coda_swiglu_bwd, coda_swiglu_bwd_fp8,
                coda_unfused_bwd, coda_unfused_fwd, coda_unfused_workspace_bytes)
-from . import (coda_fp8_block_quantize, coda_fp8_block_quantize_weight, coda_fp8_block_scale_bytes,
-               coda_gemm_fp8_block, coda_lmhead_policy, coda_lmhead_policy_workspace_bytes, coda_lmhead_score,
+from . import (CODA_DISTILL_TAIL, coda_fp8_block_quantize, coda_fp8_block_quantize_weight,
+               coda_fp8_block_scale_bytes, coda_gemm_fp8_block, coda_lmhead_distill, coda_lmhead_distill_workspace_bytes, coda_lmhead_policy, coda_lmhead_policy_workspace_bytes, coda_lmhead_score,
                coda_lmhead_score_workspace_bytes, coda_qknorm_rope, coda_qknorm_rope_bwd,
                coda_qknorm_rope_bwd_workspace_bytes, coda_rope_table)
 from . import (CODA_BLOCK_BACKWARD, CODA_BLOCK_FP8, CODA_BLOCK_FP8_DELAYED, coda_block_arena_bytes,
@@ -524,3 +524,27 @@ class ScoringHead:
         ids, top = (self.top_ids[:m], self.top_logp[:m]) if k else (None, None)
         coda_lmhead_score(H, self.Wt, labels, self.temperature, logp, self.entropy[:m], ids, top, self.ws)
         return logp, self.entropy[:m], ids, top
+
+
+class DistillHead:
+    """The LM head of a student trained on its teacher's k most probable tokens
+    (a ScoringHead's top_ids and top_logp), up to M tokens: loss statistics, the
+    rows' losses and the gradients of the hidden states and of Wt."""
+
+    def __init__(self, Wt, M: int, k: int, mode: int = CODA_DISTILL_TAIL, temperature: float = 1.0,
+                 backward: bool = True):
+        self.Wt, self.mode, self.temperature = Wt, mode, temperature
+        V, d = Wt.shape
+        e = dict(device=Wt.device)
+        self.ws = torch.empty(coda_lmhead_distill_workspace_bytes(M, d, V, k, backward), dtype=torch.uint8, **e)
+        self.stats, self.row_loss = torch.empty(4, **e), torch.empty(M, **e)
+        self.dH = torch.empty(M, d, dtype=BF, **e) if backward else None
+        self.dWt = torch.empty(V, d, dtype=BF, **e) if backward else None
+
+    def step(self, H, ids, val, weight=None):
+        """(stats, row_loss, dH, dWt); the last two None without backward."""
+        m = H.shape[0]
+        dH = None if self.dH is None else self.dH[:m]
+        coda_lmhead_distill(H, self.Wt, ids, val, weight, self.mode, self.temperature, self.stats, self.row_loss[:m],
+                            dH, self.dWt, self.ws)
+        return self.stats, self.row_loss[:m], dH, self.dWt

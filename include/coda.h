@@ -102,9 +102,10 @@ coda_status_t coda_set_wait_timeout_ns(coda_handle_t h, uint64_t ns);
  * per 128 x 256 tile.  Results are identical up to fp32 summation order
  * inside the tensor core; the choice only affects speed.
  * Not affected, because they have one form: coda_gemm_fp8_block (its form
- * follows from the sizes) and, in coda_lmhead_policy, the logits, dWt, and dHs
- * where it is summed in ranges of the vocabulary (few tokens); its logits of
- * the least workspace and dHs of many tokens follow the switch. */
+ * follows from the sizes), coda_lmhead_score, in coda_lmhead_policy the logits,
+ * dWt, and dHs where it is summed in ranges of the vocabulary (few tokens; its
+ * logits of the least workspace and dHs of many tokens follow the switch), and in
+ * coda_lmhead_distill the logits and, for few tokens, the gradients. */
 coda_status_t coda_set_sm_pairing(coda_handle_t h, int enable);
 
 /* Wide tiles for the long-K GEMMs of the backward (the RMSNorm-backward
@@ -832,6 +833,54 @@ size_t coda_lmhead_score_workspace_bytes(int64_t M, int64_t d, int64_t V, int64_
 coda_status_t coda_lmhead_score(coda_handle_t h, const void* Hs, const void* Wt, const int32_t* labels,
                                 float temperature, float* logp, float* entropy, int32_t* top_ids, float* top_logp,
                                 int64_t k, void* ws, size_t ws_bytes, int64_t M, int64_t d, int64_t V, void* stream);
+
+/* How a teacher's list is read (coda_lmhead_distill). */
+#define CODA_DISTILL_LISTED 0     /* val = log-probabilities; only the listed tokens count */
+#define CODA_DISTILL_NORMALIZED 1 /* val = logits; their softmax at the temperature */
+#define CODA_DISTILL_TAIL 2       /* val = log-probabilities; the mass they leave is the target of all others together */
+
+/* Workspace of coda_lmhead_distill: about 12 bytes per list entry, 10 per row
+ * and 128 columns of the vocabulary and 44 per row; with gradients 2 M (V + d)
+ * more (the student's exponentials in bf16 and a scaled Hs) and up to 20 MB of
+ * fp32 partial sums of dHs (used for few tokens).  A workspace for M tokens also
+ * serves any smaller number.  0 for M, d, V or k <= 0 and for k > 256. */
+size_t coda_lmhead_distill_workspace_bytes(int64_t M, int64_t d, int64_t V, int64_t k, int with_grads);
+
+/* Loss of a student's LM head against a teacher's most probable tokens, with
+ * gradients.  Row m's list has k entries (ids, val); one with a negative id is
+ * not used, entries for one token add up.  With q = softmax(Hs Wt^T /
+ * temperature)[m], targets t_v = the sum over v's entries of
+ *   exp(val)                       LISTED, TAIL
+ *   softmax(val / temperature)     NORMALIZED, over the used entries
+ * P = sum_v t_v, r = max(0, 1 - P) for TAIL and 0 otherwise, and R the sum of q
+ * over the tokens off the list:
+ *   row_loss[m] = sum_v t_v log(t_v / q_v) + r log(r / R)
+ *   loss        = sum_m weight[m] row_loss[m]
+ * the Kullback-Leibler divergence of the student from the teacher, for TAIL with
+ * all other tokens as one outcome (where the list holds the whole vocabulary
+ * there is none, and the term is left out).  weight NULL: 1 / M.
+ * stats fp32 [4] = {loss, sum weight cross-entropy (the loss without the targets'
+ * own entropy), sum weight P, sum weight (1 - R)}; row_loss fp32 [M] or NULL.
+ * The loss is computed without the cancellation of a student near its teacher,
+ * R without that of a list which holds nearly all of q.
+ * A row of weight 0 (prompt, padding) adds nothing to stats, its row_loss and its
+ * dHs row are 0, and neither its list nor its Hs row matters.  For a row with
+ * weight, an id >= V sets CODA_ERR_LABEL_RANGE in the status word; the entry is
+ * not used.  A row without a used entry has loss 0 and gradient 0.  NaN in a row
+ * with weight reaches the loss, its dHs row and dWt.
+ * If dHs is not NULL the gradients of loss are produced: dL = weight /
+ * temperature ((P + r) q_v - t_v) on the list, weight / temperature q_v (P + r -
+ * r / R) off it; dHs = dL Wt, dWt = dL^T Hs.  dL is held as a bf16 matrix and an
+ * fp32 factor per row, which dWt's contraction finds in a bf16 copy of Hs: two
+ * roundings to bf16 before that of dWt, one before that of dHs.
+ * Hs bf16 [M][d], Wt bf16 [V][d], ids int32 [M][k], val fp32 [M][k], weight fp32
+ * [M] or NULL (ids, val, weight, stats and row_loss 4-byte aligned), dHs bf16
+ * [M][d] or NULL, dWt bf16 [V][d] (required iff dHs != NULL).  1 <= k <= 256,
+ * temperature > 0 with a finite fp32 reciprocal, M >= 1. */
+coda_status_t coda_lmhead_distill(coda_handle_t h, const void* Hs, const void* Wt, const int32_t* ids, const float* val,
+                                  const float* weight, int mode, float temperature, float* stats, float* row_loss,
+                                  void* dHs, void* dWt, int64_t k, void* ws, size_t ws_bytes, int64_t M, int64_t d,
+                                  int64_t V, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* unfused ablation: the same GEMM kernel with standalone memory-bound       */
