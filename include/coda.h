@@ -871,8 +871,10 @@ size_t coda_lmhead_distill_workspace_bytes(int64_t M, int64_t d, int64_t V, int6
  * If dHs is not NULL the gradients of loss are produced: dL = weight /
  * temperature ((P + r) q_v - t_v) on the list, weight / temperature q_v (P + r -
  * r / R) off it; dHs = dL Wt, dWt = dL^T Hs.  dL is held as a bf16 matrix and an
- * fp32 factor per row, which dWt's contraction finds in a bf16 copy of Hs: two
- * roundings to bf16 before that of dWt, one before that of dHs.
+ * fp32 factor per row, chosen so that a row's largest entry is not rounded;
+ * dWt's contraction finds the factor in a bf16 copy of Hs.  Where that entry
+ * outweighs its row, the error of dHs is that of rounding it alone and of dWt 1.35
+ * to 1.45 times that; at most 1.5 and 1.8 times.
  * Hs bf16 [M][d], Wt bf16 [V][d], ids int32 [M][k], val fp32 [M][k], weight fp32
  * [M] or NULL (ids, val, weight, stats and row_loss 4-byte aligned), dHs bf16
  * [M][d] or NULL, dWt bf16 [V][d] (required iff dHs != NULL).  1 <= k <= 256,
