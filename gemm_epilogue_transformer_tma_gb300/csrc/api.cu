@@ -1499,12 +1499,12 @@ DistillWs distill_layout(uint8_t* base, int64_t M, int64_t d, int64_t V, int64_t
   take(w.w.done, 1);
   take(w.w.terms, size_t(M));
   take(w.w.mass, size_t(M));
-  take(w.w.count, size_t(M));
   take(w.w.n, size_t(M));
   take(w.w.ids, size_t(M) * k);
   take(w.w.t, size_t(M) * k);
   take(w.w.listed, size_t(M) * k);
-  take(w.w.at, size_t(M) * T);
+  take(w.w.entry, size_t(cdiv(M, 32)) * 32 * k);
+  take(w.w.at, size_t(cdiv(M, 32)) * T);
   take(w.w.pn, size_t(M) * T);
   take(w.w.psum, size_t(M) * T);
   if (grads) {

@@ -189,6 +189,7 @@ cudaError_t launch_score_rows(const LaunchCtx& c, const ScoreStats& s, const Sco
 
 // Distillation from a teacher's list (distill.cu, logits_distill.cuh).
 constexpr int kDistillMaxList = 256;
+constexpr uint32_t kNoEntry = 0xFFFFFFFFu;
 struct DistillIn {
   const int32_t* ids;   // [M][k], an entry outside [0, V) is not used
   const float* val;     // [M][k]
@@ -200,13 +201,14 @@ struct DistillIn {
 };
 struct DistillWork {
   int k, T;             // entries of a list, 128-column blocks of the vocabulary
-  int32_t* ids;         // [M][k]: a row's distinct tokens, ascending
-  float* t;             // [M][k]: their targets
-  int32_t* count;       // [M]
-  uint16_t* at;         // [M][T]: a block's first entry | its entries << 8
+  int32_t* ids;         // [M][k]: the list's tokens, each once, -1 for other entries
+  float* t;             // [M][k]: those entries' targets
+  uint32_t* at;         // [G][T], G = ceil(M / 32): where the entries of 32 rows in a block begin | how many << 16
+  uint32_t* entry;      // [G][32 k]: row of the 32 | column of the block << 5 | position in the row's list << 12, or
+                        // kNoEntry for a token that an earlier entry of its row has
   float4* mass;         // [M]: P, r, P + r - 1
   float* n;             // [M]: the exponent of the row's kept values, NaN: no weight
-  float* listed;        // [M][k]: the student's logits of those tokens
+  float* listed;        // [M][k]: the student's logits of the entries
   float* pn;            // [M][T]
   float* psum;          // [M][T]
   float4* terms;        // [M]: shares of the statistics

@@ -42,119 +42,255 @@ struct Max {
   __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
 
-// The list of a row, before its logits are known: tokens in order, each once,
-// their targets, where each vocabulary block's begin, P and r, and an exponent
-// near one of the row's logits.  A row to a CTA.  The targets' exponentials and
-// sums are in fp64, because r = 1 - P loses the digits of P where the teacher is
-// nearly certain.
-__global__ void __launch_bounds__(kThreads) distill_list_kernel(const DistillIn in, const DistillWork w,
-                                                                const __nv_bfloat16* __restrict__ H,
-                                                                const __nv_bfloat16* __restrict__ Wt, int64_t d,
-                                                                int64_t V) {
+// a b, with its rounding error
+__device__ __forceinline__ float2 mul_exact(float a, float b) {
+  const float h = a * b;
+  return make_float2(h, fmaf(a, b, -h));
+}
+// a + b for |a| >= |b|, with its rounding error
+__device__ __forceinline__ float2 add_ordered(float a, float b) {
+  const float h = a + b;
+  return make_float2(h, b - (h - a));
+}
+
+// exp(x) as an unevaluated sum of two fp32 numbers, relative error below 2^-34
+// (2^-34.9 against 64-bit mantissas over the whole range): x = n ln 2 + 16 s,
+// exp(s) from its series with the leading terms in two numbers, then four
+// squarings, which multiply its error by 16.  fp64 has 2 lanes per clock and SM:
+// 32 rows' exponentials on one SM took 8 us there.
+__device__ __forceinline__ float2 exp_exact(float x) {
+  if (!(x > -87.f)) return make_float2(expf(x), 0.f);  // 0, or NaN
+  if (x > 88.f) return make_float2(expf(x), 0.f);
+  // ln 2 in three parts: n times the first is exact
+  constexpr double kLn2 = 0.693147180559945309417232;
+  constexpr float kA = 0.693145751953125f;  // 16 bits
+  constexpr float kB = static_cast<float>(kLn2 - double(kA));
+  constexpr float kC = static_cast<float>(kLn2 - double(kA) - double(kB));
+  const float n = rintf(x * 1.44269504f);
+  float hi = x, lo = 0.f;
+  add_exact(hi, lo, -n * kA, 0.f);
+  const float2 nb = mul_exact(-n, kB);
+  add_exact(hi, lo, nb.x, fmaf(-n, kC, nb.y));
+  // s = (hi + lo) / 16, |s| < 0.022
+  const float2 s = add_ordered(hi * 0.0625f, lo * 0.0625f);
+  // exp(s) - 1 = s + s^2 / 2 + s^3 (1 / 6 + s / 24 + s^2 / 120 + s^3 / 720): the rest below 2^-50
+  const float2 sq = mul_exact(s.x, s.x);
+  const float cubic = sq.x * s.x * fmaf(s.x, fmaf(s.x, fmaf(s.x, 1.f / 720.f, 1.f / 120.f), 1.f / 24.f), 1.f / 6.f);
+  float eh = s.x, el = fmaf(sq.y, 0.5f, s.y + s.x * s.y + cubic);
+  add_exact(eh, el, sq.x * 0.5f, 0.f);
+  // e -> (1 + e)^2 - 1 = 2 e + e^2
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 q = mul_exact(eh, eh);
+    el = fmaf(2.f * eh, el, 2.f * el + q.y);
+    eh *= 2.f;
+    add_exact(eh, el, q.x, 0.f);
+    const float2 r = add_ordered(eh, el);
+    eh = r.x;
+    el = r.y;
+  }
+  add_exact(eh, el, 1.f, 0.f);
+  const float2 r = add_ordered(eh, el);
+  const float up = __int_as_float((static_cast<int>(n) + 127) << 23);  // -126 <= n <= 127
+  return make_float2(r.x * up, r.y * up);
+}
+
+// The lists, before the logits are known: one entry for each token, with its
+// target, P and r, an exponent near one of the row's logits, and, for 32 rows
+// together, which entries lie in which block of the vocabulary.  A CTA to 32
+// rows, a warp to one.  The targets and their sum are held in two fp32 numbers,
+// because r = 1 - P loses the digits of P where the teacher is nearly certain.
+constexpr int kListThreads = 1024;
+constexpr int kListBlocks = 4096;  // vocabulary blocks sorted at a time: V = 524288
+
+__host__ __device__ constexpr int list_smem(int k) { return 32 * k * 16 + (kListBlocks + 40) * 4; }
+
+__global__ void __launch_bounds__(kListThreads) distill_list_kernel(const DistillIn in, const DistillWork w,
+                                                                    const __nv_bfloat16* __restrict__ H,
+                                                                    const __nv_bfloat16* __restrict__ Wt, int64_t M,
+                                                                    int64_t d, int64_t V) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ int32_t id[kDistillMaxList], sorted[kDistillMaxList];
-  __shared__ double p[kDistillMaxList], sorted_p[kDistillMaxList];
-  __shared__ uint32_t first[kDistillMaxList / 32];
-  __shared__ double part[kWarps];
-  __shared__ float part_f[kWarps];
-  const int64_t m = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 31, k = w.k;
-  if (m == 0 && tid == 0) *w.done = 0;
-  const float weight = in.weight != nullptr ? in.weight[m] : in.uniform;
+  extern __shared__ float2 smem[];
+  const int tid = threadIdx.x, lane = tid & 31, row = tid >> 5, k = w.k;
+  float2* all_p = smem;                                            // [32][k]
+  int32_t* all_ids = reinterpret_cast<int32_t*>(smem + 32 * k);    // [32][k]
+  uint32_t* entry = reinterpret_cast<uint32_t*>(all_ids + 32 * k);  // [32 k]
+  uint32_t* start = entry + 32 * k;                                // [kListBlocks]
+  uint32_t* sums = start + kListBlocks;                            // [33]
+  float2* p = all_p + row * k;
+  int32_t* id = all_ids + row * k;
+  const int64_t m = blockIdx.x * 32ll + row;
+  if (m == 0 && lane == 0) *w.done = 0;
+  const float weight = m >= M ? 0.f : in.weight != nullptr ? in.weight[m] : in.uniform;
   if (weight == 0.f) {  // nothing of the row is looked at
-    if (tid == 0) w.n[m] = NAN;
-    return;
-  }
-  // used entries, the others behind them
-  float top = -INFINITY;
-  bool bad = false;
-  for (int j = tid; j < k; j += kThreads) {
-    const int32_t t = in.ids[m * k + j];
-    id[j] = t >= 0 && t < V ? t : INT32_MAX;
-    bad |= t >= V;
-    if (id[j] != INT32_MAX) top = fmaxf(top, in.val[m * k + j]);
-  }
-  if (bad) atomicOr(in.status, DEV_ERR_LABEL_RANGE);
-  const bool normalized = in.mode == CODA_DISTILL_NORMALIZED;
-  if (normalized) top = block_reduce(top, part_f, Max());
-  double sum = 0.0;
-  for (int j = tid; j < k; j += kThreads) {
-    double x = 0.0;
-    if (id[j] != INT32_MAX) {
-      const double v = in.val[m * k + j];
-      x = exp(normalized ? (v - double(top)) / double(in.temperature) : v);
+    if (m < M && lane == 0) w.n[m] = NAN;
+    for (int j = lane; j < k; j += 32) id[j] = -1;
+  } else {
+    float top = -INFINITY;
+    bool bad = false;
+    int lead = INT32_MAX;
+    for (int j = lane; j < k; j += 32) {
+      const int32_t t = in.ids[m * k + j];
+      const float v = in.val[m * k + j];
+      const bool used = t >= 0 && t < V;
+      id[j] = used ? t : -1;
+      p[j].x = v;
+      bad |= t >= V;
+      if (used) {
+        top = fmaxf(top, v);
+        lead = min(lead, j);
+      }
+      w.ids[m * k + j] = -1;  // found to be used below
     }
-    p[j] = x;
-    sum += x;
-  }
-  sum = block_reduce(sum, part, Add());  // its barriers also cover id and p
-  const double scale = normalized && sum > 0.0 ? 1.0 / sum : 1.0;
-  for (int j = tid; j < k; j += kThreads) {
-    int rank = 0;
-    for (int i = 0; i < k; ++i) rank += id[i] < id[j] || (id[i] == id[j] && i < j);
-    sorted[rank] = id[j];
-    sorted_p[rank] = p[j] * scale;
-  }
-  __syncthreads();
-  for (int j = tid; j < kDistillMaxList; j += kThreads) {
-    const bool f = j < k && sorted[j] != INT32_MAX && (j == 0 || sorted[j] != sorted[j - 1]);
-    const uint32_t bits = __ballot_sync(0xffffffffu, f);
-    if (lane == 0) first[j >> 5] = bits;
-  }
-  // the blocks without an entry, before the others are written below
-  for (int b = tid; b < w.T; b += kThreads) w.at[m * w.T + b] = 0;
-  __syncthreads();
-  int count = 0;
+    if (bad) atomicOr(in.status, DEV_ERR_LABEL_RANGE);
+    lead = __reduce_min_sync(0xffffffffu, lead);
+    __syncwarp();
+    // a logit of the row: of the list's first used entry, or of token 0
+    const int64_t token = lead < k ? id[lead] : 0;
+    const uint4* h = reinterpret_cast<const uint4*>(H + m * d);
+    const uint4* u = reinterpret_cast<const uint4*>(Wt + token * d);
+    float dot = 0.f;
+#pragma unroll 4
+    for (int64_t i = lane; i < d / 8; i += 32) {
+      float a[8], b[8];
+      unpack_bf16x8(__ldg(h + i), a);
+      unpack_bf16x8(__ldg(u + i), b);
 #pragma unroll
-  for (int i = 0; i < kDistillMaxList / 32; ++i) count += __popc(first[i]);
-  auto place = [&](int j) {  // distinct tokens before position j
-    int n = __popc(first[j >> 5] & ((1u << (j & 31)) - 1u));
-    for (int i = 0; i < (j >> 5); ++i) n += __popc(first[i]);
-    return n;
-  };
-  double mass = 0.0;
-  for (int j = tid; j < k; j += kThreads) {
-    if (((first[j >> 5] >> (j & 31)) & 1u) == 0u) continue;
-    const int32_t t = sorted[j];
-    const int at = place(j);
-    double x = sorted_p[j];
-    for (int i = j + 1; i < k && sorted[i] == t; ++i) x += sorted_p[i];
-    w.ids[m * k + at] = t;
-    w.t[m * k + at] = static_cast<float>(x);
-    mass += x;
-    const int32_t block = t >> 7;
-    if (j == 0 || (sorted[j - 1] >> 7) != block) {  // the block's first: how many are in it
-      int end = j;
-      while (end < k && sorted[end] != INT32_MAX && (sorted[end] >> 7) == block) ++end;
-      const int n = (end < k ? place(end) : count) - at;
-      w.at[m * w.T + block] = static_cast<uint16_t>(at | (n << 8));
+      for (int q = 0; q < 8; ++q) dot = fmaf(a[q], b[q], dot);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    const bool normalized = in.mode == CODA_DISTILL_NORMALIZED;
+    float hi = 0.f, lo = 0.f;
+    for (int j = lane; j < k; j += 32) {
+      if (id[j] < 0) continue;
+      float2 x;
+      if (normalized) {
+        // (v - top) / T with its remainder: up to 2^-24 |x| of the exponential otherwise
+        float v = p[j].x, v_lo = 0.f;
+        add_exact(v, v_lo, -top, 0.f);
+        const float z = v / in.temperature, rest = (fmaf(-z, in.temperature, v) + v_lo) / in.temperature;
+        x = make_float2(expf(z) * (1.f + (isfinite(rest) ? rest : 0.f)), 0.f);
+      } else {
+        x = exp_exact(p[j].x);
+      }
+      p[j] = x;
+      add_exact(hi, lo, x.x, x.y);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float h2 = __shfl_xor_sync(0xffffffffu, hi, o), l2 = __shfl_xor_sync(0xffffffffu, lo, o);
+      add_exact(hi, lo, h2, l2);
+    }
+    if (normalized) {  // P = 1
+      const float sum = exact_value(hi, lo);
+      for (int j = lane; j < k; j += 32)
+        if (id[j] >= 0) p[j].x /= sum;
+      hi = sum != 0.f ? sum / sum : 0.f;
+      lo = 0.f;
+    }
+    if (lane == 0) {
+      float less = hi, less_lo = lo;  // P - 1
+      add_exact(less, less_lo, -1.f, 0.f);
+      const float over = less + less_lo, P = exact_value(hi, lo);
+      const bool tail = in.mode == CODA_DISTILL_TAIL;
+      const float r = tail ? (over < 0.f ? -over : 0.f) : 0.f;
+      dot *= in.log2e_over_t;
+      w.n[m] = isfinite(dot) ? rintf(dot) : 0.f;
+      w.mass[m] = make_float4(P, r, tail && over < 0.f ? 0.f : over, 0.f);
     }
   }
-  mass = block_reduce(mass, part, Add());
-  // a logit of the row: of the list's first used entry, or of token 0
-  int lead = k;
-  for (int j = tid; j < k; j += kThreads)
-    if (id[j] != INT32_MAX) lead = min(lead, j);
-  lead = block_reduce(lead, reinterpret_cast<int*>(part_f), [](int a, int b) { return min(a, b); });
-  const int64_t token = lead < k ? id[lead] : 0;
-  const uint4* h = reinterpret_cast<const uint4*>(H + m * d);
-  const uint4* u = reinterpret_cast<const uint4*>(Wt + token * d);
-  float dot = 0.f;
-  for (int64_t i = tid; i < d / 8; i += kThreads) {
-    float a[8], b[8];
-    unpack_bf16x8(__ldg(h + i), a);
-    unpack_bf16x8(__ldg(u + i), b);
+
+  // the entries by block: counted, the counts summed, placed
+  const int64_t g = blockIdx.x;
+  uint32_t base = 0;
+  for (int b0 = 0; b0 < w.T; b0 += kListBlocks) {
+    const int nb = min(kListBlocks, w.T - b0);
+    __syncthreads();
+    for (int b = tid; b < nb; b += kListThreads) start[b] = 0;
+    __syncthreads();
+    for (int e = tid; e < 32 * k; e += kListThreads) {
+      const int b = (all_ids[e] >> 7) - b0;  // negative for an unused one
+      if (b >= 0 && b < nb) atomicAdd(&start[b], 1u);
+    }
+    __syncthreads();
+    constexpr int N = kListBlocks / kListThreads;
+    uint32_t n[N], mine = 0;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) dot = fmaf(a[q], b[q], dot);
-  }
-  dot = block_reduce(dot, part_f, Add()) * in.log2e_over_t;
-  if (tid == 0) {
-    const double r = in.mode == CODA_DISTILL_TAIL ? fmax(0.0, 1.0 - mass) : 0.0;
-    w.n[m] = isfinite(dot) ? rintf(dot) : 0.f;
-    w.mass[m] = make_float4(static_cast<float>(mass), static_cast<float>(isnan(mass) ? mass : r),
-                            static_cast<float>(mass + r - 1.0), 0.f);
-    w.count[m] = count;
+    for (int i = 0; i < N; ++i) {
+      n[i] = tid * N + i < nb ? start[tid * N + i] : 0u;
+      mine += n[i];
+    }
+    uint32_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane == 31) sums[row] = upto;
+    __syncthreads();
+    if (row == 0) {
+      uint32_t s = sums[lane], t = s;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, t, o);
+        if (lane >= o) t += x;
+      }
+      sums[lane] = t - s;
+      if (lane == 31) sums[32] = t;
+    }
+    __syncthreads();
+    uint32_t at = base + sums[row] + upto - mine;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int b = tid * N + i;
+      if (b < nb) {
+        start[b] = at;
+        w.at[g * w.T + b0 + b] = at | (n[i] << 16);
+      }
+      at += n[i];
+    }
+    __syncthreads();
+    for (int e = tid; e < 32 * k; e += kListThreads) {
+      const int32_t t = all_ids[e];
+      const int b = (t >> 7) - b0;
+      if (b >= 0 && b < nb)  // any order within a block will do
+        entry[atomicAdd(&start[b], 1u)] =
+            static_cast<uint32_t>(e / k) | static_cast<uint32_t>(t & 127) << 5 | static_cast<uint32_t>(e % k) << 12;
+    }
+    __syncthreads();
+    // start[b] is now the end of b.  Entries of one row for one token: the first
+    // in the list takes them all, summed in the list's order.
+    const uint32_t end = base + sums[32];
+    for (uint32_t i = base + tid; i < end; i += kListThreads) {
+      const uint32_t e = entry[i], r = e & 31u, j = e >> 12;
+      const int32_t t = all_ids[r * k + j];
+      const int b = (t >> 7) - b0;
+      bool first = true, more = false;
+      for (uint32_t q = b == 0 ? base : start[b - 1]; q < start[b]; ++q) {
+        const uint32_t x = entry[q];
+        if (((x ^ e) & 0xFFFu) == 0 && x != e) {
+          more = true;
+          first &= (x >> 12) > j;
+        }
+      }
+      if (first) {
+        const float2* pr = all_p + r * k;
+        float hi = pr[j].x, lo = pr[j].y;
+        if (more)
+          for (int q = j + 1; q < k; ++q)
+            if (all_ids[r * k + q] == t) add_exact(hi, lo, pr[q].x, pr[q].y);
+        const int64_t to = (g * 32 + r) * k + j;
+        w.ids[to] = t;
+        w.t[to] = exact_value(hi, lo);
+      }
+      w.entry[g * 32 * k + i] = first ? e : kNoEntry;
+    }
+    base = end;
   }
 }
 
@@ -203,7 +339,6 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
   if (weight != 0.f) {
     const float n_row = w.n[m];
     const float4 mass = w.mass[m];
-    const int count = w.count[m];
     Rest rest{n_row, 0.f};
     bool far = false;
     for (int b = tid; b < T; b += kThreads) {
@@ -224,14 +359,15 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
     const bool some = rest.s != 0.f;  // tokens off the list
     // this thread's entries
     constexpr int N = kDistillMaxList / kThreads;
+    int32_t id[N];
     float x[N], t[N], q[N];
     float top = some ? 0.f : -INFINITY;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int j = tid + i * kThreads;
-      const bool in_list = j < count;
-      x[i] = in_list ? w.listed[m * k + j] : -INFINITY;
-      t[i] = in_list ? w.t[m * k + j] : 0.f;
+      id[i] = j < k ? w.ids[m * k + j] : -1;
+      x[i] = id[i] >= 0 ? w.listed[m * k + j] : -INFINITY;
+      t[i] = id[i] >= 0 ? w.t[m * k + j] : 0.f;
       top = fmaxf(top, fmaf(x[i], c, -rest.n));
     }
     // everything in units of 2^ref, ref an integer near the largest listed logit or above it
@@ -253,7 +389,7 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
     float sum = 0.f, cross = 0.f, steep = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (tid + i * kThreads < count) {
+      if (id[i] >= 0) {
         const float lq = (x[i] - log2_S) * kLn2;
         q[i] /= S;
         sum += phi(t[i], q[i], lq);
@@ -298,10 +434,8 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
       if (exact != 0.f && isfinite(exact)) f = steep / exact;
       factor = scale * f;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int j = tid + i * kThreads;
-        if (j < count) kept[w.ids[m * k + j]] = __float2bfloat16_rn(q[i] / f);
-      }
+      for (int i = 0; i < N; ++i)
+        if (id[i] >= 0) kept[id[i]] = __float2bfloat16_rn(q[i] / f);
     }
   }
   if (GRADS) {
@@ -380,7 +514,11 @@ __global__ void __launch_bounds__(128) distill_dh_kernel(const float4* __restric
 
 cudaError_t launch_distill_list(const LaunchCtx& c, const DistillIn& in, const DistillWork& w, const __nv_bfloat16* H,
                                 const __nv_bfloat16* Wt, int64_t M, int64_t d, int64_t V) {
-  return launch_chained(c, distill_list_kernel, dim3(static_cast<unsigned>(M)), dim3(kThreads), 0, in, w, H, Wt, d, V);
+  static bool smem_ok[64] = {};
+  const cudaError_t e = allow_smem(distill_list_kernel, list_smem(kDistillMaxList), smem_ok);
+  if (e != cudaSuccess) return e;
+  return launch_chained(c, distill_list_kernel, dim3(static_cast<unsigned>((M + 31) / 32)), dim3(kListThreads),
+                        list_smem(w.k), in, w, H, Wt, M, d, V);
 }
 
 cudaError_t launch_distill_rows(const LaunchCtx& c, const DistillIn& in, const DistillWork& w, const DistillOut& o,

@@ -7,8 +7,8 @@ namespace coda {
 cudaError_t gemm_distill(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt, const DistillWork& w,
                          float log2e_over_t, int M, int d, int V) {
   auto fill = [&](auto& p) {
-    p.ids = w.ids;
     p.at = w.at;
+    p.entry = w.entry;
     p.n = w.n;
     p.listed = w.listed;
     p.pn = w.pn;

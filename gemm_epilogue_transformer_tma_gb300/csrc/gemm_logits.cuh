@@ -14,7 +14,9 @@
 // running sums start at zero, which divides the loss by the number of pieces.
 //
 // SM-pair schedule of gemm_tc2.cuh on 256 x 256 tiles; 8 epilogue warps, so
-// that a thread keeps one row's 128 sums of a half tile in registers.  2048
+// that a thread keeps one row's 128 sums of a half tile in registers, 224 of
+// them: warps 0 to 3 (TMA, MMA, two that only wait) give back what they do not
+// need.  2048
 // tokens, V = 65536, d = 2048 under the profiler: 278 us, 92 % of the tensor
 // pipe; with all exponentials kept 317, 78 % (their way through shared memory;
 // stores from the registers, a row per lane, made a whole update 5 % slower).
@@ -32,7 +34,13 @@ constexpr int kAheadKb = 8;
 struct LogitsSmem {
   static constexpr int STAGES = 6;
   static constexpr int EPI_WARPS = 8;
-  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int LEAD_WARPS = 4;  // a warpgroup
+  static constexpr int THREADS = 32 * (LEAD_WARPS + EPI_WARPS);
+  // registers: at launch, then of the two kinds of warpgroup
+  static constexpr int REGS = 168, LEAD_REGS = 56, EPI_REGS = 224;
+  static_assert(LEAD_REGS * LEAD_WARPS + EPI_REGS * EPI_WARPS <= REGS * (LEAD_WARPS + EPI_WARPS),
+                "more registers than the CTA has: setmaxnreg would wait for ever");
+  static_assert(REGS * THREADS <= 65536, "registers of an SM");
   static constexpr int A_BYTES = 128 * BK * 2;
   static constexpr int STAGE_BYTES = 2 * A_BYTES;
   static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
@@ -50,9 +58,11 @@ struct LogitsTile {
   uint32_t slot;   // this warp's two store slots in shared memory
 };
 
-// A program has Params, a State that ahead() loads while the tile's MMAs run
-// (kAhead), run(), which gets the raw products, and kStores: whether it leaves
-// bulk stores in flight.  Both are called for tiles with a row and a column only.
+// A program has Params, run(), which gets the raw products, and kStores: whether
+// it leaves bulk stores in flight.  With kAhead it also has an Early that
+// early() loads two tiles ahead and a State that ahead() makes of it and loads
+// one tile ahead, so that run() waits for neither.  All are called for tiles with
+// a row and a column only.
 template <class Prog>
 struct LogitsArgs {
   CUtensorMap H, W;  // [M][d], [V][d] bf16
@@ -83,6 +93,7 @@ struct LogitsPolicy {
     int T;
     float scale;
   };
+  using Early = int;
   struct State {};
   static __device__ __forceinline__ void run(const Params& g, const LogitsTile& t, const State&, int M,
                                              float (&v)[4][32]) {
@@ -203,131 +214,148 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
       tma_prefetch_2d(&g.W, kb * BK, tn * BN + static_cast<int>(rank) * 128);
   }
   griddep_wait();
+  __syncwarp();
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ TMA
-    // the whole warp, converged (elect_one)
-    const uint32_t leader_full = mapa_shared(smem_u32(full), 0);
-    int stage = 0;
-    uint32_t phase = 0;
-    int issued = 0, skipped = -1;
-    bool ok = true;
-    bool skip = ctl.skip_first_stage == 1 && cluster_id == 0 && leader;
-    if (ctl.skip_first_stage == 2 && cluster_id == 0 && !leader) ok = false;
-    for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
-      int tm, tn;
-      tile_coords(t, sh, tm, tn);
-      for (int kb = 0; kb < g.num_kb; ++kb) {
-        ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, ctl.timeout_ns);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          if (lane == 0 && !*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_PRODUCER);
-          break;
-        }
-        if (skip) {
-          skip = false;  // test hook: the leader never arms this stage
-          skipped = issued;
-        } else if (elect_one()) {
-          uint8_t* sa = smem + stage * L::STAGE_BYTES;
-          const uint32_t bar = leader_full + static_cast<uint32_t>(stage * 8);
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * L::STAGE_BYTES);
-          tma_load_2d_pair(sa, &g.H, bar, kb * BK, tm * BM2 + static_cast<int>(rank) * 128);
-          tma_load_2d_pair(sa + L::A_BYTES, &g.W, bar, kb * BK, tn * BN + static_cast<int>(rank) * 128);
-        }
-        __syncwarp();
-        ++issued;
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    if (lane == 0 && (skipped >= 0 || (ctl.skip_first_stage == 2 && cluster_id == 0 && !leader))) hook_hold_back(ctl);
-    if (lane == 0 &&
-        !pair_fills_landed(leader, issued, skipped, full, STAGES, L::STAGE_BYTES, fill_report, ctl.timeout_ns)) {
-      atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
-      // far longer than any copy's latency, as in gemm_tc2_kernel
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 2000000ull) {
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA
-    if (leader) {  // the whole warp, converged
+  // Every warp of a warpgroup passes the same setmaxnreg, in the branch of its
+  // roles: where the branches meet, the compiler counts with the fewer registers.
+  if (warp < L::LEAD_WARPS) {
+    regs_down<L::LEAD_REGS>();
+    if (warp == 0) {
+      // ------------------------------------------------------------------ TMA
+      // the whole warp, converged (elect_one)
+      const uint32_t leader_full = mapa_shared(smem_u32(full), 0);
       int stage = 0;
       uint32_t phase = 0;
-      int it = 0;  // pieces so far
-      // one descriptor, advanced by address / 16: the issuing warp has 512
-      // clocks per k-block and shares its scheduler with two epilogue warps
-      const uint64_t adesc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+      int issued = 0, skipped = -1;
       bool ok = true;
-      bool issued_any = false;
+      bool skip = ctl.skip_first_stage == 1 && cluster_id == 0 && leader;
+      if (ctl.skip_first_stage == 2 && cluster_id == 0 && !leader) ok = false;
       for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
+        int tm, tn;
+        tile_coords(t, sh, tm, tn);
         for (int kb = 0; kb < g.num_kb; ++kb) {
-          const bool first = kb % kPieceKb == 0;
-          const int acc = it & 1;
-          if (first)
-            ok = mbar_wait_bounded_cluster(&tempty[acc], (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u, abort_flag,
-                                           ctl.timeout_ns);
-          ok = ok && mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, ctl.timeout_ns);
+          ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, ctl.timeout_ns);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
-            if (lane == 0 && !*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_MMA);
+            if (lane == 0 && !*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_PRODUCER);
             break;
           }
-          tc_fence_after();
-          const bool last = kb % kPieceKb == kPieceKb - 1 || kb == g.num_kb - 1;
-          if (elect_one()) {
-            const uint64_t ad = adesc0 + static_cast<uint32_t>(stage * (L::STAGE_BYTES >> 4));
-            const uint64_t bd = ad + (L::A_BYTES >> 4);
-#pragma unroll
-            for (int k = 0; k < BK / UMMA_K; ++k)
-              umma_bf16_pair(tmem_base + static_cast<uint32_t>(acc * BN), ad + k * 2, bd + k * 2, IDESC,
-                             !first || k != 0 ? 1u : 0u);
-            umma_commit_pair_multicast(&empty[stage], 0x3);
-            if (last) umma_commit_pair_multicast(&tfull[acc], 0x3);
+          if (skip) {
+            skip = false;  // test hook: the leader never arms this stage
+            skipped = issued;
+          } else if (elect_one()) {
+            uint8_t* sa = smem + stage * L::STAGE_BYTES;
+            const uint32_t bar = leader_full + static_cast<uint32_t>(stage * 8);
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * L::STAGE_BYTES);
+            tma_load_2d_pair(sa, &g.H, bar, kb * BK, tm * BM2 + static_cast<int>(rank) * 128);
+            tma_load_2d_pair(sa + L::A_BYTES, &g.W, bar, kb * BK, tn * BN + static_cast<int>(rank) * 128);
           }
           __syncwarp();
-          issued_any = true;
+          ++issued;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
-          if (last) ++it;
         }
       }
-      if (issued_any) {
-        if (elect_one()) umma_commit_pair_local(drain);
-        __syncwarp();
-        if (!mbar_wait_timeout(drain, 0, ctl.timeout_ns) && lane == 0) atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
+      if (lane == 0 && (skipped >= 0 || (ctl.skip_first_stage == 2 && cluster_id == 0 && !leader))) hook_hold_back(ctl);
+      if (lane == 0 &&
+          !pair_fills_landed(leader, issued, skipped, full, STAGES, L::STAGE_BYTES, fill_report, ctl.timeout_ns)) {
+        atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
+        // far longer than any copy's latency, as in gemm_tc2_kernel
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------------ MMA
+      if (leader) {  // the whole warp, converged
+        int stage = 0;
+        uint32_t phase = 0;
+        int it = 0;  // pieces so far
+        // one descriptor, advanced by address / 16: the issuing warp has 512
+        // clocks per k-block and shares its scheduler with two epilogue warps
+        const uint64_t adesc0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+        bool ok = true;
+        bool issued_any = false;
+        for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
+          for (int kb = 0; kb < g.num_kb; ++kb) {
+            const bool first = kb % kPieceKb == 0;
+            const int acc = it & 1;
+            if (first)
+              ok = mbar_wait_bounded_cluster(&tempty[acc], (static_cast<uint32_t>(it >> 1) & 1u) ^ 1u, abort_flag,
+                                             ctl.timeout_ns);
+            ok = ok && mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, ctl.timeout_ns);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              if (lane == 0 && !*abort_flag) raise_error(ctl, abort_flag, DEV_ERR_TIMEOUT_MMA);
+              break;
+            }
+            tc_fence_after();
+            const bool last = kb % kPieceKb == kPieceKb - 1 || kb == g.num_kb - 1;
+            if (elect_one()) {
+              const uint64_t ad = adesc0 + static_cast<uint32_t>(stage * (L::STAGE_BYTES >> 4));
+              const uint64_t bd = ad + (L::A_BYTES >> 4);
+#pragma unroll
+              for (int k = 0; k < BK / UMMA_K; ++k)
+                umma_bf16_pair(tmem_base + static_cast<uint32_t>(acc * BN), ad + k * 2, bd + k * 2, IDESC,
+                               !first || k != 0 ? 1u : 0u);
+              umma_commit_pair_multicast(&empty[stage], 0x3);
+              if (last) umma_commit_pair_multicast(&tfull[acc], 0x3);
+            }
+            __syncwarp();
+            issued_any = true;
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            if (last) ++it;
+          }
+        }
+        if (issued_any) {
+          if (elect_one()) umma_commit_pair_local(drain);
+          __syncwarp();
+          if (!mbar_wait_timeout(drain, 0, ctl.timeout_ns) && lane == 0) atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
+        }
       }
     }
   } else {
     // ------------------------------------------------------------- epilogue
+    regs_up<L::EPI_REGS>();
     const int quad = warp & 3;
-    const int half = (warp - 2) >> 2;
+    const int half = (warp - L::LEAD_WARPS) >> 2;
     const uint32_t leader_tempty = mapa_shared(smem_u32(tempty), 0);
-    const uint32_t slot = smem_u32(smem + L::RING_BYTES) + static_cast<uint32_t>((warp - 2) * 2 * STORE_SLOT_BYTES);
+    const uint32_t slot =
+        smem_u32(smem + L::RING_BYTES) + static_cast<uint32_t>((warp - L::LEAD_WARPS) * 2 * STORE_SLOT_BYTES);
     const int pieces = (g.num_kb + kPieceKb - 1) / kPieceKb;
     auto tile_of = [&](int t) {
       int tm, tn;
-      tile_coords(t, sh, tm, tn);
+      tile_coords(min(t, num_tiles - 1), sh, tm, tn);
       LogitsTile tile;
       tile.m0 = (tm * 2 + static_cast<int>(rank)) * 128 + quad * 32;
       tile.n0 = tn * BN + half * (BN / 2);
-      tile.nv = g.V - tile.n0;
+      tile.nv = t < num_tiles && tile.m0 < g.M ? g.V - tile.n0 : 0;  // 0 or less: nothing to do
       tile.part = tn * 2 + half;
       tile.lane = lane;
       tile.slot = slot;
       return tile;
     };
+    // Three tiles at a time: this one's run, the next one's ahead, and early of the one after
+    LogitsTile tile = tile_of(cluster_id), next = tile_of(cluster_id + num_clusters);
+    typename Prog::Early early{};
+    typename Prog::State state{};
+    if constexpr (Prog::kAhead) {
+      if (tile.nv > 0) state = Prog::ahead(g.p, tile, Prog::early(g.p, tile), g.M);
+      if (next.nv > 0) early = Prog::early(g.p, next);
+    }
     int it = 0;
     bool ok = true;
     for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
-      typename Prog::State st{};
+      typename Prog::State next_state{};
+      const LogitsTile later = tile_of(t + 2 * num_clusters);
       if constexpr (Prog::kAhead) {
-        const LogitsTile tile = tile_of(t);
-        if (tile.m0 < g.M && tile.nv > 0) st = Prog::ahead(g.p, tile, g.M);
+        if (next.nv > 0) next_state = Prog::ahead(g.p, next, early, g.M);
+        if (later.nv > 0) early = Prog::early(g.p, later);
       }
       float v[4][32];
       for (int p = 0; p < pieces; ++p, ++it) {
@@ -357,8 +385,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
         if (lane == 0) mbar_arrive_cluster_relaxed(leader_tempty + static_cast<uint32_t>(acc * 8));
       }
       if (!ok) break;
-      const LogitsTile tile = tile_of(t);  // not held through the pieces: registers are short
-      if (tile.m0 < g.M && tile.nv > 0) Prog::run(g.p, tile, st, g.M, v);
+      if (tile.nv > 0) Prog::run(g.p, tile, state, g.M, v);
+      tile = next;
+      next = later;
+      state = next_state;
     }
     if (Prog::kStores) {
       __syncwarp();

@@ -28,36 +28,72 @@ struct LogitsDistill {
   static constexpr bool kStores = KEEP;
   struct Params {
     CUtensorMap kept;    // KEEP: [M][V] bf16, 32 x 32 boxes
-    const int32_t* ids;  // [M][k]: the row's distinct tokens, ascending
-    const uint16_t* at;  // [M][T]: a block's first entry | its entries << 8
-    const float* n;      // [M]: the row's pn, NaN for a row without weight
+    const uint32_t* at;     // [G][T], G = ceil(M / 32): where a block's entries begin | how many << 16
+    const uint32_t* entry;  // [G][32 k]: row of the 32 | column of the block << 5 | position in the row's list << 12,
+                            // or kNoEntry
+    const float* n;         // [M]: the row's pn, NaN for a row without weight
     float* listed;       // [M][k]: the entries' logits
     float* pn;           // [M][T], T = ceil(V / 128)
     float* psum;         // [M][T]
     int T, k;
     float c;             // log2(e) / temperature
   };
+  // The entries of a warp's 32 rows in its 128 columns, 2 of them where 64 are
+  // listed of 128256: one to a lane.  Where they are is loaded a tile ahead, so
+  // that no load of the epilogue waits for another (a list per row, looked
+  // through by its thread, made the tile 5000 clocks longer, and as much again
+  // for taking the entries out by a test of each column).
+  using Early = uint32_t;
   struct State {
     float n;
-    uint32_t on[4];  // the block's listed columns
-    int first;
+    uint32_t at, entry;
   };
-  static __device__ __forceinline__ State ahead(const Params& g, const LogitsTile& t, int M) {
-    State st{NAN, {0u, 0u, 0u, 0u}, 0};
+  static __device__ __forceinline__ uint32_t entry_of(const Params& g, const LogitsTile& t, uint32_t at, uint32_t i) {
+    return i < (at >> 16) ? ld_here_u32(g.entry + static_cast<int64_t>(t.m0 >> 5) * (32 * g.k) + (at & 0xFFFFu) + i) : 0u;
+  }
+  static __device__ __forceinline__ Early early(const Params& g, const LogitsTile& t) {
+    return ld_here_u32(g.at + static_cast<int64_t>(t.m0 >> 5) * g.T + t.part);
+  }
+  static __device__ __forceinline__ State ahead(const Params& g, const LogitsTile& t, Early at, int M) {
     const int m = t.m0 + t.lane;
-    if (m >= M) return st;
-    st.n = g.n[m];
-    if (isnan(st.n)) return st;
-    const uint32_t e = g.at[static_cast<int64_t>(m) * g.T + t.part];
-    st.first = static_cast<int>(e & 255u);
-    const int32_t* id = g.ids + static_cast<int64_t>(m) * g.k + st.first;
-    for (uint32_t j = 0; j < (e >> 8); ++j) {
-      const int col = id[j] - t.n0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if ((col >> 5) == c) st.on[c] |= 1u << (col & 31);
+    return State{m < M ? ld_here_f32(g.n + m) : NAN, at, entry_of(g, t, at, t.lane)};
+  }
+  // Writes the entries' logits out of v, 32 columns [32 c, 32 c + 32) of 32
+  // rows, and puts -infinity in their place: through shared memory, where a lane
+  // reaches any row's, and only if there are any.
+  static __device__ __forceinline__ void take(const Params& g, const LogitsTile& t, const State& st, int c,
+                                              float (&v)[32]) {
+    const uint32_t count = st.at >> 16;
+    bool staged = false;
+    for (uint32_t i = t.lane; i - t.lane < count; i += 32) {
+      const uint32_t e = i < 32 ? st.entry : entry_of(g, t, st.at, i);
+      const bool here = i < count && e != kNoEntry && ((e >> 10) & 3u) == static_cast<uint32_t>(c);
+      if (!__any_sync(0xffffffffu, here)) continue;
+      if (!staged) {
+        slots_acquire(t.lane);
+        stage_f32x32(t.slot, t.lane, v);
+        __syncwarp();
+        staged = true;
+      }
+      if (here) {
+        const uint32_t r = e & 31u, col = (e >> 5) & 31u;
+        const uint32_t at = t.slot + r * 128u + ((((col >> 2) ^ r) & 7u) << 4) + (col & 3u) * 4u;
+        g.listed[static_cast<int64_t>(t.m0 + static_cast<int>(r)) * g.k + (e >> 12)] = ld_shared_f1(at);
+        st_shared_f1(at, -INFINITY);
+      }
     }
-    return st;
+    if (!staged) return;
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float4 x = ld_shared_f4(t.slot + static_cast<uint32_t>(t.lane) * 128u +
+                                    ((static_cast<uint32_t>(q) ^ (static_cast<uint32_t>(t.lane) & 7u)) << 4));
+      v[4 * q] = x.x;
+      v[4 * q + 1] = x.y;
+      v[4 * q + 2] = x.z;
+      v[4 * q + 3] = x.w;
+    }
+    __syncwarp();
   }
   static __device__ __forceinline__ void run(const Params& g, const LogitsTile& t, const State& st, int M,
                                              float (&v)[4][32]) {
@@ -72,17 +108,9 @@ struct LogitsDistill {
         for (int i = 0; i < 32; ++i)
           if (c * 32 + i >= nv) v[c][i] = -INFINITY;
     }
-    float* out = g.listed + static_cast<int64_t>(m) * g.k + st.first;
+    if ((st.at >> 16) != 0) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (__any_sync(0xffffffffu, st.on[c] != 0u)) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if ((st.on[c] >> i) & 1u) {
-            *out++ = v[c][i];
-            v[c][i] = -INFINITY;
-          }
-      }
+      for (int c = 0; c < 4; ++c) take(g, t, st, c, v[c]);
     }
     float mx = -INFINITY;
 #pragma unroll

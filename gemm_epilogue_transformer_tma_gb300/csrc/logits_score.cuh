@@ -35,7 +35,9 @@ struct LogitsScore {
   struct State {
     int y;
   };
-  static __device__ __forceinline__ State ahead(const Params& g, const LogitsTile& t, int M) {
+  using Early = int;
+  static __device__ __forceinline__ Early early(const Params&, const LogitsTile&) { return 0; }
+  static __device__ __forceinline__ State ahead(const Params& g, const LogitsTile& t, Early, int M) {
     const int m = t.m0 + t.lane;
     return State{g.labels != nullptr && m < M ? g.labels[m] : -1};
   }

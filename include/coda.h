@@ -839,8 +839,8 @@ coda_status_t coda_lmhead_score(coda_handle_t h, const void* Hs, const void* Wt,
 #define CODA_DISTILL_NORMALIZED 1 /* val = logits; their softmax at the temperature */
 #define CODA_DISTILL_TAIL 2       /* val = log-probabilities; the mass they leave is the target of all others together */
 
-/* Workspace of coda_lmhead_distill: about 12 bytes per list entry, 10 per row
- * and 128 columns of the vocabulary and 44 per row; with gradients 2 M (V + d)
+/* Workspace of coda_lmhead_distill: 16 bytes per list entry, 8.2 per row and 128
+ * columns of the vocabulary and 36 per row; with gradients 2 M (V + d)
  * more (the student's exponentials in bf16 and a scaled Hs) and up to 20 MB of
  * fp32 partial sums of dHs (used for few tokens).  A workspace for M tokens also
  * serves any smaller number.  0 for M, d, V or k <= 0 and for k > 256. */
