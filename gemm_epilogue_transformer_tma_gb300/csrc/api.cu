@@ -1403,7 +1403,8 @@ struct ScoreWs {
 
 ScoreWs score_layout(uint8_t* base, int64_t M, int64_t V, int64_t k) {
   ScoreWs w{};
-  const int64_t R = score_rows(M, V, k), T = cdiv(V, ce_tile_cols());
+  const int64_t cols = M <= kScoreFew ? score_few_rows(V) : ce_tile_cols();
+  const int64_t R = score_rows(M, V, k), T = cdiv(V, cols);
   size_t off = 0;
   auto take = [&](size_t values) {
     uint8_t* p = base ? base + off : nullptr;
@@ -1411,7 +1412,7 @@ ScoreWs score_layout(uint8_t* base, int64_t M, int64_t V, int64_t k) {
     return reinterpret_cast<float*>(p);
   };
   w.s.T = static_cast<int>(T);
-  w.s.sub_cols = ce_tile_cols() / 4;
+  w.s.sub_cols = static_cast<int>(cols / 4);
   w.s.pmax = take(size_t(R) * T);
   w.s.psum = take(size_t(R) * T);
   w.s.pdot = take(size_t(R) * T);
@@ -1420,7 +1421,8 @@ ScoreWs score_layout(uint8_t* base, int64_t M, int64_t V, int64_t k) {
     w.s.sub = take(size_t(R) * T * 4);
     w.s.logits = take(size_t(R) * V);
   }
-  w.bytes = off;
+  // a workspace serves fewer rows too: of them, kScoreFew may take the most
+  w.bytes = M > kScoreFew ? std::max(off, score_layout(nullptr, kScoreFew, V, k).bytes) : off;
   return w;
 }
 }  // namespace

@@ -170,6 +170,14 @@ struct ScoreStats {
   int T;          // blocks of a row
   int sub_cols;   // a quarter of a block
 };
+// Up to kScoreFew rows take the kernel of gemm_score_few.cuh, whose blocks have
+// score_few_rows(V) columns: 128 or less, a multiple of 4, such that the blocks
+// fill the SMs of a GB300 evenly (a constant: a workspace is sized without a
+// device).  Others have blocks of 128.  At d = 4096, V = 128256 with 8
+// alternatives: 64 rows 208 us, 128 (of a kernel for so many) 293; 129 by the
+// other kernel 210.
+constexpr int64_t kScoreFew = 64, kScoreSms = 152;
+int score_few_rows(int64_t V);
 cudaError_t gemm_score(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt, const int32_t* labels,
                        const ScoreStats& s, float log2e_over_t, int M, int d, int V);
 // logp, entropy, the k highest logits' tokens and log-probabilities of M rows

@@ -101,6 +101,8 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 
 constexpr int kTopThreads = 128;
 constexpr int kTopWarps = kTopThreads / 32;
+constexpr int kTopHeld = 9;               // blocks whose statistics a thread keeps in registers: V = 147456
+constexpr int kTopSubs = 512;             // sub-blocks read again
 constexpr int kTopList = 1024;            // candidates held in shared memory
 constexpr int kTopSlack = 64;             // ranked beside the k: selecting more exactly costs a pass over the list
 constexpr int kTopFinal = kScoreMaxTop + kTopSlack;
@@ -108,10 +110,11 @@ constexpr int kTopFinal = kScoreMaxTop + kTopSlack;
 struct TopSmem {
   uint64_t list[kTopList];  // rank_key(logit) << 32 | ~token: the order of the answer, largest first
   uint64_t best[kTopFinal];
+  int keys[kTopSubs], subs[kTopSubs];
   int hist[256];
   int pick[2];
-  int n, n_best;
-  RowSum part[kTopWarps];
+  int n, n_keys, n_subs, n_best;
+  float part[kTopWarps][3];
 };
 
 // pick[0]: the largest digit with at least `need` counted at it and above,
@@ -180,32 +183,181 @@ __device__ __forceinline__ void each_logit(const float* __restrict__ sub, const 
   }
 }
 
-// With alternatives: 128 threads to a row.
+// With alternatives: 128 threads to a row.  4096 rows of V = 128256, k = 64
+// @TOP@
+// HELD: T <= kTopHeld kTopThreads; otherwise what a thread would hold is read again.
+template <bool HELD>
 __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats s, const ScoreOut o, int64_t M,
                                                                 int64_t V) {
   griddep_wait();
   griddep_launch_dependents();
   __shared__ TopSmem sm;
   const int64_t m = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = o.k;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = o.k, T = s.T;
   const float c = o.log2e_over_t;
-  RowSum r = merge_warp(row_blocks(s, m, tid, kTopThreads, c), c);
-  if (lane == 0) sm.part[warp] = r;
-  const float* sub = s.sub + m * 4 * s.T;
+  const float* pmax = s.pmax + m * T;
+  const float* psum = s.psum + m * T;
+  const float* pdot = s.pdot + m * T;
+  const float* sub = s.sub + m * 4 * T;
   const float* logits = s.logits + m * V;
   const int cols = s.sub_cols, subs = static_cast<int>((V + cols - 1) / cols);
-  for (int i = tid; i < 256; i += kTopThreads) sm.hist[i] = 0;
-  if (tid == 0) sm.n = sm.n_best = 0;
-  __syncthreads();
-  r = sm.part[0];
+  // The k-th largest is bounded by the k-th largest of the blocks' maxima, or, of
+  // k blocks or fewer, by that of the sub-blocks'.
+  const bool fine = T <= k;
+  const float* keys = fine ? sub : pmax;
+  const int num_keys = fine ? subs : T;
+  constexpr int N = HELD ? kTopHeld : 1;
+  float key[N], bm[N], bs[N], bd[N];
+  if (HELD) {
 #pragma unroll
-  for (int w = 1; w < kTopWarps; ++w) merge(r, sm.part[w], c);
+    for (int j = 0; j < N; ++j) {
+      const int b = tid + j * kTopThreads;
+      bm[j] = b < T ? pmax[b] : -INFINITY;
+      bs[j] = b < T ? psum[b] : 0.f;
+      bd[j] = b < T ? pdot[b] : 0.f;
+      key[j] = !fine ? bm[j] : b < num_keys ? keys[b] : -INFINITY;
+    }
+  }
+  auto each_key = [&](auto&& f) {
+    if (HELD) {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (tid + j * kTopThreads < num_keys) f(tid + j * kTopThreads, key[j]);
+    } else {
+      for (int b = tid; b < num_keys; b += kTopThreads) f(b, keys[b]);
+    }
+  };
+  for (int i = tid; i < 256; i += kTopThreads) sm.hist[i] = 0;
+  if (tid == 0) sm.n = sm.n_keys = sm.n_subs = sm.n_best = 0;
+
+  // the row's largest logit, and the range of the keys
+  float mx = -INFINITY, low = INFINITY;
+  each_key([&](int, float x) {
+    mx = fmaxf(mx, x);
+    low = fminf(low, x == -INFINITY ? INFINITY : x);
+  });
+#pragma unroll
+  for (int q = 16; q > 0; q >>= 1) {
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, q));
+    low = fminf(low, __shfl_xor_sync(0xffffffffu, low, q));
+  }
+  if (lane == 0) {
+    sm.part[warp][0] = mx;
+    sm.part[warp][1] = low;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kTopWarps; ++w) {
+    mx = fmaxf(mx, sm.part[w][0]);
+    low = fminf(low, sm.part[w][1]);
+  }
+  // A bin for each 256th of the range, in the same order: one count of the keys
+  // bounds the k-th of them.
+  const float width = mx > low ? 255.f / (mx - low) : 0.f;
+  auto bin = [&](float x) { return max(0, min(255, __float2int_rd((x - low) * width))); };
+  const bool select = num_keys > k;
+  if (select) each_key([&](int, float x) { atomicAdd(&sm.hist[bin(x)], 1); });
+  // the sums relative to the largest; it itself (of equal ones, one) left out
+  float equal = 0.f, sum = 0.f, dot = 0.f;
+  auto block = [&](float x, float ps, float pd) {
+    const float dx = x == mx ? 0.f : x - mx, f = ex2_f(dx * c);
+    equal += x == mx ? 1.f : 0.f;
+    sum = x == mx ? sum + ps : fmaf(f, 1.f + ps, sum);
+    dot += x == mx ? pd : f * fmaf(dx, 1.f + ps, pd);
+  };
+  if (HELD) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (tid + j * kTopThreads < T) block(bm[j], bs[j], bd[j]);
+  } else {
+    for (int b = tid; b < T; b += kTopThreads) block(pmax[b], psum[b], pdot[b]);
+  }
+#pragma unroll
+  for (int q = 16; q > 0; q >>= 1) {
+    equal += __shfl_xor_sync(0xffffffffu, equal, q);
+    sum += __shfl_xor_sync(0xffffffffu, sum, q);
+    dot += __shfl_xor_sync(0xffffffffu, dot, q);
+  }
+  __syncthreads();
+  if (lane == 0) {
+    sm.part[warp][0] = equal;
+    sm.part[warp][1] = sum;
+    sm.part[warp][2] = dot;
+  }
+  if (warp == 0 && select) pick_digit(sm, k, lane);
+  __syncthreads();
+  // what falls into that bin or above, and, since its edge is rounded (by less
+  // than 2^-20 of the larger end), perhaps a little below
+  const float edge = select ? low + static_cast<float>(sm.pick[0]) * ((mx - low) * (1.f / 255.f)) : -INFINITY;
+  const float least = select && sm.pick[0] > 0 ? edge - 2e-6f * fmaxf(fabsf(low), fabsf(mx)) : -INFINITY;
+  each_key([&](int i, float x) {
+    if (!(x < least)) {
+      const int at = atomicAdd(&sm.n_keys, 1);
+      if (at < kTopSubs) sm.keys[at] = i;
+    }
+  });
+  equal = sum = dot = 0.f;
+#pragma unroll
+  for (int w = 0; w < kTopWarps; ++w) {
+    equal += sm.part[w][0];
+    sum += sm.part[w][1];
+    dot += sm.part[w][2];
+  }
+  const RowSum r{mx, (equal - 1.f) + sum, dot};
+  __syncthreads();
   if (tid == 0) write_row(s, o, r, m, V);
+  // those blocks' sub-blocks
+  const int n_keys = sm.n_keys;
+  if (n_keys <= kTopSubs) {
+    for (int j = tid; j < n_keys; j += kTopThreads) {
+      const int i = sm.keys[j];
+      const float4 y = fine ? make_float4(0.f, 0.f, 0.f, 0.f) : reinterpret_cast<const float4*>(sub)[i];
+      const bool hit[4] = {!(y.x < least), !(y.y < least) && 4 * i + 1 < subs, !(y.z < least) && 4 * i + 2 < subs,
+                           !(y.w < least) && 4 * i + 3 < subs};
+      int to = atomicAdd(&sm.n_subs, fine ? 1 : hit[0] + hit[1] + hit[2] + hit[3]);
+      if (fine) {
+        sm.subs[to] = i;  // no more of them than keys
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (hit[q]) {
+            if (to < kTopSubs) sm.subs[to] = 4 * i + q;
+            ++to;
+          }
+      }
+    }
+  }
+  __syncthreads();
+  const int n_subs = n_keys <= kTopSubs ? sm.n_subs : kTopSubs + 1;
+  if (n_subs <= kTopSubs) {
+    constexpr int F = 8;  // sub-blocks in flight per warp
+    for (int i0 = warp; i0 < n_subs; i0 += kTopWarps * F) {
+      int64_t at[F];
+      float v[F];
+#pragma unroll
+      for (int q = 0; q < F; ++q) {
+        const int i = i0 + q * kTopWarps;
+        at[q] = i < n_subs && lane < cols ? static_cast<int64_t>(sm.subs[i]) * cols + lane : V;
+        v[q] = at[q] < V ? logits[at[q]] : 0.f;
+      }
+#pragma unroll
+      for (int q = 0; q < F; ++q)
+        if (at[q] < V && !(v[q] < least)) {
+          const int to = atomicAdd(&sm.n, 1);
+          if (to < kTopList)
+            sm.list[to] = (static_cast<uint64_t>(rank_key(v[q])) << 32) | static_cast<uint32_t>(~at[q]);
+        }
+    }
+    __syncthreads();
+  }
+  int n = n_subs <= kTopSubs ? sm.n : kTopList + 1;
+  for (int i = tid; i < 256; i += kTopThreads) sm.hist[i] = 0;
+  __syncthreads();
 
   // One step of a selection by digits of 8 bits, from the highest: counts the
   // digit of the keys that share the digits found so far, then finds the
   // largest digit that leaves `need` at or above it.  Returns how many keys
-  // of all are at least the new prefix.
+  // have the new prefix.
   auto step = [&](auto count_all, auto& prefix, int& need, int shift) {
     count_all(shift);
     __syncthreads();
@@ -219,30 +371,12 @@ __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats
     need -= above;
     return here;
   };
-
-  // a bound on the k-th largest sub-block maximum from its upper 16 bits
-  uint32_t lo = 0;
-  if (subs > k) {
-    int need = k;
-#pragma unroll 1
-    for (int shift = 24; shift >= 16; shift -= 8)
-      step(
-          [&](int sh) {
-            for (int j = tid; j < subs; j += kTopThreads) {
-              const uint32_t key = rank_key(sub[j]);
-              if (sh == 24 || (key >> 24) == (lo >> 24)) atomicAdd(&sm.hist[(key >> sh) & 255u], 1);
-            }
-          },
-          lo, need, shift);
-  }
   auto gather = [&](uint32_t least) {
     each_logit(sub, logits, subs, cols, V, least, warp, kTopWarps, lane, [&](bool there, uint32_t key, uint32_t token) {
       append(sm, there && key >= least, key, token, lane);
     });
     __syncthreads();
   };
-  gather(lo);
-  int n = sm.n;
   if (n > kTopList) {
     // Many logits are near the k-th, or equal.  Equal ones are taken in token
     // order by one warp, which ends as soon as it has them: a row of zeros
@@ -281,7 +415,7 @@ __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats
       for (int shift = 24; shift >= 0 && k - need + here > kTopList; shift -= 8)
         here = step(
             [&](int sh) {
-              each_logit(sub, logits, subs, cols, V, lo, warp, kTopWarps, lane,
+              each_logit(sub, logits, subs, cols, V, key, warp, kTopWarps, lane,
                          [&](bool there, uint32_t x, uint32_t) {
                            if (there && (sh == 24 || (x >> (sh + 8)) == (key >> (sh + 8))))
                              atomicAdd(&sm.hist[(x >> sh) & 255u], 1);
@@ -299,7 +433,7 @@ __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats
   }
 
   // more than the k and some: by digits over the list
-  uint64_t least = 0;
+  uint64_t from = 0;
   if (n > k + kTopSlack) {
     int need = k, here = n;
 #pragma unroll 1
@@ -308,13 +442,13 @@ __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats
           [&](int sh) {
             for (int i = tid; i < n; i += kTopThreads) {
               const uint64_t x = sm.list[i];
-              if (sh == 56 || (x >> (sh + 8)) == (least >> (sh + 8))) atomicAdd(&sm.hist[(x >> sh) & 255u], 1);
+              if (sh == 56 || (x >> (sh + 8)) == (from >> (sh + 8))) atomicAdd(&sm.hist[(x >> sh) & 255u], 1);
             }
           },
-          least, need, shift);
+          from, need, shift);
     for (int i = tid; i < n; i += kTopThreads) {
       const uint64_t x = sm.list[i];
-      if (x >= least) sm.best[atomicAdd(&sm.n_best, 1)] = x;
+      if (x >= from) sm.best[atomicAdd(&sm.n_best, 1)] = x;
     }
     __syncthreads();
     n = sm.n_best;
@@ -327,6 +461,7 @@ __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats
   for (int i = tid; i < n; i += kTopThreads) {
     const uint64_t x = sm.best[i];
     int rank = 0;
+#pragma unroll 4
     for (int j = 0; j < n; ++j) rank += sm.best[j] > x;
     if (rank < k) {
       const int64_t at = m * k + rank;
@@ -341,7 +476,7 @@ __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats
 cudaError_t launch_score_rows(const LaunchCtx& c, const ScoreStats& s, const ScoreOut& o, int64_t M, int64_t V) {
   if (o.k == 0)
     return launch_chained(c, score_rows_kernel, dim3(static_cast<unsigned>((M + 3) / 4)), dim3(128), 0, s, o, M, V);
-  return launch_chained(c, score_top_kernel, dim3(static_cast<unsigned>(M)), dim3(kTopThreads), 0, s, o, M, V);
+  return launch_chained(c, s.T <= kTopHeld * kTopThreads ? score_top_kernel<true> : score_top_kernel<false>, dim3(static_cast<unsigned>(M)), dim3(kTopThreads), 0, s, o, M, V);
 }
 
 }  // namespace coda
