@@ -67,6 +67,10 @@ template <class Prog>
 struct LogitsArgs {
   CUtensorMap H, W;  // [M][d], [V][d] bf16
   int M, V;
+  // The kernel before this one writes neither H nor W, and it has itself waited
+  // for the one before it ahead of its launch_dependents: copies and MMAs need
+  // not wait for it, only the epilogue does
+  int operands_ready;
   int tiles_m, tiles_n, num_kb, group_m;
   typename Prog::Params p;
 };
@@ -213,7 +217,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
     for (int kb = 0; kb < min(g.num_kb, kAheadKb); ++kb)
       tma_prefetch_2d(&g.W, kb * BK, tn * BN + static_cast<int>(rank) * 128);
   }
-  griddep_wait();
+  if (warp >= L::LEAD_WARPS || !g.operands_ready) griddep_wait();
   __syncwarp();
 
   // Every warp of a warpgroup passes the same setmaxnreg, in the branch of its

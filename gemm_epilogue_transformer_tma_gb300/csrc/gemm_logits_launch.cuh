@@ -6,15 +6,16 @@
 
 namespace coda {
 
-// p: the program's parameters, complete
+// p: the program's parameters, complete; operands_ready as in LogitsArgs
 template <class Prog>
 cudaError_t launch_logits(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt,
-                          const typename Prog::Params& p, int M, int d, int V) {
+                          const typename Prog::Params& p, int M, int d, int V, bool operands_ready = false) {
   using L = LogitsSmem;
   LogitsArgs<Prog> g{};
   if (!make_operand_maps(&g.H, &g.W, H, false, Wt, false, M, V, d, 128)) return cudaErrorInvalidValue;
   g.M = M;
   g.V = V;
+  g.operands_ready = operands_ready;
   g.tiles_m = (M + BM2 - 1) / BM2;
   g.tiles_n = (V + 255) / 256;
   g.num_kb = (d + BK - 1) / BK;
