@@ -1577,9 +1577,15 @@ coda_status_t coda_lmhead_distill(coda_handle_t h, const void* Hs, const void* W
         gemm_group_scaled_bwd(cx, w.w.kept, w.w.factor, Wb, w.w.scaled, dH, dW, int(M), int(d), int(V)));
   // few tokens: dH in ranges of the vocabulary
   CODA_CUDA(gemm_splitk(cx, w.w.kept, Wb, w.dH_parts, int(parts), false, int(M), int(d), int(V)));
-  CODA_CUDA(gemm_store_plus_rows(cx, w.w.kept, w.w.scaled, dW, nullptr, nullptr, int(M), int(d), int(V)));
-  return from_cuda(
-      launch_distill_dh(cx, w.dH_parts, int(parts), cdiv(M, 256) * 256 * d, w.w.factor, dH, M, d));
+  SplitDh finish{};
+  finish.parts = reinterpret_cast<const float4*>(w.dH_parts);
+  finish.num = static_cast<int>(parts);
+  finish.stride4 = cdiv(M, 256) * 256 * d / 4;
+  finish.n4 = M * d / 4;
+  finish.d4 = d / 4;
+  finish.factor = w.w.factor;
+  finish.out = reinterpret_cast<uint2*>(dH);
+  return from_cuda(gemm_store_plus_rows(cx, w.w.kept, w.w.scaled, dW, nullptr, nullptr, int(M), int(d), int(V), finish));
 }
 
 // ---------------------------------------------------------------------------

@@ -217,7 +217,7 @@ struct DistillWork {
   float4* mass;         // [M]: P, r, P + r - 1
   float* n;             // [M]: the exponent of the row's kept values, NaN: no weight
   float* listed;        // [M][k]: the student's logits of the entries
-  float* pn;            // [M][T]
+  float* pn;            // [M][T], logits_distill.cuh
   float* psum;          // [M][T]
   float4* terms;        // [M]: shares of the statistics
   int* done;            // rows finished
@@ -236,9 +236,6 @@ cudaError_t gemm_distill(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_
                          float log2e_over_t, int M, int d, int V);
 cudaError_t launch_distill_rows(const LaunchCtx& c, const DistillIn& in, const DistillWork& w, const DistillOut& o,
                                 const __nv_bfloat16* H, int64_t M, int64_t d, int64_t V);
-// dH[m] = bf16(factor[m] sum_p parts[p][m]), `stride` values between parts
-cudaError_t launch_distill_dh(const LaunchCtx& c, const float* parts, int num, int64_t stride, const float* factor,
-                              __nv_bfloat16* dH, int64_t M, int64_t d);
 // dH = diag(factor) E Wt and dW = E^T scaled (E [M][V], scaled [M][d]), one grouped launch
 cudaError_t gemm_group_scaled_bwd(const LaunchCtx& c, const __nv_bfloat16* E, const float* factor,
                                   const __nv_bfloat16* Wt, const __nv_bfloat16* scaled, __nv_bfloat16* dH,
@@ -288,9 +285,17 @@ cudaError_t gemm_group_ce_bwd(const LaunchCtx& c, const __nv_bfloat16* dL, const
 cudaError_t gemm_group_policy_bwd(const LaunchCtx& c, const __nv_bfloat16* dL, const __nv_bfloat16* Wc,
                                   const __nv_bfloat16* H, float* dH32, bool accumulate, __nv_bfloat16* dWc,
                                   const uint32_t* slot, const float* rows, int M, int d, int Vc);
-//   (slot null: dWc = dL^T H)
+//   (slot null: dWc = dL^T H).  It can take on the end of a split data gradient:
+struct SplitDh {
+  const float4* parts;  // [num][stride4], of which n4 are used
+  int num;
+  int64_t stride4, n4, d4;
+  const float* factor;  // [n4 / d4]
+  uint2* out;           // bf16
+};
 cudaError_t gemm_store_plus_rows(const LaunchCtx& c, const __nv_bfloat16* dL, const __nv_bfloat16* H,
-                                 __nv_bfloat16* dWc, const uint32_t* slot, const float* rows, int M, int d, int Vc);
+                                 __nv_bfloat16* dWc, const uint32_t* slot, const float* rows, int M, int d, int Vc,
+                                 const SplitDh& dh = SplitDh{});
 //   the same first-layer pair on 8-bit codes: dX = sdH sW1 dHq W1q and
 //   dW1t = sdH sX dHq^T Xq (dH format dh_fmt; W1 and X in w_fmt); two
 //   launches when pairing is off.

@@ -22,10 +22,10 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
+// v over the CTA's threads, in all of them; part: kWarps of them
 template <class T, class F>
 __device__ __forceinline__ T block_reduce(T v, T* part, F&& f) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+  v = f(v);  // over the warp, in every lane
   __syncthreads();  // part may still be read
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
@@ -34,12 +34,25 @@ __device__ __forceinline__ T block_reduce(T v, T* part, F&& f) {
   for (int w = 1; w < kWarps; ++w) s = f(s, part[w]);
   return s;
 }
-struct Add {
-  template <class T>
-  __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+// a sum, a second one, and a maximum
+struct Sums {
+  float a, b, top;
 };
-struct Max {
-  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+struct AddSums {
+  __device__ __forceinline__ Sums operator()(Sums v) const { return {warp_sum(v.a), warp_sum(v.b), warp_max(v.top)}; }
+  __device__ __forceinline__ Sums operator()(Sums v, Sums w) const {
+    return {v.a + w.a, v.b + w.b, fmaxf(v.top, w.top)};
+  }
 };
 
 // a b, with its rounding error
@@ -306,16 +319,20 @@ __device__ __forceinline__ float phi(float a, float b, float lb) {
 struct Rest {
   float n, s;
 };
-__device__ __forceinline__ void merge(Rest& a, Rest b) {
-  if (b.s == 0.f) return;
-  if (a.s == 0.f || b.n == a.n) {
-    a = Rest{b.n, a.s + b.s};
-  } else if (b.n > a.n) {
-    a = Rest{b.n, fmaf(a.s, ex2_f(a.n - b.n), b.s)};
-  } else {
-    a.s = fmaf(b.s, ex2_f(b.n - a.n), a.s);
+struct AddRests {
+  __device__ __forceinline__ Rest operator()(Rest a, Rest b) const {
+    if (b.s == 0.f) return a;
+    if (a.s == 0.f || b.n == a.n) return Rest{b.n, a.s + b.s};
+    if (b.n > a.n) return Rest{b.n, fmaf(a.s, ex2_f(a.n - b.n), b.s)};
+    return Rest{a.n, fmaf(b.s, ex2_f(b.n - a.n), a.s)};
   }
-}
+  __device__ __forceinline__ Rest operator()(Rest a) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      a = (*this)(a, Rest{__shfl_xor_sync(0xffffffffu, a.n, o), __shfl_xor_sync(0xffffffffu, a.s, o)});
+    return a;
+  }
+};
 
 // A row's loss and, with gradients, its factor on the kept exponentials, the
 // listed tokens' entries among them and its scaled hidden state.  A row to a
@@ -327,85 +344,86 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
                                                                 int64_t d, int64_t V) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ float part[kWarps];
+  __shared__ Sums part[kWarps];
   __shared__ Rest rests[kWarps];
   __shared__ bool last;
   const int64_t m = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = w.k, T = w.T;
   const float weight = in.weight != nullptr ? in.weight[m] : in.uniform;
   const float c = in.log2e_over_t;
+  const float* psum = w.psum + m * T;
+  const float* pn = w.pn + m * T;
   float4 terms = make_float4(0.f, 0.f, 0.f, 0.f);
   float loss = 0.f, factor = 0.f;
   if (weight != 0.f) {
     const float n_row = w.n[m];
     const float4 mass = w.mass[m];
-    Rest rest{n_row, 0.f};
-    bool far = false;
-    for (int b = tid; b < T; b += kThreads) {
-      const Rest x{w.pn[m * T + b], w.psum[m * T + b]};
-      far |= x.n != n_row;
-      merge(rest, x);
-    }
-#pragma unroll
-    for (int q = 16; q > 0; q >>= 1) {
-      Rest x{__shfl_xor_sync(0xffffffffu, rest.n, q), __shfl_xor_sync(0xffffffffu, rest.s, q)};
-      merge(rest, x);
-    }
-    if (lane == 0) rests[warp] = rest;
-    far = __syncthreads_or(far);
-    rest = rests[0];
-#pragma unroll
-    for (int q = 1; q < kWarps; ++q) merge(rest, rests[q]);
-    const bool some = rest.s != 0.f;  // tokens off the list
     // this thread's entries
     constexpr int N = kDistillMaxList / kThreads;
     int32_t id[N];
     float x[N], t[N], q[N];
-    float top = some ? 0.f : -INFINITY;
+    Sums all{0.f, 0.f, -INFINITY};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int j = tid + i * kThreads;
       id[i] = j < k ? w.ids[m * k + j] : -1;
       x[i] = id[i] >= 0 ? w.listed[m * k + j] : -INFINITY;
       t[i] = id[i] >= 0 ? w.t[m * k + j] : 0.f;
-      top = fmaxf(top, fmaf(x[i], c, -rest.n));
+      all.top = fmaxf(all.top, x[i]);
     }
+#pragma unroll 8
+    for (int b = tid; b < T; b += kThreads) {
+      const float s = psum[b];
+      all.a += s;
+      all.b += s < 0.f ? 1.f : 0.f;
+    }
+    all = block_reduce(all, part, AddSums());
+    Rest rest{n_row, all.a};
+    const bool far = all.b != 0.f;
+    if (far) {  // blocks at a scale of their own
+      rest.s = 0.f;
+      for (int b = tid; b < T; b += kThreads) {
+        const float s = psum[b];
+        rest = AddRests()(rest, Rest{s < 0.f ? pn[b] : n_row, fabsf(s)});
+      }
+      rest = block_reduce(rest, rests, AddRests());
+    }
+    const bool some = rest.s != 0.f;  // tokens off the list
     // everything in units of 2^ref, ref an integer near the largest listed logit or above it
-    top = block_reduce(top, part, Max());
+    float top = fmaf(all.top, c, -rest.n);
+    if (some) top = fmaxf(top, 0.f);
     const float ref = rest.n + (isfinite(top) ? rintf(top) : 0.f), down = rest.n - ref;
-    float on = 0.f;
+    Sums on{0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       x[i] = fmaf(x[i], c, -ref);
       q[i] = ex2_f(x[i]);
-      on += q[i];
+      on.a += q[i];
     }
-    on = block_reduce(on, part, Add());
-    const float rest_ref = rest.s * ex2_f(down), S = rest_ref + on, log2_S = log2f(S);
+    on = block_reduce(on, part, AddSums());
+    const float rest_ref = rest.s * ex2_f(down), S = rest_ref + on.a, log2_S = log2f(S);
     constexpr float kLn2 = 0.6931471805599453f;
     const float R = rest_ref / S, lR = (log2f(rest.s) + down - log2_S) * kLn2;
     // a tail needs a token off the list
     const float P = mass.x, r = some ? mass.y : 0.f, excess = some ? mass.z : mass.z - mass.y;
-    float sum = 0.f, cross = 0.f, steep = 0.f;
+    Sums row{0.f, 0.f, 0.f};  // loss, cross-entropy, largest entry of dL
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (id[i] >= 0) {
         const float lq = (x[i] - log2_S) * kLn2;
         q[i] /= S;
-        sum += phi(t[i], q[i], lq);
-        if (t[i] != 0.f) cross = fmaf(-t[i], lq, cross);
+        row.a += phi(t[i], q[i], lq);
+        if (t[i] != 0.f) row.b = fmaf(-t[i], lq, row.b);
         q[i] = fmaf(P + r, q[i], -t[i]);  // d loss / d z
-        steep = fmaxf(steep, fabsf(q[i]));
+        row.top = fmaxf(row.top, fabsf(q[i]));
       }
     }
-    sum = block_reduce(sum, part, Add());
-    cross = block_reduce(cross, part, Add());
-    loss = sum + (some ? phi(r, R, lR) : 0.f) + excess;
-    if (r != 0.f) cross = fmaf(-r, lR, cross);
-    terms = make_float4(weight * loss, weight * cross, weight * P, weight * (on / S));
+    row = block_reduce(row, part, AddSums());
+    loss = row.a + (some ? phi(r, R, lR) : 0.f) + excess;
+    if (r != 0.f) row.b = fmaf(-r, lR, row.b);
+    terms = make_float4(weight * loss, weight * row.b, weight * P, weight * (on.a / S));
     if (GRADS) {
-      steep = block_reduce(steep, part, Max());
-      const float scale = weight / in.temperature;
+      const float scale = weight / in.temperature, steep = row.top;
       float f = (P + r) * (ex2_f(down) / S) - (r != 0.f ? r / rest.s : 0.f);
       __nv_bfloat16* kept = w.kept + m * V;
       // A row with blocks at a scale of their own, or whose factor is too small
@@ -414,7 +432,8 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
       if (far || !some || !(fabsf(f) >= 0x1p-40f * steep)) {
         for (int64_t i = tid; i < V / 8; i += kThreads) {
           const int64_t b = i >> 4;
-          const float up = ex2_f(fminf(w.pn[m * T + b] - rest.n, 0.f));  // above it: a block of zeros, all listed
+          // above rest.n: a block of zeros, all listed
+          const float up = ex2_f(fminf((psum[b] < 0.f ? pn[b] : n_row) - rest.n, 0.f));
           const float g = some ? (P + r) * (ex2_f(down) / S) * up - (r != 0.f ? r / rest.s * up : 0.f) : 0.f;
           float v[8];
           uint4* at = reinterpret_cast<uint4*>(kept) + i;
@@ -489,27 +508,6 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
   }
 }
 
-// dH[m] = bf16(factor[m] sum of the parts), four columns to a thread
-__global__ void __launch_bounds__(128) distill_dh_kernel(const float4* __restrict__ parts, int num, int64_t stride4,
-                                                         const float* __restrict__ factor, uint2* __restrict__ out,
-                                                         int64_t n4, int64_t d4) {
-  griddep_wait();
-  griddep_launch_dependents();
-  for (int64_t i = blockIdx.x * 128ll + threadIdx.x; i < n4; i += gridDim.x * 128ll) {
-    float4 s = parts[i];
-#pragma unroll 8
-    for (int p = 1; p < num; ++p) {
-      const float4 x = parts[p * stride4 + i];
-      s.x += x.x;
-      s.y += x.y;
-      s.z += x.z;
-      s.w += x.w;
-    }
-    const float f = factor[i / d4];
-    out[i] = make_uint2(pack_bf16x2(s.x * f, s.y * f), pack_bf16x2(s.z * f, s.w * f));
-  }
-}
-
 }  // namespace
 
 cudaError_t launch_distill_list(const LaunchCtx& c, const DistillIn& in, const DistillWork& w, const __nv_bfloat16* H,
@@ -525,14 +523,6 @@ cudaError_t launch_distill_rows(const LaunchCtx& c, const DistillIn& in, const D
                                 const __nv_bfloat16* H, int64_t M, int64_t d, int64_t V) {
   return launch_chained(c, w.kept != nullptr ? distill_rows_kernel<true> : distill_rows_kernel<false>,
                         dim3(static_cast<unsigned>(M)), dim3(kThreads), 0, in, w, o, H, M, d, V);
-}
-
-cudaError_t launch_distill_dh(const LaunchCtx& c, const float* parts, int num, int64_t stride, const float* factor,
-                              __nv_bfloat16* dH, int64_t M, int64_t d) {
-  const int64_t n4 = M * d / 4, blocks = std::min<int64_t>((n4 + 127) / 128, int64_t(c.num_sms) * 16);
-  return launch_chained(c, distill_dh_kernel, dim3(static_cast<unsigned>(blocks)), dim3(128), 0,
-                        reinterpret_cast<const float4*>(parts), num, stride / 4, factor,
-                        reinterpret_cast<uint2*>(dH), n4, d / 4);
 }
 
 }  // namespace coda

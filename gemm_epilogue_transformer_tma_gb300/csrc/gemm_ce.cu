@@ -73,13 +73,15 @@ cudaError_t gemm_splitk(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_b
 }
 
 cudaError_t gemm_store_plus_rows(const LaunchCtx& c, const __nv_bfloat16* dL, const __nv_bfloat16* H,
-                                 __nv_bfloat16* dWc, const uint32_t* slot, const float* rows, int M, int d, int Vc) {
+                                 __nv_bfloat16* dWc, const uint32_t* slot, const float* rows, int M, int d, int Vc,
+                                 const SplitDh& dh) {
   using L = DwSmem;
   DwArgs g{};
   if (!make_operand_maps(&g.A, &g.B, dL, true, H, true, Vc, d, M, 128) || !make_tmap_bf16(&g.out, dWc, d, Vc, d, 64, 32))
     return cudaErrorInvalidValue;
   g.slot = slot;
   g.rows = rows;
+  g.dh = dh;
   g.M = Vc;
   g.N = d;
   g.tiles_m = (Vc + BM2 - 1) / BM2;

@@ -9,8 +9,12 @@
 //
 // dL [M][Vc] and H [M][d] bf16 are both read MN-major.  rows fp32 [tokens][d]
 // and slot [Vc] as EpiStorePlusRows; slot may be null: no rows (distillation).
+// The epilogue's warps can also finish a split data gradient before their first
+// tile is there: dH[m] = bf16(factor[m] sum of the parts) (distillation, 136
+// tokens: 10 us as a kernel of its own).
 #pragma once
 
+#include "coda_internal.h"
 #include "gemm_tc2.cuh"
 
 namespace coda {
@@ -33,9 +37,28 @@ struct DwArgs {
   CUtensorMap A, B, out;  // dL, H, dW (boxes of 64 columns x 32 rows)
   const uint32_t* slot;
   const float* rows;
+  SplitDh dh;
   int M, N;               // Vc, d
   int tiles_m, tiles_n, num_kb;
 };
+
+// four columns to a thread
+__device__ __forceinline__ void finish_dh(const SplitDh& h, int64_t first, int64_t step) {
+  for (int64_t i = first; i < h.n4; i += step) {
+    const float4* p = h.parts + i;
+    float4 s = *p;
+#pragma unroll 8
+    for (int q = 1; q < h.num; ++q) {
+      const float4 x = p[q * h.stride4];
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
+    }
+    const float f = h.factor[i / h.d4];
+    h.out[i] = make_uint2(pack_bf16x2(s.x * f, s.y * f), pack_bf16x2(s.z * f, s.w * f));
+  }
+}
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DwSmem::THREADS, 1)
     gemm_dw_kernel(const __grid_constant__ DwArgs g, const KernelCtl ctl) {
@@ -200,6 +223,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DwSmem::THREADS, 1)
       return g.slot != nullptr && t < num_tiles && m < g.M ? __ldg(g.slot + m) : kNoSlot;
     };
     uint32_t s_next = slot_of(cluster_id);
+    finish_dh(g.dh, blockIdx.x * static_cast<int64_t>(32 * L::EPI_WARPS) + threadIdx.x - 64,
+              gridDim.x * static_cast<int64_t>(32 * L::EPI_WARPS));
     for (int t = cluster_id; t < num_tiles; t += num_clusters, ++it) {
       const int m0 = row0(t);
       const uint32_t s = s_next;

@@ -2,7 +2,8 @@
 // student's row of logits L, given its teacher's list (distinct tokens, in
 // order).  With y = L log2(e) / T, per 128-column vocabulary block
 //   pn    an integer,
-//   psum  sum of 2^(y - pn) over the tokens off the list,
+//   psum  sum of 2^(y - pn) over the tokens off the list, negated where the
+//         block has a pn of its own (pn is written there only),
 // and the logits of the tokens on it.  The list's tokens are left out here and
 // not taken off afterwards: where it holds nearly all of a row's probability,
 // the little that is left would drown in that difference.
@@ -147,8 +148,9 @@ struct LogitsDistill {
     }
     if (dead) return;
     const int64_t o = static_cast<int64_t>(m) * g.T + t.part;
-    g.pn[o] = n;
-    g.psum[o] = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+    const float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+    g.psum[o] = n == st.n ? sum : -sum;
+    if (n != st.n) g.pn[o] = n;
   }
 };
 
