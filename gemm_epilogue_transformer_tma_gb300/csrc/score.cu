@@ -20,50 +20,20 @@ namespace coda {
 
 namespace {
 
-// the largest logit of some blocks, and psum and pdot relative to it
+// a row's largest logit, and psum and pdot relative to it
 struct RowSum {
   float mx, s, u;
 };
-__device__ __forceinline__ void merge(RowSum& a, RowSum b, float c) {
-  if (b.mx == -INFINITY && b.s == 0.f) return;  // no block
-  if (a.mx == -INFINITY && a.s == 0.f) {
-    a = b;
-    return;
-  }
-  if (b.mx > a.mx) {
-    const RowSum t = a;
-    a = b;
-    b = t;
-  }
-  const float dx = b.mx - a.mx, f = ex2_f(dx * c), n = 1.f + b.s;
-  a.s = fmaf(f, n, a.s);
-  a.u += f * fmaf(dx, n, b.u);
-}
 
-__device__ __forceinline__ RowSum merge_warp(RowSum r, float c) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    // the lower lane's first on both sides: all lanes end with the same bits
-    RowSum x;
-    x.mx = __shfl_xor_sync(0xffffffffu, r.mx, o);
-    x.s = __shfl_xor_sync(0xffffffffu, r.s, o);
-    x.u = __shfl_xor_sync(0xffffffffu, r.u, o);
-    if (threadIdx.x & o) {
-      merge(x, r, c);
-      r = x;
-    } else {
-      merge(r, x, c);
-    }
-  }
-  return r;
-}
-
-__device__ __forceinline__ RowSum row_blocks(const ScoreStats& s, int64_t m, int first, int step, float c) {
-  RowSum r{-INFINITY, 0.f, 0.f};
-  const int64_t at = m * s.T;
-#pragma unroll 2
-  for (int j = first; j < s.T; j += step) merge(r, RowSum{s.pmax[at + j], s.psum[at + j], s.pdot[at + j]}, c);
-  return r;
+// Adds a block to sums relative to the row's largest logit mx, of which, and of
+// equal ones, `equal` were found.  The largest itself, in a block's psum left
+// out, is left out here too: what is summed is small where the row is certain.
+__device__ __forceinline__ void add_block(float x, float ps, float pd, float mx, float c, float& equal, float& sum,
+                                          float& dot) {
+  const float dx = x == mx ? 0.f : x - mx, f = ex2_f(dx * c);
+  equal += x == mx ? 1.f : 0.f;
+  sum = x == mx ? sum + ps : fmaf(f, 1.f + ps, sum);
+  dot += x == mx ? pd : f * fmaf(dx, 1.f + ps, pd);
 }
 
 __device__ __forceinline__ void write_row(const ScoreStats& s, const ScoreOut& o, const RowSum& r, int64_t m,
@@ -84,7 +54,25 @@ __global__ void __launch_bounds__(128) score_rows_kernel(const ScoreStats s, con
   griddep_launch_dependents();
   const int64_t m = blockIdx.x * 4ll + (threadIdx.x >> 5);
   if (m >= M) return;
-  const RowSum r = merge_warp(row_blocks(s, m, threadIdx.x & 31, 32, o.log2e_over_t), o.log2e_over_t);
+  const int lane = threadIdx.x & 31;
+  const float* pmax = s.pmax + m * s.T;
+  const float* psum = s.psum + m * s.T;
+  const float* pdot = s.pdot + m * s.T;
+  float mx = -INFINITY;
+#pragma unroll 8
+  for (int b = lane; b < s.T; b += 32) mx = fmaxf(mx, pmax[b]);
+#pragma unroll
+  for (int q = 16; q > 0; q >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, q));
+  float equal = 0.f, sum = 0.f, dot = 0.f;
+#pragma unroll 8
+  for (int b = lane; b < s.T; b += 32) add_block(pmax[b], psum[b], pdot[b], mx, o.log2e_over_t, equal, sum, dot);
+#pragma unroll
+  for (int q = 16; q > 0; q >>= 1) {
+    equal += __shfl_xor_sync(0xffffffffu, equal, q);
+    sum += __shfl_xor_sync(0xffffffffu, sum, q);
+    dot += __shfl_xor_sync(0xffffffffu, dot, q);
+  }
+  const RowSum r{mx, (equal - 1.f) + sum, dot};
   if ((threadIdx.x & 31) == 0) write_row(s, o, r, m, V);
 }
 
@@ -257,20 +245,13 @@ __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats
   auto bin = [&](float x) { return max(0, min(255, __float2int_rd((x - low) * width))); };
   const bool select = num_keys > k;
   if (select) each_key([&](int, float x) { atomicAdd(&sm.hist[bin(x)], 1); });
-  // the sums relative to the largest; it itself (of equal ones, one) left out
   float equal = 0.f, sum = 0.f, dot = 0.f;
-  auto block = [&](float x, float ps, float pd) {
-    const float dx = x == mx ? 0.f : x - mx, f = ex2_f(dx * c);
-    equal += x == mx ? 1.f : 0.f;
-    sum = x == mx ? sum + ps : fmaf(f, 1.f + ps, sum);
-    dot += x == mx ? pd : f * fmaf(dx, 1.f + ps, pd);
-  };
   if (HELD) {
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      if (tid + j * kTopThreads < T) block(bm[j], bs[j], bd[j]);
+      if (tid + j * kTopThreads < T) add_block(bm[j], bs[j], bd[j], mx, c, equal, sum, dot);
   } else {
-    for (int b = tid; b < T; b += kTopThreads) block(pmax[b], psum[b], pdot[b]);
+    for (int b = tid; b < T; b += kTopThreads) add_block(pmax[b], psum[b], pdot[b], mx, c, equal, sum, dot);
   }
 #pragma unroll
   for (int q = 16; q > 0; q >>= 1) {
