@@ -1417,7 +1417,9 @@ ScoreWs score_layout(uint8_t* base, int64_t M, int64_t V, int64_t k) {
   w.s.psum = take(size_t(R) * T);
   w.s.pdot = take(size_t(R) * T);
   w.s.zy = take(size_t(R));
+  w.s.k = static_cast<int>(k);
   if (k > 0) {
+    w.s.bound = take(size_t(R));
     w.s.sub = take(size_t(R) * T * 4);
     w.s.logits = take(size_t(R) * V);
   }
@@ -1473,9 +1475,11 @@ coda_status_t coda_lmhead_score(coda_handle_t h, const void* Hs, const void* Wt,
     o.temperature = temperature;
     o.log2e_over_t = c;
     o.status = cx.status;
-    CODA_CUDA(gemm_score(cx, static_cast<const bf16*>(Hs) + m0 * d, static_cast<const bf16*>(Wt), o.labels, w.s, c,
+    ScoreStats s = w.s;
+    if (rows <= kScoreFew || score_first_columns(rows, V, k) == V) s.bound = nullptr;  // all logits are kept
+    CODA_CUDA(gemm_score(cx, static_cast<const bf16*>(Hs) + m0 * d, static_cast<const bf16*>(Wt), o.labels, s, c,
                          int(rows), int(d), int(V)));
-    CODA_CUDA(launch_score_rows(cx, w.s, o, rows, V));
+    CODA_CUDA(launch_score_rows(cx, s, o, rows, V));
   }
   return CODA_OK;
 }

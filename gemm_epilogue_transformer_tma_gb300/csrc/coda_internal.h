@@ -167,6 +167,8 @@ struct ScoreStats {
   float* zy;      // [M]: the logit of the row's token
   float* logits;  // [M][V], or null: no alternatives
   float* sub;     // [M][4 T]: maxima of sub_cols columns each, with logits
+  float* bound;   // [M], or null: below it a row's logits from score_first_columns on need not be there
+  int k;          // alternatives
   int T;          // blocks of a row
   int sub_cols;   // a quarter of a block
 };
@@ -180,6 +182,10 @@ constexpr int64_t kScoreFew = 64, kScoreSms = 152;
 int score_few_rows(int64_t V);
 cudaError_t gemm_score(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt, const int32_t* labels,
                        const ScoreStats& s, float log2e_over_t, int M, int d, int V);
+// Columns whose logits are all kept, a multiple of 256, or V; a bound on each row's
+// k-th largest from their sub-blocks' maxima is in s.bound for the others.
+int score_first_columns(int64_t M, int64_t V, int64_t k);
+cudaError_t launch_score_bound(const LaunchCtx& c, const ScoreStats& s, int64_t M, int64_t first);
 // logp, entropy, the k highest logits' tokens and log-probabilities of M rows
 // (score.cu); any of the outputs may be null, top_ids and top_logp together
 constexpr int kScoreMaxTop = 256;

@@ -31,8 +31,9 @@ constexpr int kPieceKb = 8;  // k-blocks of 64 per piece
 // tokens, V = 32000, d = 1024 22.9 to 22.4 us, 16 tokens at d = 4096 53.8 to 53.4)
 constexpr int kAheadKb = 8;
 
+template <class Prog>
 struct LogitsSmem {
-  static constexpr int STAGES = 6;
+  static constexpr int STAGES = Prog::kStages;
   static constexpr int EPI_WARPS = 8;
   static constexpr int LEAD_WARPS = 4;  // a warpgroup
   static constexpr int THREADS = 32 * (LEAD_WARPS + EPI_WARPS);
@@ -44,7 +45,7 @@ struct LogitsSmem {
   static constexpr int A_BYTES = 128 * BK * 2;
   static constexpr int STAGE_BYTES = 2 * A_BYTES;
   static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
-  static constexpr int STORE_BYTES = EPI_WARPS * 2 * STORE_SLOT_BYTES;
+  static constexpr int STORE_BYTES = EPI_WARPS * Prog::kSlots * STORE_SLOT_BYTES;
   static constexpr int BAR_BYTES = 512;
   static constexpr int TOTAL = RING_BYTES + STORE_BYTES + BAR_BYTES + 1024;
   static_assert(TOTAL <= MAX_DYN_SMEM, "shared memory budget");
@@ -55,11 +56,12 @@ struct LogitsTile {
   int m0, n0, nv;  // nv >= 128 where all of them exist
   int part;        // n0 / 128, the block
   int lane;
-  uint32_t slot;   // this warp's two store slots in shared memory
+  uint32_t slot;   // this warp's store slots in shared memory
 };
 
-// A program has Params, run(), which gets the raw products, and kStores: whether
-// it leaves bulk stores in flight.  With kAhead it also has an Early that
+// A program has Params, run(), which gets the raw products, kStores: whether it
+// leaves bulk stores in flight, and its split of shared memory, kStages of the
+// ring and kSlots of 2 KB to a warp.  With kAhead it also has an Early that
 // early() loads two tiles ahead and a State that ahead() makes of it and loads
 // one tile ahead, so that run() waits for neither.  All are called for tiles with
 // a row and a column only.
@@ -84,6 +86,7 @@ template <bool KEEP>
 struct LogitsPolicy {
   static constexpr bool kAhead = false;
   static constexpr bool kStores = KEEP;
+  static constexpr int kStages = 6, kSlots = 2;
   struct Params {
     const int32_t* labels;  // [M]
     float* pmax;            // [M][T], T = ceil(V / 128)
@@ -155,9 +158,9 @@ struct LogitsPolicy {
 };
 
 template <class Prog>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem<Prog>::THREADS, 1)
     gemm_logits_kernel(const __grid_constant__ LogitsArgs<Prog> g, const KernelCtl ctl) {
-  using L = LogitsSmem;
+  using L = LogitsSmem<Prog>;
   constexpr int STAGES = L::STAGES;
   constexpr int BN = 256;
   constexpr uint32_t IDESC = idesc_bf16_f32(BM2, BN, false, false);
@@ -330,7 +333,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LogitsSmem::THREADS,
     const int half = (warp - L::LEAD_WARPS) >> 2;
     const uint32_t leader_tempty = mapa_shared(smem_u32(tempty), 0);
     const uint32_t slot =
-        smem_u32(smem + L::RING_BYTES) + static_cast<uint32_t>((warp - L::LEAD_WARPS) * 2 * STORE_SLOT_BYTES);
+        smem_u32(smem + L::RING_BYTES) + static_cast<uint32_t>((warp - L::LEAD_WARPS) * Prog::kSlots * STORE_SLOT_BYTES);
     const int pieces = (g.num_kb + kPieceKb - 1) / kPieceKb;
     auto tile_of = [&](int t) {
       int tm, tn;

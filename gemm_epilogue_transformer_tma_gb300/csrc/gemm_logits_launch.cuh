@@ -10,7 +10,7 @@ namespace coda {
 template <class Prog>
 cudaError_t launch_logits(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt,
                           const typename Prog::Params& p, int M, int d, int V, bool operands_ready = false) {
-  using L = LogitsSmem;
+  using L = LogitsSmem<Prog>;
   LogitsArgs<Prog> g{};
   if (!make_operand_maps(&g.H, &g.W, H, false, Wt, false, M, V, d, 128)) return cudaErrorInvalidValue;
   g.M = M;

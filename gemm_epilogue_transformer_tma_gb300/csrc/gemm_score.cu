@@ -25,6 +25,18 @@ int score_few_rows(int64_t V) {
   return static_cast<int>(std::max<int64_t>(16, (r + 3) / 4 * 4));
 }
 
+int score_first_columns(int64_t M, int64_t V, int64_t k) {
+  constexpr int64_t kPairs = 76;
+  const int64_t tiles_m = (M + BM2 - 1) / BM2, tiles_n = (V + 255) / 256;
+  // An eighth of the vocabulary, and at least 4 k of its sub-blocks of 32 (then a
+  // sub-block of the rest reaches the bound with a chance of 1 in 5 or less), in
+  // whole waves of the SM pairs; where a second launch costs too much, all of it.
+  int64_t first = std::max((tiles_n + 7) / 8, (4 * k + 7) / 8);
+  const int64_t waves = (first * tiles_m + kPairs - 1) / kPairs;
+  first = waves * kPairs / tiles_m;
+  return first * 2 > tiles_n || tiles_m * tiles_n < 16 * kPairs ? static_cast<int>(V) : static_cast<int>(first * 256);
+}
+
 cudaError_t gemm_score(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt, const int32_t* labels,
                        const ScoreStats& s, float log2e_over_t, int M, int d, int V) {
   if (M <= kScoreFew) {
@@ -47,26 +59,31 @@ cudaError_t gemm_score(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bf
            : M <= 48 ? launch_few<48>(c, H, Wt, g, d)
                      : launch_few<64>(c, H, Wt, g, d);
   }
-  auto fill = [&](auto& p) {
+  auto launch = [&](auto prog, int v0, int v1, bool operands_ready) {
+    using Prog = decltype(prog);
+    typename Prog::Params p{};
     p.labels = labels;
     p.pmax = s.pmax;
     p.psum = s.psum;
     p.pdot = s.pdot;
     p.zy = s.zy;
-    p.logits = s.logits;
+    p.some = s.logits;
+    p.bound = s.bound;
     p.sub = reinterpret_cast<float4*>(s.sub);
     p.T = s.T;
     p.V = V;
+    p.v0 = v0;
     p.c = log2e_over_t;
+    if (Prog::kStores && !make_tmap_store_f32(&p.all, s.logits + v0, v1 - v0, M, V)) return cudaErrorInvalidValue;
+    return launch_logits<Prog>(c, H, Wt + static_cast<int64_t>(v0) * d, p, M, d, v1 - v0, operands_ready);
   };
-  if (s.logits != nullptr) {
-    LogitsScore<true>::Params p{};
-    fill(p);
-    return launch_logits<LogitsScore<true>>(c, H, Wt, p, M, d, V);
-  }
-  LogitsScore<false>::Params p{};
-  fill(p);
-  return launch_logits<LogitsScore<false>>(c, H, Wt, p, M, d, V);
+  if (s.logits == nullptr) return launch(LogitsScore<KEEP_NONE>{}, 0, V, false);
+  const int first = s.bound != nullptr ? score_first_columns(M, V, s.k) : V;
+  cudaError_t e = launch(LogitsScore<KEEP_ALL>{}, 0, first, false);
+  if (e != cudaSuccess || first == V) return e;
+  e = launch_score_bound(c, s, M, first);
+  if (e != cudaSuccess) return e;
+  return launch(LogitsScore<KEEP_SOME>{}, first, V, true);
 }
 
 }  // namespace coda

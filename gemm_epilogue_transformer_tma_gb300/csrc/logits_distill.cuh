@@ -27,6 +27,7 @@ template <bool KEEP>
 struct LogitsDistill {
   static constexpr bool kAhead = true;
   static constexpr bool kStores = KEEP;
+  static constexpr int kStages = 6, kSlots = 2;
   struct Params {
     CUtensorMap kept;    // KEEP: [M][V] bf16, 32 x 32 boxes
     const uint32_t* at;     // [G][T], G = ceil(M / 32): where a block's entries begin | how many << 16

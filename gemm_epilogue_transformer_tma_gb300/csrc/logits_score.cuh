@@ -4,9 +4,12 @@
 //   psum  sum exp(x / T) - 1: without the largest itself, so that the digits
 //         below one of a row that is nearly certain are kept
 //   pdot  sum x exp(x / T)
-// and the logit of the row's token.  TOP: the logits in fp32 as well, with the
-// maxima of every 32 columns, by which the row kernel finds the few of them it
-// reads again.
+// and the logit of the row's token.  For the most probable tokens the logits in
+// fp32 as well, with the maxima of every 32 columns, by which the row kernel finds
+// the few of them it reads again: ALL of them, or only SOME, 32 columns of a row
+// whose maximum reaches a bound on the row's k-th largest.  Writing all takes a
+// fifth of the tensor pipe (2048 tokens, V = 65536, d = 2048: 263 us without, 329
+// with): the bound comes from the first columns (score_bound_kernel).
 #pragma once
 
 #include "gemm_logits.cuh"
@@ -17,34 +20,47 @@ namespace coda {
 // exponential, 0, is 0
 constexpr float kNoLogit = -3.4e38f;
 
-template <bool TOP>
+enum ScoreKeep { KEEP_NONE, KEEP_ALL, KEEP_SOME };
+
+template <int KEEP>
 struct LogitsScore {
   static constexpr bool kAhead = true;
-  static constexpr bool kStores = false;
+  static constexpr bool kStores = KEEP == KEEP_ALL;
+  static constexpr int kStages = 6, kSlots = 2;  // one box of 32 x 32 fp32
   struct Params {
     const int32_t* labels;  // [M] or null
     float* pmax;            // [M][T], T = ceil(V / 128)
     float* psum;            // [M][T]
     float* pdot;            // [M][T]
     float* zy;              // [M], written where the token is found
-    float* logits;          // TOP: [M][V]
-    float4* sub;            // TOP: [M][T] of four maxima
+    CUtensorMap all;        // KEEP_ALL: the logits, [M] rows of fp32, 32 x 32 boxes
+    float* some;            // KEEP_SOME: the logits, [M][V]
+    const float* bound;     // KEEP_SOME: [M]
+    float4* sub;            // with logits: [M][T] of four maxima
     int T, V;
+    int v0;                 // the launch's first column, a multiple of 256: Wt starts there
     float c;                // log2(e) / temperature
   };
   struct State {
     int y;
+    float bound;
   };
   using Early = int;
   static __device__ __forceinline__ Early early(const Params&, const LogitsTile&) { return 0; }
   static __device__ __forceinline__ State ahead(const Params& g, const LogitsTile& t, Early, int M) {
     const int m = t.m0 + t.lane;
-    return State{g.labels != nullptr && m < M ? g.labels[m] : -1};
+    State st{-1, 0.f};
+    if (m < M) {
+      if (g.labels != nullptr) st.y = g.labels[m];
+      if (KEEP == KEEP_SOME) st.bound = ld_here_f32(g.bound + m);
+    }
+    return st;
   }
   static __device__ __forceinline__ void run(const Params& g, const LogitsTile& t, const State& st, int M,
                                              float (&v)[4][32]) {
     const int m = t.m0 + t.lane;
-    if (m >= M) return;  // nothing below involves other lanes
+    const bool row = m < M;
+    if (KEEP != KEEP_ALL && !row) return;  // nothing below involves other lanes
     if (t.nv < PART_COLS) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -52,7 +68,7 @@ struct LogitsScore {
         for (int i = 0; i < 32; ++i)
           if (c * 32 + i >= t.nv) v[c][i] = kNoLogit;
     }
-    const int64_t y = static_cast<int64_t>(st.y) - t.n0;
+    const int64_t y = static_cast<int64_t>(st.y) - g.v0 - t.n0;
     if (y >= 0 && y < PART_COLS && y < t.nv) {
       float z = 0.f;
 #pragma unroll
@@ -60,9 +76,9 @@ struct LogitsScore {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (c * 32 + i == y) z = v[c][i];
-      g.zy[m] = z;
+      g.zy[m] = z;  // a label is loaded for a row of H only
     }
-    const int64_t o = static_cast<int64_t>(m) * g.T + t.part;
+    const int64_t o = static_cast<int64_t>(m) * g.T + (g.v0 / PART_COLS + t.part);
     float cm[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -71,13 +87,30 @@ struct LogitsScore {
       for (int i = 0; i < 32; ++i) cm[c] = fmaxf(cm[c], v[c][i]);
     }
     const float mx = fmaxf(fmaxf(cm[0], cm[1]), fmaxf(cm[2], cm[3]));
-    if (TOP) {
-      float* at = g.logits + static_cast<int64_t>(m) * g.V + t.n0;
+    if (KEEP == KEEP_ALL) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c * 32 >= t.nv) break;
+        slots_acquire(t.lane);
+        stage_f32x32(t.slot, t.lane, v[c]);
+        slots_publish();
+        if (t.lane == 0) {
+          tma_store_2d(&g.all, t.slot, t.n0 + c * 32, t.m0);
+          bulk_commit_group();
+        }
+      }
+      if (!row) return;
+    }
+    if (KEEP == KEEP_SOME) {
+      float* at = g.some + static_cast<int64_t>(m) * g.V + (g.v0 + t.n0);
 #pragma unroll
       for (int c = 0; c < 4; ++c)
+        if (cm[c] >= st.bound)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)  // V is a multiple of 8
-          if (c * 32 + q * 8 < t.nv) st_global_v8(at + c * 32 + q * 8, &v[c][q * 8]);
+          for (int q = 0; q < 4; ++q)  // V is a multiple of 8
+            if (c * 32 + q * 8 < t.nv) st_global_v8(at + c * 32 + q * 8, &v[c][q * 8]);
+    }
+    if (KEEP != KEEP_NONE) {
       g.sub[o] = make_float4(cm[0], cm[1], cm[2], cm[3]);
     }
     float n = -1.f, s4[4] = {0.f, 0.f, 0.f, 0.f}, u4[4] = {0.f, 0.f, 0.f, 0.f};

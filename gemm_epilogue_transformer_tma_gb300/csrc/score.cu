@@ -171,6 +171,66 @@ __device__ __forceinline__ void each_logit(const float* __restrict__ sub, const 
   }
 }
 
+// A bin for each 256th of the range from low to mx, in the order of the numbers.
+struct Bins {
+  float low, width;
+  __device__ __forceinline__ Bins(float low, float mx) : low(low), width(mx > low ? 255.f / (mx - low) : 0.f) {}
+  __device__ __forceinline__ int operator()(float x) const {
+    return max(0, min(255, __float2int_rd((x - low) * width)));
+  }
+  // below all that falls into bin b or above: its edge is rounded, by less than
+  // 2^-20 of the larger end
+  __device__ __forceinline__ float edge(int b, float mx) const {
+    if (b <= 0) return -INFINITY;
+    const float e = low + static_cast<float>(b) * ((mx - low) * (1.f / 255.f));
+    return e - 2e-6f * fmaxf(fabsf(low), fabsf(mx));
+  }
+};
+
+// The bound on a row's k-th largest logit: of the sub-blocks of the first
+// `first` columns, k maxima are at least as large.  A row to a CTA.
+__global__ void __launch_bounds__(kTopThreads) score_bound_kernel(const ScoreStats s, int first) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ TopSmem sm;
+  const int64_t m = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float* sub = s.sub + m * 4 * s.T;
+  const int subs = first / 32;
+  for (int i = tid; i < 256; i += kTopThreads) sm.hist[i] = 0;
+  float mx = -INFINITY, low = INFINITY;
+#pragma unroll 8
+  for (int j = tid; j < subs; j += kTopThreads) {
+    const float x = sub[j];
+    mx = fmaxf(mx, x);
+    low = fminf(low, x == -INFINITY ? INFINITY : x);
+  }
+#pragma unroll
+  for (int q = 16; q > 0; q >>= 1) {
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, q));
+    low = fminf(low, __shfl_xor_sync(0xffffffffu, low, q));
+  }
+  if (lane == 0) {
+    sm.part[warp][0] = mx;
+    sm.part[warp][1] = low;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kTopWarps; ++w) {
+    mx = fmaxf(mx, sm.part[w][0]);
+    low = fminf(low, sm.part[w][1]);
+  }
+  const Bins bin(low, mx);
+#pragma unroll 8
+  for (int j = tid; j < subs; j += kTopThreads) atomicAdd(&sm.hist[bin(sub[j])], 1);
+  __syncthreads();
+  if (warp == 0) {
+    pick_digit(sm, s.k, lane);
+    __syncwarp();
+    if (lane == 0) s.bound[m] = bin.edge(sm.pick[0], mx);
+  }
+}
+
 // With alternatives: 128 threads to a row.  4096 rows of V = 128256, k = 64
 // @TOP@
 // HELD: T <= kTopHeld kTopThreads; otherwise what a thread would hold is read again.
@@ -239,10 +299,8 @@ __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats
     mx = fmaxf(mx, sm.part[w][0]);
     low = fminf(low, sm.part[w][1]);
   }
-  // A bin for each 256th of the range, in the same order: one count of the keys
-  // bounds the k-th of them.
-  const float width = mx > low ? 255.f / (mx - low) : 0.f;
-  auto bin = [&](float x) { return max(0, min(255, __float2int_rd((x - low) * width))); };
+  // one count of the keys by bins of their range bounds the k-th of them
+  const Bins bin(low, mx);
   const bool select = num_keys > k;
   if (select) each_key([&](int, float x) { atomicAdd(&sm.hist[bin(x)], 1); });
   float equal = 0.f, sum = 0.f, dot = 0.f;
@@ -267,10 +325,9 @@ __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats
   }
   if (warp == 0 && select) pick_digit(sm, k, lane);
   __syncthreads();
-  // what falls into that bin or above, and, since its edge is rounded (by less
-  // than 2^-20 of the larger end), perhaps a little below
-  const float edge = select ? low + static_cast<float>(sm.pick[0]) * ((mx - low) * (1.f / 255.f)) : -INFINITY;
-  const float least = select && sm.pick[0] > 0 ? edge - 2e-6f * fmaxf(fabsf(low), fabsf(mx)) : -INFINITY;
+  // what falls into that bin or above, and perhaps a little below; nothing that is not kept
+  const float kept = s.bound != nullptr ? s.bound[m] : -INFINITY;
+  const float least = fmaxf(kept, select ? bin.edge(sm.pick[0], mx) : -INFINITY);
   each_key([&](int i, float x) {
     if (!(x < least)) {
       const int at = atomicAdd(&sm.n_keys, 1);
@@ -353,7 +410,7 @@ __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats
     return here;
   };
   auto gather = [&](uint32_t least) {
-    each_logit(sub, logits, subs, cols, V, least, warp, kTopWarps, lane, [&](bool there, uint32_t key, uint32_t token) {
+    each_logit(sub, logits, subs, cols, V, max(least, rank_key(kept)), warp, kTopWarps, lane, [&](bool there, uint32_t key, uint32_t token) {
       append(sm, there && key >= least, key, token, lane);
     });
     __syncthreads();
@@ -366,7 +423,7 @@ __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats
       int have = 0;
       for (int j0 = 0; j0 < subs && have < want; j0 += 32) {
         const int j = j0 + lane;
-        unsigned hit = __ballot_sync(0xffffffffu, j < subs && rank_key(sub[j]) >= key0);
+        unsigned hit = __ballot_sync(0xffffffffu, j < subs && !(sub[j] < kept) && rank_key(sub[j]) >= key0);
         while (hit != 0 && have < want) {
           const int64_t at = static_cast<int64_t>(j0 + __ffs(hit) - 1) * cols + lane;
           hit &= hit - 1;
@@ -396,7 +453,7 @@ __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats
       for (int shift = 24; shift >= 0 && k - need + here > kTopList; shift -= 8)
         here = step(
             [&](int sh) {
-              each_logit(sub, logits, subs, cols, V, key, warp, kTopWarps, lane,
+              each_logit(sub, logits, subs, cols, V, max(key, rank_key(kept)), warp, kTopWarps, lane,
                          [&](bool there, uint32_t x, uint32_t) {
                            if (there && (sh == 24 || (x >> (sh + 8)) == (key >> (sh + 8))))
                              atomicAdd(&sm.hist[(x >> sh) & 255u], 1);
@@ -453,6 +510,11 @@ __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats
 }
 
 }  // namespace
+
+cudaError_t launch_score_bound(const LaunchCtx& c, const ScoreStats& s, int64_t M, int64_t first) {
+  return launch_chained(c, score_bound_kernel, dim3(static_cast<unsigned>(M)), dim3(kTopThreads), 0, s,
+                        static_cast<int>(first));
+}
 
 cudaError_t launch_score_rows(const LaunchCtx& c, const ScoreStats& s, const ScoreOut& o, int64_t M, int64_t V) {
   if (o.k == 0)

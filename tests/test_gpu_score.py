@@ -271,3 +271,33 @@ def test_refusals():
     with pytest.raises(C.CodaError):
         C.coda_lmhead_score(H, W, y, 0.0, f, None, None, None, b)
     assert_device_ok()
+
+
+@pytest.mark.parametrize("V,k", [(20000, 8), (50280, 64), (40008, 256)])
+def test_only_some_logits_kept(V, k):
+    """Many rows and columns: the first columns bound what of the others is
+    kept.  Among the rows: zeros, one value but for the last columns, logits that
+    rise and fall with the token, NaN, and all but a few equal."""
+    M = 4100
+    H, W, y = R.grid_inputs(M, 64, V, seed=7)
+    v = torch.arange(V, device="cuda")
+    W[:, :3] = 0
+    W[:, 0] = (v // 256).to(W.dtype)
+    W[:, 1] = (v >= V - 40).to(W.dtype)
+    W[:, 2] = (v % 7 == 0).to(W.dtype)
+    H[:, :3] = 0
+    for i, (a, b, c) in enumerate(((0, 0, 0), (0, 2, 0), (0.125, 0, 0), (-0.125, 0, 0), (0, 0, 1), (0, 0, -1),
+                                   (0.125, -3, 0.5))):
+        H[64 * i] = 0
+        H[64 * i, :3] = torch.tensor([a, b, c], dtype=torch.float32).to(H.dtype)
+    c = Call(H, W, y, 1.0, k).run()
+    for m in (0, 1000, 4000):
+        c.grade(slice(m, m + 100))
+    c.grade(torch.arange(0, 448, 64, device="cuda"))
+    want = [t.clone() for t in c.outputs()]
+    H[70] = float("nan")
+    c.run()
+    keep = torch.arange(M, device="cuda") != 70
+    assert all(torch.equal(a[keep], b[keep]) for a, b in zip(want, c.outputs()))
+    assert torch.equal(c.ids[70], torch.arange(k, dtype=I32, device="cuda")) and torch.isnan(c.logp[70])
+    assert_device_ok()
