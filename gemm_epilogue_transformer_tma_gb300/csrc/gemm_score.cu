@@ -30,11 +30,13 @@ int score_first_columns(int64_t M, int64_t V, int64_t k) {
   const int64_t tiles_m = (M + BM2 - 1) / BM2, tiles_n = (V + 255) / 256;
   // An eighth of the vocabulary, and at least 4 k of its sub-blocks of 32 (then a
   // sub-block of the rest reaches the bound with a chance of 1 in 5 or less), in
-  // whole waves of the SM pairs; where a second launch costs too much, all of it.
+  // whole waves of the SM pairs; all of it below 8 waves, where a second launch
+  // costs more (600 tokens, V = 32000, 4.9 waves: 74 us in one, 80 in two; 1000,
+  // V = 50280, 10.4 waves: 144 and 138).
   int64_t first = std::max((tiles_n + 7) / 8, (4 * k + 7) / 8);
   const int64_t waves = (first * tiles_m + kPairs - 1) / kPairs;
   first = waves * kPairs / tiles_m;
-  return first * 2 > tiles_n || tiles_m * tiles_n < 16 * kPairs ? static_cast<int>(V) : static_cast<int>(first * 256);
+  return first * 2 > tiles_n || tiles_m * tiles_n < 8 * kPairs ? static_cast<int>(V) : static_cast<int>(first * 256);
 }
 
 cudaError_t gemm_score(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt, const int32_t* labels,
