@@ -1405,7 +1405,8 @@ ScoreWs score_layout(uint8_t* base, int64_t M, int64_t V, int64_t k) {
   ScoreWs w{};
   const int64_t cols = M <= kScoreFew ? score_few_rows(V) : ce_tile_cols();
   const int64_t R = score_rows(M, V, k), T = cdiv(V, cols);
-  size_t off = 0;
+  // a workspace is aligned to 16 bytes, the logits are written 32 at a time
+  size_t off = base ? align256(reinterpret_cast<uintptr_t>(base)) - reinterpret_cast<uintptr_t>(base) : 256;
   auto take = [&](size_t values) {
     uint8_t* p = base ? base + off : nullptr;
     off += align256(values * 4);

@@ -25,6 +25,16 @@ cudaError_t launch_logits(const LaunchCtx& c, const __nv_bfloat16* H, const __nv
   static bool smem_ok[64] = {};
   cudaError_t e = allow_smem(kern, L::TOTAL, smem_ok);
   if (e != cudaSuccess) return e;
+  // the epilogue's registers come out of what the CTA is launched with: with
+  // fewer than the kernel counts on it would wait for them for ever
+  static int regs = 0;
+  if (regs == 0) {
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, kern);
+    if (e != cudaSuccess) return e;
+    regs = a.numRegs;
+  }
+  if (regs < L::REGS) return cudaErrorInvalidConfiguration;
   static int cap[64] = {};
   int pairs = 0;
   e = pair_capacity(reinterpret_cast<const void*>(kern), L::THREADS, L::TOTAL, c.num_sms, cap, &pairs);

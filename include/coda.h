@@ -808,9 +808,10 @@ coda_status_t coda_lmhead_policy(coda_handle_t h, const void* Hs, const void* Wt
                                  float temperature, float* stats, float* logp, void* dHs, void* dWt, void* ws,
                                  size_t ws_bytes, int64_t M, int64_t d, int64_t V, void* stream);
 
-/* Workspace of coda_lmhead_score: about 12 bytes per row and 128 columns of the
- * vocabulary, and with alternatives (k > 0) 16 more and the fp32 logits of up
- * to 2 GB of rows (256 at least), which it works through in turn.  A workspace
+/* Workspace of coda_lmhead_score: 12 bytes per row and 128 columns of the
+ * vocabulary (of 64 rows and fewer, per as many columns as spread it over the
+ * GPU), and with alternatives (k > 0) 16 more and the fp32 logits of up to 2 GB of
+ * rows (256 at least), which it works through in turn.  A workspace
  * for M tokens also serves any smaller number.  0 for M, d or V <= 0 or a k
  * that coda_lmhead_score refuses. */
 size_t coda_lmhead_score_workspace_bytes(int64_t M, int64_t d, int64_t V, int64_t k);
@@ -824,7 +825,7 @@ size_t coda_lmhead_score_workspace_bytes(int64_t M, int64_t d, int64_t V, int64_
  * keeps the relative precision of its entropy and of its token's log-probability.
  * A negative label is a position without a token: its logp is 0.  A label >= V
  * sets CODA_ERR_LABEL_RANGE in the status word; its logp is 0.  A row with a NaN
- * logit has NaN log-probabilities and entropy; NaN logits rank last.
+ * or infinite logit has NaN log-probabilities and entropy; NaN logits rank last.
  * Hs bf16 [M][d], Wt bf16 [V][d], labels int32 [M] and logp fp32 [M] (both or
  * neither), entropy fp32 [M] or NULL, top_ids int32 [M][k] and top_logp fp32
  * [M][k] (NULL iff k = 0), all of these but Hs and Wt 4-byte aligned; one of the

@@ -301,6 +301,36 @@ def test_captured_graph_and_other_stream(M, d):
     assert_device_ok()
 
 
+@pytest.mark.parametrize("M,d", [(100, 64), (1100, 2560)])
+def test_a_workspace_aligned_to_16_bytes_serves_smaller_batches(M, d):
+    c = make(M, d, 520, 6, R.TAIL).run()
+    big = torch.empty(C.coda_lmhead_distill_workspace_bytes(M + 300, d, 520, 6, True) + 16, dtype=torch.uint8,
+                      device="cuda")[16:]
+    want = [t.clone() for t in c.outputs()]
+    C.coda_lmhead_distill(*c.args[:-1], big)
+    assert all(torch.equal(a, b) for a, b in zip(want, c.outputs()))
+    assert_device_ok()
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    """Calls that overlap on the GPU."""
+    calls = [make(136, 1024, 4096, 9, R.TAIL, seed=s) for s in range(3)] + [make(1100, 2560, 1048, 5, R.TAIL)]
+    want = [[t.clone() for t in c.run().outputs()] for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    for c in calls:
+        for t in c.outputs():
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                C.coda_lmhead_distill(*c.args)
+    torch.cuda.synchronize()
+    for c, w in zip(calls, want):
+        assert all(torch.equal(a, b) for a, b in zip(w, c.outputs()))
+    assert_device_ok()
+
+
 def test_from_a_teachers_scores_to_a_students_gradients():
     """A ScoringHead's lists go into a DistillHead as they are."""
     from gemm_epilogue_transformer_tma_gb300.path import DistillHead, ScoringHead

@@ -212,6 +212,23 @@ def test_captured_graph(M, k):
     c.grade()
 
 
+@pytest.mark.parametrize("M,V", [(2, 3000), (200, 3000), (2100, 20000)])
+def test_a_workspace_aligned_to_16_bytes(M, V):
+    """As the entry points ask for, and other outputs to 4."""
+    H, W, y = R.grid_inputs(M, 64, V)
+    k = 5
+    n = C.coda_lmhead_score_workspace_bytes(M, 64, V, k)
+    f = torch.empty(M * (2 + 2 * k) + 8, device="cuda")
+    logp, entropy, top = f[1:1 + M], f[1 + M:1 + 2 * M], f[3 + 2 * M:3 + (2 + k) * M].view(M, k)
+    ids = f[5 + (2 + k) * M:5 + (2 + 2 * k) * M].view(torch.int32).view(M, k)
+    r = R.score(H, W, y, 1.0, k)
+    for off in (16, 48, 240):
+        ws = torch.empty(n + off, dtype=torch.uint8, device="cuda")[off:]
+        C.coda_lmhead_score(H, W, y, 1.0, logp, entropy, ids, top, ws)
+        assert torch.equal(ids, r["ids"]) and near(logp, r["logp"]) and near(top, r["top"])
+        assert_device_ok()
+
+
 def test_rows_in_turn():
     """More logits than a workspace holds at a time: 4096 rows of this
     vocabulary, then the others."""
