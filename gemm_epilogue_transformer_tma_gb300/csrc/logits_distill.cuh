@@ -60,10 +60,32 @@ struct LogitsDistill {
     const int m = t.m0 + t.lane;
     return State{m < M ? ld_here_f32(g.n + m) : NAN, at, entry_of(g, t, at, t.lane)};
   }
-  // Writes the entries' logits out of v, 32 columns [32 c, 32 c + 32) of 32
-  // rows, and puts -infinity in their place: through shared memory, where a lane
-  // reaches any row's, and only if there are any.
-  static __device__ __forceinline__ void take(const Params& g, const LogitsTile& t, const State& st, int c,
+  // The entries' logits are written out of v, and -infinity put in their place: a
+  // few one by one, many through shared memory.  2048 tokens, forward: with 4
+  // entries to a tile (d = 2048, V = 65536) 274 us and, all through shared memory,
+  // 290, with 10 (V = 50280) 240 and 252; with 33, all one by one, a tile of d = 256
+  // takes half as long again.
+  static constexpr uint32_t kFewEntries = 10;
+  // v[col], col the same in all lanes, and -infinity in its place in one lane:
+  // four branches, then eight tests
+  template <int LO, int N>
+  static __device__ __forceinline__ float take_one(float (&v)[4][32], int col, bool here) {
+    if constexpr (N <= 8) {
+      float x = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const bool is = col == LO + i;
+        x = is ? v[(LO + i) / 32][(LO + i) % 32] : x;
+        v[(LO + i) / 32][(LO + i) % 32] = is && here ? -INFINITY : v[(LO + i) / 32][(LO + i) % 32];
+      }
+      return x;
+    } else {
+      return col < LO + N / 2 ? take_one<LO, N / 2>(v, col, here) : take_one<LO + N / 2, N / 2>(v, col, here);
+    }
+  }
+  // those of 32 columns [32 c, 32 c + 32): shared memory, where a lane reaches any
+  // row's, is used only if there are any
+  static __device__ __forceinline__ void take_many(const Params& g, const LogitsTile& t, const State& st, int c,
                                               float (&v)[32]) {
     const uint32_t count = st.at >> 16;
     bool staged = false;
@@ -110,9 +132,18 @@ struct LogitsDistill {
         for (int i = 0; i < 32; ++i)
           if (c * 32 + i >= nv) v[c][i] = -INFINITY;
     }
-    if ((st.at >> 16) != 0) {
+    const uint32_t count = st.at >> 16;
+    if (count > kFewEntries) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) take(g, t, st, c, v[c]);
+      for (int c = 0; c < 4; ++c) take_many(g, t, st, c, v[c]);
+    } else {
+      for (uint32_t i = 0; i < count; ++i) {
+        const uint32_t e = __shfl_sync(0xffffffffu, st.entry, i);
+        if (e == kNoEntry) continue;
+        const bool here = t.lane == static_cast<int>(e & 31u);
+        const float x = take_one<0, PART_COLS>(v, static_cast<int>(e >> 5) & 127, here);
+        if (here) g.listed[static_cast<int64_t>(m) * g.k + (e >> 12)] = x;
+      }
     }
     float mx = -INFINITY;
 #pragma unroll
