@@ -1516,9 +1516,10 @@ DistillWs distill_layout(uint8_t* base, int64_t M, int64_t d, int64_t V, int64_t
   take(w.w.psum, size_t(M) * T);
   if (grads) {
     take(w.w.factor, size_t(M));
-    take(w.w.scaled, size_t(M) * d);
+    const size_t rows = size_t(std::max(M, std::min(2 * M, 2 * kDistillTwice)));
+    take(w.w.scaled, rows * d);
     take(w.dH_parts, dh_parts_bytes(M, d, V) / 4);
-    take(w.w.kept, size_t(M) * V);
+    take(w.w.kept, rows * V);
   }
   w.bytes = off;
   return w;
@@ -1576,10 +1577,10 @@ coda_status_t coda_lmhead_distill(coda_handle_t h, const void* Hs, const void* W
   if (!grads) return CODA_OK;
   bf16* dH = static_cast<bf16*>(dHs);
   bf16* dW = static_cast<bf16*>(dWt);
-  const int64_t parts = dh_parts(M, d, V);
+  const int64_t parts = dh_parts(M, d, V), rows = M <= kDistillTwice ? 2 * M : M;
   if (parts == 1)
     return from_cuda(
-        gemm_group_scaled_bwd(cx, w.w.kept, w.w.factor, Wb, w.w.scaled, dH, dW, int(M), int(d), int(V)));
+        gemm_group_scaled_bwd(cx, w.w.kept, w.w.factor, Wb, w.w.scaled, dH, dW, int(M), int(rows), int(d), int(V)));
   // few tokens: dH in ranges of the vocabulary
   CODA_CUDA(gemm_splitk(cx, w.w.kept, Wb, w.dH_parts, int(parts), false, int(M), int(d), int(V)));
   SplitDh finish{};
@@ -1590,7 +1591,8 @@ coda_status_t coda_lmhead_distill(coda_handle_t h, const void* Hs, const void* W
   finish.d4 = d / 4;
   finish.factor = w.w.factor;
   finish.out = reinterpret_cast<uint2*>(dH);
-  return from_cuda(gemm_store_plus_rows(cx, w.w.kept, w.w.scaled, dW, nullptr, nullptr, int(M), int(d), int(V), finish));
+  return from_cuda(gemm_store_plus_rows(cx, w.w.kept, w.w.scaled, dW, nullptr, nullptr, int(rows), int(d), int(V),
+                                        finish));
 }
 
 // ---------------------------------------------------------------------------

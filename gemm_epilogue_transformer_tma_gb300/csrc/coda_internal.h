@@ -203,6 +203,12 @@ cudaError_t launch_score_rows(const LaunchCtx& c, const ScoreStats& s, const Sco
 
 // Distillation from a teacher's list (distill.cu, logits_distill.cuh).
 constexpr int kDistillMaxList = 256;
+// So few rows take part in dW's contraction twice, the second time with what the
+// rounding of factor H to bf16 takes from their listed entries: the error of dW,
+// 1.4 times that of rounding it alone on average, spreads to 1.7 where few rows make
+// it.  8 tokens, d = 2048, V = 50280: 145 us, 140 without; 64, d = 1024, V = 32000: 69
+// and 64; 128 of d = 4096, V = 128256: 615 and 557, which is not done.
+constexpr int64_t kDistillTwice = 64;
 constexpr uint32_t kNoEntry = 0xFFFFFFFFu;
 struct DistillIn {
   const int32_t* ids;   // [M][k], an entry outside [0, V) is not used
@@ -227,10 +233,12 @@ struct DistillWork {
   float* psum;          // [M][T]
   float4* terms;        // [M]: shares of the statistics
   int* done;            // rows finished
-  // with gradients
-  __nv_bfloat16* kept;    // [M][V]: dL up to a factor per row
+  // with gradients, dL = factor kept, scaled = factor H: [M][V] and [M][d].  Up to
+  // kDistillTwice rows as many more behind them: the listed entries of kept alone,
+  // and what bf16 takes from scaled
+  __nv_bfloat16* kept;
   float* factor;          // [M]
-  __nv_bfloat16* scaled;  // [M][d]: factor H
+  __nv_bfloat16* scaled;
 };
 struct DistillOut {
   float* stats;
@@ -242,10 +250,11 @@ cudaError_t gemm_distill(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_
                          float log2e_over_t, int M, int d, int V);
 cudaError_t launch_distill_rows(const LaunchCtx& c, const DistillIn& in, const DistillWork& w, const DistillOut& o,
                                 const __nv_bfloat16* H, int64_t M, int64_t d, int64_t V);
-// dH = diag(factor) E Wt and dW = E^T scaled (E [M][V], scaled [M][d]), one grouped launch
+// dH = diag(factor) E Wt of the first M rows of E and dW = E^T scaled of all
+// (E [rows][V], scaled [rows][d]), one grouped launch
 cudaError_t gemm_group_scaled_bwd(const LaunchCtx& c, const __nv_bfloat16* E, const float* factor,
                                   const __nv_bfloat16* Wt, const __nv_bfloat16* scaled, __nv_bfloat16* dH,
-                                  __nv_bfloat16* dW, int M, int d, int V);
+                                  __nv_bfloat16* dW, int M, int rows, int d, int V);
 
 // parts_buf [parts][M rounded up to 256][N] fp32 (+)= the K ranges of A B, A
 // [M][K], B [K][N] (gemm_splitk.cuh); parts <= the k-blocks of 64 in K

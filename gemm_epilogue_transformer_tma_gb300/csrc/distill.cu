@@ -9,6 +9,8 @@
 // The loss is summed as phi(a, b) = a log(a / b) - a + b >= 0 over the targets,
 // plus phi(r, R) and the constant P + r - 1: where student and teacher agree,
 // the phi are small one by one, while the logarithms' products cancel in sum.
+// Of a list alone, without normalisation or tail, R + P - 1 would be taken from
+// the phi again; there the products are summed as they are.
 #include <algorithm>
 
 #include "../../include/coda.h"
@@ -19,11 +21,8 @@ namespace coda {
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
-
-// v over the CTA's threads, in all of them; part: kWarps of them
-template <class T, class F>
+// v over the CTA's warps, in all threads; part: one to a warp
+template <int WARPS, class T, class F>
 __device__ __forceinline__ T block_reduce(T v, T* part, F&& f) {
   v = f(v);  // over the warp, in every lane
   __syncthreads();  // part may still be read
@@ -31,7 +30,7 @@ __device__ __forceinline__ T block_reduce(T v, T* part, F&& f) {
   __syncthreads();
   T s = part[0];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) s = f(s, part[w]);
+  for (int w = 1; w < WARPS; ++w) s = f(s, part[w]);
   return s;
 }
 __device__ __forceinline__ float warp_sum(float v) {
@@ -307,12 +306,18 @@ __global__ void __launch_bounds__(kListThreads) distill_list_kernel(const Distil
   }
 }
 
-// a log(a / b) - a + b; lb = log b, good where b itself has underflowed
-__device__ __forceinline__ float phi(float a, float b, float lb) {
+// a log(a / b) - a + b; u = b - a; lb = log b, good where b itself has underflowed
+__device__ __forceinline__ float phi(float a, float b, float u, float lb) {
   if (a == 0.f) return b;
-  const float u = b - a;
   if (fabsf(u) <= 0.5f * a) return u - a * log1pf(u / a);
   return a * (logf(a) - lb) + u;
+}
+
+// a log(a / b) alone
+__device__ __forceinline__ float t_log_ratio(float a, float b, float lb) {
+  if (a == 0.f) return 0.f;
+  const float u = b - a;
+  return fabsf(u) <= 0.5f * a ? -a * log1pf(u / a) : a * (logf(a) - lb);
 }
 
 // psum of some blocks together, in units of 2^n
@@ -334,16 +339,23 @@ struct AddRests {
   }
 };
 
-// A row's loss and, with gradients, its factor on the kept exponentials, the
-// listed tokens' entries among them and its scaled hidden state.  A row to a
-// CTA; the last to end adds up the statistics, in a fixed order.
-template <bool GRADS>
+// What the gradients' GEMMs find (DistillWork): nothing, the kept exponentials and
+// H times the row's factor in bf16, or, of few rows, with what bf16 takes from that.
+enum RowGrads { NO_GRADS, GRADS_ONCE, GRADS_TWICE };
+
+// A row's loss and what its gradients need.  A row to a CTA; the last to end adds
+// up the statistics, in a fixed order.  512 threads where rows are few (the same
+// for both forms of a size: the loss has the same bits with gradients and without).
+constexpr int kRowThreads = 128, kFewRowThreads = 512;
+
+template <int GRADS, int kThreads>
 __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn in, const DistillWork w,
                                                                 const DistillOut o,
                                                                 const __nv_bfloat16* __restrict__ H, int64_t M,
                                                                 int64_t d, int64_t V) {
   griddep_wait();
   griddep_launch_dependents();
+  constexpr int kWarps = kThreads / 32;
   __shared__ Sums part[kWarps];
   __shared__ Rest rests[kWarps];
   __shared__ bool last;
@@ -355,11 +367,15 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
   const float* pn = w.pn + m * T;
   float4 terms = make_float4(0.f, 0.f, 0.f, 0.f);
   float loss = 0.f, factor = 0.f;
+  auto zero_row = [&](__nv_bfloat16* to) {
+    for (int64_t i = tid; i < V / 8; i += kThreads) reinterpret_cast<uint4*>(to)[i] = make_uint4(0u, 0u, 0u, 0u);
+  };
   if (weight != 0.f) {
     const float n_row = w.n[m];
     const float4 mass = w.mass[m];
+    constexpr float kLn2 = 0.6931471805599453f;
     // this thread's entries
-    constexpr int N = kDistillMaxList / kThreads;
+    constexpr int N = (kDistillMaxList + kThreads - 1) / kThreads;
     int32_t id[N];
     float x[N], t[N], q[N];
     Sums all{0.f, 0.f, -INFINITY};
@@ -377,7 +393,7 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
       all.a += s;
       all.b += s < 0.f ? 1.f : 0.f;
     }
-    all = block_reduce(all, part, AddSums());
+    all = block_reduce<kWarps>(all, part, AddSums());
     Rest rest{n_row, all.a};
     const bool far = all.b != 0.f;
     if (far) {  // blocks at a scale of their own
@@ -386,7 +402,7 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
         const float s = psum[b];
         rest = AddRests()(rest, Rest{s < 0.f ? pn[b] : n_row, fabsf(s)});
       }
-      rest = block_reduce(rest, rests, AddRests());
+      rest = block_reduce<kWarps>(rest, rests, AddRests());
     }
     const bool some = rest.s != 0.f;  // tokens off the list
     // everything in units of 2^ref, ref an integer near the largest listed logit or above it
@@ -396,50 +412,57 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
     Sums on{0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      x[i] = fmaf(x[i], c, -ref);
-      q[i] = ex2_f(x[i]);
+      // the product's rounding error into the power of two: 2^-24 of an x of 16 is 2^-20 of q
+      const float2 y = mul_exact(x[i], c);
+      x[i] = y.x - ref;
+      const float low = isfinite(x[i]) ? y.y + (y.x - (x[i] + ref)) : 0.f;
+      q[i] = ex2_f(x[i]) * fmaf(low, kLn2, 1.f);
+      x[i] += low;
       on.a += q[i];
     }
-    on = block_reduce(on, part, AddSums());
+    on = block_reduce<kWarps>(on, part, AddSums());
     const float rest_ref = rest.s * ex2_f(down), S = rest_ref + on.a, log2_S = log2f(S);
-    constexpr float kLn2 = 0.6931471805599453f;
-    const float R = rest_ref / S, lR = (log2f(rest.s) + down - log2_S) * kLn2;
+    const float R = rest_ref / S, Q = on.a / S;
+    const float lR = Q < 0.5f ? log1pf(-Q) : (log2f(rest.s) + down - log2_S) * kLn2;
     // a tail needs a token off the list
     const float P = mass.x, r = some ? mass.y : 0.f, excess = some ? mass.z : mass.z - mass.y;
+    const float less = r != 0.f && Q < 0.5f ? P - Q : R - r;  // R - r, of which both may be nearly 1
+    const bool direct = in.mode == CODA_DISTILL_LISTED;
     Sums row{0.f, 0.f, 0.f};  // loss, cross-entropy, largest entry of dL
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (id[i] >= 0) {
         const float lq = (x[i] - log2_S) * kLn2;
         q[i] /= S;
-        row.a += phi(t[i], q[i], lq);
+        row.a += direct ? t_log_ratio(t[i], q[i], lq) : phi(t[i], q[i], q[i] - t[i], lq);
         if (t[i] != 0.f) row.b = fmaf(-t[i], lq, row.b);
         q[i] = fmaf(P + r, q[i], -t[i]);  // d loss / d z
         row.top = fmaxf(row.top, fabsf(q[i]));
       }
     }
-    row = block_reduce(row, part, AddSums());
-    loss = row.a + (some ? phi(r, R, lR) : 0.f) + excess;
+    row = block_reduce<kWarps>(row, part, AddSums());
+    loss = direct ? row.a : row.a + (some ? phi(r, R, less, lR) : 0.f) + excess;
     if (r != 0.f) row.b = fmaf(-r, lR, row.b);
-    terms = make_float4(weight * loss, weight * row.b, weight * P, weight * (on.a / S));
-    if (GRADS) {
+    terms = make_float4(weight * loss, weight * row.b, weight * P, weight * Q);
+    if (GRADS != NO_GRADS) {
       const float scale = weight / in.temperature, steep = row.top;
-      float f = (P + r) * (ex2_f(down) / S) - (r != 0.f ? r / rest.s : 0.f);
       __nv_bfloat16* kept = w.kept + m * V;
+      float f = (P + r) * (ex2_f(down) / S) - (r != 0.f ? r / rest.s : 0.f);
       // A row with blocks at a scale of their own, or whose factor is too small
       // to divide by, as it is where student and teacher agree on R: the kept
-      // exponentials are made d loss / d z.
+      // exponentials are made d loss / d z, those listed stay 0.
       if (far || !some || !(fabsf(f) >= 0x1p-40f * steep)) {
+        const float all = (P + r) * (ex2_f(down) / S), tail = r != 0.f ? r / rest.s : 0.f;
+        uint4* at = reinterpret_cast<uint4*>(kept);
         for (int64_t i = tid; i < V / 8; i += kThreads) {
           const int64_t b = i >> 4;
           // above rest.n: a block of zeros, all listed
           const float up = ex2_f(fminf((psum[b] < 0.f ? pn[b] : n_row) - rest.n, 0.f));
-          const float g = some ? (P + r) * (ex2_f(down) / S) * up - (r != 0.f ? r / rest.s * up : 0.f) : 0.f;
+          const float g = some ? all * up - tail * up : 0.f;
           float v[8];
-          uint4* at = reinterpret_cast<uint4*>(kept) + i;
-          unpack_bf16x8(*at, v);
-          *at = make_uint4(pack_bf16x2(v[0] * g, v[1] * g), pack_bf16x2(v[2] * g, v[3] * g),
-                           pack_bf16x2(v[4] * g, v[5] * g), pack_bf16x2(v[6] * g, v[7] * g));
+          unpack_bf16x8(at[i], v);
+          at[i] = make_uint4(pack_bf16x2(v[0] * g, v[1] * g), pack_bf16x2(v[2] * g, v[3] * g),
+                             pack_bf16x2(v[4] * g, v[5] * g), pack_bf16x2(v[6] * g, v[7] * g));
         }
         f = 1.f;
         __syncthreads();
@@ -448,31 +471,49 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
       // largest entry, which has nearly all of the square of dL, is a bf16 number:
       // it keeps its fp32 value, and the tokens off the list move together by no
       // more than each is rounded.  The gradients' error over that of rounding
-      // them alone, dH and dW: 1.0 and 1.35, 1.3 to 1.6 and 1.7 with f as it is.
+      // them alone, dH and dW: 1.0 and 1.4, 1.3 to 1.6 and 1.7 with f as it is.
       const float largest = steep / f, exact = bf16_round(largest);
       if (exact != 0.f && isfinite(exact)) f = steep / exact;
       factor = scale * f;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (id[i] >= 0) kept[id[i]] = __float2bfloat16_rn(q[i] / f);
+      for (int i = 0; i < N; ++i) {
+        q[i] /= f;
+        if (id[i] >= 0) kept[id[i]] = __float2bfloat16_rn(q[i]);
+      }
+      if (GRADS == GRADS_TWICE) {
+        __nv_bfloat16* again = kept + M * V;
+        zero_row(again);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (id[i] >= 0) again[id[i]] = __float2bfloat16_rn(q[i]);
+      }
     }
   }
-  if (GRADS) {
+  if (GRADS != NO_GRADS) {
     // an exact 0 without weight, whatever the hidden state holds
     const uint4* h = reinterpret_cast<const uint4*>(H + m * d);
     uint4* to = reinterpret_cast<uint4*>(w.scaled + m * d);
     for (int64_t i = tid; i < d / 8; i += kThreads) {
-      float v[8];
+      float v[8], low[8];
       unpack_bf16x8(__ldg(h + i), v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = weight != 0.f ? v[j] * factor : 0.f;
+      for (int j = 0; j < 8; ++j) {
+        const float x = weight != 0.f ? v[j] * factor : 0.f;
+        v[j] = bf16_round(x);
+        low[j] = x - v[j];
+      }
       to[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                          pack_bf16x2(v[6], v[7]));
+      if (GRADS == GRADS_TWICE)
+        to[M * (d / 8) + i] = make_uint4(pack_bf16x2(low[0], low[1]), pack_bf16x2(low[2], low[3]),
+                                         pack_bf16x2(low[4], low[5]), pack_bf16x2(low[6], low[7]));
     }
+    if (GRADS == GRADS_TWICE && weight == 0.f) zero_row(w.kept + (M + m) * V);
   }
   if (tid == 0) {
     if (o.row_loss != nullptr) o.row_loss[m] = loss;
-    if (GRADS) w.factor[m] = factor;
+    if (GRADS != NO_GRADS) w.factor[m] = factor;
     w.terms[m] = terms;
     __threadfence();
     last = atomicAdd(w.done, 1) == static_cast<int>(M - 1);
@@ -521,8 +562,13 @@ cudaError_t launch_distill_list(const LaunchCtx& c, const DistillIn& in, const D
 
 cudaError_t launch_distill_rows(const LaunchCtx& c, const DistillIn& in, const DistillWork& w, const DistillOut& o,
                                 const __nv_bfloat16* H, int64_t M, int64_t d, int64_t V) {
-  return launch_chained(c, w.kept != nullptr ? distill_rows_kernel<true> : distill_rows_kernel<false>,
-                        dim3(static_cast<unsigned>(M)), dim3(kThreads), 0, in, w, o, H, M, d, V);
+  const bool few = M <= kDistillTwice, grads = w.kept != nullptr;
+  auto kern = few ? grads ? distill_rows_kernel<GRADS_TWICE, kFewRowThreads>
+                          : distill_rows_kernel<NO_GRADS, kFewRowThreads>
+              : grads ? distill_rows_kernel<GRADS_ONCE, kRowThreads>
+                      : distill_rows_kernel<NO_GRADS, kRowThreads>;
+  return launch_chained(c, kern, dim3(static_cast<unsigned>(M)), dim3(few ? kFewRowThreads : kRowThreads), 0, in, w, o,
+                        H, M, d, V);
 }
 
 }  // namespace coda

@@ -182,21 +182,21 @@ cudaError_t gemm_group_policy_bwd(const LaunchCtx& c, const __nv_bfloat16* dL, c
 
 cudaError_t gemm_group_scaled_bwd(const LaunchCtx& c, const __nv_bfloat16* E, const float* factor,
                                   const __nv_bfloat16* Wt, const __nv_bfloat16* scaled, __nv_bfloat16* dH,
-                                  __nv_bfloat16* dW, int M, int d, int V) {
+                                  __nv_bfloat16* dW, int M, int rows, int d, int V) {
   if (!c.pair) {
     cudaError_t e = gemm_store(c, E, false, Wt, true, dH, M, d, V, factor, nullptr);
     if (e != cudaSuccess) return e;
-    return gemm_store(c, E, true, scaled, true, dW, V, d, M, nullptr, nullptr);
+    return gemm_store(c, E, true, scaled, true, dW, V, d, rows, nullptr, nullptr);
   }
   GroupArgs<EpiStore, EpiStore> ga{};
   // The whole vocabulary is one contraction: 8016 products of 16 at V = 128256,
   // each of which costs the running sum half of its last place at most (2^-25),
   // 2.4e-4 in all beside the 2^-9 of the result's rounding.
   if (!make_operand_maps(&ga.tmA0, &ga.tmB0, E, false, Wt, true, M, d, V, b_box_rows(c)) ||
-      !make_operand_maps(&ga.tmA1, &ga.tmB1, E, true, scaled, true, V, d, M, b_box_rows(c)))
+      !make_operand_maps(&ga.tmA1, &ga.tmB1, E, true, scaled, true, V, d, rows, b_box_rows(c)))
     return cudaErrorInvalidValue;
   ga.sh0 = pair_shape(M, d, V);
-  ga.sh1 = pair_shape(V, d, M);
+  ga.sh1 = pair_shape(V, d, rows);
   if (!make_tmap_store_bf16(&ga.ep0.out, dH, d, M, d) || !make_tmap_store_bf16(&ga.ep1.out, dW, d, V, d))
     return cudaErrorInvalidValue;
   ga.ep0.row_scale = factor;

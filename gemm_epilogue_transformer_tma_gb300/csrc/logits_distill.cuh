@@ -29,16 +29,16 @@ struct LogitsDistill {
   static constexpr bool kStores = KEEP;
   static constexpr int kStages = 6, kSlots = 2;
   struct Params {
-    CUtensorMap kept;    // KEEP: [M][V] bf16, 32 x 32 boxes
+    CUtensorMap kept;       // KEEP: [M][V] bf16, 32 x 32 boxes
     const uint32_t* at;     // [G][T], G = ceil(M / 32): where a block's entries begin | how many << 16
     const uint32_t* entry;  // [G][32 k]: row of the 32 | column of the block << 5 | position in the row's list << 12,
                             // or kNoEntry
     const float* n;         // [M]: the row's pn, NaN for a row without weight
-    float* listed;       // [M][k]: the entries' logits
-    float* pn;           // [M][T], T = ceil(V / 128)
-    float* psum;         // [M][T]
+    float* listed;          // [M][k]: the entries' logits
+    float* pn;              // [M][T], T = ceil(V / 128)
+    float* psum;            // [M][T]
     int T, k;
-    float c;             // log2(e) / temperature
+    float c;                // log2(e) / temperature
   };
   // The entries of a warp's 32 rows in its 128 columns, 2 of them where 64 are
   // listed of 128256: one to a lane.  Where they are is loaded a tile ahead, so
@@ -51,7 +51,8 @@ struct LogitsDistill {
     uint32_t at, entry;
   };
   static __device__ __forceinline__ uint32_t entry_of(const Params& g, const LogitsTile& t, uint32_t at, uint32_t i) {
-    return i < (at >> 16) ? ld_here_u32(g.entry + static_cast<int64_t>(t.m0 >> 5) * (32 * g.k) + (at & 0xFFFFu) + i) : 0u;
+    const uint32_t* e = g.entry + static_cast<int64_t>(t.m0 >> 5) * (32 * g.k) + (at & 0xFFFFu);
+    return i < (at >> 16) ? ld_here_u32(e + i) : 0u;
   }
   static __device__ __forceinline__ Early early(const Params& g, const LogitsTile& t) {
     return ld_here_u32(g.at + static_cast<int64_t>(t.m0 >> 5) * g.T + t.part);
@@ -86,7 +87,7 @@ struct LogitsDistill {
   // those of 32 columns [32 c, 32 c + 32): shared memory, where a lane reaches any
   // row's, is used only if there are any
   static __device__ __forceinline__ void take_many(const Params& g, const LogitsTile& t, const State& st, int c,
-                                              float (&v)[32]) {
+                                                   float (&v)[32]) {
     const uint32_t count = st.at >> 16;
     bool staged = false;
     for (uint32_t i = t.lane; i - t.lane < count; i += 32) {

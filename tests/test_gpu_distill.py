@@ -104,8 +104,9 @@ def test_loss_and_gradients(M, d, V, k, mode):
 
 
 @pytest.mark.parametrize("mode", MODES)
-def test_forward_only_equals_the_full_call(mode):
-    c = make(200, 64, 3000, 20, mode).run()
+@pytest.mark.parametrize("M", [50, 200])
+def test_forward_only_equals_the_full_call(mode, M):
+    c = make(M, 64, 3000, 20, mode).run()
     f = Call(c.H, c.W, c.ids, c.val, c.w, mode, grads=False).run()
     f.grade()
     assert torch.equal(c.stats, f.stats) and torch.equal(c.loss, f.loss)
@@ -114,6 +115,49 @@ def test_forward_only_equals_the_full_call(mode):
     again = [t.clone() for t in c.outputs()]
     c.run()
     assert all(torch.equal(a, b) for a, b in zip(again, c.outputs()))
+
+
+@pytest.mark.parametrize("M,d,V,k", [(1, 256, 9000, 1), (1, 256, 520, 40), (7, 256, 9000, 3), (40, 1024, 1000, 20),
+                                     (64, 512, 9000, 64), (65, 512, 9000, 20), (700, 512, 4096, 16),
+                                     (1100, 2560, 1048, 33)])
+@pytest.mark.parametrize("mode", MODES)
+def test_a_largest_entry_that_outweighs_its_row_is_not_rounded(M, d, V, k, mode):
+    """dH carries one rounding, and dW up to 64 rows; of more, dW also that of
+    the scaled Hs, half a step (2^-8) of each of its products: a bound, as rows that
+    are few and values of Hs that repeat do not average.  The other entries of dL
+    are rounded once or twice: half a step each, of independent signs."""
+    c = make(M, d, V, k, mode, seed=M + k).run()
+    r = c.grade()
+    dL, H, W = r["dL"], c.H.double(), c.W.double()
+    rest = dL.scatter(1, dL.abs().argmax(1, keepdim=True), 0.0).abs()
+    for got, ref, others, scaled in ((c.dH, r["dH"], rest ** 2 @ W ** 2, None),
+                                     (c.dW, r["dW"], (rest ** 2).t() @ H ** 2, dL.abs().t() @ H.abs())):
+        one = (ref.to(BF).double() - ref).norm()
+        bar = ((1.02 * one) ** 2 + 2 * 2.0 ** -16 * others.sum()).sqrt()
+        if scaled is not None and M > 64:
+            bar += 2.0 ** -8 * scaled.norm()
+        assert (got.double() - ref).norm() <= bar
+
+
+@pytest.mark.parametrize("M", [6, 200])
+@pytest.mark.parametrize("mode", MODES)
+def test_small_masses_keep_their_digits(mode, M):
+    """Teachers and students whose lists hold a thousandth of the probability:
+    the loss, far below the logarithms it is made of, and the cross-entropy of a
+    tail that is nearly everything.  Terms of one sign, or taken as they are:
+    relative 2^-18 of each."""
+    V, k = 20000, 4
+    H, W, y = R.grid_inputs(M, 64, V, sure=0.5, seed=M)
+    H = (H.float() / 4).to(BF)
+    ids = torch.randint(0, V, (M, k), generator=torch.Generator().manual_seed(2)).to(I32).cuda()
+    lq = torch.log_softmax(R.logits(H, W), 1).gather(1, ids.long())
+    val = (lq + 0.7 * torch.randn(M, k, generator=torch.Generator().manual_seed(3)).cuda()).float()
+    c = Call(H, W, ids, val, torch.full((M,), 1 / M, device="cuda"), mode, grads=False).run()
+    r = R.distill(H, W, ids, val, c.w, mode)
+    t = (torch.softmax(val.double(), 1) if mode == R.NORMALIZED else val.double().exp())
+    size = (t * (val.double() - lq).abs()).sum(1) + (t - lq.exp()).abs().sum(1)
+    assert ((c.loss.double() - r["loss"]).abs() <= 2.0 ** -18 * size + 2.0 ** -22 * r["loss"].abs() + 1e-12).all()
+    assert ((c.stats.double() - r["stats"]).abs() <= 2.0 ** -18 * r["stats"].abs() + 2.0 ** -18 * size.mean()).all()
 
 
 def test_single_sm_gemms():
