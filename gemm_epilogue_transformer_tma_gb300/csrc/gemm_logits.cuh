@@ -16,10 +16,13 @@
 // SM-pair schedule of gemm_tc2.cuh on 256 x 256 tiles; 8 epilogue warps, so
 // that a thread keeps one row's 128 sums of a half tile in registers, 224 of
 // them: warps 0 to 3 (TMA, MMA, two that only wait) give back what they do not
-// need.  2048
-// tokens, V = 65536, d = 2048 under the profiler: 278 us, 92 % of the tensor
-// pipe; with all exponentials kept 317, 78 % (their way through shared memory;
-// stores from the registers, a row per lane, made a whole update 5 % slower).
+// need.  With 168, what was spilled and what was loaded within a tile made the
+// tile's epilogue longer than the two pieces of MMAs that run beside it.  2048
+// tokens, V = 65536, d = 2048 under the profiler: the policy loss's statistics 289
+// us, 90 % of the tensor pipe (dense random operands, at the clock they leave),
+// with all exponentials kept 307, 84 % (their way through shared memory; stores
+// from the registers, a row per lane, made a whole update 5 % slower);
+// distillation 263 and 300, 91 and 80 %.
 #pragma once
 
 #include "gemm_tc2.cuh"

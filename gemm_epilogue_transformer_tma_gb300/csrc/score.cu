@@ -10,7 +10,8 @@
 //
 // The k largest logits lie in sub-blocks whose maximum is at least the k-th
 // largest of those maxima, so nearly all of a row's logits are never read
-// again: 64 of 128256 read some 70 sub-blocks of 32.
+// again: 64 of 128256 read some 70 sub-blocks of 32.  Nor are all of them written:
+// see launch_score_bound in gemm_score.
 #include <algorithm>
 
 #include "coda_internal.h"
@@ -231,8 +232,10 @@ __global__ void __launch_bounds__(kTopThreads) score_bound_kernel(const ScoreSta
   }
 }
 
-// With alternatives: 128 threads to a row.  4096 rows of V = 128256, k = 64
-// @TOP@
+// With alternatives: 128 threads to a row.  2048 rows of V = 65536, k = 64: 29 us
+// under the profiler, half of the issue slots (the blocks' statistics, 42 MB, are
+// what it reads); one row of V = 32000, k = 20: 10 us, the latency of its four
+// rounds of loads and nine barriers.
 // HELD: T <= kTopHeld kTopThreads; otherwise what a thread would hold is read again.
 template <bool HELD>
 __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats s, const ScoreOut o, int64_t M,
