@@ -241,7 +241,7 @@ struct DistillWork {
   __nv_bfloat16* scaled;
 };
 struct DistillOut {
-  float* stats;
+  float* stats;     // or null: the shares stay in DistillWork::terms
   float* row_loss;  // or null
 };
 cudaError_t launch_distill_list(const LaunchCtx& c, const DistillIn& in, const DistillWork& w, const __nv_bfloat16* H,
@@ -307,6 +307,8 @@ struct SplitDh {
   int64_t stride4, n4, d4;
   const float* factor;  // [n4 / d4]
   uint2* out;           // bf16
+  const float4* terms;  // [n4 / d4], or null: their sum to stats
+  float* stats;
 };
 cudaError_t gemm_store_plus_rows(const LaunchCtx& c, const __nv_bfloat16* dL, const __nv_bfloat16* H,
                                  __nv_bfloat16* dWc, const uint32_t* slot, const float* rows, int M, int d, int Vc,

@@ -363,34 +363,55 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
   __shared__ bool last;
   const int64_t m = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = w.k, T = w.T;
-  const float weight = in.weight != nullptr ? in.weight[m] : in.uniform;
   const float c = in.log2e_over_t;
   const float* psum = w.psum + m * T;
   const float* pn = w.pn + m * T;
+  // All that a row needs is loaded before any of it is looked at (rubbish in a row
+  // without weight): its time is the latency of the loads that wait for others.
+  const float weight = in.weight != nullptr ? in.weight[m] : in.uniform;
+  const float n_row = w.n[m];
+  const float4 mass = w.mass[m];
+  constexpr int N = (kDistillMaxList + kThreads - 1) / kThreads;
+  int32_t id[N];
+  float x[N], t[N], q[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int64_t j = m * k + tid + i * kThreads;
+    const bool there = tid + i * kThreads < k;
+    id[i] = there ? w.ids[j] : -1;
+    x[i] = there ? w.listed[j] : 0.f;
+    t[i] = there ? w.t[j] : 0.f;
+  }
+  constexpr int kHeld = kThreads == kFewRowThreads ? 2 : 8;  // blocks to a thread
+  float held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) held[i] = tid + i * kThreads < T ? psum[tid + i * kThreads] : 0.f;
+  const uint4* h = reinterpret_cast<const uint4*>(H + m * d);
+  uint4 first_h = make_uint4(0u, 0u, 0u, 0u);
+  if (GRADS != NO_GRADS && tid < d / 8) first_h = __ldg(h + tid);
+
   float4 terms = make_float4(0.f, 0.f, 0.f, 0.f);
   float loss = 0.f, factor = 0.f;
   auto zero_row = [&](__nv_bfloat16* to) {
     for (int64_t i = tid; i < V / 8; i += kThreads) reinterpret_cast<uint4*>(to)[i] = make_uint4(0u, 0u, 0u, 0u);
   };
   if (weight != 0.f) {
-    const float n_row = w.n[m];
-    const float4 mass = w.mass[m];
     constexpr float kLn2 = 0.6931471805599453f;
-    // this thread's entries
-    constexpr int N = (kDistillMaxList + kThreads - 1) / kThreads;
-    int32_t id[N];
-    float x[N], t[N], q[N];
     Sums all{0.f, 0.f, -INFINITY};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int j = tid + i * kThreads;
-      id[i] = j < k ? w.ids[m * k + j] : -1;
-      x[i] = id[i] >= 0 ? w.listed[m * k + j] : -INFINITY;
-      t[i] = id[i] >= 0 ? w.t[m * k + j] : 0.f;
+      if (id[i] < 0) {
+        x[i] = -INFINITY;
+        t[i] = 0.f;
+      }
       all.top = fmaxf(all.top, x[i]);
     }
-#pragma unroll 8
-    for (int b = tid; b < T; b += kThreads) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      all.a += held[i];
+      all.b += held[i] < 0.f ? 1.f : 0.f;
+    }
+    for (int b = tid + kHeld * kThreads; b < T; b += kThreads) {
       const float s = psum[b];
       all.a += s;
       all.b += s < 0.f ? 1.f : 0.f;
@@ -494,11 +515,10 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
   }
   if (GRADS != NO_GRADS) {
     // an exact 0 without weight, whatever the hidden state holds
-    const uint4* h = reinterpret_cast<const uint4*>(H + m * d);
     uint4* to = reinterpret_cast<uint4*>(w.scaled + m * d);
     for (int64_t i = tid; i < d / 8; i += kThreads) {
       float v[8], low[8];
-      unpack_bf16x8(__ldg(h + i), v);
+      unpack_bf16x8(i == tid ? first_h : __ldg(h + i), v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float x = weight != 0.f ? v[j] * factor : 0.f;
@@ -517,9 +537,13 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
     if (o.row_loss != nullptr) o.row_loss[m] = loss;
     if (GRADS != NO_GRADS) w.factor[m] = factor;
     w.terms[m] = terms;
-    __threadfence();
-    last = atomicAdd(w.done, 1) == static_cast<int>(M - 1);
+    last = false;
+    if (o.stats != nullptr) {
+      __threadfence();
+      last = atomicAdd(w.done, 1) == static_cast<int>(M - 1);
+    }
   }
+  if (o.stats == nullptr) return;
   __syncthreads();
   if (!last) return;
   __threadfence();

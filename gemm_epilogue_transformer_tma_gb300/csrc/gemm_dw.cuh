@@ -9,9 +9,9 @@
 //
 // dL [M][Vc] and H [M][d] bf16 are both read MN-major.  rows fp32 [tokens][d]
 // and slot [Vc] as EpiStorePlusRows; slot may be null: no rows (distillation).
-// The epilogue's warps can also finish a split data gradient before their first
-// tile is there: dH[m] = bf16(factor[m] sum of the parts) (distillation, 136
-// tokens: 10 us as a kernel of its own).
+// Four more warps finish a split data gradient beside that, dH[m] = bf16(factor[m]
+// sum of the parts), and a sum over its rows (distillation, 136 tokens: 10 us as a
+// kernel of its own).
 #pragma once
 
 #include "coda_internal.h"
@@ -22,7 +22,8 @@ namespace coda {
 struct DwSmem {
   static constexpr int STAGES = 5;
   static constexpr int EPI_WARPS = 8;
-  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int DH_WARPS = 4;
+  static constexpr int THREADS = 64 + 32 * (EPI_WARPS + DH_WARPS);
   static constexpr int A_BYTES = 128 * BK * 2;
   static constexpr int STAGE_BYTES = 2 * A_BYTES;
   static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
@@ -41,6 +42,30 @@ struct DwArgs {
   int M, N;               // Vc, d
   int tiles_m, tiles_n, num_kb;
 };
+
+// stats[i] = sum over the rows of terms[m][i], in a fixed order; one warp
+__device__ __forceinline__ void sum_terms(const float4* terms, int64_t M, int lane, float* stats) {
+  float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int64_t i = lane; i < M; i += 32) {
+    const float4 x = terms[i];
+    add_exact(hi[0], lo[0], x.x, 0.f);
+    add_exact(hi[1], lo[1], x.y, 0.f);
+    add_exact(hi[2], lo[2], x.z, 0.f);
+    add_exact(hi[3], lo[3], x.w, 0.f);
+  }
+#pragma unroll
+  for (int q = 16; q > 0; q >>= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float h = __shfl_xor_sync(0xffffffffu, hi[i], q), l = __shfl_xor_sync(0xffffffffu, lo[i], q);
+      add_exact(hi[i], lo[i], h, l);
+    }
+  if (lane < 4)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (lane == i) stats[i] = exact_value(hi[i], lo[i]);
+}
 
 // four columns to a thread
 __device__ __forceinline__ void finish_dh(const SplitDh& h, int64_t first, int64_t step) {
@@ -209,6 +234,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DwSmem::THREADS, 1)
         if (!mbar_wait_timeout(drain, 0, ctl.timeout_ns) && lane == 0) atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
       }
     }
+  } else if (warp >= 2 + L::EPI_WARPS) {
+    constexpr int N = 32 * L::DH_WARPS;
+    if (g.dh.terms != nullptr && blockIdx.x == 0 && warp == 2 + L::EPI_WARPS) {
+      sum_terms(g.dh.terms, g.dh.n4 / g.dh.d4, lane, g.dh.stats);
+    }
+    finish_dh(g.dh, blockIdx.x * static_cast<int64_t>(N) + threadIdx.x - (L::THREADS - N),
+              gridDim.x * static_cast<int64_t>(N));
   } else {
     const int quad = warp & 3;
     const int half = (warp - 2) >> 2;
@@ -223,8 +255,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DwSmem::THREADS, 1)
       return g.slot != nullptr && t < num_tiles && m < g.M ? __ldg(g.slot + m) : kNoSlot;
     };
     uint32_t s_next = slot_of(cluster_id);
-    finish_dh(g.dh, blockIdx.x * static_cast<int64_t>(32 * L::EPI_WARPS) + threadIdx.x - 64,
-              gridDim.x * static_cast<int64_t>(32 * L::EPI_WARPS));
     for (int t = cluster_id; t < num_tiles; t += num_clusters, ++it) {
       const int m0 = row0(t);
       const uint32_t s = s_next;
