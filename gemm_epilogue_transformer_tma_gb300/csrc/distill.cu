@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
       factor = scale * f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        q[i] /= f;
+        q[i] = f != 0.f ? q[i] / f : 0.f;  // 0 only with a row of zeros: no mass, or a student beyond doubt
         if (id[i] >= 0) kept[id[i]] = __float2bfloat16_rn(q[i]);
       }
       if (GRADS == GRADS_TWICE) {

@@ -413,9 +413,10 @@ __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats
     return here;
   };
   auto gather = [&](uint32_t least) {
-    each_logit(sub, logits, subs, cols, V, max(least, rank_key(kept)), warp, kTopWarps, lane, [&](bool there, uint32_t key, uint32_t token) {
-      append(sm, there && key >= least, key, token, lane);
-    });
+    each_logit(sub, logits, subs, cols, V, max(least, rank_key(kept)), warp, kTopWarps, lane,
+               [&](bool there, uint32_t key, uint32_t token) {
+                 append(sm, there && key >= least, key, token, lane);
+               });
     __syncthreads();
   };
   if (n > kTopList) {
@@ -522,7 +523,8 @@ cudaError_t launch_score_bound(const LaunchCtx& c, const ScoreStats& s, int64_t 
 cudaError_t launch_score_rows(const LaunchCtx& c, const ScoreStats& s, const ScoreOut& o, int64_t M, int64_t V) {
   if (o.k == 0)
     return launch_chained(c, score_rows_kernel, dim3(static_cast<unsigned>((M + 3) / 4)), dim3(128), 0, s, o, M, V);
-  return launch_chained(c, s.T <= kTopHeld * kTopThreads ? score_top_kernel<true> : score_top_kernel<false>, dim3(static_cast<unsigned>(M)), dim3(kTopThreads), 0, s, o, M, V);
+  return launch_chained(c, s.T <= kTopHeld * kTopThreads ? score_top_kernel<true> : score_top_kernel<false>,
+                        dim3(static_cast<unsigned>(M)), dim3(kTopThreads), 0, s, o, M, V);
 }
 
 }  // namespace coda

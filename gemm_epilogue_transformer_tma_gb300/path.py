@@ -19,8 +19,9 @@ from . import (CODA_EPI_PLAIN, CODA_EPI_SWIGLU, E4M3, E5M2, coda_bwd_workspace_b
                coda_gemm_wgrad_gscale, coda_prms_num_tiles, coda_rstd_combine, coda_swiglu_bwd, coda_swiglu_bwd_fp8,
                coda_unfused_bwd, coda_unfused_fwd, coda_unfused_workspace_bytes)
 from . import (CODA_DISTILL_TAIL, coda_fp8_block_quantize, coda_fp8_block_quantize_weight,
-               coda_fp8_block_scale_bytes, coda_gemm_fp8_block, coda_lmhead_distill, coda_lmhead_distill_workspace_bytes, coda_lmhead_policy, coda_lmhead_policy_workspace_bytes, coda_lmhead_score,
-               coda_lmhead_score_workspace_bytes, coda_qknorm_rope, coda_qknorm_rope_bwd,
+               coda_fp8_block_scale_bytes, coda_gemm_fp8_block, coda_lmhead_distill,
+               coda_lmhead_distill_workspace_bytes, coda_lmhead_policy, coda_lmhead_policy_workspace_bytes,
+               coda_lmhead_score, coda_lmhead_score_workspace_bytes, coda_qknorm_rope, coda_qknorm_rope_bwd,
                coda_qknorm_rope_bwd_workspace_bytes, coda_rope_table)
 from . import (CODA_BLOCK_BACKWARD, CODA_BLOCK_FP8, CODA_BLOCK_FP8_DELAYED, coda_block_arena_bytes,
                coda_block_create, coda_block_destroy, coda_block_quantize_weights, coda_block_step_host,

@@ -208,6 +208,44 @@ def test_rows_without_entries(mode):
     assert_device_ok()
 
 
+@pytest.mark.parametrize("mode", [R.LISTED, R.TAIL])
+@pytest.mark.parametrize("M", [24, 200])
+def test_targets_of_zero(mode, M):
+    """Entries with a probability of 0, or one that fp32 does not hold, in all of
+    a row's list: with LISTED nothing is asked of the row, with TAIL all of it off
+    the list."""
+    c = make(M, 64, 264, 4, mode)
+    c.ids.copy_((torch.arange(M, device="cuda")[:, None] + 50 * torch.arange(4, device="cuda")[None]).to(I32))
+    for i, v in enumerate([-float("inf"), torch.finfo(F32).min, -200.0]):
+        c.val[i::4] = v
+    c.run()
+    # tokens up to M - 1 + 150: of 200 rows some lie outside the vocabulary
+    assert C.coda_sync_status()[0] == (7 if M == 200 else 0)
+    r = c.grade()
+    assert torch.isfinite(c.dH.float()).all() and torch.isfinite(c.dW.float()).all()
+    if mode == R.LISTED:
+        none = torch.arange(M, device="cuda") % 4 < 3
+        assert (c.loss[none] == 0).all() and (c.dH[none] == 0).all()
+        assert r["dL"][none].abs().max() < 1e-80
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("M", [24, 200])
+def test_a_student_beyond_doubt_of_its_label(mode, M):
+    """All of the target on one token, which the student has at 1 - e^-200: what
+    is left of the gradient is below fp32, and is 0."""
+    H = torch.zeros(M, 64, device="cuda")
+    W = torch.zeros(1000, 64, device="cuda")
+    H[:, 0], H[:, 1] = 1.0, torch.arange(M, device="cuda") % 16 / 8.0
+    W[7, 0], W[:, 1] = 200.0, torch.arange(1000, device="cuda") % 8 / 8.0
+    ids = torch.tensor([[3, 7]], dtype=I32, device="cuda").repeat(M, 1)
+    val = torch.tensor([[-float("inf"), 0.0]], device="cuda").repeat(M, 1)
+    c = Call(H.to(BF), W.to(BF), ids, val, None, mode).run()
+    assert (c.loss.abs() <= 2.0 ** -20).all()
+    assert (c.dH == 0).all() and (c.dW == 0).all()
+    assert_device_ok()
+
+
 def test_a_token_outside_the_vocabulary_is_reported():
     c = make(40, 64, 264, 4, R.TAIL)
     live = int(torch.nonzero(c.w != 0)[5])
