@@ -150,6 +150,8 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // the temperature of a softmax on the LM head
 bool temperature_ok(float t) { return t > 0.f && !std::isinf(t) && !std::isinf(1.0f / t); }
+// of one whose exponentials are powers of two: log2(e) / t is a number too
+float log2e_over(float t) { return static_cast<float>(1.4426950408889634 / double(t)); }
 
 }  // namespace
 
@@ -1452,7 +1454,7 @@ coda_status_t coda_lmhead_score(coda_handle_t h, const void* Hs, const void* Wt,
                .cols(d)
                .cols(V)
                .st);
-  if (!temperature_ok(temperature)) return CODA_ERR_INVALID_ARG;
+  if (!temperature_ok(temperature) || std::isinf(log2e_over(temperature))) return CODA_ERR_INVALID_ARG;
   if (k < 0 || k > std::min<int64_t>(V, kScoreMaxTop)) return CODA_ERR_INVALID_ARG;
   if (M == 0) return CODA_OK;
   if ((labels != nullptr) != (logp != nullptr) || (top_ids != nullptr) != (top_logp != nullptr) ||
@@ -1462,7 +1464,7 @@ coda_status_t coda_lmhead_score(coda_handle_t h, const void* Hs, const void* Wt,
   const OnDevice dev(h->device);
   const LaunchCtx cx = ctx_of(h, stream);
   const ScoreWs w = score_layout(static_cast<uint8_t*>(ws), M, V, k);
-  const float c = static_cast<float>(1.4426950408889634 / double(temperature));
+  const float c = log2e_over(temperature);
   const int64_t R = score_rows(M, V, k);
   for (int64_t m0 = 0; m0 < M; m0 += R) {
     const int64_t rows = std::min(R, M - m0);
@@ -1555,7 +1557,8 @@ coda_status_t coda_lmhead_distill(coda_handle_t h, const void* Hs, const void* W
                .cols(d)
                .cols(V)
                .st);
-  if (M == 0 || k < 1 || k > kDistillMaxList || !temperature_ok(temperature)) return CODA_ERR_INVALID_ARG;
+  if (M == 0 || k < 1 || k > kDistillMaxList || !temperature_ok(temperature) || std::isinf(log2e_over(temperature)))
+    return CODA_ERR_INVALID_ARG;
   if (mode != CODA_DISTILL_LISTED && mode != CODA_DISTILL_NORMALIZED && mode != CODA_DISTILL_TAIL)
     return CODA_ERR_INVALID_ARG;
   const bool grads = dHs != nullptr;
@@ -1573,7 +1576,8 @@ coda_status_t coda_lmhead_distill(coda_handle_t h, const void* Hs, const void* W
   in.uniform = 1.0f / static_cast<float>(M);
   in.mode = mode;
   in.temperature = temperature;
-  in.log2e_over_t = static_cast<float>(1.4426950408889634 / double(temperature));
+  in.log2e_over_t = log2e_over(temperature);
+  in.log2e_over_t_low = static_cast<float>(1.4426950408889634 / double(temperature) - double(in.log2e_over_t));
   in.status = cx.status;
   CODA_CUDA(launch_distill_list(cx, in, w.w, Hb, Wb, M, d, V));
   CODA_CUDA(gemm_distill(cx, Hb, Wb, w.w, in.log2e_over_t, int(M), int(d), int(V)));

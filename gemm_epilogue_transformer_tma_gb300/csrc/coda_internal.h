@@ -216,17 +216,17 @@ struct DistillIn {
   const float* weight;  // [M], or null: uniform
   float uniform;
   int mode;             // CODA_DISTILL_*
-  float temperature, log2e_over_t;
+  float temperature, log2e_over_t, log2e_over_t_low;  // the quotient in two parts
   int* status;
 };
 struct DistillWork {
   int k, T;             // entries of a list, 128-column blocks of the vocabulary
   int32_t* ids;         // [M][k]: the list's tokens, each once, -1 for other entries
-  float* t;             // [M][k]: those entries' targets
+  float2* t;            // [M][k]: those entries' targets, in two parts
   uint32_t* at;         // [G][T], G = ceil(M / 32): where the entries of 32 rows in a block begin | how many << 16
   uint32_t* entry;      // [G][32 k]: row of the 32 | column of the block << 5 | position in the row's list << 12, or
                         // kNoEntry for a token that an earlier entry of its row has
-  float4* mass;         // [M]: P, r, P + r - 1
+  float4* mass;         // [M]: P, r, P + r - 1, what P's fp32 leaves of it
   float* n;             // [M]: the exponent of the row's kept values, NaN: no weight
   float* listed;        // [M][k]: the student's logits of the entries
   float* pn;            // [M][T], logits_distill.cuh

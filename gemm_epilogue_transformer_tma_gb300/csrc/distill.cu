@@ -47,6 +47,18 @@ __device__ __forceinline__ float warp_max(float v) {
 struct Sums {
   float a, b, top;
 };
+struct AddExact {
+  __device__ __forceinline__ float2 operator()(float2 v) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      v = (*this)(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+    return v;
+  }
+  __device__ __forceinline__ float2 operator()(float2 v, float2 w) const {
+    add_exact(v.x, v.y, w.x, w.y);
+    return v;
+  }
+};
 struct AddSums {
   __device__ __forceinline__ Sums operator()(Sums v) const { return {warp_sum(v.a), warp_sum(v.b), warp_max(v.top)}; }
   __device__ __forceinline__ Sums operator()(Sums v, Sums w) const {
@@ -65,25 +77,26 @@ __device__ __forceinline__ float2 add_ordered(float a, float b) {
   return make_float2(h, b - (h - a));
 }
 
-// exp(x) as an unevaluated sum of two fp32 numbers, relative error below 2^-34
-// (2^-34.9 against 64-bit mantissas over the whole range): x = n ln 2 + 16 s,
-// exp(s) from its series with the leading terms in two numbers, then four
-// squarings, which multiply its error by 16.  fp64 has 2 lanes per clock and SM:
-// 32 rows' exponentials on one SM took 8 us there.
-__device__ __forceinline__ float2 exp_exact(float x) {
-  if (!(x > -87.f)) return make_float2(expf(x), 0.f);  // 0, or NaN
-  if (x > 88.f) return make_float2(expf(x), 0.f);
-  // ln 2 in three parts: n times the first is exact
-  constexpr double kLn2 = 0.693147180559945309417232;
-  constexpr float kA = 0.693145751953125f;  // 16 bits
-  constexpr float kB = static_cast<float>(kLn2 - double(kA));
-  constexpr float kC = static_cast<float>(kLn2 - double(kA) - double(kB));
-  const float n = rintf(x * 1.44269504f);
-  float hi = x, lo = 0.f;
-  add_exact(hi, lo, -n * kA, 0.f);
-  const float2 nb = mul_exact(-n, kB);
-  add_exact(hi, lo, nb.x, fmaf(-n, kC, nb.y));
-  // s = (hi + lo) / 16, |s| < 0.022
+// a / b of numbers in two parts, 1 where they are the same; inv = 1 / b.x
+__device__ __forceinline__ float2 div_exact(float2 a, float2 b, float inv) {
+  const float q = a.x / b.x;
+  return add_ordered(q, (fmaf(-q, b.x, a.x) + fmaf(-q, b.y, a.y)) * inv);
+}
+// hi + lo in two parts that do not overlap; of an infinite sum there is one
+__device__ __forceinline__ float2 in_order(float hi, float lo) {
+  const float2 r = add_ordered(hi, lo);
+  return isfinite(r.x) ? r : make_float2(exact_value(hi, lo), 0.f);
+}
+
+constexpr double kLn2 = 0.693147180559945309417232;
+
+// 2^n exp(hi + lo), |hi + lo| < 0.35, as an unevaluated sum of two fp32 numbers,
+// relative error below 2^-34: exp(s), s = (hi + lo) / 16, from its series with the
+// leading terms in two numbers, then four squarings, which multiply its error by
+// 16.  fp64 has 2 lanes per clock and SM: 32 rows' exponentials on one SM took 8 us
+// there.
+__device__ __forceinline__ float2 exp_scaled(float hi, float lo, float n) {
+  // |s| < 0.022
   const float2 s = add_ordered(hi * 0.0625f, lo * 0.0625f);
   // exp(s) - 1 = s + s^2 / 2 + s^3 (1 / 6 + s / 24 + s^2 / 120 + s^3 / 720): the rest below 2^-50
   const float2 sq = mul_exact(s.x, s.x);
@@ -105,6 +118,30 @@ __device__ __forceinline__ float2 exp_exact(float x) {
   const float2 r = add_ordered(eh, el);
   const float up = __int_as_float((static_cast<int>(n) + 127) << 23);  // -126 <= n <= 127
   return make_float2(r.x * up, r.y * up);
+}
+
+// exp(x + x_lo) in two numbers (2^-34.9 against 64-bit mantissas over the whole range)
+__device__ __forceinline__ float2 exp_exact(float x, float x_lo) {
+  if (!(x > -87.f)) return make_float2(expf(x), 0.f);  // 0, or NaN
+  if (x > 88.f) return make_float2(expf(x), 0.f);
+  // ln 2 in three parts: n times the first is exact
+  constexpr float kA = 0.693145751953125f;  // 16 bits
+  constexpr float kB = static_cast<float>(kLn2 - double(kA));
+  constexpr float kC = static_cast<float>(kLn2 - double(kA) - double(kB));
+  const float n = rintf(x * 1.44269504f);
+  float hi = x, lo = x_lo;
+  add_exact(hi, lo, -n * kA, 0.f);
+  const float2 nb = mul_exact(-n, kB);
+  add_exact(hi, lo, nb.x, fmaf(-n, kC, nb.y));
+  return exp_scaled(hi, lo, n);
+}
+// 2^(y + y_lo) in two numbers where it is not far from 1, in one elsewhere
+__device__ __forceinline__ float2 exp2_exact(float y, float y_lo) {
+  if (!(fabsf(y) < 120.f)) return make_float2(ex2_f(y), 0.f);
+  constexpr float kA = static_cast<float>(kLn2), kB = static_cast<float>(kLn2 - double(kA));
+  const float n = rintf(y), f = y - n;
+  const float2 p = mul_exact(f, kA);
+  return exp_scaled(p.x, fmaf(f, kB, fmaf(y_lo, kA, p.y)), n);
 }
 
 // The lists, before the logits are known: one entry for each token, with its
@@ -187,9 +224,9 @@ __global__ void __launch_bounds__(kListThreads) distill_list_kernel(const Distil
         float v = p[j].x, v_lo = 0.f;
         add_exact(v, v_lo, -top, 0.f);
         const float z = v / in.temperature, rest = (fmaf(-z, in.temperature, v) + v_lo) / in.temperature;
-        x = make_float2(expf(z) * (1.f + (isfinite(rest) ? rest : 0.f)), 0.f);
+        x = exp_exact(z, isfinite(rest) ? rest : 0.f);
       } else {
-        x = exp_exact(p[j].x);
+        x = exp_exact(p[j].x, 0.f);
       }
       p[j] = x;
       add_exact(hi, lo, x.x, x.y);
@@ -200,21 +237,23 @@ __global__ void __launch_bounds__(kListThreads) distill_list_kernel(const Distil
       add_exact(hi, lo, h2, l2);
     }
     if (normalized) {  // P = 1
-      const float sum = exact_value(hi, lo);
+      const float2 sum = in_order(hi, lo);
+      const float inv = 1.f / sum.x;
       for (int j = lane; j < k; j += 32)
-        if (id[j] >= 0) p[j].x /= sum;
-      hi = sum != 0.f ? sum / sum : 0.f;
+        if (id[j] >= 0) p[j] = div_exact(p[j], sum, inv);
+      hi = sum.x != 0.f ? sum.x / sum.x : 0.f;
       lo = 0.f;
     }
     if (lane == 0) {
       float less = hi, less_lo = lo;  // P - 1
       add_exact(less, less_lo, -1.f, 0.f);
-      const float over = less + less_lo, P = exact_value(hi, lo);
+      const float over = less + less_lo;
+      const float2 P = in_order(hi, lo);
       const bool tail = in.mode == CODA_DISTILL_TAIL;
       const float r = tail ? (over < 0.f ? -over : 0.f) : 0.f;
       dot *= in.log2e_over_t;
       w.n[m] = isfinite(dot) ? rintf(dot) : 0.f;
-      w.mass[m] = make_float4(P, r, tail && over < 0.f ? 0.f : over, 0.f);
+      w.mass[m] = make_float4(P.x, r, tail && over < 0.f ? 0.f : over, P.y);
     }
   }
 
@@ -299,7 +338,7 @@ __global__ void __launch_bounds__(kListThreads) distill_list_kernel(const Distil
             if (all_ids[r * k + q] == t) add_exact(hi, lo, pr[q].x, pr[q].y);
         const int64_t to = (g * 32 + r) * k + j;
         w.ids[to] = t;
-        w.t[to] = exact_value(hi, lo);
+        w.t[to] = in_order(hi, lo);
       }
       w.entry[g * 32 * k + i] = first ? e : kNoEntry;
     }
@@ -310,14 +349,26 @@ __global__ void __launch_bounds__(kListThreads) distill_list_kernel(const Distil
 // a log(a / b) - a + b; u = b - a; lb = log b, good where b itself has underflowed
 __device__ __forceinline__ float phi(float a, float b, float u, float lb) {
   if (a == 0.f) return b;
-  if (fabsf(u) <= 0.5f * a) return u - a * log1pf(u / a);
+  if (fabsf(u) <= 0.5f * a) {
+    // a (z - log(1 + z)), z = u / a: with w = z / (2 + z) the logarithm is 2 (w + w^3
+    // / 3 + w^5 / 5 + ...) and z = 2 w + w z, so the linear terms, beside which z^2 /
+    // 2 would lose its digits, are gone.  w^2 <= 1 / 9: the rest is below 2^-25.
+    const float z = u / a, w = __fdividef(z, 2.f + z), v = w * w;
+    float s = 1.f / 15.f;
+    s = fmaf(s, v, 1.f / 13.f);
+    s = fmaf(s, v, 1.f / 11.f);
+    s = fmaf(s, v, 1.f / 9.f);
+    s = fmaf(s, v, 1.f / 7.f);
+    s = fmaf(s, v, 1.f / 5.f);
+    s = fmaf(s, v, 1.f / 3.f);
+    return a * w * fmaf(-2.f * v, s, z);
+  }
   return a * (logf(a) - lb) + u;
 }
 
 // a log(a / b) alone
-__device__ __forceinline__ float t_log_ratio(float a, float b, float lb) {
+__device__ __forceinline__ float t_log_ratio(float a, float u, float lb) {
   if (a == 0.f) return 0.f;
-  const float u = b - a;
   return fabsf(u) <= 0.5f * a ? -a * log1pf(u / a) : a * (logf(a) - lb);
 }
 
@@ -360,6 +411,7 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
   constexpr int kWarps = kThreads / 32;
   __shared__ Sums part[kWarps];
   __shared__ Rest rests[kWarps];
+  __shared__ float2 exact_part[kWarps];
   __shared__ bool last;
   const int64_t m = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = w.k, T = w.T;
@@ -373,14 +425,15 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
   const float4 mass = w.mass[m];
   constexpr int N = (kDistillMaxList + kThreads - 1) / kThreads;
   int32_t id[N];
-  float x[N], t[N], q[N];
+  float x[N], q[N];
+  float2 t[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int64_t j = m * k + tid + i * kThreads;
     const bool there = tid + i * kThreads < k;
     id[i] = there ? w.ids[j] : -1;
     x[i] = there ? w.listed[j] : 0.f;
-    t[i] = there ? w.t[j] : 0.f;
+    t[i] = there ? w.t[j] : make_float2(0.f, 0.f);
   }
   constexpr int kHeld = kThreads == kFewRowThreads ? 2 : 8;  // blocks to a thread
   float held[kHeld];
@@ -396,13 +449,13 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
     for (int64_t i = tid; i < V / 8; i += kThreads) reinterpret_cast<uint4*>(to)[i] = make_uint4(0u, 0u, 0u, 0u);
   };
   if (weight != 0.f) {
-    constexpr float kLn2 = 0.6931471805599453f;
+    constexpr float kLn2f = static_cast<float>(kLn2);
     Sums all{0.f, 0.f, -INFINITY};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (id[i] < 0) {
         x[i] = -INFINITY;
-        t[i] = 0.f;
+        t[i] = make_float2(0.f, 0.f);
       }
       all.top = fmaxf(all.top, x[i]);
     }
@@ -432,34 +485,47 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
     float top = fmaf(all.top, c, -rest.n);
     if (some) top = fmaxf(top, 0.f);
     const float ref = rest.n + (isfinite(top) ? rintf(top) : 0.f), down = rest.n - ref;
-    Sums on{0.f, 0.f, 0.f};
+    // The list's exponentials and their sum are held in two numbers, as its targets
+    // are: near the teacher the loss is made of the squares of the differences, and
+    // with 1e-7 of q, or of log2(e) / T, in them a row's of 8e-4 was 4e-6 off.
+    float2 e[N], on = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      // the product's rounding error into the power of two: 2^-24 of an x of 16 is 2^-20 of q
       const float2 y = mul_exact(x[i], c);
-      x[i] = y.x - ref;
-      const float low = isfinite(x[i]) ? y.y + (y.x - (x[i] + ref)) : 0.f;
-      q[i] = ex2_f(x[i]) * fmaf(low, kLn2, 1.f);
-      x[i] += low;
-      on.a += q[i];
+      float hi = y.x, lo = fmaf(x[i], in.log2e_over_t_low, y.y);
+      add_exact(hi, lo, -ref, 0.f);
+      e[i] = exp2_exact(hi, lo);
+      x[i] = hi + (isfinite(lo) ? lo : 0.f);
+      add_exact(on.x, on.y, e[i].x, e[i].y);
     }
-    on = block_reduce<kWarps>(on, part, AddSums());
-    const float rest_ref = rest.s * ex2_f(down), S = rest_ref + on.a, log2_S = log2f(S);
-    const float R = rest_ref / S, Q = on.a / S;
-    const float lR = Q < 0.5f ? log1pf(-Q) : (log2f(rest.s) + down - log2_S) * kLn2;
+    on = block_reduce<kWarps>(on, exact_part, AddExact());
+    on = add_ordered(on.x, on.y);
+    // ex2's results are low by 5.1e-8 to 5.6e-8 on average (five sizes, d from 312 to 4096)
+    constexpr float kEx2Low = 5.3e-8f;
+    const float rest_ref = rest.s * ex2_f(down);
+    const float2 off = make_float2(rest_ref, rest_ref * kEx2Low);
+    float sum = on.x, sum_lo = on.y;
+    add_exact(sum, sum_lo, off.x, off.y);
+    const float2 both = add_ordered(sum, sum_lo);
+    const float S = both.x, inv = 1.f / S, log2_S = log2f(S);
+    const float2 listed = div_exact(on, both, inv);
+    const float R = div_exact(off, both, inv).x, Q = listed.x;
+    const float lR = Q < 0.5f ? log1pf(-Q) : (log2f(rest.s) + down - log2_S) * kLn2f;
     // a tail needs a token off the list
     const float P = mass.x, r = some ? mass.y : 0.f, excess = some ? mass.z : mass.z - mass.y;
-    const float less = r != 0.f && Q < 0.5f ? P - Q : R - r;  // R - r, of which both may be nearly 1
+    // R - r, as P - Q where that holds the digits of both
+    const float less = r != 0.f && R > 0x1p-12f ? (P - Q) + (mass.w - listed.y) : R - r;
     const bool direct = in.mode == CODA_DISTILL_LISTED;
     Sums row{0.f, 0.f, 0.f};  // loss, cross-entropy, largest entry of dL
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (id[i] >= 0) {
-        const float lq = (x[i] - log2_S) * kLn2;
-        q[i] /= S;
-        row.a += direct ? t_log_ratio(t[i], q[i], lq) : phi(t[i], q[i], q[i] - t[i], lq);
-        if (t[i] != 0.f) row.b = fmaf(-t[i], lq, row.b);
-        q[i] = fmaf(P + r, q[i], -t[i]);  // d loss / d z
+        const float lq = (x[i] - log2_S) * kLn2f;
+        const float2 own = div_exact(e[i], both, inv);
+        const float u = (own.x - t[i].x) + (own.y - t[i].y);
+        row.a += direct ? t_log_ratio(t[i].x, u, lq) : phi(t[i].x, own.x, u, lq);
+        if (t[i].x != 0.f) row.b = fmaf(-t[i].x, lq, row.b);
+        q[i] = excess == 0.f ? u : fmaf(P + r, own.x, -t[i].x);  // d loss / d z; P + r = 1
         row.top = fmaxf(row.top, fabsf(q[i]));
       }
     }

@@ -830,7 +830,7 @@ size_t coda_lmhead_score_workspace_bytes(int64_t M, int64_t d, int64_t V, int64_
  * neither), entropy fp32 [M] or NULL, top_ids int32 [M][k] and top_logp fp32
  * [M][k] (NULL iff k = 0), all of these but Hs and Wt 4-byte aligned; one of the
  * outputs at least.  0 <= k <= min(V, 256), temperature > 0 with a finite fp32
- * reciprocal.  M = 0 does nothing. */
+ * log2(e) / temperature.  M = 0 does nothing. */
 coda_status_t coda_lmhead_score(coda_handle_t h, const void* Hs, const void* Wt, const int32_t* labels,
                                 float temperature, float* logp, float* entropy, int32_t* top_ids, float* top_logp,
                                 int64_t k, void* ws, size_t ws_bytes, int64_t M, int64_t d, int64_t V, void* stream);
@@ -840,7 +840,7 @@ coda_status_t coda_lmhead_score(coda_handle_t h, const void* Hs, const void* Wt,
 #define CODA_DISTILL_NORMALIZED 1 /* val = logits; their softmax at the temperature */
 #define CODA_DISTILL_TAIL 2       /* val = log-probabilities; what they leave is the target of all others together */
 
-/* Workspace of coda_lmhead_distill: 16 bytes per list entry, 8.2 per row and 128
+/* Workspace of coda_lmhead_distill: 20 bytes per list entry, 8.2 per row and 128
  * columns of the vocabulary and 36 per row; with gradients 2 M (V + d) more (the
  * student's exponentials in bf16 and a scaled Hs; twice as much for 64 rows and
  * fewer) and up to 20 MB of fp32 partial sums of dHs (used for few tokens).  A
@@ -882,7 +882,7 @@ size_t coda_lmhead_distill_workspace_bytes(int64_t M, int64_t d, int64_t V, int6
  * Hs bf16 [M][d], Wt bf16 [V][d], ids int32 [M][k], val fp32 [M][k], weight fp32
  * [M] or NULL (ids, val, weight, stats and row_loss 4-byte aligned), dHs bf16
  * [M][d] or NULL, dWt bf16 [V][d] (required iff dHs != NULL).  1 <= k <= 256,
- * temperature > 0 with a finite fp32 reciprocal, M >= 1. */
+ * temperature > 0 with a finite fp32 log2(e) / temperature, M >= 1. */
 coda_status_t coda_lmhead_distill(coda_handle_t h, const void* Hs, const void* Wt, const int32_t* ids, const float* val,
                                   const float* weight, int mode, float temperature, float* stats, float* row_loss,
                                   void* dHs, void* dWt, int64_t k, void* ws, size_t ws_bytes, int64_t M, int64_t d,

@@ -294,6 +294,27 @@ def test_a_student_near_its_teacher(noise):
     assert_device_ok()
 
 
+@pytest.mark.parametrize("T", [1.0, 1.3])
+@pytest.mark.parametrize("M", [40, 300])
+def test_a_difference_within_the_list_keeps_its_digits(M, T):
+    """Two tokens' targets moved by 2^-8 of the smaller one, against each other, so
+    that the list's mass stays: the loss, 2^-17 of that target and more, is made of the
+    differences alone.  The exponentials off the list may be off by 2^-21 together,
+    which the loss meets times R - r; the list's and their quotients by 2^-34, times
+    the 2^-8 of their logarithms' ratio; sums and logarithms by 2^-20 of the loss."""
+    H, W, _ = R.grid_inputs(M, 64, 2000, seed=9)
+    q = torch.softmax(R.logits(H, W) / T, 1)
+    top, ids = torch.topk(q, 2, 1)
+    step = top[:, 1] * 2.0 ** -8
+    val = torch.stack([top[:, 0] + step, top[:, 1] - step], 1).log().float()
+    c = Call(H, W, ids.to(I32), val, None, R.TAIL, T).run()
+    r = R.distill(H, W, c.ids, val, None, R.TAIL, float(np.float32(T)))  # the temperature of the call
+    apart = (top.sum(1) - val.double().exp().sum(1)).abs()
+    bar = 2.0 ** -20 * r["loss"] + 2.0 ** -21 * apart + 2.0 ** -41
+    assert ((c.loss.double() - r["loss"]).abs() <= bar).all()
+    assert_device_ok()
+
+
 @pytest.mark.parametrize("mode", MODES)
 @pytest.mark.parametrize("gap", [50.0, 200.0])
 def test_logits_far_from_the_listed_ones(mode, gap):
