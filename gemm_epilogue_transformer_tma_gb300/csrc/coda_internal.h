@@ -206,7 +206,7 @@ constexpr int kDistillMaxList = 256;
 // So few rows take part in dW's contraction twice, the second time with what the
 // rounding of factor H to bf16 takes from their listed entries: the error of dW,
 // 1.4 times that of rounding it alone on average, spreads to 1.7 where few rows make
-// it.  8 tokens, d = 2048, V = 50280: 145 us, 140 without; 64, d = 1024, V = 32000: 69
+// it.  8 tokens, d = 2048, V = 50280: 140 us, 139 without; 64, d = 1024, V = 32000: 67
 // and 64; 128 of d = 4096, V = 128256: 615 and 557, which is not done.
 constexpr int64_t kDistillTwice = 64;
 constexpr uint32_t kNoEntry = 0xFFFFFFFFu;

@@ -22,7 +22,7 @@
 // us, 90 % of the tensor pipe (dense random operands, at the clock they leave),
 // with all exponentials kept 307, 84 % (their way through shared memory; stores
 // from the registers, a row per lane, made a whole update 5 % slower);
-// distillation 263 and 300, 91 and 80 %.
+// distillation 251 and 287, 96 and 84 %.
 #pragma once
 
 #include "gemm_tc2.cuh"
