@@ -502,3 +502,17 @@ def test_refusals():
         with pytest.raises((ValueError, TypeError, C.CodaError)):
             C.coda_lmhead_distill(*a)
     assert_device_ok()
+
+
+def test_a_temperature_without_its_power_of_two_is_refused():
+    """1 / 4e-39 is an fp32 number, log2(e) / 4e-39 is not."""
+    c = make(16, 64, 136, 4, R.TAIL)
+    for T, fine in ((4e-39, False), (5e-39, True)):
+        a = list(c.args)
+        a[6] = T
+        if fine:
+            C.coda_lmhead_distill(*a)
+        else:
+            with pytest.raises(C.CodaError):
+                C.coda_lmhead_distill(*a)
+    assert_device_ok()

@@ -318,3 +318,18 @@ def test_only_some_logits_kept(V, k):
     assert all(torch.equal(a[keep], b[keep]) for a, b in zip(want, c.outputs()))
     assert torch.equal(c.ids[70], torch.arange(k, dtype=I32, device="cuda")) and torch.isnan(c.logp[70])
     assert_device_ok()
+
+
+def test_a_temperature_without_its_power_of_two_is_refused():
+    """1 / 4e-39 is an fp32 number, log2(e) / 4e-39 is not.  At 5e-39 a row is its
+    largest logits' alone."""
+    H, W, y = R.grid_inputs(16, 64, 136)
+    f, e = torch.empty(16, device="cuda"), torch.empty(16, device="cuda")
+    ws = torch.empty(C.coda_lmhead_score_workspace_bytes(16, 64, 136, 0), dtype=torch.uint8, device="cuda")
+    with pytest.raises(C.CodaError):
+        C.coda_lmhead_score(H, W, y, 4e-39, f, e, None, None, ws)
+    C.coda_lmhead_score(H, W, y, 5e-39, f, e, None, None, ws)
+    L = R.logits(H, W)
+    equal = (L == L.amax(1, keepdim=True)).sum(1).double()
+    assert ((e.double() - equal.log()).abs() <= 2.0 ** -20).all()
+    assert_device_ok()
