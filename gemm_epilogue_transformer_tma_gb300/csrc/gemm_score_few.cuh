@@ -249,8 +249,8 @@ __global__ void __launch_bounds__(ScoreFewSmem<NT>::THREADS, 1)
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           there[s] = lane < ws && v0 + s * ws + lane < g.V;
-          x[s] = there[s] ? z[s * ws + lane] : kNoLogit;
-          m4[s] = there[s] ? x[s] : -INFINITY;
+          x[s] = there[s] ? z[s * ws + lane] : -INFINITY;
+          m4[s] = x[s];
         }
         if (g.logits != nullptr) {
           float* at = g.logits + static_cast<int64_t>(n) * g.V + v0 + lane;
@@ -267,9 +267,10 @@ __global__ void __launch_bounds__(ScoreFewSmem<NT>::THREADS, 1)
         float s1 = 0.f, u1 = 0.f;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          const float y = x[s] - mx, e = ex2_f(y * g.c);
+          // a column that does not exist is given the largest logit: it adds nothing at any temperature
+          const float y = there[s] ? x[s] - mx : 0.f, e = ex2_f(y * g.c);
           const bool top = y == 0.f;
-          equal += __popc(__ballot_sync(0xffffffffu, top));
+          equal += __popc(__ballot_sync(0xffffffffu, top && there[s]));
           if (!top) s1 += e;
           u1 = fmaf(e, y, u1);
         }

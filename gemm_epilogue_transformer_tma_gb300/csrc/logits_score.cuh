@@ -17,10 +17,6 @@
 
 namespace coda {
 
-// a logit below all others of a bf16 product, finite: its x times its
-// exponential, 0, is 0
-constexpr float kNoLogit = -3.4e38f;
-
 enum ScoreKeep { KEEP_NONE, KEEP_ALL, KEEP_SOME };
 
 template <int KEEP>
@@ -67,7 +63,7 @@ struct LogitsScore {
       for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          if (c * 32 + i >= t.nv) v[c][i] = kNoLogit;
+          if (c * 32 + i >= t.nv) v[c][i] = -INFINITY;
     }
     const int64_t y = static_cast<int64_t>(st.y) - g.v0 - t.n0;
     if (y >= 0 && y < PART_COLS && y < t.nv) {
@@ -114,7 +110,17 @@ struct LogitsScore {
     if (KEEP != KEEP_NONE) {
       g.sub[o] = make_float4(cm[0], cm[1], cm[2], cm[3]);
     }
+    // Columns that do not exist are given the largest logit from here on: x = 0 adds
+    // nothing to s and u at any temperature, and n does not count them.
     float n = -1.f, s4[4] = {0.f, 0.f, 0.f, 0.f}, u4[4] = {0.f, 0.f, 0.f, 0.f};
+    if (t.nv < PART_COLS) {
+      n -= static_cast<float>(PART_COLS - t.nv);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c * 32 + i >= t.nv) v[c][i] = mx;
+    }
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll

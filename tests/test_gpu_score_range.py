@@ -1,0 +1,23 @@
+"""Scoring at the ends of what it accepts.  Tolerances as tests/test_gpu_score.py."""
+import pytest
+import torch
+
+from tests import _lmhead as R
+from tests._parity import assert_device_ok
+from tests.test_gpu_score import Call
+
+pytestmark = pytest.mark.gpu
+
+C = pytest.importorskip("gemm_epilogue_transformer_tma_gb300")
+
+
+@pytest.mark.parametrize("T", [1e30, 3e36, 1e38, 3e38])
+@pytest.mark.parametrize("M,V", [(1, 8), (3, 1000), (33, 32000), (64, 50280), (100, 264), (200, 1000), (300, 2056)])
+@pytest.mark.parametrize("k", [0, 5])
+def test_temperatures_that_flatten_every_row(M, V, T, k):
+    """All V tokens are equally probable, and columns that do not exist, in the
+    last block of a row or beside a narrow one, are not among them."""
+    H, W, y = R.grid_inputs(M, 64, V, seed=M)
+    c = Call(H, W, y, T, k).run()
+    c.grade()
+    assert ((c.entropy - torch.log(torch.tensor(float(V)))).abs() <= 2.0 ** -16 * 12).all()
