@@ -34,12 +34,16 @@ __device__ __forceinline__ void add_block(float x, float ps, float pd, float mx,
   const float dx = x == mx ? 0.f : x - mx, f = ex2_f(dx * c);
   equal += x == mx ? 1.f : 0.f;
   sum = x == mx ? sum + ps : fmaf(f, 1.f + ps, sum);
-  dot += x == mx ? pd : f * fmaf(dx, 1.f + ps, pd);
+  dot += x == mx ? pd : fmaf(f * (1.f + ps), dx, f * pd);
 }
+
+// log(1 + s).  NaN where the row has an infinite logit: one of -infinity adds 0 to
+// s, and NaN (0 times -infinity) to u alone.
+__device__ __forceinline__ float log_sum(const RowSum& r) { return isnan(r.u) ? r.u : log1pf(r.s); }
 
 __device__ __forceinline__ void write_row(const ScoreStats& s, const ScoreOut& o, const RowSum& r, int64_t m,
                                           int64_t V) {
-  const float log_s = log1pf(r.s);
+  const float log_s = log_sum(r);
   if (o.entropy != nullptr) o.entropy[m] = log_s - r.u / o.temperature / (1.f + r.s);
   if (o.logp != nullptr) {
     const int32_t y = o.labels[m];
@@ -499,7 +503,7 @@ __global__ void __launch_bounds__(kTopThreads) score_top_kernel(const ScoreStats
     __syncthreads();
   }
   // all different: each one's place is the number of larger ones
-  const float log_s = log1pf(r.s);
+  const float log_s = log_sum(r);
   for (int i = tid; i < n; i += kTopThreads) {
     const uint64_t x = sm.best[i];
     int rank = 0;

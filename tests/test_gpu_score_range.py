@@ -21,3 +21,25 @@ def test_temperatures_that_flatten_every_row(M, V, T, k):
     c = Call(H, W, y, T, k).run()
     c.grade()
     assert ((c.entropy - torch.log(torch.tensor(float(V)))).abs() <= 2.0 ** -16 * 12).all()
+
+
+@pytest.mark.parametrize("M,V,k", [(3, 1000, 5), (64, 4096, 0), (200, 1000, 5), (300, 5000, 0), (4100, 20000, 8)])
+@pytest.mark.parametrize("sign", [-1.0, 1.0], ids=["minus", "plus"])
+def test_an_infinite_logit(M, V, k, sign):
+    """Of one token in every row: its log-probabilities and entropy are NaN, the
+    others keep their ranks."""
+    H, W, y = R.grid_inputs(M, 64, V, seed=5)
+    H[:, 0], W[:, 0] = 1.0, 0.0
+    a = Call(H, W, y, 1.0, k).run()
+    W2, v = W.clone(), V // 2
+    W2[v, 0] = sign * float("inf")
+    c = Call(H, W2, y, 1.0, k).run()
+    for t in (c.logp, c.entropy) + ((c.top,) if k else ()):
+        assert torch.isnan(t).all()
+    if k:
+        for m in range(0, M, max(1, M // 7)):
+            others = [i for i in a.ids[m].tolist() if i != v]
+            want = [v] + others if sign > 0 else others
+            n = min(k, len(want))
+            assert c.ids[m, :n].tolist() == want[:n]
+    assert_device_ok()
