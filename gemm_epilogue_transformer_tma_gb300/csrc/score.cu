@@ -176,10 +176,13 @@ __device__ __forceinline__ void each_logit(const float* __restrict__ sub, const 
   }
 }
 
-// A bin for each 256th of the range from low to mx, in the order of the numbers.
+// A bin for each 256th of the range from low to mx, in the order of the numbers; one
+// for all where the range, or its reciprocal times 255, is not finite.
 struct Bins {
   float low, width;
-  __device__ __forceinline__ Bins(float low, float mx) : low(low), width(mx > low ? 255.f / (mx - low) : 0.f) {}
+  __device__ __forceinline__ Bins(float low, float mx) : low(low), width(mx > low ? 255.f / (mx - low) : 0.f) {
+    if (isinf(width)) width = 0.f;
+  }
   __device__ __forceinline__ int operator()(float x) const {
     return max(0, min(255, __float2int_rd((x - low) * width)));
   }

@@ -43,3 +43,18 @@ def test_an_infinite_logit(M, V, k, sign):
             n = min(k, len(want))
             assert c.ids[m, :n].tolist() == want[:n]
     assert_device_ok()
+
+
+@pytest.mark.parametrize("M,V,k", [(1, 1000, 20), (40, 9000, 256), (200, 1000, 20), (300, 50280, 64), (4100, 20000, 8)])
+def test_logits_within_2_to_the_minus_122(M, V, k):
+    """Their range has no finite reciprocal; each token keeps its rank."""
+    H, W, y = R.grid_inputs(M, 64, V, seed=6)
+    H.zero_()
+    W.zero_()
+    H[:, 0] = 2.0 ** -60
+    mix = torch.randint(0, 128, (V,), generator=torch.Generator().manual_seed(3)).cuda()
+    W[:, 0] = ((1 + mix / 128.0) * 2.0 ** -62).to(W.dtype)
+    H[1::3] = 0
+    c = Call(H, W, y, 1.0, k).run()
+    for rows in (slice(0, 50), slice(M - min(M, 50), M)):
+        c.grade(rows)
