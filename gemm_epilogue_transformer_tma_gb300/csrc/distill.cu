@@ -536,18 +536,20 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
     if (GRADS != NO_GRADS) {
       const float scale = weight / in.temperature, steep = row.top;
       __nv_bfloat16* kept = w.kept + m * V;
-      float f = (P + r) * (ex2_f(down) / S) - (r != 0.f ? r / rest.s : 0.f);
+      // Off the list d loss / d z_v = q_v ((P + r) - r / R): with a tail P + r = 1, and
+      // (R - r) / R of q_v is (R - r) / rest.s of the kept value.  The difference of two
+      // quotients would leave 1e-7 of q where R is near r, all of a row one way.
+      float f = r != 0.f ? less / rest.s : P * (ex2_f(down) / S);
       // A row with blocks at a scale of their own, or whose factor is too small
       // to divide by, as it is where student and teacher agree on R: the kept
       // exponentials are made d loss / d z, those listed stay 0.
       if (far || !some || !(fabsf(f) >= 0x1p-40f * steep)) {
-        const float all = (P + r) * (ex2_f(down) / S), tail = r != 0.f ? r / rest.s : 0.f;
         uint4* at = reinterpret_cast<uint4*>(kept);
         for (int64_t i = tid; i < V / 8; i += kThreads) {
           const int64_t b = i >> 4;
           // above rest.n: a block of zeros, all listed
           const float up = ex2_f(fminf((psum[b] < 0.f ? pn[b] : n_row) - rest.n, 0.f));
-          const float g = some ? all * up - tail * up : 0.f;
+          const float g = some ? f * up : 0.f;
           float v[8];
           unpack_bf16x8(at[i], v);
           at[i] = make_uint4(pack_bf16x2(v[0] * g, v[1] * g), pack_bf16x2(v[2] * g, v[3] * g),

@@ -1,0 +1,70 @@
+"""What is left of distillation's gradients when the formula cancels: against
+fp64 on inputs whose logits are exact in fp32 (tests/_lmhead.py)."""
+import pytest
+import torch
+
+from tests import _lmhead as R
+from tests._parity import assert_device_ok
+from tests.test_gpu_distill import MODES, Call, make
+
+pytestmark = pytest.mark.gpu
+
+C = pytest.importorskip("gemm_epilogue_transformer_tma_gb300")
+
+BF, I32 = torch.bfloat16, torch.int32
+
+
+@pytest.mark.parametrize("M,d,V", [(20, 64, 264), (64, 64, 9000), (200, 64, 3000), (700, 512, 1048), (1100, 2560, 1048)])
+@pytest.mark.parametrize("mode", MODES)
+def test_a_row_without_entries_has_no_loss_and_no_gradient(mode, M, d, V):
+    c = make(M, d, V, 4, mode)
+    c.ids.fill_(-1)
+    c.run()
+    assert (c.loss == 0).all() and (c.dH == 0).all() and (c.dW == 0).all()
+    # beside rows that have some
+    c = make(M, d, V, 4, mode)
+    c.ids[::2] = -1
+    c.run()
+    c.grade()
+    assert (c.loss[::2] == 0).all() and (c.dH[::2] == 0).all()
+    assert_device_ok()
+
+
+def _readable(M, d, V, k, noise, seed):
+    """The same k tokens for all rows, with P = Q (1 + noise).  Column 1 of the
+    head is 1 off the list and 0 on it and meets a 0 in Hs, so that dHs[:, 1] is
+    the sum of dL off the list; column 2 of Hs is 1 and meets 0 in the head."""
+    H, W, _ = R.grid_inputs(M, d, V, sure=0.5, seed=seed)
+    H = (H.float() / 4).to(BF)
+    H[:, 1], H[:, 2] = 0.0, 1.0
+    W[:, 1] = (torch.arange(V, device="cuda") >= k).to(BF)
+    W[:, 2] = 0.0
+    ids = torch.arange(k, dtype=I32, device="cuda").expand(M, k).contiguous()
+    lq = torch.log_softmax(R.logits(H, W), 1)[:, :k]
+    sign = torch.where(torch.arange(M, device="cuda") % 2 == 0, 1.0, -1.0)[:, None]
+    val = (lq + torch.log1p(sign * noise).double()).float()
+    return Call(H, W, ids, val.contiguous(), torch.full((M,), 1 / M, device="cuda"), R.TAIL)
+
+
+@pytest.mark.parametrize("M,d,V", [(40, 64, 2000), (300, 64, 2000), (1100, 2560, 1048)])
+@pytest.mark.parametrize("noise", [2.0 ** -13, 2.0 ** -16])
+def test_the_gradient_off_the_list_of_a_student_near_its_teacher(M, d, V, noise):
+    """Off the list dL = weight q (1 - r / R), and 1 - r / R = (P - Q) / R.  The
+    list's exponentials and targets are good to 2^-33, and those off the list may be
+    off by 2^-21 together: Q is off by 2^-21 Q R, and so is the sum of dL.  The
+    gradients carry three roundings to bf16 of terms of one sign, dWt four: 2^-8
+    each."""
+    c = _readable(M, d, V, 8, noise, M).run()
+    r = R.distill(c.H, c.W, c.ids, c.val, c.w, R.TAIL)
+    q = torch.softmax(R.logits(c.H, c.W), 1)
+    Q, w = q[:, :8].sum(1), c.w.double()
+    assert Q.max() < 0.1
+    ref = r["dH"][:, 1]
+    assert (ref.abs() <= 2 * w * noise * Q).all()   # the difference that is looked at
+    bar = 2.0 ** -21 * w * Q * (1 - Q) + 3 * 2.0 ** -8 * ref.abs()
+    assert ((c.dH[:, 1].double() - ref).abs() <= bar).all()
+    ref = r["dW"][8:, 2]
+    off = r["dL"][:, 8:].abs().sum(0)
+    bar = 2.0 ** -21 * (w * Q)[:, None].mul(q[:, 8:]).sum(0) + 4 * 2.0 ** -8 * off
+    assert ((c.dW[8:, 2].double() - ref).abs() <= bar).all()
+    assert_device_ok()
