@@ -1523,6 +1523,9 @@ DistillWs distill_layout(uint8_t* base, int64_t M, int64_t d, int64_t V, int64_t
   if (grads) {
     take(w.w.factor, size_t(M));
     const size_t rows = size_t(std::max(M, std::min(2 * M, 2 * kDistillTwice)));
+    take(w.w.add, size_t(M) * d);
+    take(w.w.carry, size_t(M) * k);
+    take(w.w.carry_n, size_t(M));
     take(w.w.scaled, rows * d);
     take(w.dH_parts, dh_parts_bytes(M, d, V, kDistillRange) / 4);
     take(w.w.kept, rows * V);
@@ -1566,7 +1569,7 @@ coda_status_t coda_lmhead_distill(coda_handle_t h, const void* Hs, const void* W
   if (ws_bytes < coda_lmhead_distill_workspace_bytes(M, d, V, k, grads)) return CODA_ERR_WORKSPACE_TOO_SMALL;
   const OnDevice dev(h->device);
   const LaunchCtx cx = ctx_of(h, stream);
-  const DistillWs w = distill_layout(static_cast<uint8_t*>(ws), M, d, V, k, grads);
+  DistillWs w = distill_layout(static_cast<uint8_t*>(ws), M, d, V, k, grads);
   const bf16* Hb = static_cast<const bf16*>(Hs);
   const bf16* Wb = static_cast<const bf16*>(Wt);
   DistillIn in{};
@@ -1582,27 +1585,33 @@ coda_status_t coda_lmhead_distill(coda_handle_t h, const void* Hs, const void* W
   CODA_CUDA(launch_distill_list(cx, in, w.w, Hb, Wb, M, d, V));
   CODA_CUDA(gemm_distill(cx, Hb, Wb, w.w, in.log2e_over_t, int(M), int(d), int(V)));
   const int64_t parts = grads ? dh_parts(M, d, V, kDistillRange) : 1;
-  // with dH in ranges, the kernel that ends it sums the statistics
-  CODA_CUDA(launch_distill_rows(cx, in, w.w, DistillOut{parts == 1 ? stats : nullptr, row_loss}, Hb, M, d, V));
+  // with dH in ranges, the kernel that ends it sums the statistics and adds what it carries
+  if (parts > 1) w.w.add = nullptr;
+  CODA_CUDA(launch_distill_rows(cx, in, w.w, DistillOut{parts == 1 ? stats : nullptr, row_loss}, Hb, Wb, M, d, V));
   if (!grads) return CODA_OK;
   bf16* dH = static_cast<bf16*>(dHs);
   bf16* dW = static_cast<bf16*>(dWt);
   const int64_t rows = M <= kDistillTwice ? 2 * M : M;
   if (parts == 1)
     return from_cuda(
-        gemm_group_scaled_bwd(cx, w.w.kept, w.w.factor, Wb, w.w.scaled, dH, dW, int(M), int(rows), int(d), int(V)));
+        gemm_group_scaled_bwd(cx, w.w.kept, w.w.factor, Wb, w.w.add, w.w.scaled, dH, dW, int(M), int(rows), int(d),
+                              int(V)));
   // few tokens: dH in ranges of the vocabulary
   CODA_CUDA(gemm_splitk(cx, w.w.kept, Wb, w.dH_parts, int(parts), false, int(M), int(d), int(V)));
   SplitDh finish{};
   finish.parts = reinterpret_cast<const float4*>(w.dH_parts);
   finish.num = static_cast<int>(parts);
   finish.stride4 = cdiv(M, 256) * 256 * d / 4;
-  finish.n4 = M * d / 4;
-  finish.d4 = d / 4;
+  finish.n8 = M * d / 8;
+  finish.d8 = d / 8;
   finish.factor = w.w.factor;
+  finish.Wt = reinterpret_cast<const uint4*>(Wb);
+  finish.carry = w.w.carry;
+  finish.carry_n = w.w.carry_n;
+  finish.k = static_cast<int>(k);
   finish.terms = w.w.terms;
   finish.stats = stats;
-  finish.out = reinterpret_cast<uint2*>(dH);
+  finish.out = reinterpret_cast<uint4*>(dH);
   return from_cuda(gemm_store_plus_rows(cx, w.w.kept, w.w.scaled, dW, nullptr, nullptr, int(rows), int(d), int(V),
                                         finish));
 }

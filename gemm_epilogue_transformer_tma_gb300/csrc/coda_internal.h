@@ -113,6 +113,10 @@ cudaError_t gemm_store(const LaunchCtx& c, const __nv_bfloat16* A, bool a_mn, co
                        __nv_bfloat16* C, int M, int N, int K, const float* row_scale,
                        const __nv_bfloat16* col_scale);
 
+// C = bf16(row_scale[m] (A B)[m][n] + add[m][n]), A [M][K], B [K][N]
+cudaError_t gemm_scale_add(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_bfloat16* B, const float* row_scale,
+                           const __nv_bfloat16* add, __nv_bfloat16* C, int M, int N, int K);
+
 // C (fp32) = A B  or  C += A B.
 cudaError_t gemm_store_f32(const LaunchCtx& c, const __nv_bfloat16* A, bool a_mn, const __nv_bfloat16* B, bool b_mn,
                            float* C, int M, int N, int K, bool accumulate);
@@ -233,11 +237,14 @@ struct DistillWork {
   float* psum;          // [M][T]
   float4* terms;        // [M]: shares of the statistics
   int* done;            // rows finished
-  // with gradients, dL = factor kept, scaled = factor H: [M][V] and [M][d].  Up to
-  // kDistillTwice rows as many more behind them: the listed entries of kept alone,
-  // and what bf16 takes from scaled
+  // with gradients, dH = factor kept Wt + add, dW = kept^T scaled: [M][V], [M], [M][d]
+  // and [M][d].  Up to kDistillTwice rows as many more behind kept and scaled: the
+  // listed entries of kept alone, and what bf16 takes from scaled
   __nv_bfloat16* kept;
-  float* factor;          // [M]
+  float* factor;
+  __nv_bfloat16* add;  // or null: left to SplitDh, by its list
+  float2* carry;       // [M][k]
+  int* carry_n;        // [M]
   __nv_bfloat16* scaled;
 };
 struct DistillOut {
@@ -249,12 +256,12 @@ cudaError_t launch_distill_list(const LaunchCtx& c, const DistillIn& in, const D
 cudaError_t gemm_distill(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt, const DistillWork& w,
                          float log2e_over_t, int M, int d, int V);
 cudaError_t launch_distill_rows(const LaunchCtx& c, const DistillIn& in, const DistillWork& w, const DistillOut& o,
-                                const __nv_bfloat16* H, int64_t M, int64_t d, int64_t V);
-// dH = diag(factor) E Wt of the first M rows of E and dW = E^T scaled of all
+                                const __nv_bfloat16* H, const __nv_bfloat16* Wt, int64_t M, int64_t d, int64_t V);
+// dH = diag(factor) E Wt + add of the first M rows of E and dW = E^T scaled of all
 // (E [rows][V], scaled [rows][d]), one grouped launch
 cudaError_t gemm_group_scaled_bwd(const LaunchCtx& c, const __nv_bfloat16* E, const float* factor,
-                                  const __nv_bfloat16* Wt, const __nv_bfloat16* scaled, __nv_bfloat16* dH,
-                                  __nv_bfloat16* dW, int M, int rows, int d, int V);
+                                  const __nv_bfloat16* Wt, const __nv_bfloat16* add, const __nv_bfloat16* scaled,
+                                  __nv_bfloat16* dH, __nv_bfloat16* dW, int M, int rows, int d, int V);
 
 // parts_buf [parts][M rounded up to 256][N] fp32 (+)= the K ranges of A B, A
 // [M][K], B [K][N] (gemm_splitk.cuh); parts <= the k-blocks of 64 in K
@@ -302,12 +309,16 @@ cudaError_t gemm_group_policy_bwd(const LaunchCtx& c, const __nv_bfloat16* dL, c
                                   const uint32_t* slot, const float* rows, int M, int d, int Vc);
 //   (slot null: dWc = dL^T H).  It can take on the end of a split data gradient:
 struct SplitDh {
-  const float4* parts;  // [num][stride4], of which n4 are used
+  const float4* parts;  // [num][stride4], of which 2 n8 are used
   int num;
-  int64_t stride4, n4, d4;
-  const float* factor;  // [n4 / d4]
-  uint2* out;           // bf16
-  const float4* terms;  // [n4 / d4], or null: their sum to stats
+  int64_t stride4, n8, d8;
+  const float* factor;  // [n8 / d8]
+  const uint4* Wt;      // [.][d8], bf16
+  const float2* carry;  // [n8 / d8][k], of which carry_n[m] are used: a factor and, as bits, a row of Wt
+  const int* carry_n;
+  int k;
+  uint4* out;           // bf16
+  const float4* terms;  // [n8 / d8], or null: their sum to stats
   float* stats;
 };
 cudaError_t gemm_store_plus_rows(const LaunchCtx& c, const __nv_bfloat16* dL, const __nv_bfloat16* H,

@@ -400,11 +400,22 @@ enum RowGrads { NO_GRADS, GRADS_ONCE, GRADS_TWICE };
 // for both forms of a size: the loss has the same bits with gradients and without).
 // 4096 rows of V = 128256, d = 2048 27 us, 136 of V = 32000, d = 1024 5.5: latency.
 constexpr int kRowThreads = 128, kFewRowThreads = 512;
+// What bf16 takes from the listed entries of dL is carried to dH in fp32, as a sum of
+// rows of Wt.  A row of dL sums to 0, so a mean that the rows of the head share leaves
+// dH; a rounded entry brings a part of it back.  dH's error over that of rounding it
+// alone, 300 tokens, V = 4096, k = 20, means of 1, 5 and 20 times the rows' spread:
+// 1.0, 1.0 and 1.05; with a factor for dH that makes the largest entry exact and
+// nothing carried 1.4, 5.9 and 24.  Entries below kCarried of the row's largest stay
+// out: all together they are off by 2^-13 of it (k = 256).  A step of 136 tokens, d =
+// 1024, V = 32000, k = 32 66.5 to 69 us, of 4096, d = 2048, V = 128256 2 % more
+// with k = 64, 7 % with k = 256.
+constexpr float kCarried = 0x1p-9f;
 
 template <int GRADS, int kThreads>
 __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn in, const DistillWork w,
                                                                 const DistillOut o,
-                                                                const __nv_bfloat16* __restrict__ H, int64_t M,
+                                                                const __nv_bfloat16* __restrict__ H,
+                                                                const __nv_bfloat16* __restrict__ Wt, int64_t M,
                                                                 int64_t d, int64_t V) {
   griddep_wait();
   griddep_launch_dependents();
@@ -424,6 +435,12 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
   const float n_row = w.n[m];
   const float4 mass = w.mass[m];
   constexpr int N = (kDistillMaxList + kThreads - 1) / kThreads;
+  // what dH lacks of the listed entries, carry_n of them, in the list's order
+  constexpr int kCarry = GRADS != NO_GRADS ? kDistillMaxList : 1;
+  __shared__ float carry[kCarry];
+  __shared__ int32_t carry_id[kCarry];
+  __shared__ int carry_count[N * kWarps];
+  int carry_n = 0;
   int32_t id[N];
   float x[N], q[N];
   float2 t[N];
@@ -444,7 +461,7 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
   if (GRADS != NO_GRADS && tid < d / 8) first_h = __ldg(h + tid);
 
   float4 terms = make_float4(0.f, 0.f, 0.f, 0.f);
-  float loss = 0.f, factor = 0.f;
+  float loss = 0.f, factor = 0.f, factor_w = 0.f;  // of dH's row, and the row's share of dW
   auto zero_row = [&](__nv_bfloat16* to) {
     for (int64_t i = tid; i < V / 8; i += kThreads) reinterpret_cast<uint4*>(to)[i] = make_uint4(0u, 0u, 0u, 0u);
   };
@@ -558,19 +575,41 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
         f = 1.f;
         __syncthreads();
       }
-      // The factor is moved by at most half a step of bf16 so that the row's
+      // For dW the factor is moved by at most half a step of bf16 so that the row's
       // largest entry, which has nearly all of the square of dL, is a bf16 number:
       // it keeps its fp32 value, and the tokens off the list move together by no
-      // more than each is rounded.  The gradients' error over that of rounding
-      // them alone, dH and dW: 1.0 and 1.4, 1.3 to 1.6 and 1.7 with f as it is.
+      // more than each is rounded, in one direction for each of a sum's rows.  The
+      // gradient's error over that of rounding it alone: 1.4, and 1.7 with f as it is.
       const float largest = steep / f, exact = bf16_round(largest);
-      if (exact != 0.f && isfinite(exact)) f = steep / exact;
+      const float f_w = exact != 0.f && isfinite(exact) ? steep / exact : f;
       factor = scale * f;
+      factor_w = scale * f_w;
+      unsigned who[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        q[i] = f != 0.f ? q[i] / f : 0.f;  // 0 only with a row of zeros: no mass, or a student beyond doubt
-        if (id[i] >= 0) kept[id[i]] = __float2bfloat16_rn(q[i]);
+        const float own = q[i];
+        q[i] = f != 0.f ? own / f_w : 0.f;  // 0 only with a row of zeros: no mass, or a student beyond doubt
+        const float held = bf16_round(q[i]);
+        if (id[i] >= 0) kept[id[i]] = __float2bfloat16_rn(held);
+        // dH takes f as it is
+        x[i] = scale * fmaf(-f, held, own);
+        who[i] = __ballot_sync(0xffffffffu, id[i] >= 0 && fabsf(own) > kCarried * steep && x[i] != 0.f);
+        if (lane == 0) carry_count[i * kWarps + warp] = __popc(who[i]);
       }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int p = 0; p < kWarps; ++p) {
+          if (p == warp && (who[i] >> lane & 1u) != 0u) {
+            const int at = carry_n + __popc(who[i] & ((1u << lane) - 1u));
+            carry[at] = x[i];
+            carry_id[at] = id[i];
+          }
+          carry_n += carry_count[i * kWarps + p];
+        }
+      }
+      __syncthreads();
       if (GRADS == GRADS_TWICE) {
         __nv_bfloat16* again = kept + M * V;
         zero_row(again);
@@ -589,7 +628,7 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
       unpack_bf16x8(i == tid ? first_h : __ldg(h + i), v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float x = weight != 0.f ? v[j] * factor : 0.f;
+        const float x = weight != 0.f ? v[j] * factor_w : 0.f;
         v[j] = bf16_round(x);
         low[j] = x - v[j];
       }
@@ -598,6 +637,25 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
       if (GRADS == GRADS_TWICE)
         to[M * (d / 8) + i] = make_uint4(pack_bf16x2(low[0], low[1]), pack_bf16x2(low[2], low[3]),
                                          pack_bf16x2(low[4], low[5]), pack_bf16x2(low[6], low[7]));
+    }
+    if (w.add == nullptr) {  // few tokens: left to the kernel that ends dH, beside the weight gradient's tiles
+      for (int j = tid; j < carry_n; j += kThreads)
+        w.carry[m * k + j] = make_float2(carry[j], __int_as_float(carry_id[j]));
+      if (tid == 0) w.carry_n[m] = carry_n;
+    } else {
+      uint4* add = reinterpret_cast<uint4*>(w.add + m * d);
+      for (int64_t i = tid; i < d / 8; i += kThreads) {
+        float a[8] = {};
+#pragma unroll 8
+        for (int j = 0; j < carry_n; ++j) {
+          float u[8];
+          unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(Wt + carry_id[j] * d) + i), u);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) a[q] = fmaf(carry[j], u[q], a[q]);
+        }
+        add[i] = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                            pack_bf16x2(a[6], a[7]));
+      }
     }
     if (GRADS == GRADS_TWICE && weight == 0.f) zero_row(w.kept + (M + m) * V);
   }
@@ -655,14 +713,14 @@ cudaError_t launch_distill_list(const LaunchCtx& c, const DistillIn& in, const D
 }
 
 cudaError_t launch_distill_rows(const LaunchCtx& c, const DistillIn& in, const DistillWork& w, const DistillOut& o,
-                                const __nv_bfloat16* H, int64_t M, int64_t d, int64_t V) {
+                                const __nv_bfloat16* H, const __nv_bfloat16* Wt, int64_t M, int64_t d, int64_t V) {
   const bool few = M <= kDistillTwice, grads = w.kept != nullptr;
   auto kern = few ? grads ? distill_rows_kernel<GRADS_TWICE, kFewRowThreads>
                           : distill_rows_kernel<NO_GRADS, kFewRowThreads>
               : grads ? distill_rows_kernel<GRADS_ONCE, kRowThreads>
                       : distill_rows_kernel<NO_GRADS, kRowThreads>;
   return launch_chained(c, kern, dim3(static_cast<unsigned>(M)), dim3(few ? kFewRowThreads : kRowThreads), 0, in, w, o,
-                        H, M, d, V);
+                        H, Wt, M, d, V);
 }
 
 }  // namespace coda

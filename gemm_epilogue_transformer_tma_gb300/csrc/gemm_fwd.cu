@@ -84,6 +84,17 @@ cudaError_t gemm_store(const LaunchCtx& c, const __nv_bfloat16* A, bool a_mn, co
   return cudaErrorNotSupported;  // MN-major A with K-major B is not used on this path
 }
 
+cudaError_t gemm_scale_add(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_bfloat16* B, const float* row_scale,
+                           const __nv_bfloat16* add, __nv_bfloat16* C, int M, int N, int K) {
+  CUtensorMap ta, tb;
+  if (!make_operand_maps(&ta, &tb, A, false, B, true, M, N, K, b_box_rows(c))) return cudaErrorInvalidValue;
+  EpiScaleAdd::Params ep{};
+  if (!make_tmap_store_bf16(&ep.out, C, N, M, N)) return cudaErrorInvalidValue;
+  ep.row_scale = row_scale;
+  ep.add = add;
+  return run_gemm<false, true, false, EpiScaleAdd>(c, ta, tb, tb, M, N, K, (N + kBN - 1) / kBN, ep);
+}
+
 cudaError_t gemm_store_f32(const LaunchCtx& c, const __nv_bfloat16* A, bool a_mn, const __nv_bfloat16* B, bool b_mn,
                            float* C, int M, int N, int K, bool accumulate) {
   if (a_mn || !b_mn) return cudaErrorNotSupported;  // only [M][K] x [K][N] is used

@@ -181,14 +181,14 @@ cudaError_t gemm_group_policy_bwd(const LaunchCtx& c, const __nv_bfloat16* dL, c
 }
 
 cudaError_t gemm_group_scaled_bwd(const LaunchCtx& c, const __nv_bfloat16* E, const float* factor,
-                                  const __nv_bfloat16* Wt, const __nv_bfloat16* scaled, __nv_bfloat16* dH,
-                                  __nv_bfloat16* dW, int M, int rows, int d, int V) {
+                                  const __nv_bfloat16* Wt, const __nv_bfloat16* add, const __nv_bfloat16* scaled,
+                                  __nv_bfloat16* dH, __nv_bfloat16* dW, int M, int rows, int d, int V) {
   if (!c.pair) {
-    cudaError_t e = gemm_store(c, E, false, Wt, true, dH, M, d, V, factor, nullptr);
+    cudaError_t e = gemm_scale_add(c, E, Wt, factor, add, dH, M, d, V);
     if (e != cudaSuccess) return e;
     return gemm_store(c, E, true, scaled, true, dW, V, d, rows, nullptr, nullptr);
   }
-  GroupArgs<EpiStore, EpiStore> ga{};
+  GroupArgs<EpiScaleAdd, EpiStore> ga{};
   // The whole vocabulary is one contraction: 8016 products of 16 at V = 128256,
   // each of which costs the running sum half of its last place at most (2^-25),
   // 2.4e-4 in all beside the 2^-9 of the result's rounding.
@@ -200,7 +200,8 @@ cudaError_t gemm_group_scaled_bwd(const LaunchCtx& c, const __nv_bfloat16* E, co
   if (!make_tmap_store_bf16(&ga.ep0.out, dH, d, M, d) || !make_tmap_store_bf16(&ga.ep1.out, dW, d, V, d))
     return cudaErrorInvalidValue;
   ga.ep0.row_scale = factor;
-  return launch_group<false, true, true, true, EpiStore, EpiStore>(c, ga);
+  ga.ep0.add = add;
+  return launch_group<false, true, true, true, EpiScaleAdd, EpiStore>(c, ga);
 }
 
 cudaError_t gemm_group_ce_bwd_fp8(const LaunchCtx& c0, const uint8_t* dLq, float s_dL, const uint8_t* Wq_chunk,

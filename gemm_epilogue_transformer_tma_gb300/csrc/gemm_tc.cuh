@@ -634,6 +634,50 @@ struct EpiStore {
   }
 };
 
+// C = bf16(row_scale[m] * acc + add[m][n]).  The data gradient of distillation:
+// what the bf16 entries of dL lost.
+struct EpiScaleAdd {
+  static constexpr int kEpiWarps = 4;
+  static constexpr int kStoreSlots = 2;  // two slots used alternately
+  static constexpr bool kAccScale = false;  // bf16 operands only
+  struct Params {
+    CUtensorMap out;  // [M][N] bf16
+    const float* row_scale;
+    const __nv_bfloat16* add;  // [M][N]
+  };
+  template <int BN>
+  static __device__ __forceinline__ void run(const Params& p, const EpiCtx& c) {
+    const bool row_ok = c.m < c.M;
+    const float rs = row_ok ? p.row_scale[c.m] : 0.f;
+    const __nv_bfloat16* row = p.add + static_cast<int64_t>(c.m) * c.N;
+    const int nb = c.tn * BN;
+    // loaded one chunk ahead of its use
+    uint4 rq[4];
+    load_bf16x32_raw(row, nb + c.c0, row_ok ? c.N - nb - c.c0 : 0, rq);
+#pragma unroll 1
+    for (int cc = c.c0; cc < c.c1; cc += 32) {
+      float v[32], r[32];
+      acc_ld32(c, cc, v);
+      const int n0 = nb + cc;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) unpack_bf16x8(rq[g], &r[g * 8]);
+      if (cc + 32 < c.c1) load_bf16x32_raw(row, n0 + 32, row_ok ? c.N - n0 - 32 : 0, rq);
+      if (n0 < c.N && c.m0 < c.M) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], rs, r[i]);
+        const int slot = ((cc - c.c0) >> 5) & 1;
+        slots_acquire_db(c.lane, cc == c.c0);
+        stage_bf16x32(slot_addr(c, slot), c.lane, v);
+        slots_publish();
+        if (c.lane == 0) {
+          tma_store_2d(&p.out, slot_addr(c, slot), n0, c.m0);
+          bulk_commit_group();
+        }
+      }
+    }
+  }
+};
+
 // C = bf16(acc + rows[slot[m]]): an fp32 row added where row m has a slot
 // (slot[m] != kNoSlot).  The weight gradient of the policy loss: what the bf16
 // label entries of dL lost, summed over a vocabulary row's tokens.

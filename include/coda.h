@@ -841,11 +841,11 @@ coda_status_t coda_lmhead_score(coda_handle_t h, const void* Hs, const void* Wt,
 #define CODA_DISTILL_TAIL 2       /* val = log-probabilities; what they leave is the target of all others together */
 
 /* Workspace of coda_lmhead_distill: 20 bytes per list entry, 8.2 per row and 128
- * columns of the vocabulary and 36 per row; with gradients 2 M (V + d) more (the
- * student's exponentials in bf16 and a scaled Hs; twice as much for 64 rows and
- * fewer) and up to 20 MB of fp32 partial sums of dHs (used for few tokens).  A
- * workspace for M tokens also serves any smaller number.  0 for M, d, V or k <= 0
- * and for k > 256. */
+ * columns of the vocabulary and 36 per row; with gradients 2 M (V + 2 d) more (the
+ * student's exponentials in bf16, a scaled Hs and a part of dHs; 2 M (2 V + 3 d) for
+ * 64 rows and fewer), 8 per list entry and per row, and up to 20 MB of fp32 partial
+ * sums of dHs (used for few tokens).  A workspace for M tokens also serves any
+ * smaller number.  0 for M, d, V or k <= 0 and for k > 256. */
 size_t coda_lmhead_distill_workspace_bytes(int64_t M, int64_t d, int64_t V, int64_t k, int with_grads);
 
 /* Loss of a student's LM head against a teacher's most probable tokens, with
@@ -873,12 +873,15 @@ size_t coda_lmhead_distill_workspace_bytes(int64_t M, int64_t d, int64_t V, int6
  * If dHs is not NULL the gradients of loss are produced: dL = weight /
  * temperature ((P + r) q_v - t_v) on the list, weight / temperature q_v (P + r -
  * r / R) off it; dHs = dL Wt, dWt = dL^T Hs.  dL is held as a bf16 matrix and an
- * fp32 factor per row, chosen so that a row's largest entry is not rounded; dWt's
- * contraction finds the factor in a copy of Hs, in bf16, up to 64 rows in twice
- * the digits.  Where that entry outweighs its row, the error of dHs is that of
- * rounding it alone, and of dWt too up to 64 rows; dWt of more carries the rounding
- * of the scaled Hs as well (1.4 times the error of rounding it alone, on average).
- * The other listed entries are rounded once, entries off the list twice.
+ * fp32 factor per row.  For dHs what that takes from the listed entries (of 2^-9 of
+ * the row's largest and more) is added in fp32, so that dHs carries its own rounding
+ * and that of the entries off the list, each rounded by itself, whatever mean the
+ * rows of Wt share.  For dWt the factor is moved, by 2^-8 at most, so that the row's
+ * largest entry is not rounded, and the contraction finds it in a copy of Hs, in
+ * bf16, up to 64 rows in twice the digits.  Where that entry outweighs its row, the
+ * error of dWt is that of rounding it alone up to 64 rows; of more it carries the
+ * rounding of the scaled Hs as well (1.4 times the error of rounding it alone, on
+ * average).  The other listed entries are rounded once, entries off the list twice.
  * Hs bf16 [M][d], Wt bf16 [V][d], ids int32 [M][k], val fp32 [M][k], weight fp32
  * [M] or NULL (ids, val, weight, stats and row_loss 4-byte aligned), dHs bf16
  * [M][d] or NULL, dWt bf16 [V][d] (required iff dHs != NULL).  1 <= k <= 256,

@@ -5,7 +5,7 @@ import torch
 
 from tests import _lmhead as R
 from tests._parity import assert_device_ok
-from tests.test_gpu_distill import MODES, Call, make
+from tests.test_gpu_distill import MODES, Call, make, teacher
 
 pytestmark = pytest.mark.gpu
 
@@ -67,4 +67,33 @@ def test_the_gradient_off_the_list_of_a_student_near_its_teacher(M, d, V, noise)
     off = r["dL"][:, 8:].abs().sum(0)
     bar = 2.0 ** -21 * (w * Q)[:, None].mul(q[:, 8:]).sum(0) + 4 * 2.0 ** -8 * off
     assert ((c.dW[8:, 2].double() - ref).abs() <= bar).all()
+    assert_device_ok()
+
+
+@pytest.mark.parametrize("M,d,V,k", [(1, 256, 9000, 1), (40, 512, 4096, 1), (40, 1024, 1000, 20), (64, 512, 9000, 64),
+                                     (65, 512, 9000, 20), (300, 256, 4096, 1), (700, 512, 4096, 33),
+                                     (1100, 2560, 1048, 1), (1100, 2560, 1048, 33)])
+@pytest.mark.parametrize("mean", [0.25, 1.0])
+@pytest.mark.parametrize("mode", MODES)
+def test_a_head_whose_rows_share_a_mean(M, d, V, k, mean, mode):
+    """5 and 20 times their spread.  A row of dL sums to 0, so the
+    mean leaves dHs; it stays out of it as far as the entries keep their digits: off
+    the list each is rounded by itself (half a step, 2^-8 at most and of independent
+    signs), twice at most, on the list those below 2^-9 of the row's largest.
+    The fp32 sum over the vocabulary may be off by 2^-23 of its parts every 16
+    columns."""
+    H, W, y = R.grid_inputs(M, d, V, seed=M + k)
+    W = (W.float() + mean).to(BF)
+    H = (H.float() / 8).to(BF)
+    c = Call(H, W, *teacher(H, W, y, k, mode, 1.0, M), mode).run()
+    r = c.grade(grads=False)
+    dL, Wd, ref = r["dL"], W.double(), r["dH"]
+    used = (c.ids >= 0) & (c.ids < V)
+    on = torch.zeros_like(dL).scatter_add_(1, torch.where(used, c.ids, 0).long(), used.double()) > 0
+    steep = torch.where(on, dL.abs(), 0.0).amax(1, keepdim=True)
+    rounded = torch.where(on & (dL.abs() > 2.0 ** -9 * steep), 0.0, dL)
+    one = (ref.to(BF).double() - ref).norm()
+    bar = ((1.02 * one) ** 2 + 4 * 2.0 ** -16 * (rounded ** 2 @ Wd ** 2).sum()).sqrt()
+    bar += (2.0 ** -15 + 2.0 ** -23 * V / 16) * (dL.abs() @ Wd.abs()).norm()
+    assert (c.dH.double() - ref).norm() <= bar
     assert_device_ok()
