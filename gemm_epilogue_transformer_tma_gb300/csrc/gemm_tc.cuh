@@ -651,9 +651,15 @@ struct EpiScaleAdd {
     const float rs = row_ok ? p.row_scale[c.m] : 0.f;
     const __nv_bfloat16* row = p.add + static_cast<int64_t>(c.m) * c.N;
     const int nb = c.tn * BN;
-    // loaded one chunk ahead of its use
+    // loaded one chunk ahead of its use; the kernel before writes it while this one has started, so not .nc
     uint4 rq[4];
-    load_bf16x32_raw(row, nb + c.c0, row_ok ? c.N - nb - c.c0 : 0, rq);
+    auto load = [&](int n0) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        rq[g] = row_ok && n0 + g * 8 < c.N ? *reinterpret_cast<const uint4*>(row + n0 + g * 8)
+                                           : make_uint4(0u, 0u, 0u, 0u);
+    };
+    load(nb + c.c0);
 #pragma unroll 1
     for (int cc = c.c0; cc < c.c1; cc += 32) {
       float v[32], r[32];
@@ -661,7 +667,7 @@ struct EpiScaleAdd {
       const int n0 = nb + cc;
 #pragma unroll
       for (int g = 0; g < 4; ++g) unpack_bf16x8(rq[g], &r[g * 8]);
-      if (cc + 32 < c.c1) load_bf16x32_raw(row, n0 + 32, row_ok ? c.N - n0 - 32 : 0, rq);
+      if (cc + 32 < c.c1) load(n0 + 32);
       if (n0 < c.N && c.m0 < c.M) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = fmaf(v[i], rs, r[i]);

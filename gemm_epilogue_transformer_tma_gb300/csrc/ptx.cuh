@@ -589,15 +589,16 @@ __device__ __forceinline__ void add_exact(float& hi, float& lo, float b, float b
 // the pair as one number; an infinite sum has no rounding error to add
 __device__ __forceinline__ float exact_value(float hi, float lo) { return isinf(hi) ? hi : hi + lo; }
 
-// Loads of constant data that stay where they are written: ahead of a wait.
+// Loads that stay where they are written: ahead of a wait for something else.  Not
+// .nc: the kernel before writes some of what they read while this one has started.
 __device__ __forceinline__ uint32_t ld_here_u32(const uint32_t* p) {
   uint32_t v;
-  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
 __device__ __forceinline__ float ld_here_f32(const float* p) {
   float v;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
   return v;
 }
 

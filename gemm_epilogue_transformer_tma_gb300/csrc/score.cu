@@ -153,8 +153,8 @@ __device__ __forceinline__ void append(TopSmem& sm, bool take, uint32_t key, uin
 // lo; all lanes of a warp call it, with `there` false past the end.  A warp
 // takes 32 sub-blocks at a time.
 template <class F>
-__device__ __forceinline__ void each_logit(const float* __restrict__ sub, const float* __restrict__ logits, int subs,
-                                           int cols, int64_t V, uint32_t lo, int warp, int warps, int lane, F&& f) {
+__device__ __forceinline__ void each_logit(const float* sub, const float* logits, int subs, int cols, int64_t V,
+                                           uint32_t lo, int warp, int warps, int lane, F&& f) {
   for (int j0 = warp * 32; j0 < subs; j0 += warps * 32) {
     const int j = j0 + lane;
     unsigned hit = __ballot_sync(0xffffffffu, j < subs && rank_key(sub[j]) >= lo);
