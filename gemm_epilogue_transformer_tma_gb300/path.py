@@ -455,12 +455,12 @@ class QKVProjection:
         self.gq, self.gk, self.eps = gq, gk, eps
         self.heads = (n_q_heads, n_kv_heads, gq.shape[0])
         D, dev = gq.shape[0], Wqkv.device
-        self.cos_t, self.sin_t = torch.empty(S, D // 2, device=dev), torch.empty(S, D // 2, device=dev)
+        self.cos_t, self.sin_t = (torch.empty(S, D // 2, dtype=F32, device=dev) for _ in range(2))
         coda_rope_table(self.cos_t, self.sin_t, base)
         self.out = torch.empty_like(self.linear.Y)
         if backward:
             self.dqkv = torch.empty_like(self.linear.Y)
-            self.dgq, self.dgk = torch.empty(D, device=dev), torch.empty(D, device=dev)
+            self.dgq, self.dgk = (torch.empty(D, dtype=F32, device=dev) for _ in range(2))
             self.ws = torch.empty(coda_qknorm_rope_bwd_workspace_bytes(max(M, 1), D), dtype=torch.uint8, device=dev)
 
     def forward(self, X, positions=None):
@@ -492,7 +492,7 @@ class PolicyHead:
         e = dict(device=Wt.device)
         form = 2 if backward and least_memory else int(backward)
         self.ws = torch.empty(coda_lmhead_policy_workspace_bytes(M, d, V, form), dtype=torch.uint8, **e)
-        self.stats, self.logp = torch.empty(4, **e), torch.empty(M, **e)
+        self.stats, self.logp = torch.empty(4, dtype=F32, **e), torch.empty(M, dtype=F32, **e)
         self.dH = torch.empty(M, d, dtype=BF, **e) if backward else None
         self.dWt = torch.empty(V, d, dtype=BF, **e) if backward else None
 
@@ -514,8 +514,9 @@ class ScoringHead:
         V, d = Wt.shape
         e = dict(device=Wt.device)
         self.ws = torch.empty(coda_lmhead_score_workspace_bytes(M, d, V, k), dtype=torch.uint8, **e)
-        self.logp, self.entropy = torch.empty(M, **e), torch.empty(M, **e)
-        self.top_ids, self.top_logp = torch.empty(M, k, dtype=torch.int32, **e), torch.empty(M, k, **e)
+        self.logp, self.entropy = torch.empty(M, dtype=F32, **e), torch.empty(M, dtype=F32, **e)
+        self.top_ids = torch.empty(M, k, dtype=torch.int32, **e)
+        self.top_logp = torch.empty(M, k, dtype=F32, **e)
 
     def score(self, H, labels=None):
         """(logp, entropy, top_ids, top_logp) of H [m, d]; logp None without
@@ -538,7 +539,7 @@ class DistillHead:
         V, d = Wt.shape
         e = dict(device=Wt.device)
         self.ws = torch.empty(coda_lmhead_distill_workspace_bytes(M, d, V, k, backward), dtype=torch.uint8, **e)
-        self.stats, self.row_loss = torch.empty(4, **e), torch.empty(M, **e)
+        self.stats, self.row_loss = torch.empty(4, dtype=F32, **e), torch.empty(M, dtype=F32, **e)
         self.dH = torch.empty(M, d, dtype=BF, **e) if backward else None
         self.dWt = torch.empty(V, d, dtype=BF, **e) if backward else None
 
