@@ -97,3 +97,12 @@ def test_a_head_whose_rows_share_a_mean(M, d, V, k, mean, mode):
     bar += (2.0 ** -15 + 2.0 ** -23 * V / 16) * (dL.abs() @ Wd.abs()).norm()
     assert (c.dH.double() - ref).norm() <= bar
     assert_device_ok()
+
+
+@pytest.mark.parametrize("M,d,V", [(40, 64, 1000), (300, 64, 1000), (1100, 2560, 1048)])
+@pytest.mark.parametrize("mode", MODES)
+def test_temperatures_that_flatten_every_row(mode, M, d, V):
+    """All tokens are equally probable, and columns that do not exist are not among
+    them.  The gradients, 1 / T of others, are fp32 numbers at 1e30."""
+    for T, grads in ((1e30, True), (3e36, False), (3e38, False)):
+        make(M, d, V, 7, mode, T=T, grads=grads).run().grade()
