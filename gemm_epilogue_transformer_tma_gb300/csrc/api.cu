@@ -1585,8 +1585,8 @@ coda_status_t coda_lmhead_distill(coda_handle_t h, const void* Hs, const void* W
   CODA_CUDA(launch_distill_list(cx, in, w.w, Hb, Wb, M, d, V));
   CODA_CUDA(gemm_distill(cx, Hb, Wb, w.w, in.log2e_over_t, int(M), int(d), int(V)));
   const int64_t parts = grads ? dh_parts(M, d, V, kDistillRange) : 1;
-  // with dH in ranges, the kernel that ends it sums the statistics and adds what it carries
-  if (parts > 1) w.w.add = nullptr;
+  // with dH in ranges, the kernel that ends it sums the statistics, and what the lists carry is summed beside them
+  if (parts == 1) w.w.carry = nullptr;
   CODA_CUDA(launch_distill_rows(cx, in, w.w, DistillOut{parts == 1 ? stats : nullptr, row_loss}, Hb, Wb, M, d, V));
   if (!grads) return CODA_OK;
   bf16* dH = static_cast<bf16*>(dHs);
@@ -1597,21 +1597,26 @@ coda_status_t coda_lmhead_distill(coda_handle_t h, const void* Hs, const void* W
         gemm_group_scaled_bwd(cx, w.w.kept, w.w.factor, Wb, w.w.add, w.w.scaled, dH, dW, int(M), int(rows), int(d),
                               int(V)));
   // few tokens: dH in ranges of the vocabulary
-  CODA_CUDA(gemm_splitk(cx, w.w.kept, Wb, w.dH_parts, int(parts), false, int(M), int(d), int(V)));
+  RowSums carried{};
+  carried.list = w.w.carry;
+  carried.n = w.w.carry_n;
+  carried.k = static_cast<int>(k);
+  carried.Wt = reinterpret_cast<const uint4*>(Wb);
+  carried.d8 = d / 8;
+  carried.n8 = M * d / 8;
+  carried.out = reinterpret_cast<uint4*>(w.w.add);
+  CODA_CUDA(gemm_splitk(cx, w.w.kept, Wb, w.dH_parts, int(parts), false, int(M), int(d), int(V), carried));
   SplitDh finish{};
   finish.parts = reinterpret_cast<const float4*>(w.dH_parts);
   finish.num = static_cast<int>(parts);
   finish.stride4 = cdiv(M, 256) * 256 * d / 4;
-  finish.n8 = M * d / 8;
-  finish.d8 = d / 8;
+  finish.n4 = M * d / 4;
+  finish.d4 = d / 4;
   finish.factor = w.w.factor;
-  finish.Wt = reinterpret_cast<const uint4*>(Wb);
-  finish.carry = w.w.carry;
-  finish.carry_n = w.w.carry_n;
-  finish.k = static_cast<int>(k);
+  finish.add = reinterpret_cast<const uint2*>(w.w.add);
   finish.terms = w.w.terms;
   finish.stats = stats;
-  finish.out = reinterpret_cast<uint4*>(dH);
+  finish.out = reinterpret_cast<uint2*>(dH);
   return from_cuda(gemm_store_plus_rows(cx, w.w.kept, w.w.scaled, dW, nullptr, nullptr, int(rows), int(d), int(V),
                                         finish));
 }

@@ -242,10 +242,10 @@ struct DistillWork {
   // listed entries of kept alone, and what bf16 takes from scaled
   __nv_bfloat16* kept;
   float* factor;
-  __nv_bfloat16* add;  // or null: left to SplitDh, by its list
-  float2* carry;       // [M][k]
-  int* carry_n;        // [M]
+  __nv_bfloat16* add;
   __nv_bfloat16* scaled;
+  float2* carry;          // [M][k], or null.  Else add is left to gemm_splitk, by this list
+  int* carry_n;           // [M]
 };
 struct DistillOut {
   float* stats;     // or null: the shares stay in DistillWork::terms
@@ -263,10 +263,20 @@ cudaError_t gemm_group_scaled_bwd(const LaunchCtx& c, const __nv_bfloat16* E, co
                                   const __nv_bfloat16* Wt, const __nv_bfloat16* add, const __nv_bfloat16* scaled,
                                   __nv_bfloat16* dH, __nv_bfloat16* dW, int M, int rows, int d, int V);
 
+// out[m] = bf16(sum of factor times row of Wt over list[m][0 .. n[m])), rows of 8 d8
+struct RowSums {
+  const float2* list;  // [M][k]: a factor and, as its bits, a row
+  const int* n;        // [M]
+  int k;
+  const uint4* Wt;
+  int64_t n8, d8;      // n8 = M d8
+  uint4* out;
+};
 // parts_buf [parts][M rounded up to 256][N] fp32 (+)= the K ranges of A B, A
-// [M][K], B [K][N] (gemm_splitk.cuh); parts <= the k-blocks of 64 in K
+// [M][K], B [K][N] (gemm_splitk.cuh); parts <= the k-blocks of 64 in K; beside them
+// the sums, if there are any
 cudaError_t gemm_splitk(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_bfloat16* B, float* parts_buf, int parts,
-                        bool accumulate, int M, int N, int K);
+                        bool accumulate, int M, int N, int K, const RowSums& sums = RowSums{});
 
 // dL chunk = (softmax - onehot) / M for vocabulary rows [v0, v0 + Vc).
 cudaError_t gemm_ce_grad(const LaunchCtx& c, const __nv_bfloat16* H, const __nv_bfloat16* Wt_chunk,
@@ -309,16 +319,13 @@ cudaError_t gemm_group_policy_bwd(const LaunchCtx& c, const __nv_bfloat16* dL, c
                                   const uint32_t* slot, const float* rows, int M, int d, int Vc);
 //   (slot null: dWc = dL^T H).  It can take on the end of a split data gradient:
 struct SplitDh {
-  const float4* parts;  // [num][stride4], of which 2 n8 are used
+  const float4* parts;  // [num][stride4], of which n4 are used
   int num;
-  int64_t stride4, n8, d8;
-  const float* factor;  // [n8 / d8]
-  const uint4* Wt;      // [.][d8], bf16
-  const float2* carry;  // [n8 / d8][k], of which carry_n[m] are used: a factor and, as bits, a row of Wt
-  const int* carry_n;
-  int k;
-  uint4* out;           // bf16
-  const float4* terms;  // [n8 / d8], or null: their sum to stats
+  int64_t stride4, n4, d4;
+  const float* factor;  // [n4 / d4]
+  const uint2* add;     // bf16
+  uint2* out;           // bf16
+  const float4* terms;  // [n4 / d4], or null: their sum to stats
   float* stats;
 };
 cudaError_t gemm_store_plus_rows(const LaunchCtx& c, const __nv_bfloat16* dL, const __nv_bfloat16* H,

@@ -407,7 +407,7 @@ constexpr int kRowThreads = 128, kFewRowThreads = 512;
 // 1.0, 1.0 and 1.05; with a factor for dH that makes the largest entry exact and
 // nothing carried 1.4, 5.9 and 24.  Entries below kCarried of the row's largest stay
 // out: all together they are off by 2^-13 of it (k = 256).  A step of 136 tokens, d =
-// 1024, V = 32000, k = 32 66.5 to 69 us, of 4096, d = 2048, V = 128256 2 % more
+// 1024, V = 32000, k = 32 66.6 to 68.4 us, of 4096, d = 2048, V = 128256 2 % more
 // with k = 64, 7 % with k = 256.
 constexpr float kCarried = 0x1p-9f;
 
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
         to[M * (d / 8) + i] = make_uint4(pack_bf16x2(low[0], low[1]), pack_bf16x2(low[2], low[3]),
                                          pack_bf16x2(low[4], low[5]), pack_bf16x2(low[6], low[7]));
     }
-    if (w.add == nullptr) {  // few tokens: left to the kernel that ends dH, beside the weight gradient's tiles
+    if (w.carry != nullptr) {  // few tokens: left to gemm_splitk
       for (int j = tid; j < carry_n; j += kThreads)
         w.carry[m * k + j] = make_float2(carry[j], __int_as_float(carry_id[j]));
       if (tid == 0) w.carry_n[m] = carry_n;

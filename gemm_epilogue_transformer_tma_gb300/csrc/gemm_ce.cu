@@ -50,7 +50,7 @@ cudaError_t gemm_logit_stats(const LaunchCtx& c, const __nv_bfloat16* H, const _
 }
 
 cudaError_t gemm_splitk(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_bfloat16* B, float* parts_buf, int parts,
-                        bool accumulate, int M, int N, int K) {
+                        bool accumulate, int M, int N, int K, const RowSums& sums) {
   using L = SplitKSmem;
   SplitKArgs g{};
   g.M = M;
@@ -61,6 +61,7 @@ cudaError_t gemm_splitk(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_b
   g.parts = parts;
   g.rows = g.tiles_m * BM2;
   g.beta = accumulate ? 1 : 0;
+  g.sums = sums;
   if (parts < 1 || parts > g.num_kb || !make_operand_maps(&g.A, &g.B, A, false, B, true, M, N, K, 128) ||
       !make_tmap_store_f32(&g.out, parts_buf, N, uint64_t(parts) * g.rows, N))
     return cudaErrorInvalidValue;
@@ -68,7 +69,8 @@ cudaError_t gemm_splitk(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_b
   const cudaError_t e = allow_smem(gemm_splitk_kernel, L::TOTAL, smem_ok);
   if (e != cudaSuccess) return e;
   KernelCtl ctl{c.status, c.timeout_ns, c.skip_first_stage};
-  return launch_chained(c, gemm_splitk_kernel, dim3(2 * g.tiles_m * g.tiles_n * parts), dim3(L::THREADS), L::TOTAL, g,
+  const int threads = sums.n8 > 0 ? L::THREADS : L::THREADS - 32 * L::SUM_WARPS;
+  return launch_chained(c, gemm_splitk_kernel, dim3(2 * g.tiles_m * g.tiles_n * parts), dim3(threads), L::TOTAL, g,
                         ctl);
 }
 
@@ -98,7 +100,7 @@ cudaError_t gemm_store_plus_rows(const LaunchCtx& c, const __nv_bfloat16* dL, co
   const int clusters = std::max(1, std::min(g.tiles_m * g.tiles_n, pairs));
   // Without a data gradient to finish its warps are left out: the policy loss's own kernel for that then finds
   // the registers to start beside this one (64 tokens, d = 1024, V = 32000 72.7 us, with idle warps 78.2).
-  const int threads = dh.n8 > 0 ? L::THREADS : L::THREADS - 32 * L::DH_WARPS;
+  const int threads = dh.n4 > 0 ? L::THREADS : L::THREADS - 32 * L::DH_WARPS;
   return launch_chained(c, gemm_dw_kernel, dim3(2 * clusters), dim3(threads), L::TOTAL, g, ctl);
 }
 

@@ -10,7 +10,7 @@
 // dL [M][Vc] and H [M][d] bf16 are both read MN-major.  rows fp32 [tokens][d]
 // and slot [Vc] as EpiStorePlusRows; slot may be null: no rows (distillation).
 // Four more warps finish a split data gradient beside that, dH[m] = bf16(factor[m]
-// sum of the parts + sum_j carry[m][j] Wt[j's row]), and a sum over its rows (distillation, 136 tokens: 10 us as a
+// sum of the parts + add[m]), and a sum over its rows (distillation, 136 tokens: 10 us as a
 // kernel of its own).
 #pragma once
 
@@ -67,38 +67,23 @@ __device__ __forceinline__ void sum_terms(const float4* terms, int64_t M, int la
       if (lane == i) stats[i] = exact_value(hi[i], lo[i]);
 }
 
-// eight columns to a thread
+// four columns to a thread
 __device__ __forceinline__ void finish_dh(const SplitDh& h, int64_t first, int64_t step) {
-  for (int64_t i = first; i < h.n8; i += step) {
-    float s[8] = {}, a[8] = {};
-#pragma unroll 4
-    for (int q = 0; q < h.num; ++q) {
-      const float4 x = h.parts[q * h.stride4 + 2 * i], y = h.parts[q * h.stride4 + 2 * i + 1];
-      s[0] += x.x;
-      s[1] += x.y;
-      s[2] += x.z;
-      s[3] += x.w;
-      s[4] += y.x;
-      s[5] += y.y;
-      s[6] += y.z;
-      s[7] += y.w;
-    }
-    const int64_t m = i / h.d8;
-    const float f = h.factor[m];
-    const uint4* w = h.Wt + (i - m * h.d8);
-    const int n = h.carry_n[m];
+  for (int64_t i = first; i < h.n4; i += step) {
+    const float4* p = h.parts + i;
+    float4 s = *p;
 #pragma unroll 8
-    for (int j = 0; j < n; ++j) {
-      const float2 e = h.carry[m * h.k + j];
-      float u[8];
-      unpack_bf16x8(__ldg(w + __float_as_int(e.y) * h.d8), u);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) a[c] = fmaf(e.x, u[c], a[c]);
+    for (int q = 1; q < h.num; ++q) {
+      const float4 x = p[q * h.stride4];
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
     }
-#pragma unroll
-    for (int c = 0; c < 8; ++c) a[c] = fmaf(s[c], f, a[c]);
-    h.out[i] = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
-                          pack_bf16x2(a[6], a[7]));
+    const float f = h.factor[i / h.d4];
+    const uint2 a = h.add[i];
+    h.out[i] = make_uint2(pack_bf16x2(fmaf(s.x, f, bf16_lo(a.x)), fmaf(s.y, f, bf16_hi(a.x))),
+                          pack_bf16x2(fmaf(s.z, f, bf16_lo(a.y)), fmaf(s.w, f, bf16_hi(a.y))));
   }
 }
 
@@ -254,7 +239,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DwSmem::THREADS, 1)
   } else if (warp >= 2 + L::EPI_WARPS) {
     constexpr int N = 32 * L::DH_WARPS;
     if (g.dh.terms != nullptr && blockIdx.x == 0 && warp == 2 + L::EPI_WARPS) {
-      sum_terms(g.dh.terms, g.dh.n8 / g.dh.d8, lane, g.dh.stats);
+      sum_terms(g.dh.terms, g.dh.n4 / g.dh.d4, lane, g.dh.stats);
     }
     finish_dh(g.dh, blockIdx.x * static_cast<int64_t>(N) + threadIdx.x - (L::THREADS - N),
               gridDim.x * static_cast<int64_t>(N));

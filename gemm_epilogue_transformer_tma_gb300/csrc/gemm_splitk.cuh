@@ -10,16 +10,20 @@
 // A K-major [M][K] bf16, B MN-major [K][N] bf16.  One unit per cluster of two
 // CTAs: warp 0 TMA, warp 1 TMEM and MMA (both converged, one elected lane),
 // warps 2-5 store the accumulator, or add it to the slice (beta) with TMA
-// reductions, one per element and launch.
+// reductions, one per element and launch.  Eight more sum rows of Wt beside that
+// (distillation: what bf16 takes from dL's listed entries; in the row kernel before
+// it 6 us of 136 tokens, d = 1024, k = 32).
 #pragma once
 
+#include "coda_internal.h"
 #include "gemm_tc2.cuh"
 
 namespace coda {
 
 struct SplitKSmem {
   static constexpr int STAGES = 6;
-  static constexpr int THREADS = 192;
+  static constexpr int SUM_WARPS = 8;
+  static constexpr int THREADS = 192 + 32 * SUM_WARPS;
   static constexpr int A_BYTES = 128 * BK * 2;
   static constexpr int STAGE_BYTES = 2 * A_BYTES;
   static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
@@ -36,7 +40,28 @@ struct SplitKArgs {
   int tiles_m, tiles_n, parts;
   int rows;               // of a slice: M rounded up to whole tiles
   int beta;
+  RowSums sums;
 };
+
+// eight columns to a thread
+__device__ __forceinline__ void sum_rows(const RowSums& r, int64_t first, int64_t step) {
+  for (int64_t i = first; i < r.n8; i += step) {
+    const int64_t m = i / r.d8;
+    const uint4* w = r.Wt + (i - m * r.d8);
+    const int n = r.n[m];
+    float a[8] = {};
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) {
+      const float2 e = r.list[m * r.k + j];
+      float u[8];
+      unpack_bf16x8(__ldg(w + __float_as_int(e.y) * r.d8), u);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) a[c] = fmaf(e.x, u[c], a[c]);
+    }
+    r.out[i] = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                          pack_bf16x2(a[6], a[7]));
+  }
+}
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SplitKSmem::THREADS, 1)
     gemm_splitk_kernel(const __grid_constant__ SplitKArgs g, const KernelCtl ctl) {
@@ -169,6 +194,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SplitKSmem::THREADS,
         if (!mbar_wait_timeout(drain, 0, ctl.timeout_ns) && lane == 0) atomicOr(ctl.status, DEV_ERR_TIMEOUT_DRAIN);
       }
     }
+  } else if (warp >= 6) {
+    constexpr int N = 32 * L::SUM_WARPS;
+    sum_rows(g.sums, blockIdx.x * static_cast<int64_t>(N) + threadIdx.x - (L::THREADS - N),
+             gridDim.x * static_cast<int64_t>(N));
   } else {
     const int quad = warp & 3;
     const uint32_t slots = smem_u32(smem + L::RING_BYTES) + static_cast<uint32_t>((warp - 2) * 2 * L::SLOT_BYTES);
