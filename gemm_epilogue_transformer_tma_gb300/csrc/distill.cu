@@ -149,7 +149,10 @@ __device__ __forceinline__ float2 exp2_exact(float y, float y_lo) {
 // together, which entries lie in which block of the vocabulary.  A CTA to 32
 // rows, a warp to one.  The targets and their sum are held in two fp32 numbers,
 // because r = 1 - P loses the digits of P where the teacher is nearly certain.
-// 4096 rows of 64: 17 us, 136 of 32: 10, both beside the first tiles of the logits.
+// 2048 rows of 64 tokens spread over 65536: 16 us, 136 of 32: 11, both beside the
+// first tiles of the logits.  The search for repeated tokens goes over a block's
+// entries for each of them: 136 rows of 64, V = 128256, take 14 us where the tokens
+// are spread evenly and 69 where they are small (token = V^u), 128 of V = 1000 157 and 621.
 constexpr int kListThreads = 1024;
 constexpr int kListBlocks = 4096;  // vocabulary blocks sorted at a time: V = 524288
 
@@ -398,7 +401,9 @@ enum RowGrads { NO_GRADS, GRADS_ONCE, GRADS_TWICE };
 // A row's loss and what its gradients need.  A row to a CTA; the last to end adds
 // up the statistics, in a fixed order.  512 threads where rows are few (the same
 // for both forms of a size: the loss has the same bits with gradients and without).
-// 4096 rows of V = 128256, d = 2048 27 us, 136 of V = 32000, d = 1024 5.5: latency.
+// 2048 rows of V = 65536: 14 us, 17 with gradients and 62 more for the rows of Wt that
+// 64 entries of each carry to dH (d = 2048: 268 MB, DRAM at 51 %); 136 rows of V =
+// 32000 6: latency.
 constexpr int kRowThreads = 128, kFewRowThreads = 512;
 // What bf16 takes from the listed entries of dL is carried to dH in fp32, as a sum of
 // rows of Wt.  A row of dL sums to 0, so a mean that the rows of the head share leaves
@@ -517,7 +522,9 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
     }
     on = block_reduce<kWarps>(on, exact_part, AddExact());
     on = add_ordered(on.x, on.y);
-    // ex2's results are low by 5.1e-8 to 5.6e-8 on average (five sizes, d from 312 to 4096)
+    // ex2's results are low by 5.1e-8 to 5.6e-8 on average (five sizes, d from 312 to
+    // 4096; 5.0e-8 over 2^26 arguments in [-8, 0)).  One alone lies between 1.4e-7 below
+    // and 6.2e-8 above: R of few tokens, or of many equal ones, may be as far off.
     constexpr float kEx2Low = 5.3e-8f;
     const float rest_ref = rest.s * ex2_f(down);
     const float2 off = make_float2(rest_ref, rest_ref * kEx2Low);
