@@ -66,12 +66,12 @@ struct AddSums {
   }
 };
 
-// a b, with its rounding error
+// a b, with its rounding error (exact with a fused multiply-add)
 __device__ __forceinline__ float2 mul_exact(float a, float b) {
   const float h = a * b;
   return make_float2(h, fmaf(a, b, -h));
 }
-// a + b for |a| >= |b|, with its rounding error
+// a + b for |a| >= |b|, with its rounding error (Dekker's fast two-sum)
 __device__ __forceinline__ float2 add_ordered(float a, float b) {
   const float h = a + b;
   return make_float2(h, b - (h - a));
@@ -124,7 +124,7 @@ __device__ __forceinline__ float2 exp_scaled(float hi, float lo, float n) {
 __device__ __forceinline__ float2 exp_exact(float x, float x_lo) {
   if (!(x > -87.f)) return make_float2(expf(x), 0.f);  // 0, or NaN
   if (x > 88.f) return make_float2(expf(x), 0.f);
-  // ln 2 in three parts: n times the first is exact
+  // ln 2 in three parts (Cody and Waite): n times the first is exact
   constexpr float kA = 0.693145751953125f;  // 16 bits
   constexpr float kB = static_cast<float>(kLn2 - double(kA));
   constexpr float kC = static_cast<float>(kLn2 - double(kA) - double(kB));

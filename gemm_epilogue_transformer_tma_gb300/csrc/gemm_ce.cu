@@ -69,6 +69,7 @@ cudaError_t gemm_splitk(const LaunchCtx& c, const __nv_bfloat16* A, const __nv_b
   const cudaError_t e = allow_smem(gemm_splitk_kernel, L::TOTAL, smem_ok);
   if (e != cudaSuccess) return e;
   KernelCtl ctl{c.status, c.timeout_ns, c.skip_first_stage};
+  // idle warps would keep what follows from starting (gemm_store_plus_rows)
   const int threads = sums.n8 > 0 ? L::THREADS : L::THREADS - 32 * L::SUM_WARPS;
   return launch_chained(c, gemm_splitk_kernel, dim3(2 * g.tiles_m * g.tiles_n * parts), dim3(threads), L::TOTAL, g,
                         ctl);

@@ -577,8 +577,8 @@ __device__ __forceinline__ float ex2_f(float x) {
   return y;
 }
 
-// a + b and its rounding error, added to lo: sums that nearly cancel keep the
-// digits fp32 drops (fp64 units are scarce on this GPU: the same kernel in
+// a + b and its rounding error (Knuth's two-sum), added to lo: sums that nearly
+// cancel keep the digits fp32 drops (fp64 units are scarce on this GPU: the same kernel in
 // fp64 took 10 us for 136 rows)
 __device__ __forceinline__ void add_exact(float& hi, float& lo, float b, float b_lo) {
   const float s = hi + b;

@@ -106,3 +106,28 @@ def test_temperatures_that_flatten_every_row(mode, M, d, V):
     them.  The gradients, 1 / T of others, are fp32 numbers at 1e30."""
     for T, grads in ((1e30, True), (3e36, False), (3e38, False)):
         make(M, d, V, 7, mode, T=T, grads=grads).run().grade()
+
+
+@pytest.mark.parametrize("M,d", [(64, 64), (300, 64), (1100, 2560)])
+def test_the_mass_that_a_list_leaves(M, d):
+    """r = 1 - P down to 2^-29, of lists whose probabilities lie between 1e-6 and 1:
+    as good as the sum of their exponentials, 2^-34.5 of P.  The student has all on
+    the list, so that dL off it sums to -weight r; it is read off column 1 of dHs
+    (_readable), with four roundings to bf16 of terms of one sign."""
+    V, k = 1048, 40
+    g = torch.Generator().manual_seed(M)
+    H, W = torch.zeros(M, d), torch.zeros(V, d)
+    H[:, 0], W[:k, 0], W[k:, 1] = 1.0, 100.0, 1.0
+    p = torch.rand(M, k - 1, generator=g, dtype=torch.float64) ** 3 + 1e-5
+    left = 2.0 ** (-29 + 6 * torch.rand(M, 1, generator=g, dtype=torch.float64))
+    val = torch.log(p / p.sum(1, keepdim=True) * (1 - 1e-6)).float()
+    last = torch.log(1 - left - val.double().exp().sum(1, keepdim=True)).float()
+    val = torch.cat([val, last], 1).cuda()
+    ids = torch.arange(k, dtype=I32, device="cuda").expand(M, k).contiguous()
+    w = torch.full((M,), 1 / M, device="cuda")
+    c = Call(H.to(BF).cuda(), W.to(BF).cuda(), ids, val, w, R.TAIL).run()
+    r = 1 - val.double().exp().sum(1)
+    assert r.min() > 2.0 ** -30 and r.max() < 2.0 ** -22
+    got = -c.dH[:, 1].double() / w.double()
+    assert ((got - r).abs() <= 2.0 ** -34.5 + 4 * 2.0 ** -8 * r).all()
+    assert_device_ok()
