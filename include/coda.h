@@ -874,15 +874,15 @@ size_t coda_lmhead_distill_workspace_bytes(int64_t M, int64_t d, int64_t V, int6
  * temperature ((P + r) q_v - t_v) on the list, weight / temperature q_v (P + r -
  * r / R) off it; dHs = dL Wt, dWt = dL^T Hs.  dL is held as a bf16 matrix and an
  * fp32 factor per row.  For dHs what that takes from the listed entries (of 2^-9 of
- * the row's largest and more) is added in fp32, so that dHs carries its own rounding
- * and that of the entries off the list, each rounded by itself, whatever mean the
- * rows of Wt share.  For dWt the factor is moved, by 2^-8 at most, so that the row's
- * largest entry is not rounded, and the contraction finds it in a copy of Hs, in
- * bf16, up to 64 rows in twice the digits.  Where that entry outweighs its row, and
- * a token's rows do not cancel, the error of dWt is that of rounding it alone up to
- * 64 rows; of more it carries the rounding of the scaled Hs as well (1.4 times the
- * error of rounding it alone, on average).  The other listed entries are rounded
- * once, entries off the list twice.
+ * the row's largest listed one and more) is added in fp32, so that dHs carries its
+ * own rounding and that of the entries off the list, each rounded by itself,
+ * whatever mean the rows of Wt share.  For dWt the factor is moved, by 2^-8 at most,
+ * so that the row's largest listed entry is not rounded, and the contraction finds
+ * the factor in a copy of Hs, in bf16, up to 64 rows in twice the digits.  Where
+ * that entry outweighs its row, and a token's rows do not cancel, the error of dWt
+ * is that of rounding it alone up to 64 rows; of more it carries the rounding of the
+ * scaled Hs as well (1.4 times the error of rounding it alone, on average).  The
+ * other listed entries are rounded once, entries off the list twice.
  * Logits over the temperature that leave fp32's range give NaN; gradients want
  * weight / temperature times dL's entries in its normal range.
  * Hs bf16 [M][d], Wt bf16 [V][d], ids int32 [M][k], val fp32 [M][k], weight fp32
