@@ -349,6 +349,15 @@ __global__ void __launch_bounds__(kListThreads) distill_list_kernel(const Distil
   }
 }
 
+// log(a / b) for |u| > a / 2, u = b - a.  The logarithms of a and b apart round by
+// 2^-24 of their own size, 1e-6 of a loss whose targets are 1e-5; lb = log b stays
+// where a quotient could overflow or b has underflowed.
+__device__ __forceinline__ float log_ratio(float a, float b, float u, float lb) {
+  if (u > 0.f && u < 0x1p24f * a) return -log1pf(u / a);
+  if (u < 0.f && b > 0x1p-100f && a < 0x1p20f) return logf(a / b);
+  return logf(a) - lb;
+}
+
 // a log(a / b) - a + b; u = b - a; lb = log b, good where b itself has underflowed
 __device__ __forceinline__ float phi(float a, float b, float u, float lb) {
   if (a == 0.f) return b;
@@ -366,13 +375,13 @@ __device__ __forceinline__ float phi(float a, float b, float u, float lb) {
     s = fmaf(s, v, 1.f / 3.f);
     return a * w * fmaf(-2.f * v, s, z);
   }
-  return a * (logf(a) - lb) + u;
+  return fmaf(a, log_ratio(a, b, u, lb), u);
 }
 
 // a log(a / b) alone
-__device__ __forceinline__ float t_log_ratio(float a, float u, float lb) {
+__device__ __forceinline__ float t_log_ratio(float a, float b, float u, float lb) {
   if (a == 0.f) return 0.f;
-  return fabsf(u) <= 0.5f * a ? -a * log1pf(u / a) : a * (logf(a) - lb);
+  return a * (fabsf(u) <= 0.5f * a ? -log1pf(u / a) : log_ratio(a, b, u, lb));
 }
 
 // psum of some blocks together, in units of 2^n
@@ -547,7 +556,7 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(const DistillIn 
         const float lq = (x[i] - log2_S) * kLn2f;
         const float2 own = div_exact(e[i], both, inv);
         const float u = (own.x - t[i].x) + (own.y - t[i].y);
-        row.a += direct ? t_log_ratio(t[i].x, u, lq) : phi(t[i].x, own.x, u, lq);
+        row.a += direct ? t_log_ratio(t[i].x, own.x, u, lq) : phi(t[i].x, own.x, u, lq);
         if (t[i].x != 0.f) row.b = fmaf(-t[i].x, lq, row.b);
         q[i] = excess == 0.f ? u : fmaf(P + r, own.x, -t[i].x);  // d loss / d z; P + r = 1
         row.top = fmaxf(row.top, fabsf(q[i]));

@@ -131,3 +131,28 @@ def test_the_mass_that_a_list_leaves(M, d):
     got = -c.dH[:, 1].double() / w.double()
     assert ((got - r).abs() <= 2.0 ** -34.5 + 4 * 2.0 ** -8 * r).all()
     assert_device_ok()
+
+
+@pytest.mark.parametrize("M", [24, 200])
+@pytest.mark.parametrize("mode", [R.LISTED, R.TAIL])
+@pytest.mark.parametrize("ratio", [1.6, 0.4])
+def test_small_targets_far_from_the_student(ratio, mode, M):
+    """Targets of 1e-5, q / ratio.  u = q - t is good to 2^-32 of
+    t.  log(t / q) from log1p(u / t) or the quotient is off by 4 2^-24 at most, and a
+    term of the loss, t (log(t / q) - 1 + q / t) >= 0.13 t, by 5 2^-24 t; with LISTED
+    t log(t / q) itself, the more so.  Off the list the powers of two are off by 2^-22
+    together, which the loss meets times R - r (TAIL) or times the sum of t (LISTED);
+    the fp32 sums by 2^-22."""
+    V, k = 60000, 40
+    H, W, _ = R.grid_inputs(M, 64, V, sure=0.5, seed=M)
+    H = (H.float() / 4).to(BF)
+    ids = torch.randint(0, V, (M, k), generator=torch.Generator().manual_seed(5)).cuda()
+    lq = torch.log_softmax(R.logits(H, W), 1).gather(1, ids)
+    val = (lq - torch.log(torch.tensor(ratio, dtype=torch.float64))).float()
+    c = Call(H, W, ids.to(I32), val, None, mode, grads=False).run()
+    r = R.distill(H, W, c.ids, val, None, mode)
+    t, q = val.double().exp().sum(1), lq.exp().sum(1)
+    off = (q - t).abs() if mode == R.TAIL else t
+    bar = 5 * 2.0 ** -24 * t + 2.0 ** -22 * (off + r["loss"].abs())
+    assert ((c.loss.double() - r["loss"]).abs() <= bar).all()
+    assert_device_ok()
